@@ -15,6 +15,10 @@ Both layouts also come as gemm1 of the expert MLP with its silu_mul epilogue
 (third reference page, the MoE gemm1/gemm2 pull request, section "Changes"):
 ``out = silu(gate) * up`` with gate and up the two halves of ``A . B[g]^T``,
 and as an MXFP8 GEMM (one E8M0 scale per 32 K elements of every row of A and B).
+
+``serving.py`` adds what decoding from the same weights needs: a top-k router,
+the whole expert layer for a few tokens, and 8-bit integer products with one
+scale per token and per output channel.
 """
 from __future__ import annotations
 
@@ -33,7 +37,10 @@ __all__ = [
     "raw_mx_contiguous", "raw_mx_masked",
     "grouped_mxfp4_gemm_contiguous", "grouped_mxfp4_gemm_masked", "fp4_quantize_mx_1x32",
     "raw_mx4_contiguous", "raw_mx4_masked",
-    "OUT_BF16", "OUT_F16", "IN_F32", "IN_BF16",
+    "int8_quantize_token_device", "int8_gemm", "int8_linear", "int8_linear_workspace_bytes",
+    "grouped_int8_gemm_contiguous", "grouped_int8_gemm_masked",
+    "moe_topk", "moe_fp8_layer", "moe_int8_layer", "moe_layer_workspace_bytes",
+    "OUT_BF16", "OUT_F16", "IN_F32", "IN_BF16", "IN_F16",
     "set_tile_order", "set_tile_shape", "set_grid_limit", "TILE_AUTO", "TILE_128x256", "TILE_256x256",
 ]
 
@@ -41,9 +48,22 @@ __all__ = [
 # build of the CPU tests); by default the in-tree libgfg.so.
 _LIB_PATH = os.environ.get("GFG_LIBRARY") or os.path.join(os.path.dirname(os.path.abspath(__file__)), "libgfg.so")
 OUT_BF16, OUT_F16 = 0, 1
-IN_F32, IN_BF16 = 0, 1
+IN_F32, IN_BF16, IN_F16 = 0, 1, 2
 _STATUS = {0: "GFG_OK", 1: "GFG_EINVAL", 2: "GFG_EUNSUPPORTED", 3: "GFG_EHIP", 4: "GFG_ERANGE"}
 _lib = None
+
+# the calls of serving.py, which needs torch at import: loaded on first use
+_SERVING = ("int8_quantize_token_device", "int8_gemm", "int8_linear", "int8_linear_workspace_bytes",
+            "grouped_int8_gemm_contiguous", "grouped_int8_gemm_masked",
+            "moe_topk", "moe_fp8_layer", "moe_int8_layer", "moe_layer_workspace_bytes")
+
+
+def __getattr__(name):
+    if name not in _SERVING:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    from . import serving
+    globals()[name] = getattr(serving, name)
+    return globals()[name]
 
 
 class GfgError(RuntimeError):
@@ -92,6 +112,26 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     lib.fp8_quantize_weight_128x128.restype = ctypes.c_int
     lib.fp8_quantize_act_1x128_device.argtypes = [vp, i32, i32, i64, i64, vp, vp, vp]
     lib.fp8_quantize_act_1x128_device.restype = ctypes.c_int
+    f32 = ctypes.c_float
+    lib.int8_quantize_token_device.argtypes = [vp, i32, i64, i64, vp, vp, vp]
+    lib.int8_quantize_token_device.restype = ctypes.c_int
+    lib.int8_gemm.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, i64, i32, vp]
+    lib.int8_gemm.restype = ctypes.c_int
+    lib.int8_linear_workspace_bytes.argtypes = [i64, i64]
+    lib.int8_linear_workspace_bytes.restype = i64
+    lib.int8_linear.argtypes = [vp, i32, vp, vp, vp, vp, i64, i64, i64, i32, vp, i64, vp]
+    lib.int8_linear.restype = ctypes.c_int
+    lib.grouped_int8_gemm_contiguous.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, i64, i32, i32, vp]
+    lib.grouped_int8_gemm_contiguous.restype = ctypes.c_int
+    lib.grouped_int8_gemm_masked.argtypes = [vp, vp, vp, vp, vp, vp, i32, i64, i64, i64, i32, vp]
+    lib.grouped_int8_gemm_masked.restype = ctypes.c_int
+    lib.moe_topk.argtypes = [vp, i32, vp, vp, vp, i64, i64, i64, i32, i32, f32, vp]
+    lib.moe_topk.restype = ctypes.c_int
+    lib.moe_layer_workspace_bytes.argtypes = [i64, i64, i64]
+    lib.moe_layer_workspace_bytes.restype = i64
+    for layer in (lib.moe_fp8_layer, lib.moe_int8_layer):
+        layer.argtypes = [vp, i32, vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, i64, vp, i64, vp]
+        layer.restype = ctypes.c_int
     lib.grouped_fp8_last_error.argtypes = []
     lib.grouped_fp8_last_error.restype = ctypes.c_char_p
     lib.grouped_fp8_set_tile_order.argtypes = [i32, i32]

@@ -31,7 +31,8 @@ HIP_FLAGS = ["-O3", "-std=c++17", "-fPIC", "-fvisibility=hidden", f"--offload-ar
 
 
 # The device sources, compiled one object each.
-HIP_SOURCES = ["gfg_gemm.hip", "gfg_gemm256.hip", "gfg_quant.hip", "gfg_ceiling.hip"]
+HIP_SOURCES = ["gfg_gemm.hip", "gfg_gemm256.hip", "gfg_quant.hip", "gfg_int8.hip", "gfg_moe.hip",
+               "gfg_ceiling.hip"]
 
 
 def build(verbose: bool = False) -> str:

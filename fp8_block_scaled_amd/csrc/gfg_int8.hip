@@ -1,0 +1,466 @@
+// 8-bit integer matrix product with one scale per token and per output
+// channel, and the token quantizer that makes its operand, for gfx950 (MI355X).
+//
+//   q[m, k] = rint(x[m, k] * (127 / amax[m])),  s[m] = amax[m] / 127,
+//   amax[m] = max(max_k |x[m, k]|, 2^-100)
+//   d[m, n] = (sum_k a[m, k] b[n, k]) * a_scale[m] * b_scale[n] (+ bias[n])
+//
+// The sums are 32-bit integers, which v_mfma_i32_16x16x64_i8 accumulates
+// exactly (K < 2^17, so |sum| <= 2^14 K < 2^31), so neither the order of the
+// K steps nor a split of K changes a bit; the two scales are applied in fp32
+// and the output is rounded once.
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "gfg.h"
+#include "gfg_device.h"
+#include "gfg_internal.h"
+
+namespace gfg {
+namespace {
+
+typedef int v4i __attribute__((ext_vector_type(4)));
+typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+
+// ------------------------------------------------------------------ token quantizer
+//
+// One pass over memory: a row's 16-byte chunks stay in registers between the
+// maximum and the encoding (rows longer than kHeld chunks a lane read the rest
+// again, from the cache).  LPR lanes share a row: a wave for short rows, a
+// workgroup for long ones, whose maximum then crosses the waves through LDS.
+constexpr int QT = 256;
+constexpr int kHeld = 4;
+
+template <typename T> struct Chunk;            // 8 elements of a row
+template <> struct Chunk<__bf16> {
+    u32x4 w;
+    __device__ __forceinline__ void load(const __bf16* p) { w = *reinterpret_cast<const u32x4*>(p); }
+    __device__ __forceinline__ float at(int i) const {
+        return __uint_as_float((i & 1) ? w[i >> 1] & 0xFFFF0000u : w[i >> 1] << 16);
+    }
+};
+template <> struct Chunk<_Float16> {
+    u32x4 w;
+    __device__ __forceinline__ void load(const _Float16* p) { w = *reinterpret_cast<const u32x4*>(p); }
+    __device__ __forceinline__ float at(int i) const {
+        return float(__builtin_bit_cast(_Float16, uint16_t(w[i >> 1] >> (16 * (i & 1)))));
+    }
+};
+template <> struct Chunk<float> {
+    u32x4 w[2];
+    __device__ __forceinline__ void load(const float* p) {
+        w[0] = reinterpret_cast<const u32x4*>(p)[0];
+        w[1] = reinterpret_cast<const u32x4*>(p)[1];
+    }
+    __device__ __forceinline__ float at(int i) const { return __uint_as_float(w[i >> 2][i & 3]); }
+};
+
+// Maximum of the magnitude bits: for finite floats the integer order is the
+// order of the magnitudes, and an infinity or a NaN lands above all of them.
+template <typename T>
+__device__ __forceinline__ uint32_t chunk_amax(const Chunk<T>& c) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(c.at(i)) & 0x7FFFFFFFu);
+    return m;
+}
+
+// Eight codes; |x * r| <= 127 up to one rounding, so rint never leaves [-127, 127].
+template <typename T>
+__device__ __forceinline__ u32x2 chunk_encode(const Chunk<T>& c, float r) {
+    u32x2 o = {0u, 0u};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int v = int(__builtin_rintf(c.at(i) * r));
+        o[i >> 2] |= uint32_t(v & 0xFF) << (8 * (i & 3));
+    }
+    return o;
+}
+
+// The scale of a row with magnitude bits ab, and the factor 127 / amax of its codes.
+__device__ __forceinline__ void row_scale(uint32_t ab, float* scale, float* r) {
+    if (ab >= 0x7F800000u) {                   // a NaN or an infinity: no scale, codes 0
+        *scale = __uint_as_float(0x7FC00000u);
+        *r = 0.0f;
+    } else {
+        const float amax = fmaxf(__uint_as_float(ab), 0x1p-100f);
+        *scale = amax / 127.0f;
+        *r = 127.0f / amax;
+    }
+}
+
+template <typename T, int LPR>
+__global__ __launch_bounds__(QT) void quant_token_kernel(const T* __restrict__ x, uint8_t* __restrict__ q,
+                                                         float* __restrict__ scale, int64_t M, int K) {
+    constexpr int RPB = QT / LPR;              // rows per workgroup
+    __shared__ uint32_t part[QT / 64];
+    const int lane = threadIdx.x % LPR;
+    const int64_t m = int64_t(blockIdx.x) * RPB + threadIdx.x / LPR;
+    const bool live = m < M;                   // a whole wave (LPR >= 64) is live or not
+    const T* row = x + (live ? m : 0) * K;
+    const int chunks = K / 8;
+    Chunk<T> held[kHeld];
+    uint32_t ab = 0;
+#pragma unroll
+    for (int j = 0; j < kHeld; ++j)
+        if (lane + j * LPR < chunks) {
+            held[j].load(row + (lane + j * LPR) * 8);
+        }
+#pragma unroll
+    for (int j = 0; j < kHeld; ++j)
+        if (lane + j * LPR < chunks) ab = max(ab, chunk_amax(held[j]));
+    for (int c = lane + kHeld * LPR; c < chunks; c += LPR) {
+        Chunk<T> t;
+        t.load(row + c * 8);
+        ab = max(ab, chunk_amax(t));
+    }
+#pragma unroll
+    for (int w = 32; w >= 1; w >>= 1) ab = max(ab, uint32_t(__shfl_xor(int(ab), w, 64)));
+    if constexpr (LPR > 64) {
+        if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = ab;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < QT / 64; ++w) ab = max(ab, part[w]);
+    }
+    if (!live) return;
+    float s, r;
+    row_scale(ab, &s, &r);
+    if (lane == 0) scale[m] = s;
+    uint8_t* out = q + m * K;
+    const bool bad = r == 0.0f;                // 0 * infinity would be NaN
+#pragma unroll
+    for (int j = 0; j < kHeld; ++j)
+        if (lane + j * LPR < chunks)
+            *reinterpret_cast<u32x2*>(out + (lane + j * LPR) * 8) = bad ? u32x2{0u, 0u} : chunk_encode(held[j], r);
+    for (int c = lane + kHeld * LPR; c < chunks; c += LPR) {
+        Chunk<T> t;
+        t.load(row + c * 8);
+        *reinterpret_cast<u32x2*>(out + c * 8) = bad ? u32x2{0u, 0u} : chunk_encode(t, r);
+    }
+}
+
+template <typename T>
+void launch_quant(const void* x, uint8_t* q, float* scale, int64_t M, int K, hipStream_t s) {
+    // a wave for rows that it holds in registers (2048 elements), else a workgroup
+    if (K <= 64 * 8 * kHeld)
+        hipLaunchKernelGGL((quant_token_kernel<T, 64>), dim3(unsigned((M + 3) / 4)), dim3(QT), 0, s,
+                           static_cast<const T*>(x), q, scale, M, K);
+    else
+        hipLaunchKernelGGL((quant_token_kernel<T, QT>), dim3(unsigned(M)), dim3(QT), 0, s, static_cast<const T*>(x), q,
+                           scale, M, K);
+}
+
+// ------------------------------------------------------------------ tiled product
+//
+// 128 x 128 output tiles, four waves of 64 x 64 each (a 4 x 4 grid of 16 x 16
+// MFMA blocks), K in steps of 128 bytes through two 32 KB LDS stages filled by
+// direct-to-LDS loads.  LDS row R (128 bytes) holds its 16-byte chunks
+// XOR-swizzled by R & 7, so that the 16 rows that a fragment read touches
+// spread over all banks.  Rows past the operand's end and chunks past K lie
+// outside the buffer window, where the hardware returns zeros, so no size
+// needs its own path: zeros add nothing to an integer sum.
+constexpr int TM = 128, TN = 128, TK = 128;
+constexpr int TT = 256;
+constexpr uint32_t kOutside = 0x80000000u;     // past every buffer window used here (all below 2^31 bytes)
+
+enum Layout { DENSE = 0, CONTIG = 1, MASKED = 2 };
+
+struct I8Params {
+    const uint8_t* a;        // [rows][K] (masked: [G][rows][K])
+    const float* a_scale;    // [rows] (masked: [G][rows])
+    const uint8_t* b;        // [G][N][K]
+    const float* b_scale;    // [G][N]
+    const float* bias;       // [N] or null
+    const int32_t* meta;     // grouped_layout or masked_m
+    void* d;                 // [rows][N] (masked: [G][rows][N])
+    int64_t rows;
+    int N, K, G;
+    int m_tiles;             // row tiles (masked: per group)
+};
+
+// One output element row piece: columns n .. n+3 of a row, from the integer sums.
+template <typename OutT>
+__device__ __forceinline__ void store4(OutT* row, int n, int N, bool vec, const float (&v)[4]) {
+    typedef OutT o4 __attribute__((ext_vector_type(4)));
+    if (vec && n + 4 <= N) {
+        *reinterpret_cast<o4*>(row + n) = o4{OutT(v[0]), OutT(v[1]), OutT(v[2]), OutT(v[3])};
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (n + i < N) row[n + i] = OutT(v[i]);
+    }
+}
+
+template <int LAYOUT, typename OutT>
+__global__ __launch_bounds__(TT, 2) void int8_gemm_kernel(I8Params p) {
+    __shared__ __attribute__((aligned(1024))) uint8_t smem0[(TM + TN) * TK];
+    __shared__ __attribute__((aligned(1024))) uint8_t smem1[(TM + TN) * TK];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int l16 = lane & 15, lq = lane >> 4;
+    const int n0 = int(blockIdx.x) * TN;
+    const int mt = int(blockIdx.y);
+    int g = 0, row0, lim;
+    int64_t region = 0;
+    if (LAYOUT == MASKED) {
+        g = mt / p.m_tiles;
+        row0 = (mt - g * p.m_tiles) * TM;
+        int mm = p.meta[g];
+        mm = mm < 0 ? 0 : (mm > p.rows ? int(p.rows) : mm);
+        lim = min(TM, mm - row0);
+        region = int64_t(g) * p.rows;
+    } else {
+        row0 = mt * TM;
+        lim = int(p.rows - row0 < TM ? p.rows - row0 : TM);
+        if (LAYOUT == CONTIG) {
+            g = p.meta[row0];
+            if (g < 0 || g >= p.G) return;
+        }
+    }
+    if (lim <= 0) return;
+    g = __builtin_amdgcn_readfirstlane(g);
+    lim = __builtin_amdgcn_readfirstlane(lim);
+    const int64_t arow = region + row0;
+    const int ncols = min(TN, p.N - n0);
+    const auto ra = make_rsrc(p.a + arow * p.K, uint32_t(lim) * uint32_t(p.K));
+    const auto rb = make_rsrc(p.b + (int64_t(g) * p.N + n0) * p.K, uint32_t(ncols) * uint32_t(p.K));
+    GFG_LDS uint8_t* const buf0 = (GFG_LDS uint8_t*)smem0;
+    GFG_LDS uint8_t* const buf1 = (GFG_LDS uint8_t*)smem1;
+
+    // DMA chunk j (0..7) of a wave: LDS rows 8 (4 j + wave) .. +7 of the stage
+    // (A's 128 rows, then B's); lane i writes physical chunk i & 7 of row
+    // i >> 3 of them, the logical chunk (i & 7) ^ (i >> 3)
+    const int kc = ((lane & 7) ^ (lane >> 3)) * 16;
+    const uint32_t src0 = uint32_t(8 * wave + (lane >> 3)) * uint32_t(p.K) + uint32_t(kc);
+    auto issue = [&](GFG_LDS uint8_t* dst, int kb) {
+        const bool in = kb * TK + kc < p.K;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t off = src0 + uint32_t(kb) * TK + uint32_t(32 * (j & 3)) * uint32_t(p.K);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(j < 4 ? ra : rb, (GFG_LDS void*)(dst + (4 * j + wave) * 1024), 16,
+                                                     in ? off : kOutside, 0, 0, 0);
+        }
+    };
+    const int wm = (wave >> 1) * 64, wn = (wave & 1) * 64;
+    auto frag = [&](GFG_LDS uint8_t* src, int row, int chunk) {
+        return *reinterpret_cast<GFG_LDS v4i*>(src + (row + l16) * TK + ((chunk ^ (l16 & 7)) << 4));
+    };
+    v4i acc[4][4] = {};                        // [row block][column block]
+    auto compute = [&](GFG_LDS uint8_t* src) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            v4i af[4], bf[4];
+#pragma unroll
+            for (int f = 0; f < 4; ++f) af[f] = frag(src, wm + 16 * f, 4 * h + lq);
+#pragma unroll
+            for (int f = 0; f < 4; ++f) bf[f] = frag(src + TM * TK, wn + 16 * f, 4 * h + lq);
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    acc[y][x] = __builtin_amdgcn_mfma_i32_16x16x64_i8(bf[x], af[y], acc[y][x], 0, 0, 0);
+        }
+    };
+    const int KB = (p.K + TK - 1) / TK;
+    issue(buf0, 0);
+    for (int kb = 0; kb < KB; kb += 2) {
+        // a stage past K holds zeros
+        issue(buf1, kb + 1);
+        GFG_WAITCNT(8, 15);
+        __syncthreads();
+        compute(buf0);
+        __syncthreads();
+        issue(buf0, kb + 2);
+        GFG_WAITCNT(8, 15);
+        __syncthreads();
+        compute(buf1);
+        __syncthreads();
+    }
+    GFG_WAITCNT(0, 15);
+
+    // acc[y][x] of lane (l16, lq): row 16 y + l16, columns 16 x + 4 lq .. +3
+    const bool vec = (p.N & 3) == 0;
+    OutT* const d = static_cast<OutT*>(p.d);
+#pragma unroll
+    for (int y = 0; y < 4; ++y) {
+        const int r = wm + 16 * y + l16;
+        bool ok = r < lim;
+        if (LAYOUT == CONTIG) ok = ok && p.meta[row0 + min(r, lim - 1)] == g;
+        if (!ok) continue;
+        const float sa = p.a_scale[arow + r];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            const int n = n0 + wn + 16 * x + 4 * lq;
+            float v[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int nn = min(n + i, p.N - 1);
+                v[i] = float(acc[y][x][i]) * sa * p.b_scale[int64_t(g) * p.N + nn];
+                if (LAYOUT == DENSE && p.bias) v[i] += p.bias[nn];
+            }
+            store4(d + (arow + r) * p.N, n, p.N, vec, v);
+        }
+    }
+}
+
+template <int LAYOUT>
+int launch_i8(const I8Params& p, int64_t row_tiles, int out_dtype, hipStream_t s) {
+    const dim3 grid(unsigned((p.N + TN - 1) / TN), unsigned(row_tiles));
+    if (out_dtype == GFG_OUT_BF16)
+        hipLaunchKernelGGL((int8_gemm_kernel<LAYOUT, __bf16>), grid, dim3(TT), 0, s, p);
+    else
+        hipLaunchKernelGGL((int8_gemm_kernel<LAYOUT, _Float16>), grid, dim3(TT), 0, s, p);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return fail(GFG_EHIP, "kernel launch failed: %s", hipGetErrorString(e));
+    return GFG_OK;
+}
+
+// ------------------------------------------------------------------ argument checks
+constexpr int64_t kMaxK = (int64_t(1) << 17) - 16;     // |sum| <= 2^14 K stays below 2^31
+
+int check_quant(const char* fn, const void* x, int32_t in_dtype, int64_t M, int64_t K, const void* q, const void* scale) {
+    if (in_dtype != GFG_IN_F32 && in_dtype != GFG_IN_BF16 && in_dtype != GFG_IN_F16)
+        return fail(GFG_EINVAL, "%s: in_dtype %d is not a GFG_IN_* value", fn, in_dtype);
+    if (M < 0 || K <= 0) return fail(GFG_EINVAL, "%s: bad sizes M=%lld K=%lld", fn, (long long)M, (long long)K);
+    if (K % 16 || K > kMaxK)
+        return fail(GFG_EUNSUPPORTED, "%s: K=%lld must be a multiple of 16 and at most %lld", fn, (long long)K,
+                    (long long)kMaxK);
+    if (M >= int64_t(1) << 31) return fail(GFG_EUNSUPPORTED, "%s: M=%lld is 2^31 or more", fn, (long long)M);
+    if (M == 0) return GFG_OK;
+    if (!x || !q || !scale) return fail(GFG_EINVAL, "%s: null pointer argument", fn);
+    if ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(q)) % 16 || reinterpret_cast<uintptr_t>(scale) % 4)
+        return fail(GFG_EINVAL, "%s: x and q must be 16-byte aligned, scale 4-byte aligned", fn);
+    return GFG_OK;
+}
+
+// Sizes of a product; *empty is set when there is nothing to compute.
+int check_product(const char* fn, int64_t rows, int64_t N, int64_t K, int64_t G, int32_t out_dtype, bool* empty) {
+    *empty = false;
+    if (out_dtype != GFG_OUT_BF16 && out_dtype != GFG_OUT_F16)
+        return fail(GFG_EINVAL, "%s: out_dtype %d is not GFG_OUT_BF16 or GFG_OUT_F16", fn, out_dtype);
+    if (rows < 0 || N <= 0 || K <= 0 || G <= 0 || G > 65535)
+        return fail(GFG_EINVAL, "%s: bad sizes rows=%lld N=%lld K=%lld G=%lld", fn, (long long)rows, (long long)N,
+                    (long long)K, (long long)G);
+    if (K % 16 || K > kMaxK)
+        return fail(GFG_EUNSUPPORTED, "%s: K=%lld must be a multiple of 16 and at most %lld", fn, (long long)K,
+                    (long long)kMaxK);
+    if (N > int64_t(1) << 30) return fail(GFG_EUNSUPPORTED, "%s: N=%lld above 2^30", fn, (long long)N);
+    *empty = rows == 0;
+    return GFG_OK;
+}
+
+int check_operands(const char* fn, const void* a, const void* a_scale, const void* b, const void* b_scale,
+                   const void* meta, bool need_meta, const void* d) {
+    if (!a || !a_scale || !b || !b_scale || !d || (need_meta && !meta))
+        return fail(GFG_EINVAL, "%s: null pointer argument", fn);
+    if ((reinterpret_cast<uintptr_t>(a) | reinterpret_cast<uintptr_t>(b)) % 16)
+        return fail(GFG_EINVAL, "%s: a and b must be 16-byte aligned", fn);
+    if ((reinterpret_cast<uintptr_t>(a_scale) | reinterpret_cast<uintptr_t>(b_scale) | reinterpret_cast<uintptr_t>(meta)) % 4 ||
+        reinterpret_cast<uintptr_t>(d) % 8)
+        return fail(GFG_EINVAL, "%s: scales and metadata must be 4-byte aligned, d 8-byte aligned", fn);
+    return GFG_OK;
+}
+
+int quantize(const void* x, int32_t in_dtype, int64_t M, int64_t K, uint8_t* q, float* scale, hipStream_t s) {
+    if (in_dtype == GFG_IN_F32) launch_quant<float>(x, q, scale, M, int(K), s);
+    else if (in_dtype == GFG_IN_BF16) launch_quant<__bf16>(x, q, scale, M, int(K), s);
+    else launch_quant<_Float16>(x, q, scale, M, int(K), s);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return fail(GFG_EHIP, "kernel launch failed: %s", hipGetErrorString(e));
+    return GFG_OK;
+}
+
+constexpr int64_t kMaxRowTiles = 65535;        // the grid's second dimension
+
+}  // namespace
+}  // namespace gfg
+
+using namespace gfg;
+
+extern "C" int int8_quantize_token_device(const void* x, int32_t in_dtype, int64_t M, int64_t K, int8_t* q,
+                                          float* scale, void* stream) {
+    clear_error();
+    if (int rc = check_quant("int8_quantize_token_device", x, in_dtype, M, K, q, scale)) return rc;
+    if (M == 0) return GFG_OK;
+    return quantize(x, in_dtype, M, K, reinterpret_cast<uint8_t*>(q), scale, static_cast<hipStream_t>(stream));
+}
+
+extern "C" int int8_gemm(const int8_t* a, const float* a_scale, const int8_t* b, const float* b_scale,
+                         const float* bias, void* d, int64_t M, int64_t N, int64_t K, int32_t out_dtype, void* stream) {
+    clear_error();
+    const char* fn = "int8_gemm";
+    bool empty;
+    if (int rc = check_product(fn, M, N, K, 1, out_dtype, &empty)) return rc;
+    if (empty) return GFG_OK;
+    if (int rc = check_operands(fn, a, a_scale, b, b_scale, bias, false, d)) return rc;
+    const int64_t tiles = (M + TM - 1) / TM;
+    if (tiles > kMaxRowTiles) return fail(GFG_EUNSUPPORTED, "%s: M=%lld above %lld", fn, (long long)M, (long long)(kMaxRowTiles * TM));
+    const I8Params p{reinterpret_cast<const uint8_t*>(a), a_scale, reinterpret_cast<const uint8_t*>(b), b_scale, bias,
+                     nullptr, d, M, int(N), int(K), 1, int(tiles)};
+    return launch_i8<DENSE>(p, tiles, out_dtype, static_cast<hipStream_t>(stream));
+}
+
+extern "C" int64_t int8_linear_workspace_bytes(int64_t M, int64_t K) {
+    return M > 0 && K > 0 ? M * ((K + 15) / 16 * 16) + M * 4 : 0;
+}
+
+extern "C" int int8_linear(const void* x, int32_t in_dtype, const int8_t* b, const float* b_scale, const float* bias,
+                           void* d, int64_t M, int64_t N, int64_t K, int32_t out_dtype, void* workspace,
+                           int64_t workspace_bytes, void* stream) {
+    clear_error();
+    const char* fn = "int8_linear";
+    bool empty;
+    if (int rc = check_product(fn, M, N, K, 1, out_dtype, &empty)) return rc;
+    if (in_dtype != GFG_IN_F32 && in_dtype != GFG_IN_BF16 && in_dtype != GFG_IN_F16)
+        return fail(GFG_EINVAL, "%s: in_dtype %d is not a GFG_IN_* value", fn, in_dtype);
+    if (empty) return GFG_OK;
+    if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 16)
+        return fail(GFG_EINVAL, "%s: workspace must be a 16-byte aligned device pointer", fn);
+    if (workspace_bytes < int8_linear_workspace_bytes(M, K))
+        return fail(GFG_EINVAL, "%s: workspace of %lld bytes, %lld are needed", fn, (long long)workspace_bytes,
+                    (long long)int8_linear_workspace_bytes(M, K));
+    uint8_t* const q = static_cast<uint8_t*>(workspace);
+    float* const scale = reinterpret_cast<float*>(q + M * K);
+    if (int rc = check_quant(fn, x, in_dtype, M, K, q, scale)) return rc;
+    if (int rc = check_operands(fn, q, scale, b, b_scale, bias, false, d)) return rc;
+    const int64_t tiles = (M + TM - 1) / TM;
+    if (tiles > kMaxRowTiles) return fail(GFG_EUNSUPPORTED, "%s: M=%lld above %lld", fn, (long long)M, (long long)(kMaxRowTiles * TM));
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (int rc = quantize(x, in_dtype, M, K, q, scale, s)) return rc;
+    const I8Params p{q, scale, reinterpret_cast<const uint8_t*>(b), b_scale, bias, nullptr, d, M, int(N), int(K), 1, int(tiles)};
+    return launch_i8<DENSE>(p, tiles, out_dtype, s);
+}
+
+extern "C" int grouped_int8_gemm_contiguous(const int8_t* a, const float* a_scale, const int8_t* b, const float* b_scale,
+                                            const int32_t* grouped_layout, void* d, int64_t M, int64_t N, int64_t K,
+                                            int32_t G, int32_t out_dtype, void* stream) {
+    clear_error();
+    const char* fn = "grouped_int8_gemm_contiguous";
+    bool empty;
+    if (int rc = check_product(fn, M, N, K, G, out_dtype, &empty)) return rc;
+    if (empty) return GFG_OK;
+    if (int rc = check_operands(fn, a, a_scale, b, b_scale, grouped_layout, true, d)) return rc;
+    const int64_t tiles = (M + TM - 1) / TM;
+    if (tiles > 4096) return fail(GFG_EUNSUPPORTED, "%s: M=%lld is more than 4096 tiles of 128 rows", fn, (long long)M);
+    const I8Params p{reinterpret_cast<const uint8_t*>(a), a_scale, reinterpret_cast<const uint8_t*>(b), b_scale, nullptr,
+                     grouped_layout, d, M, int(N), int(K), G, int(tiles)};
+    return launch_i8<CONTIG>(p, tiles, out_dtype, static_cast<hipStream_t>(stream));
+}
+
+extern "C" int grouped_int8_gemm_masked(const int8_t* a, const float* a_scale, const int8_t* b, const float* b_scale,
+                                        const int32_t* masked_m, void* d, int32_t G, int64_t M_max, int64_t N, int64_t K,
+                                        int32_t out_dtype, void* stream) {
+    clear_error();
+    const char* fn = "grouped_int8_gemm_masked";
+    bool empty;
+    if (int rc = check_product(fn, M_max, N, K, G, out_dtype, &empty)) return rc;
+    if (empty) return GFG_OK;
+    if (int rc = check_operands(fn, a, a_scale, b, b_scale, masked_m, true, d)) return rc;
+    const int64_t tiles = (M_max + TM - 1) / TM;
+    if (tiles > 4096 || tiles * G > 4096)
+        return fail(GFG_EUNSUPPORTED, "%s: G=%d x M_max=%lld is more than 4096 tiles of 128 rows", fn, G, (long long)M_max);
+    const I8Params p{reinterpret_cast<const uint8_t*>(a), a_scale, reinterpret_cast<const uint8_t*>(b), b_scale, nullptr,
+                     masked_m, d, M_max, int(N), int(K), G, int(tiles)};
+    return launch_i8<MASKED>(p, tiles * G, out_dtype, static_cast<hipStream_t>(stream));
+}

@@ -54,7 +54,7 @@ enum gfg_status {
 };
 
 enum gfg_out_dtype { GFG_OUT_BF16 = 0, GFG_OUT_F16 = 1 };
-enum gfg_in_dtype { GFG_IN_F32 = 0, GFG_IN_BF16 = 1 };
+enum gfg_in_dtype { GFG_IN_F32 = 0, GFG_IN_BF16 = 1, GFG_IN_F16 = 2 };
 
 /*
  * Contiguous grouped GEMM (the DeepGEMM-style m_grouped ... contiguous op).
@@ -299,6 +299,132 @@ GFG_API int fp8_quantize_weight_128x128(const float* w, int32_t G, int64_t N, in
  */
 GFG_API int fp8_quantize_act_1x128_device(const void* x, int32_t in_dtype, int32_t G, int64_t M, int64_t K,
                                           uint8_t* q, uint8_t* scale_t, void* stream);
+
+/*
+ * Token quantizer for the 8-bit integer products below (GPU, asynchronous on
+ * `stream`): one scale per row.  With amax = max(max_k |x[m, k]|, 2^-100),
+ *
+ *   scale[m] = amax / 127,   q[m, k] = rint(x[m, k] * (127 / amax))
+ *
+ * every operation a single fp32 rounding to nearest, rint to even, so codes
+ * lie in [-127, 127].  A row of zeros has codes 0.  A row with a NaN or an
+ * infinity gets scale NaN and codes 0, which makes its products NaN.  Weights
+ * [G][N][K] are G * N rows: the same call makes their per-channel scales.
+ *
+ *   x [M][K] GFG_IN_F32, _BF16 or _F16 ; q [M][K] int8 ; scale [M] float
+ *   (x and q 16-byte aligned, scale 4-byte aligned, else GFG_EINVAL)
+ *
+ * Sizes: M >= 0 (0 is a no-op) and below 2^31, K a multiple of 16 up to
+ * 2^17 - 16 (else GFG_EUNSUPPORTED).
+ */
+GFG_API int int8_quantize_token_device(const void* x, int32_t in_dtype, int64_t M, int64_t K, int8_t* q,
+                                       float* scale, void* stream);
+
+/*
+ * 8-bit integer matrix product with one scale per token and per channel:
+ *
+ *   d[m, n] = (sum_k a[m, k] b[n, k]) * a_scale[m] * b_scale[n] + bias[n]
+ *
+ * The sum is an exact 32-bit integer; the scales and the bias are applied in
+ * fp32 and d is rounded once.
+ *
+ *   a [M][K] int8 ; a_scale [M] float ; b [N][K] int8 ; b_scale [N] float
+ *   bias [N] float or NULL ; d [M][N] bf16 or f16
+ *   (a and b 16-byte aligned, d 8-byte aligned, the rest 4-byte aligned, else
+ *   GFG_EINVAL)
+ *
+ * Sizes: M >= 0 (0 is a no-op), M <= 128 * 65535, any N in [1, 2^30], K a
+ * multiple of 16 up to 2^17 - 16 (else GFG_EUNSUPPORTED).
+ *
+ * int8_linear is the token quantizer and this product in one call, from
+ * x [M][K] in 32 or 16 bits: a 16-byte aligned device workspace of at least
+ * int8_linear_workspace_bytes(M, K) bytes holds the codes and scales between
+ * them (it needs no initialization; a call leaves nothing in it for the next).
+ */
+GFG_API int int8_gemm(const int8_t* a, const float* a_scale, const int8_t* b, const float* b_scale,
+                      const float* bias, void* d, int64_t M, int64_t N, int64_t K, int32_t out_dtype, void* stream);
+GFG_API int64_t int8_linear_workspace_bytes(int64_t M, int64_t K);
+GFG_API int int8_linear(const void* x, int32_t in_dtype, const int8_t* b, const float* b_scale, const float* bias,
+                        void* d, int64_t M, int64_t N, int64_t K, int32_t out_dtype, void* workspace,
+                        int64_t workspace_bytes, void* stream);
+
+/*
+ * The 8-bit integer product in the two grouped layouts of the FP8 GEMM, with
+ * the same rules for grouped_layout and masked_m: rows that belong to no
+ * expert are left untouched.
+ *
+ *   contiguous: a [M][K], a_scale [M], grouped_layout [M], d [M][N]
+ *   masked:     a [G][M_max][K], a_scale [G][M_max], masked_m [G], d [G][M_max][N]
+ *   both:       b [G][N][K], b_scale [G][N]
+ *
+ * Sizes: N and K as in int8_gemm, 1 <= G <= 65535, at most 4096 tiles of 128
+ * rows (ceil(M / 128), or G * ceil(M_max / 128)), else GFG_EUNSUPPORTED.
+ */
+GFG_API int grouped_int8_gemm_contiguous(const int8_t* a, const float* a_scale, const int8_t* b,
+                                         const float* b_scale, const int32_t* grouped_layout, void* d, int64_t M,
+                                         int64_t N, int64_t K, int32_t G, int32_t out_dtype, void* stream);
+GFG_API int grouped_int8_gemm_masked(const int8_t* a, const float* a_scale, const int8_t* b, const float* b_scale,
+                                     const int32_t* masked_m, void* d, int32_t G, int64_t M_max, int64_t N,
+                                     int64_t K, int32_t out_dtype, void* stream);
+
+/*
+ * Top-k router of a mixture-of-experts layer: for every token the k experts
+ * of the largest logits, in falling order, ties to the lowest index.
+ *
+ *   score     softmax over all E experts, or sigmoid of each logit
+ *   chosen by the logit, or, with a bias, by score + bias[e] (which selects
+ *             only; the weight stays the score)
+ *   weights   score * scale, or, renormalized, score / (sum of the chosen
+ *             scores) * scale (0 where that sum is 0)
+ *
+ * An expert whose logit is -infinity or NaN is never chosen; where fewer than
+ * k are left, the remaining ids are -1 with weight 0 (the layers below skip
+ * them).
+ *
+ *   logits [T][E] GFG_IN_F32, _BF16 or _F16 ; bias [E] float or NULL
+ *   ids [T][k] int32 ; weights [T][k] float
+ *
+ * Sizes: T >= 0 (0 is a no-op) and below 2^31, 1 <= k <= E (else GFG_EINVAL),
+ * E <= 1024 and k <= 64 (else GFG_EUNSUPPORTED).
+ */
+enum gfg_moe_score { GFG_SCORE_SOFTMAX = 0, GFG_SCORE_SIGMOID = 1 };
+GFG_API int moe_topk(const void* logits, int32_t in_dtype, const float* bias, int32_t* ids, float* weights, int64_t T,
+                     int64_t E, int64_t k, int32_t score, int32_t renormalize, float scale, void* stream);
+
+/*
+ * A whole mixture-of-experts layer for a few tokens (two launches):
+ *
+ *   g | u = W1[e] x[t],  h = silu(g) * u,
+ *   out[t] = sum over j of topk_weights[t, j] * (W2[e] h),  e = topk_ids[t, j]
+ *
+ * Ids outside [0, E) (another rank's experts, or none) contribute nothing; a
+ * token with no expert here gets zeros.  A token may name an expert twice.
+ * The tokens stay in 16 bits, the hidden rows keep 16 significant bits, all
+ * sums are fp32 and out is rounded once.  For more than 1024 pairs use the
+ * grouped products on the same weights.
+ *
+ *   x, out [T][H] bf16 or f16 (dtype GFG_OUT_*) ; topk_ids [T][k] int32 ;
+ *   topk_weights [T][k] float
+ *   moe_fp8_layer:  w1 [E][2*I][H] e4m3 (gate rows, then up rows), w1_scale
+ *                   [E][2*I/128][H/128] E8M0 ; w2 [E][H][I], w2_scale
+ *                   [E][H/128][I/128]: the B operands of the FP8 GEMMs
+ *   moe_int8_layer: w1 [E][2*I][H] int8, w1_scale [E][2*I] float ; w2
+ *                   [E][H][I], w2_scale [E][H]: those of the int8 products
+ *   workspace       16-byte aligned device memory, at least
+ *                   moe_layer_workspace_bytes(T, k, I) bytes, uninitialized
+ *
+ * Sizes: T >= 0 (0 is a no-op), T * k <= 1024, E <= 1024, H and I multiples of
+ * 128 up to 65536 (else GFG_EUNSUPPORTED).
+ */
+GFG_API int64_t moe_layer_workspace_bytes(int64_t T, int64_t k, int64_t I);
+GFG_API int moe_fp8_layer(const void* x, int32_t dtype, const int32_t* topk_ids, const float* topk_weights,
+                          const void* w1, const uint8_t* w1_scale, const void* w2, const uint8_t* w2_scale, void* out,
+                          int64_t T, int64_t k, int64_t E, int64_t H, int64_t I, void* workspace,
+                          int64_t workspace_bytes, void* stream);
+GFG_API int moe_int8_layer(const void* x, int32_t dtype, const int32_t* topk_ids, const float* topk_weights,
+                           const int8_t* w1, const float* w1_scale, const int8_t* w2, const float* w2_scale, void* out,
+                           int64_t T, int64_t k, int64_t E, int64_t H, int64_t I, void* workspace,
+                           int64_t workspace_bytes, void* stream);
 
 /*
  * Launch settings (process-wide, read at every GEMM call; not synchronized
