@@ -31,7 +31,7 @@ HIP_FLAGS = ["-O3", "-std=c++17", "-fPIC", "-fvisibility=hidden", f"--offload-ar
 
 
 # The device sources, compiled one object each.
-HIP_SOURCES = ["gfg_gemm.hip", "gfg_gemm256.hip", "gfg_quant.hip", "gfg_int8.hip", "gfg_moe.hip",
+HIP_SOURCES = ["gfg_gemm.hip", "gfg_gemm256.hip", "gfg_quant.hip", "gfg_int8.hip", "gfg_int8_gemm256.hip", "gfg_moe.hip",
                "gfg_ceiling.hip"]
 
 

@@ -15,12 +15,12 @@
 
 #include "gfg.h"
 #include "gfg_device.h"
+#include "gfg_int8.h"
 #include "gfg_internal.h"
 
 namespace gfg {
 namespace {
 
-typedef int v4i __attribute__((ext_vector_type(4)));
 typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
 
 // ------------------------------------------------------------------ token quantizer
@@ -164,21 +164,6 @@ constexpr int TM = 128, TN = 128, TK = 128;
 constexpr int TT = 256;
 constexpr uint32_t kOutside = 0x80000000u;     // past every buffer window used here (all below 2^31 bytes)
 
-enum Layout { DENSE = 0, CONTIG = 1, MASKED = 2 };
-
-struct I8Params {
-    const uint8_t* a;        // [rows][K] (masked: [G][rows][K])
-    const float* a_scale;    // [rows] (masked: [G][rows])
-    const uint8_t* b;        // [G][N][K]
-    const float* b_scale;    // [G][N]
-    const float* bias;       // [N] or null
-    const int32_t* meta;     // grouped_layout or masked_m
-    void* d;                 // [rows][N] (masked: [G][rows][N])
-    int64_t rows;
-    int N, K, G;
-    int m_tiles;             // row tiles (masked: per group)
-};
-
 // One output element row piece: columns n .. n+3 of a row, from the integer sums.
 template <typename OutT>
 __device__ __forceinline__ void store4(OutT* row, int n, int N, bool vec, const float (&v)[4]) {
@@ -204,8 +189,8 @@ __global__ __launch_bounds__(TT, 2) void int8_gemm_kernel(I8Params p) {
     int g = 0, row0, lim;
     int64_t region = 0;
     if (LAYOUT == MASKED) {
-        g = mt / p.m_tiles;
-        row0 = (mt - g * p.m_tiles) * TM;
+        g = mt / p.tiles_per_group;
+        row0 = (mt - g * p.tiles_per_group) * TM;
         int mm = p.meta[g];
         mm = mm < 0 ? 0 : (mm > p.rows ? int(p.rows) : mm);
         lim = min(TM, mm - row0);
@@ -296,8 +281,9 @@ __global__ __launch_bounds__(TT, 2) void int8_gemm_kernel(I8Params p) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int nn = min(n + i, p.N - 1);
-                v[i] = float(acc[y][x][i]) * sa * p.b_scale[int64_t(g) * p.N + nn];
-                if (LAYOUT == DENSE && p.bias) v[i] += p.bias[nn];
+                // adding -0 changes nothing, not even a zero's sign
+                v[i] = fmaf(float(acc[y][x][i]) * sa, p.b_scale[int64_t(g) * p.N + nn],
+                            LAYOUT == DENSE && p.bias ? p.bias[nn] : -0.0f);
             }
             store4(d + (arow + r) * p.N, n, p.N, vec, v);
         }
@@ -305,8 +291,8 @@ __global__ __launch_bounds__(TT, 2) void int8_gemm_kernel(I8Params p) {
 }
 
 template <int LAYOUT>
-int launch_i8(const I8Params& p, int64_t row_tiles, int out_dtype, hipStream_t s) {
-    const dim3 grid(unsigned((p.N + TN - 1) / TN), unsigned(row_tiles));
+int launch_128(const I8Params& p, int out_dtype, hipStream_t s) {
+    const dim3 grid(unsigned((p.N + TN - 1) / TN), unsigned(p.m_tiles));
     if (out_dtype == GFG_OUT_BF16)
         hipLaunchKernelGGL((int8_gemm_kernel<LAYOUT, __bf16>), grid, dim3(TT), 0, s, p);
     else
@@ -314,6 +300,49 @@ int launch_i8(const I8Params& p, int64_t row_tiles, int out_dtype, hipStream_t s
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return fail(GFG_EHIP, "kernel launch failed: %s", hipGetErrorString(e));
     return GFG_OK;
+}
+
+// Launch the product on the tile that suits it.  `p` holds everything but the
+// tile counts.
+int launch_i8(const char* fn, I8Params p, int layout, int out_dtype, hipStream_t s) {
+    int cus = 0;
+    if (int rc = device_cus(&cus)) return rc;
+    const int groups = layout == MASKED ? p.G : 1;
+    const int64_t t128 = (p.rows + TM - 1) / TM * groups, t256 = (p.rows + 255) / 256 * groups;
+    const int64_t n256 = (int64_t(p.N) + 255) / 256;
+    const bool fits = p.N <= 1 << 22;
+    const int choice = tile_shape_choice();
+    if (choice == GFG_TILE_256x256 && !fits)
+        return fail(GFG_EUNSUPPORTED, "%s: the 256 x 256 tile needs N=%d at most 2^22", fn, p.N);
+    if (choice == GFG_TILE_256x256 || (choice == GFG_TILE_AUTO && fits && t256 * n256 >= cus / 2)) {
+        p.m_tiles = int(layout == CONTIG ? t128 : t256);
+        p.tiles_per_group = int(t256 / groups);
+        return launch_int8_256(p, layout, out_dtype, s);
+    }
+    p.m_tiles = int(t128);
+    p.tiles_per_group = int(t128 / groups);
+    if (layout == DENSE) return launch_128<DENSE>(p, out_dtype, s);
+    if (layout == CONTIG) return launch_128<CONTIG>(p, out_dtype, s);
+    return launch_128<MASKED>(p, out_dtype, s);
+}
+
+I8Params product(const int8_t* a, const float* a_scale, const int8_t* b, const float* b_scale, const float* bias,
+                 const int32_t* meta, void* d, int64_t rows, int64_t N, int64_t K, int G) {
+    I8Params p{};
+    p.a = reinterpret_cast<const uint8_t*>(a);
+    p.a_scale = a_scale;
+    p.b = reinterpret_cast<const uint8_t*>(b);
+    p.b_scale = b_scale;
+    p.bias = bias;
+    p.meta = meta;
+    p.d = d;
+    p.rows = rows;
+    p.N = int(N);
+    p.K = int(K);
+    p.G = G;
+    p.group_m = locality_group_m();
+    p.num_xcd = locality_num_xcd();
+    return p;
 }
 
 // ------------------------------------------------------------------ argument checks
@@ -396,9 +425,8 @@ extern "C" int int8_gemm(const int8_t* a, const float* a_scale, const int8_t* b,
     if (int rc = check_operands(fn, a, a_scale, b, b_scale, bias, false, d)) return rc;
     const int64_t tiles = (M + TM - 1) / TM;
     if (tiles > kMaxRowTiles) return fail(GFG_EUNSUPPORTED, "%s: M=%lld above %lld", fn, (long long)M, (long long)(kMaxRowTiles * TM));
-    const I8Params p{reinterpret_cast<const uint8_t*>(a), a_scale, reinterpret_cast<const uint8_t*>(b), b_scale, bias,
-                     nullptr, d, M, int(N), int(K), 1, int(tiles)};
-    return launch_i8<DENSE>(p, tiles, out_dtype, static_cast<hipStream_t>(stream));
+    return launch_i8(fn, product(a, a_scale, b, b_scale, bias, nullptr, d, M, N, K, 1), DENSE, out_dtype,
+                     static_cast<hipStream_t>(stream));
 }
 
 extern "C" int64_t int8_linear_workspace_bytes(int64_t M, int64_t K) {
@@ -428,8 +456,8 @@ extern "C" int int8_linear(const void* x, int32_t in_dtype, const int8_t* b, con
     if (tiles > kMaxRowTiles) return fail(GFG_EUNSUPPORTED, "%s: M=%lld above %lld", fn, (long long)M, (long long)(kMaxRowTiles * TM));
     hipStream_t s = static_cast<hipStream_t>(stream);
     if (int rc = quantize(x, in_dtype, M, K, q, scale, s)) return rc;
-    const I8Params p{q, scale, reinterpret_cast<const uint8_t*>(b), b_scale, bias, nullptr, d, M, int(N), int(K), 1, int(tiles)};
-    return launch_i8<DENSE>(p, tiles, out_dtype, s);
+    return launch_i8(fn, product(reinterpret_cast<const int8_t*>(q), scale, b, b_scale, bias, nullptr, d, M, N, K, 1), DENSE,
+                     out_dtype, s);
 }
 
 extern "C" int grouped_int8_gemm_contiguous(const int8_t* a, const float* a_scale, const int8_t* b, const float* b_scale,
@@ -443,9 +471,8 @@ extern "C" int grouped_int8_gemm_contiguous(const int8_t* a, const float* a_scal
     if (int rc = check_operands(fn, a, a_scale, b, b_scale, grouped_layout, true, d)) return rc;
     const int64_t tiles = (M + TM - 1) / TM;
     if (tiles > 4096) return fail(GFG_EUNSUPPORTED, "%s: M=%lld is more than 4096 tiles of 128 rows", fn, (long long)M);
-    const I8Params p{reinterpret_cast<const uint8_t*>(a), a_scale, reinterpret_cast<const uint8_t*>(b), b_scale, nullptr,
-                     grouped_layout, d, M, int(N), int(K), G, int(tiles)};
-    return launch_i8<CONTIG>(p, tiles, out_dtype, static_cast<hipStream_t>(stream));
+    return launch_i8(fn, product(a, a_scale, b, b_scale, nullptr, grouped_layout, d, M, N, K, G), CONTIG, out_dtype,
+                     static_cast<hipStream_t>(stream));
 }
 
 extern "C" int grouped_int8_gemm_masked(const int8_t* a, const float* a_scale, const int8_t* b, const float* b_scale,
@@ -460,7 +487,6 @@ extern "C" int grouped_int8_gemm_masked(const int8_t* a, const float* a_scale, c
     const int64_t tiles = (M_max + TM - 1) / TM;
     if (tiles > 4096 || tiles * G > 4096)
         return fail(GFG_EUNSUPPORTED, "%s: G=%d x M_max=%lld is more than 4096 tiles of 128 rows", fn, G, (long long)M_max);
-    const I8Params p{reinterpret_cast<const uint8_t*>(a), a_scale, reinterpret_cast<const uint8_t*>(b), b_scale, nullptr,
-                     masked_m, d, M_max, int(N), int(K), G, int(tiles)};
-    return launch_i8<MASKED>(p, tiles * G, out_dtype, static_cast<hipStream_t>(stream));
+    return launch_i8(fn, product(a, a_scale, b, b_scale, nullptr, masked_m, d, M_max, N, K, G), MASKED, out_dtype,
+                     static_cast<hipStream_t>(stream));
 }

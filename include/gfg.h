@@ -454,7 +454,10 @@ GFG_API int moe_int8_layer(const void* x, int32_t dtype, const int32_t* topk_ids
  * at most 2^22, K/128 even, scale rows a multiple of 4 and scale_a 4-byte
  * aligned; a call that misses them then returns GFG_EUNSUPPORTED.  Other
  * values: GFG_EINVAL.  Results of the two tiles agree to the parity
- * tolerance; they are not promised to agree bit for bit.
+ * tolerance; they are not promised to agree bit for bit.  The int8 products
+ * follow the setting too: GFG_TILE_AUTO takes 256 x 256 from half as many such
+ * tiles as CUs on, GFG_TILE_128x256 their smaller tiles, GFG_TILE_256x256 needs
+ * N at most 2^22; their results do not depend on it.
  *
  * grouped_fp8_set_grid_limit: at most max_workgroups workgroups per GEMM
  * launch (0, the default: one per CU, fewer when there are fewer tiles).  The

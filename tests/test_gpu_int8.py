@@ -78,6 +78,14 @@ def test_quantizer_ties_extremes_and_non_finite_rows():
 
 
 # ------------------------------------------------------------------ dense product
+@pytest.fixture(params=[gfg.TILE_AUTO, gfg.TILE_128x256, gfg.TILE_256x256], ids=["auto", "small", "large"])
+def tile(request):
+    """Every product runs on the automatic choice and on each tile shape, forced."""
+    gfg.set_tile_shape(request.param)
+    yield request.param
+    gfg.set_tile_shape(gfg.TILE_AUTO)
+
+
 @pytest.mark.parametrize("M,N,K,out,bias", [
     (1, 1, 16, "bf16", False), (1, 128, 128, "f16", True), (1, 7168, 2304, "bf16", False), (2, 515, 1040, "bf16", True),
     (15, 33, 48, "f16", False), (16, 256, 256, "bf16", False), (17, 100, 112, "f16", True), (33, 1000, 7168, "bf16", False),
@@ -85,7 +93,7 @@ def test_quantizer_ties_extremes_and_non_finite_rows():
     (129, 130, 272, "bf16", True), (300, 770, 384, "f16", False), (513, 1024, 2048, "bf16", False),
     (1000, 517, 656, "f16", True), (2100, 2050, 400, "bf16", False),
 ])
-def test_dense(M, N, K, out, bias):
+def test_dense(M, N, K, out, bias, tile):
     what = f"dense M={M} N={N} K={K} {out} bias={bias}"
     print(f"[int8] {what}", flush=True)
     rng = np.random.default_rng(M * 7 + N * 3 + K)
@@ -106,7 +114,7 @@ def test_dense(M, N, K, out, bias):
 
 
 @pytest.mark.parametrize("M", [2, 70, 300])
-def test_dense_extreme_sums_are_exact(M):
+def test_dense_extreme_sums_are_exact(M, tile):
     """All products 127 * 127 or -128 * -128 at the largest K: sums near 2^31, and integer outputs."""
     K, N = 131056, 5
     a = np.full((M, K), -128, np.int8)
@@ -176,7 +184,7 @@ def test_linear_without_rows_and_stream():
     ([100, 1, 128, 129, 300], 256, 256, "bf16"), ([5, 250], 130, 400, "f16"), ([0, 128, 77], 384, 128, "bf16"),
     ([1000, 30], 641, 656, "bf16"), ([700, 0, 513, 256], 512, 1024, "f16"), ([1], 7, 16, "bf16"),
 ])
-def test_contiguous(m_per_group, N, K, out):
+def test_contiguous(m_per_group, N, K, out, tile):
     from fp8_block_scaled_amd import workloads as wl
     what = f"contiguous {m_per_group} N={N} K={K} {out}"
     print(f"[int8] {what}", flush=True)
@@ -200,7 +208,7 @@ def test_contiguous(m_per_group, N, K, out):
             check(d[torch.from_numpy(rows).cuda()], ref, out, np.abs(ref), f"{what} expert {g}")
 
 
-def test_contiguous_all_padding():
+def test_contiguous_all_padding(tile):
     d = torch.full((256, 24), SENTINEL, dtype=torch.bfloat16, device="cuda")
     z = torch.zeros
     gfg.grouped_int8_gemm_contiguous(z(256, 64, dtype=torch.int8, device="cuda"), z(256, device="cuda"),
@@ -213,7 +221,7 @@ def test_contiguous_all_padding():
     ([0, 64, 200], 256, 256, 384, "bf16"), ([512, 3, 129, 0], 512, 133, 272, "f16"), ([-5, 900, 37], 300, 512, 512, "bf16"),
     ([1], 1, 16, 16, "bf16"), ([600, 1024, 0, 257], 1024, 520, 1024, "bf16"),
 ])
-def test_masked(masked_m, Mmax, N, K, out):
+def test_masked(masked_m, Mmax, N, K, out, tile):
     what = f"masked {masked_m} M_max={Mmax} N={N} K={K} {out}"
     print(f"[int8] {what}", flush=True)
     rng = np.random.default_rng(Mmax + N + K)
@@ -228,6 +236,27 @@ def test_masked(masked_m, Mmax, N, K, out):
         if mm:
             ref = so.int8_product(a[g, :mm], sa[g, :mm], b[g], sb[g])
             check(d[g, :mm], ref, out, np.abs(ref), f"{what} group {g}")
+
+
+def test_large_product_on_both_tiles():
+    """Several tiles for every workgroup of the 256 x 256 kernel, and both tiles bit for bit: the sums are exact."""
+    rng = np.random.default_rng(21)
+    M, N, K = 5000, 5128, 400
+    a, b, sa, sb = codes(rng, (M, K)), codes(rng, (N, K)), scales(rng, M, 1), scales(rng, N, K)
+    bias = to_dev(rng.standard_normal(N).astype(np.float32))
+    ops = to_dev(a), to_dev(sa), to_dev(b), to_dev(sb)
+    got = []
+    try:
+        for shape in (gfg.TILE_AUTO, gfg.TILE_128x256, gfg.TILE_256x256):
+            gfg.set_tile_shape(shape)
+            got.append(gfg.int8_gemm(*ops, torch.empty(M, N, dtype=torch.bfloat16, device="cuda"), bias=bias))
+    finally:
+        gfg.set_tile_shape(gfg.TILE_AUTO)
+    assert torch.equal(got[0], got[1]) and torch.equal(got[1], got[2])
+    rows = rng.permutation(M)[:64]
+    prod = so.int8_product(a[rows], sa[rows], b, sb)
+    bi = bias.cpu().numpy()
+    check(got[0][torch.from_numpy(rows).cuda()], prod + bi, "bf16", np.abs(prod) + np.abs(bi), "large product")
 
 
 def test_graph_replays_match_eager():
