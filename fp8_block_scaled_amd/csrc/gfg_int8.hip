@@ -153,15 +153,18 @@ void launch_quant(const void* x, uint8_t* q, float* scale, int64_t M, int K, hip
 
 // ------------------------------------------------------------------ tiled product
 //
-// 128 x 128 output tiles, four waves of 64 x 64 each (a 4 x 4 grid of 16 x 16
-// MFMA blocks), K in steps of 128 bytes through two 32 KB LDS stages filled by
-// direct-to-LDS loads.  LDS row R (128 bytes) holds its 16-byte chunks
+// TM x TN output tiles, WM x WN waves, K in steps of 128 bytes through S LDS
+// stages filled by direct-to-LDS loads: S - 1 stages are in flight while one
+// is consumed, and a step has one barrier (a wave that passes it has seen
+// every wave finish the previous step, whose buffer the new loads go to).
+// These are the launches with too few 256 x 256 tiles, whose time is the
+// latency of a tile's first loads plus a chain of steps, so depth matters
+// more than the bytes per step.  LDS row R (128 bytes) holds its 16-byte chunks
 // XOR-swizzled by R & 7, so that the 16 rows that a fragment read touches
 // spread over all banks.  Rows past the operand's end and chunks past K lie
 // outside the buffer window, where the hardware returns zeros, so no size
 // needs its own path: zeros add nothing to an integer sum.
-constexpr int TM = 128, TN = 128, TK = 128;
-constexpr int TT = 256;
+constexpr int TK = 128;
 constexpr uint32_t kOutside = 0x80000000u;     // past every buffer window used here (all below 2^31 bytes)
 
 // One output element row piece: columns n .. n+3 of a row, from the integer sums.
@@ -177,15 +180,28 @@ __device__ __forceinline__ void store4(OutT* row, int n, int N, bool vec, const 
     }
 }
 
-template <int LAYOUT, typename OutT>
-__global__ __launch_bounds__(TT, 2) void int8_gemm_kernel(I8Params p) {
-    __shared__ __attribute__((aligned(1024))) uint8_t smem0[(TM + TN) * TK];
-    __shared__ __attribute__((aligned(1024))) uint8_t smem1[(TM + TN) * TK];
+template <int LAYOUT, int TM, int TN, int S, int WM, int WN, typename OutT>
+__global__ __launch_bounds__(WM * WN * 64) void int8_gemm_kernel(I8Params p) {
+    constexpr int WAVES = WM * WN, BYTES = (TM + TN) * TK;
+    constexpr int PER = BYTES / 1024 / WAVES;      // 1 KB loads per wave and stage
+    constexpr int RB = TM / WM / 16, CB = TN / WN / 16;
+    static_assert(S >= 3 && S <= 8 && BYTES % (1024 * WAVES) == 0 && TM % (8 * WAVES) == 0, "stage shape");
+    // an array for each stage: the compiler then knows that reading one need
+    // not wait for the loads into another
+    __shared__ __attribute__((aligned(1024))) uint8_t s0[BYTES], s1[BYTES], s2[BYTES];
+    __shared__ __attribute__((aligned(1024))) uint8_t s3[S > 3 ? BYTES : 1024], s4[S > 4 ? BYTES : 1024],
+        s5[S > 5 ? BYTES : 1024], s6[S > 6 ? BYTES : 1024], s7[S > 7 ? BYTES : 1024];
+    GFG_LDS uint8_t* const buf[8] = {(GFG_LDS uint8_t*)s0, (GFG_LDS uint8_t*)s1, (GFG_LDS uint8_t*)s2, (GFG_LDS uint8_t*)s3,
+                                     (GFG_LDS uint8_t*)s4, (GFG_LDS uint8_t*)s5, (GFG_LDS uint8_t*)s6, (GFG_LDS uint8_t*)s7};
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int l16 = lane & 15, lq = lane >> 4;
-    const int n0 = int(blockIdx.x) * TN;
-    const int mt = int(blockIdx.y);
+    // tiles in ranges, one for each XCD (the hardware deals workgroup w to XCD
+    // w % num_xcd), row tiles first, so that a B panel stays in one L2
+    const unsigned nx = unsigned(p.num_xcd), T = gridDim.x;
+    const unsigned x = blockIdx.x % nx, per = T / nx, rem = T % nx;
+    const unsigned item = x * per + min(x, rem) + blockIdx.x / nx;
+    const int mt = int(item % unsigned(p.m_tiles)), n0 = int(item / unsigned(p.m_tiles)) * TN;
     int g = 0, row0, lim;
     int64_t region = 0;
     if (LAYOUT == MASKED) {
@@ -199,7 +215,7 @@ __global__ __launch_bounds__(TT, 2) void int8_gemm_kernel(I8Params p) {
         row0 = mt * TM;
         lim = int(p.rows - row0 < TM ? p.rows - row0 : TM);
         if (LAYOUT == CONTIG) {
-            g = p.meta[row0];
+            g = p.meta[row0 & ~127];               // the expert of the aligned 128 rows
             if (g < 0 || g >= p.G) return;
         }
     }
@@ -210,79 +226,106 @@ __global__ __launch_bounds__(TT, 2) void int8_gemm_kernel(I8Params p) {
     const int ncols = min(TN, p.N - n0);
     const auto ra = make_rsrc(p.a + arow * p.K, uint32_t(lim) * uint32_t(p.K));
     const auto rb = make_rsrc(p.b + (int64_t(g) * p.N + n0) * p.K, uint32_t(ncols) * uint32_t(p.K));
-    GFG_LDS uint8_t* const buf0 = (GFG_LDS uint8_t*)smem0;
-    GFG_LDS uint8_t* const buf1 = (GFG_LDS uint8_t*)smem1;
 
-    // DMA chunk j (0..7) of a wave: LDS rows 8 (4 j + wave) .. +7 of the stage
-    // (A's 128 rows, then B's); lane i writes physical chunk i & 7 of row
-    // i >> 3 of them, the logical chunk (i & 7) ^ (i >> 3)
+    // load j of a wave: LDS rows 8 (WAVES j + wave) .. +7 of the stage (A's TM
+    // rows, then B's); lane i writes physical chunk i & 7 of row i >> 3 of
+    // them, the logical chunk (i & 7) ^ (i >> 3)
     const int kc = ((lane & 7) ^ (lane >> 3)) * 16;
     const uint32_t src0 = uint32_t(8 * wave + (lane >> 3)) * uint32_t(p.K) + uint32_t(kc);
     auto issue = [&](GFG_LDS uint8_t* dst, int kb) {
-        const bool in = kb * TK + kc < p.K;
+        const uint32_t base = kb * TK + kc < p.K ? src0 + uint32_t(kb) * TK : kOutside;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const uint32_t off = src0 + uint32_t(kb) * TK + uint32_t(32 * (j & 3)) * uint32_t(p.K);
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(j < 4 ? ra : rb, (GFG_LDS void*)(dst + (4 * j + wave) * 1024), 16,
-                                                     in ? off : kOutside, 0, 0, 0);
+        for (int j = 0; j < PER; ++j) {
+            constexpr int A_LOADS = TM / 8 / WAVES;
+            const int jr = j < A_LOADS ? j : j - A_LOADS;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(j < A_LOADS ? ra : rb, (GFG_LDS void*)(dst + (WAVES * j + wave) * 1024), 16,
+                                                     base + uint32_t(8 * WAVES * jr) * uint32_t(p.K), 0, 0, 0);
         }
     };
-    const int wm = (wave >> 1) * 64, wn = (wave & 1) * 64;
+    const int wm = (wave / WN) * (TM / WM), wn = (wave % WN) * (TN / WN);
     auto frag = [&](GFG_LDS uint8_t* src, int row, int chunk) {
         return *reinterpret_cast<GFG_LDS v4i*>(src + (row + l16) * TK + ((chunk ^ (l16 & 7)) << 4));
     };
-    v4i acc[4][4] = {};                        // [row block][column block]
-    auto compute = [&](GFG_LDS uint8_t* src) {
+    v4i acc[RB][CB] = {};                          // [row block][column block]
+    const int KB = (p.K + TK - 1) / TK;
+#pragma unroll
+    for (int j = 0; j < S - 1; ++j) issue(buf[j], j);
+    // one step on stage j's buffer: stage kb has landed here, and this wave's
+    // reads of the stage before it are done; after the barrier, everyone's
+    auto step = [&](GFG_LDS uint8_t* cur, GFG_LDS uint8_t* freed, int kb) {
+        __builtin_amdgcn_sched_barrier(0);
+        GFG_WAITCNT((S - 2) * PER, 0);
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+        issue(freed, kb + S - 1);                  // a stage past K loads zeros
+        __builtin_amdgcn_sched_barrier(0);
+        v4i af[2][RB], bf[2][CB];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            v4i af[4], bf[4];
 #pragma unroll
-            for (int f = 0; f < 4; ++f) af[f] = frag(src, wm + 16 * f, 4 * h + lq);
+            for (int f = 0; f < RB; ++f) af[h][f] = frag(cur, wm + 16 * f, 4 * h + lq);
 #pragma unroll
-            for (int f = 0; f < 4; ++f) bf[f] = frag(src + TM * TK, wn + 16 * f, 4 * h + lq);
-#pragma unroll
-            for (int y = 0; y < 4; ++y)
-#pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    acc[y][x] = __builtin_amdgcn_mfma_i32_16x16x64_i8(bf[x], af[y], acc[y][x], 0, 0, 0);
+            for (int f = 0; f < CB; ++f) bf[h][f] = frag(cur + TM * TK, wn + 16 * f, 4 * h + lq);
         }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int y = 0; y < RB; ++y)
+#pragma unroll
+                for (int c = 0; c < CB; ++c)
+                    acc[y][c] = __builtin_amdgcn_mfma_i32_16x16x64_i8(bf[h][c], af[h][y], acc[y][c], 0, 0, 0);
     };
-    const int KB = (p.K + TK - 1) / TK;
-    issue(buf0, 0);
-    for (int kb = 0; kb < KB; kb += 2) {
-        // a stage past K holds zeros
-        issue(buf1, kb + 1);
-        GFG_WAITCNT(8, 15);
-        __syncthreads();
-        compute(buf0);
-        __syncthreads();
-        issue(buf0, kb + 2);
-        GFG_WAITCNT(8, 15);
-        __syncthreads();
-        compute(buf1);
-        __syncthreads();
+    // every step leaves the loop from its own place, so that the order of the
+    // loads is the same on every path and the compiler's own waits stay exact
+    for (int kb = 0;; kb += S) {
+        step(buf[0], buf[S - 1], kb);
+        if (kb + 1 >= KB) break;
+        step(buf[1], buf[0], kb + 1);
+        if (kb + 2 >= KB) break;
+        step(buf[2], buf[1], kb + 2);
+        if (kb + 3 >= KB) break;
+        if constexpr (S > 3) {
+            step(buf[3], buf[2], kb + 3);
+            if (kb + 4 >= KB) break;
+        }
+        if constexpr (S > 4) {
+            step(buf[4], buf[3], kb + 4);
+            if (kb + 5 >= KB) break;
+        }
+        if constexpr (S > 5) {
+            step(buf[5], buf[4], kb + 5);
+            if (kb + 6 >= KB) break;
+        }
+        if constexpr (S > 6) {
+            step(buf[6], buf[5], kb + 6);
+            if (kb + 7 >= KB) break;
+        }
+        if constexpr (S > 7) {
+            step(buf[7], buf[6], kb + 7);
+            if (kb + 8 >= KB) break;
+        }
     }
-    GFG_WAITCNT(0, 15);
+    GFG_WAITCNT(0, 15);                            // the last loads land before the workgroup ends
 
-    // acc[y][x] of lane (l16, lq): row 16 y + l16, columns 16 x + 4 lq .. +3
+    // acc[y][c] of lane (l16, lq): row 16 y + l16, columns 16 c + 4 lq .. +3
     const bool vec = (p.N & 3) == 0;
     OutT* const d = static_cast<OutT*>(p.d);
 #pragma unroll
-    for (int y = 0; y < 4; ++y) {
+    for (int y = 0; y < RB; ++y) {
         const int r = wm + 16 * y + l16;
         bool ok = r < lim;
         if (LAYOUT == CONTIG) ok = ok && p.meta[row0 + min(r, lim - 1)] == g;
         if (!ok) continue;
         const float sa = p.a_scale[arow + r];
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            const int n = n0 + wn + 16 * x + 4 * lq;
+        for (int c = 0; c < CB; ++c) {
+            const int n = n0 + wn + 16 * c + 4 * lq;
             float v[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int nn = min(n + i, p.N - 1);
                 // adding -0 changes nothing, not even a zero's sign
-                v[i] = fmaf(float(acc[y][x][i]) * sa, p.b_scale[int64_t(g) * p.N + nn],
+                v[i] = fmaf(float(acc[y][c][i]) * sa, p.b_scale[int64_t(g) * p.N + nn],
                             LAYOUT == DENSE && p.bias ? p.bias[nn] : -0.0f);
             }
             store4(d + (arow + r) * p.N, n, p.N, vec, v);
@@ -290,40 +333,237 @@ __global__ __launch_bounds__(TT, 2) void int8_gemm_kernel(I8Params p) {
     }
 }
 
-template <int LAYOUT>
-int launch_128(const I8Params& p, int out_dtype, hipStream_t s) {
-    const dim3 grid(unsigned((p.N + TN - 1) / TN), unsigned(p.m_tiles));
+// ------------------------------------------------------------------ streamed product
+//
+// 16 RB x 16 CB output tiles whose NW waves split K: wave w takes the 128-byte
+// units w, w + NW, ... of the tile's rows through its own ring of D LDS stages,
+// filled by direct-to-LDS loads.  No barrier stands between a load and its
+// MFMAs, every byte of the tile's rows enters the CU once and leaves the LDS
+// once; the waves' sums meet in LDS at the end (integers: exact in any order).
+// (Loading the fragments straight into registers instead is slower: a
+// fragment's adjacent lanes are adjacent rows, so four lanes touch four cache
+// lines, and the load path then passes 16 bytes a cycle, not 64.)
+template <int LAYOUT, int RB, int CB, int NW, int D, typename OutT>
+__global__ __launch_bounds__(NW * 64) void int8_stream_kernel(I8Params p) {
+    constexpr int TM = 16 * RB, TN = 16 * CB;
+    constexpr int UNIT = (TM + TN) * TK;           // bytes of a stage: A's rows, then B's
+    constexpr int PER = UNIT / 1024;               // loads per stage
+    static_assert(D >= 2 && D <= 6 && PER * D < 64, "ring depth");
+    // an array for each stage: the compiler then knows that reading one need
+    // not wait for the loads into another
+    __shared__ __attribute__((aligned(1024))) uint8_t s0[NW * UNIT], s1[NW * UNIT];
+    __shared__ __attribute__((aligned(1024))) uint8_t s2[D > 2 ? NW * UNIT : 1024], s3[D > 3 ? NW * UNIT : 1024],
+        s4[D > 4 ? NW * UNIT : 1024], s5[D > 5 ? NW * UNIT : 1024];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int l16 = lane & 15, lq = lane >> 4;
+    GFG_LDS uint8_t* const ring[6] = {(GFG_LDS uint8_t*)s0 + wave * UNIT, (GFG_LDS uint8_t*)s1 + wave * UNIT,
+                                      (GFG_LDS uint8_t*)s2 + (D > 2 ? wave * UNIT : 0), (GFG_LDS uint8_t*)s3 + (D > 3 ? wave * UNIT : 0),
+                                      (GFG_LDS uint8_t*)s4 + (D > 4 ? wave * UNIT : 0), (GFG_LDS uint8_t*)s5 + (D > 5 ? wave * UNIT : 0)};
+    const unsigned nx = unsigned(p.num_xcd), T = gridDim.x;
+    const unsigned x = blockIdx.x % nx, per = T / nx, rem = T % nx;
+    const unsigned item = x * per + min(x, rem) + blockIdx.x / nx;
+    const int mt = int(item % unsigned(p.m_tiles)), n0 = int(item / unsigned(p.m_tiles)) * TN;
+    int g = 0, row0, lim;
+    int64_t region = 0;
+    if (LAYOUT == MASKED) {
+        g = mt / p.tiles_per_group;
+        row0 = (mt - g * p.tiles_per_group) * TM;
+        int mm = p.meta[g];
+        mm = mm < 0 ? 0 : (mm > p.rows ? int(p.rows) : mm);
+        lim = min(TM, mm - row0);
+        region = int64_t(g) * p.rows;
+    } else {
+        row0 = mt * TM;
+        lim = int(p.rows - row0 < TM ? p.rows - row0 : TM);
+        if (LAYOUT == CONTIG) {
+            g = p.meta[row0 & ~127];               // the expert of the aligned 128 rows
+            if (g < 0 || g >= p.G) return;
+        }
+    }
+    if (lim <= 0) return;
+    g = __builtin_amdgcn_readfirstlane(g);
+    lim = __builtin_amdgcn_readfirstlane(lim);
+    const int64_t arow = region + row0;
+    const int ncols = min(TN, p.N - n0);
+    const auto ra = make_rsrc(p.a + arow * p.K, uint32_t(lim) * uint32_t(p.K));
+    const auto rb = make_rsrc(p.b + (int64_t(g) * p.N + n0) * p.K, uint32_t(ncols) * uint32_t(p.K));
+
+    // load j: LDS rows 8 j .. +7 of the stage; lane i writes physical chunk
+    // i & 7 of row i >> 3 of them, the logical chunk (i & 7) ^ (i >> 3)
+    const int kc = ((lane & 7) ^ (lane >> 3)) * 16;
+    const uint32_t src0 = uint32_t(lane >> 3) * uint32_t(p.K) + uint32_t(kc);
+    auto load = [&](GFG_LDS uint8_t* dst, int k) {
+        const uint32_t base = k + kc < p.K ? src0 + uint32_t(k) : kOutside;
+#pragma unroll
+        for (int j = 0; j < PER; ++j)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(j < TM / 8 ? ra : rb, (GFG_LDS void*)(dst + j * 1024), 16,
+                                                     base + uint32_t(8 * (j < TM / 8 ? j : j - TM / 8)) * uint32_t(p.K), 0, 0, 0);
+    };
+    v4i acc[RB][CB] = {};
+    auto frag = [&](GFG_LDS uint8_t* src, int row, int chunk) {
+        return *reinterpret_cast<GFG_LDS v4i*>(src + (row + l16) * TK + ((chunk ^ (l16 & 7)) << 4));
+    };
+    // consume a unit, then load the one that takes its place, D units ahead
+    auto step = [&](GFG_LDS uint8_t* cur, int k) {
+        __builtin_amdgcn_sched_barrier(0);
+        GFG_WAITCNT((D - 1) * PER, 15);
+        v4i af[2][RB], bf[2][CB];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int f = 0; f < RB; ++f) af[h][f] = frag(cur, 16 * f, 4 * h + lq);
+#pragma unroll
+            for (int f = 0; f < CB; ++f) bf[h][f] = frag(cur + TM * TK, 16 * f, 4 * h + lq);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int y = 0; y < RB; ++y)
+#pragma unroll
+                for (int c = 0; c < CB; ++c)
+                    acc[y][c] = __builtin_amdgcn_mfma_i32_16x16x64_i8(bf[h][c], af[h][y], acc[y][c], 0, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
+        load(cur, k + D * NW * TK);                // past K: zeros
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    constexpr int STEP = NW * TK;
+#pragma unroll
+    for (int d = 0; d < D; ++d) load(ring[d], wave * TK + d * STEP);
+    // every step leaves the loop from its own place, so that the order of the
+    // loads is the same on every path and the compiler's own waits stay exact
+    for (int k = wave * TK; k < p.K; k += D * STEP) {
+        step(ring[0], k);
+        if (k + STEP >= p.K) break;
+        step(ring[1], k + STEP);
+        if constexpr (D > 2) {
+            if (k + 2 * STEP >= p.K) break;
+            step(ring[2], k + 2 * STEP);
+        }
+        if constexpr (D > 3) {
+            if (k + 3 * STEP >= p.K) break;
+            step(ring[3], k + 3 * STEP);
+        }
+        if constexpr (D > 4) {
+            if (k + 4 * STEP >= p.K) break;
+            step(ring[4], k + 4 * STEP);
+        }
+        if constexpr (D > 5) {
+            if (k + 5 * STEP >= p.K) break;
+            step(ring[5], k + 5 * STEP);
+        }
+    }
+    GFG_WAITCNT(0, 15);                            // the last loads land before the workgroup ends
+    // a wave's sums go where its first stage was
+    static_assert(RB * CB * 1024 <= UNIT, "the sums fit a stage");
+    auto sums = [&](int w, int i) -> GFG_LDS v4i& { return reinterpret_cast<GFG_LDS v4i*>((GFG_LDS uint8_t*)s0 + w * UNIT)[i * 64 + lane]; };
+#pragma unroll
+    for (int y = 0; y < RB; ++y)
+#pragma unroll
+        for (int c = 0; c < CB; ++c) sums(wave, y * CB + c) = acc[y][c];
+    __syncthreads();
+    const bool vec = (p.N & 3) == 0;
+    OutT* const d = static_cast<OutT*>(p.d);
+#pragma unroll
+    for (int i0 = 0; i0 < RB * CB; i0 += NW) {
+        const int i = i0 + wave;
+        if (i >= RB * CB) break;
+        v4i v4 = sums(0, i);
+#pragma unroll
+        for (int w = 1; w < NW; ++w) v4 += sums(w, i);
+        const int r = 16 * (i / CB) + l16, n = n0 + 16 * (i % CB) + 4 * lq;
+        bool ok = r < lim;
+        if (LAYOUT == CONTIG) ok = ok && p.meta[row0 + min(r, lim - 1)] == g;
+        if (!ok) continue;
+        const float sa = p.a_scale[arow + r];
+        float v[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int nn = min(n + q, p.N - 1);
+            v[q] = fmaf(float(v4[q]) * sa, p.b_scale[int64_t(g) * p.N + nn], LAYOUT == DENSE && p.bias ? p.bias[nn] : -0.0f);
+        }
+        store4(d + (arow + r) * p.N, n, p.N, vec, v);
+    }
+}
+
+template <int LAYOUT, int RB, int CB, int NW, int D>
+int launch_stream(I8Params p, int out_dtype, hipStream_t s) {
+    const int groups = LAYOUT == MASKED ? p.G : 1;
+    p.tiles_per_group = int((p.rows + 16 * RB - 1) / (16 * RB));
+    p.m_tiles = p.tiles_per_group * groups;
+    const int64_t tiles = int64_t(p.m_tiles) * ((p.N + 16 * CB - 1) / (16 * CB));
+    const dim3 grid{unsigned(tiles)}, block(NW * 64);
     if (out_dtype == GFG_OUT_BF16)
-        hipLaunchKernelGGL((int8_gemm_kernel<LAYOUT, __bf16>), grid, dim3(TT), 0, s, p);
+        hipLaunchKernelGGL((int8_stream_kernel<LAYOUT, RB, CB, NW, D, __bf16>), grid, block, 0, s, p);
     else
-        hipLaunchKernelGGL((int8_gemm_kernel<LAYOUT, _Float16>), grid, dim3(TT), 0, s, p);
+        hipLaunchKernelGGL((int8_stream_kernel<LAYOUT, RB, CB, NW, D, _Float16>), grid, block, 0, s, p);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return fail(GFG_EHIP, "kernel launch failed: %s", hipGetErrorString(e));
     return GFG_OK;
 }
 
-// Launch the product on the tile that suits it.  `p` holds everything but the
-// tile counts.
+template <int LAYOUT, int TM, int TN, int S, int WM, int WN>
+int launch_ring(I8Params p, int out_dtype, hipStream_t s) {
+    const int groups = LAYOUT == MASKED ? p.G : 1;
+    p.tiles_per_group = int((p.rows + TM - 1) / TM);
+    p.m_tiles = p.tiles_per_group * groups;
+    const int64_t tiles = int64_t(p.m_tiles) * ((p.N + TN - 1) / TN);
+    const dim3 grid{unsigned(tiles)}, block(WM * WN * 64);
+    if (out_dtype == GFG_OUT_BF16)
+        hipLaunchKernelGGL((int8_gemm_kernel<LAYOUT, TM, TN, S, WM, WN, __bf16>), grid, block, 0, s, p);
+    else
+        hipLaunchKernelGGL((int8_gemm_kernel<LAYOUT, TM, TN, S, WM, WN, _Float16>), grid, block, 0, s, p);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return fail(GFG_EHIP, "kernel launch failed: %s", hipGetErrorString(e));
+    return GFG_OK;
+}
+
+// The launches with too few 256 x 256 tiles, by how many tiles of each size
+// there are (one sweep of M x N x K, us, the chosen tile first):
+//  * few rows: the streamed 16 x 32 tile (1 x 7168 x 2304: 5.9, 32 x 32 6.2,
+//    64 x 64 7.7; 16 x 4096 x 4096: 6.3, 6.8, 11.1), or 32 x 32 up to 32 rows;
+//  * 192 tiles of 128 x 128 or more: those (512 x 7168 x 2304: 18.8, 64 x 64
+//    25.8; 1024 x 4096 x 4096: 26.4, 39.2);
+//  * 256 tiles of 64 x 64 or more: those, in shared stages (512 x 4096 x 4096:
+//    21.2, 128 x 128 24.6; 256 x 7168 x 7168: 36.3, 40.4);
+//  * below, the streamed tiles, 32 x 32 up to 512 of them (128 x 4096 x 4096:
+//    10.0, 64 x 64 12.6; 4096 x 64 x 16384: 24, 44), then 64 x 64 (2000 x 300 x
+//    16384: 37.9, 32 x 32 52).
+template <int LAYOUT>
+int launch_small(const I8Params& p, int out_dtype, hipStream_t s) {
+    auto tiles = [&](int64_t tm, int64_t tn) {
+        return (p.rows + tm - 1) / tm * (LAYOUT == MASKED ? p.G : 1) * ((p.N + tn - 1) / tn);
+    };
+    if (p.rows <= 16) return launch_stream<LAYOUT, 1, 2, 4, 4>(p, out_dtype, s);
+    if (p.rows <= 32) return launch_stream<LAYOUT, 2, 2, 4, 2>(p, out_dtype, s);
+    if (tiles(128, 128) >= 192) return launch_ring<LAYOUT, 128, 128, 4, 2, 4>(p, out_dtype, s);
+    if (tiles(64, 64) >= 256) return launch_ring<LAYOUT, 64, 64, 4, 2, 2>(p, out_dtype, s);
+    if (tiles(32, 32) <= 512) return launch_stream<LAYOUT, 2, 2, 4, 2>(p, out_dtype, s);
+    return launch_stream<LAYOUT, 4, 4, 4, 2>(p, out_dtype, s);
+}
+
+// Launch the product on the tile that suits it: 256 x 256 from 7/16 as many
+// such tiles as CUs on (1024 x 7168 x 2304, 112 tiles: 31.5 us, 35.2 on 128 x
+// 128; 2048 x 4096 x 4096, 128 tiles: 48.6, 50.7; but 2048^3, 64 tiles: 26.8,
+// 16.0).  `p` holds everything but the tile counts.
 int launch_i8(const char* fn, I8Params p, int layout, int out_dtype, hipStream_t s) {
     int cus = 0;
     if (int rc = device_cus(&cus)) return rc;
     const int groups = layout == MASKED ? p.G : 1;
-    const int64_t t128 = (p.rows + TM - 1) / TM * groups, t256 = (p.rows + 255) / 256 * groups;
+    const int64_t t128 = (p.rows + 127) / 128 * groups, t256 = (p.rows + 255) / 256 * groups;
     const int64_t n256 = (int64_t(p.N) + 255) / 256;
     const bool fits = p.N <= 1 << 22;
     const int choice = tile_shape_choice();
     if (choice == GFG_TILE_256x256 && !fits)
         return fail(GFG_EUNSUPPORTED, "%s: the 256 x 256 tile needs N=%d at most 2^22", fn, p.N);
-    if (choice == GFG_TILE_256x256 || (choice == GFG_TILE_AUTO && fits && t256 * n256 >= cus / 2)) {
+    if (choice == GFG_TILE_256x256 || (choice == GFG_TILE_AUTO && fits && t256 * n256 * 16 >= cus * 7)) {
         p.m_tiles = int(layout == CONTIG ? t128 : t256);
         p.tiles_per_group = int(t256 / groups);
         return launch_int8_256(p, layout, out_dtype, s);
     }
-    p.m_tiles = int(t128);
-    p.tiles_per_group = int(t128 / groups);
-    if (layout == DENSE) return launch_128<DENSE>(p, out_dtype, s);
-    if (layout == CONTIG) return launch_128<CONTIG>(p, out_dtype, s);
-    return launch_128<MASKED>(p, out_dtype, s);
+    if (layout == DENSE) return launch_small<DENSE>(p, out_dtype, s);
+    if (layout == CONTIG) return launch_small<CONTIG>(p, out_dtype, s);
+    return launch_small<MASKED>(p, out_dtype, s);
 }
 
 I8Params product(const int8_t* a, const float* a_scale, const int8_t* b, const float* b_scale, const float* bias,
@@ -423,8 +663,8 @@ extern "C" int int8_gemm(const int8_t* a, const float* a_scale, const int8_t* b,
     if (int rc = check_product(fn, M, N, K, 1, out_dtype, &empty)) return rc;
     if (empty) return GFG_OK;
     if (int rc = check_operands(fn, a, a_scale, b, b_scale, bias, false, d)) return rc;
-    const int64_t tiles = (M + TM - 1) / TM;
-    if (tiles > kMaxRowTiles) return fail(GFG_EUNSUPPORTED, "%s: M=%lld above %lld", fn, (long long)M, (long long)(kMaxRowTiles * TM));
+    const int64_t tiles = (M + 127) / 128;
+    if (tiles > kMaxRowTiles) return fail(GFG_EUNSUPPORTED, "%s: M=%lld above %lld", fn, (long long)M, (long long)(kMaxRowTiles * 128));
     return launch_i8(fn, product(a, a_scale, b, b_scale, bias, nullptr, d, M, N, K, 1), DENSE, out_dtype,
                      static_cast<hipStream_t>(stream));
 }
@@ -452,8 +692,8 @@ extern "C" int int8_linear(const void* x, int32_t in_dtype, const int8_t* b, con
     float* const scale = reinterpret_cast<float*>(q + M * K);
     if (int rc = check_quant(fn, x, in_dtype, M, K, q, scale)) return rc;
     if (int rc = check_operands(fn, q, scale, b, b_scale, bias, false, d)) return rc;
-    const int64_t tiles = (M + TM - 1) / TM;
-    if (tiles > kMaxRowTiles) return fail(GFG_EUNSUPPORTED, "%s: M=%lld above %lld", fn, (long long)M, (long long)(kMaxRowTiles * TM));
+    const int64_t tiles = (M + 127) / 128;
+    if (tiles > kMaxRowTiles) return fail(GFG_EUNSUPPORTED, "%s: M=%lld above %lld", fn, (long long)M, (long long)(kMaxRowTiles * 128));
     hipStream_t s = static_cast<hipStream_t>(stream);
     if (int rc = quantize(x, in_dtype, M, K, q, scale, s)) return rc;
     return launch_i8(fn, product(reinterpret_cast<const int8_t*>(q), scale, b, b_scale, bias, nullptr, d, M, N, K, 1), DENSE,
@@ -469,7 +709,7 @@ extern "C" int grouped_int8_gemm_contiguous(const int8_t* a, const float* a_scal
     if (int rc = check_product(fn, M, N, K, G, out_dtype, &empty)) return rc;
     if (empty) return GFG_OK;
     if (int rc = check_operands(fn, a, a_scale, b, b_scale, grouped_layout, true, d)) return rc;
-    const int64_t tiles = (M + TM - 1) / TM;
+    const int64_t tiles = (M + 127) / 128;
     if (tiles > 4096) return fail(GFG_EUNSUPPORTED, "%s: M=%lld is more than 4096 tiles of 128 rows", fn, (long long)M);
     return launch_i8(fn, product(a, a_scale, b, b_scale, nullptr, grouped_layout, d, M, N, K, G), CONTIG, out_dtype,
                      static_cast<hipStream_t>(stream));
@@ -484,7 +724,7 @@ extern "C" int grouped_int8_gemm_masked(const int8_t* a, const float* a_scale, c
     if (int rc = check_product(fn, M_max, N, K, G, out_dtype, &empty)) return rc;
     if (empty) return GFG_OK;
     if (int rc = check_operands(fn, a, a_scale, b, b_scale, masked_m, true, d)) return rc;
-    const int64_t tiles = (M_max + TM - 1) / TM;
+    const int64_t tiles = (M_max + 127) / 128;
     if (tiles > 4096 || tiles * G > 4096)
         return fail(GFG_EUNSUPPORTED, "%s: G=%d x M_max=%lld is more than 4096 tiles of 128 rows", fn, G, (long long)M_max);
     return launch_i8(fn, product(a, a_scale, b, b_scale, nullptr, masked_m, d, M_max, N, K, G), MASKED, out_dtype,

@@ -386,12 +386,19 @@ __device__ __forceinline__ void up_tile(const MoeParams& p, const GFG_LDS Routin
             }
     };
 #pragma unroll
-    for (int d = 0; d < D; ++d) load(st[d], kb0 + d);
+    for (int d = 0; d < D; ++d) {
+        load(st[d], kb0 + d);
+        __builtin_amdgcn_sched_barrier(0);
+    }
+    // the barriers keep the order as written: consume a block, load the one
+    // that takes its registers, D blocks ahead
     for (int kb = kb0; kb < kb1; kb += D) {
 #pragma unroll
         for (int d = 0; d < D; ++d) {
             if (kb + d < kb1) consume(st[d]);
+            __builtin_amdgcn_sched_barrier(0);
             load(st[d], kb + d + D);
+            __builtin_amdgcn_sched_barrier(0);
         }
     }
     // the waves' sums meet in LDS; wave t finishes token tile t
@@ -484,8 +491,18 @@ __device__ __forceinline__ void down_tile(const MoeParams& p, const GFG_LDS Rout
     Unit un{};
     uint32_t hoff[NT];
     __amdgpu_buffer_rsrc_t rw = make_rsrc(p.w2, 0), rs = make_rsrc(p.w2, 0);
+#pragma unroll
+    for (int t = 0; t < NT; ++t) hoff[t] = kOutside;
+    // past the last unit the windows are empty: the loads stay in the stream,
+    // so that the compiler's waits count the same on every path, and touch nothing
     auto enter = [&]() {
-        if (cu >= units) return;
+        if (cu >= units) {
+            rw = make_rsrc(p.w2, 0);
+            rs = make_rsrc(p.w2, 0);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) hoff[t] = kOutside;
+            return;
+        }
         un = unit_of(r, cu);
         rw = make_rsrc(p.w2 + (int64_t(un.e) * p.H + tile * 16) * p.I, 16u * uint32_t(p.I));
         rs = make_rsrc(static_cast<const uint8_t*>(p.s2) + (int64_t(un.e) * (p.H / 128) + tile / 8) * KB, uint32_t(KB));
@@ -500,7 +517,6 @@ __device__ __forceinline__ void down_tile(const MoeParams& p, const GFG_LDS Rout
     DownStage<NT> st[D];
     auto load = [&](DownStage<NT>& s) {
         s.unit = cu < units ? cu : -1;
-        if (cu >= units) return;
 #pragma unroll
         for (int j = 0; j < 2; ++j) s.w[j] = load16(rw, woff + uint32_t(ck) * 128u + 64u * j);
 #pragma unroll
@@ -556,12 +572,17 @@ __device__ __forceinline__ void down_tile(const MoeParams& p, const GFG_LDS Rout
         }
     };
 #pragma unroll
-    for (int d = 0; d < D; ++d) load(st[d]);
+    for (int d = 0; d < D; ++d) {
+        load(st[d]);
+        __builtin_amdgcn_sched_barrier(0);
+    }
     while (st[0].unit >= 0) {
 #pragma unroll
         for (int d = 0; d < D; ++d) {
             if (st[d].unit >= 0) consume(st[d]);
+            __builtin_amdgcn_sched_barrier(0);
             load(st[d]);
+            __builtin_amdgcn_sched_barrier(0);
         }
     }
 }

@@ -455,7 +455,7 @@ GFG_API int moe_int8_layer(const void* x, int32_t dtype, const int32_t* topk_ids
  * aligned; a call that misses them then returns GFG_EUNSUPPORTED.  Other
  * values: GFG_EINVAL.  Results of the two tiles agree to the parity
  * tolerance; they are not promised to agree bit for bit.  The int8 products
- * follow the setting too: GFG_TILE_AUTO takes 256 x 256 from half as many such
+ * follow the setting too: GFG_TILE_AUTO takes 256 x 256 from 7/16 as many such
  * tiles as CUs on, GFG_TILE_128x256 their smaller tiles, GFG_TILE_256x256 needs
  * N at most 2^22; their results do not depend on it.
  *

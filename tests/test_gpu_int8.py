@@ -91,7 +91,7 @@ def tile(request):
     (15, 33, 48, "f16", False), (16, 256, 256, "bf16", False), (17, 100, 112, "f16", True), (33, 1000, 7168, "bf16", False),
     (64, 384, 512, "bf16", True), (65, 129, 144, "f16", False), (77, 1003, 1072, "f16", True), (128, 128, 256, "bf16", False),
     (129, 130, 272, "bf16", True), (300, 770, 384, "f16", False), (513, 1024, 2048, "bf16", False),
-    (1000, 517, 656, "f16", True), (2100, 2050, 400, "bf16", False),
+    (1000, 517, 656, "f16", True), (2100, 2050, 400, "bf16", False), (700, 1501, 528, "bf16", True), (20, 90, 2000, "f16", True),
 ])
 def test_dense(M, N, K, out, bias, tile):
     what = f"dense M={M} N={N} K={K} {out} bias={bias}"
@@ -183,6 +183,7 @@ def test_linear_without_rows_and_stream():
 @pytest.mark.parametrize("m_per_group,N,K,out", [
     ([100, 1, 128, 129, 300], 256, 256, "bf16"), ([5, 250], 130, 400, "f16"), ([0, 128, 77], 384, 128, "bf16"),
     ([1000, 30], 641, 656, "bf16"), ([700, 0, 513, 256], 512, 1024, "f16"), ([1], 7, 16, "bf16"),
+    ([1000, 900, 700], 700, 272, "bf16"), ([3000, 2000], 701, 144, "f16"),
 ])
 def test_contiguous(m_per_group, N, K, out, tile):
     from fp8_block_scaled_amd import workloads as wl
@@ -220,6 +221,7 @@ def test_contiguous_all_padding(tile):
 @pytest.mark.parametrize("masked_m,Mmax,N,K,out", [
     ([0, 64, 200], 256, 256, 384, "bf16"), ([512, 3, 129, 0], 512, 133, 272, "f16"), ([-5, 900, 37], 300, 512, 512, "bf16"),
     ([1], 1, 16, 16, "bf16"), ([600, 1024, 0, 257], 1024, 520, 1024, "bf16"),
+    ([1000, 100, 300, 1024], 1024, 803, 144, "f16"), ([3, 0, 9, 16], 16, 200, 656, "bf16"), ([30, 17, 0], 32, 136, 528, "f16"),
 ])
 def test_masked(masked_m, Mmax, N, K, out, tile):
     what = f"masked {masked_m} M_max={Mmax} N={N} K={K} {out}"
