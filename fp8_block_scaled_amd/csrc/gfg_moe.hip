@@ -19,6 +19,7 @@
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
+#include <cstdlib>
 
 #include "gfg.h"
 #include "gfg_device.h"
@@ -141,11 +142,12 @@ void launch_topk(const void* logits, const float* bias, int32_t* ids, float* wei
 // ------------------------------------------------------------------ layer
 constexpr int NT_THREADS = 256, NW = 4;
 constexpr int kMaxPairs = 1024;
-constexpr int kUnitRows = 64;                  // pairs of one expert that share a pass over its weights
+constexpr int kUnitRows = 32;                  // most pairs of one expert that share a pass over its weights
+constexpr int kMaxDepth = 6;                   // LDS stages of a wave's ring
 constexpr uint32_t kOutside = 0x80000000u;     // past every buffer window used here (all below 2^30 bytes)
 
-typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
 typedef _Float16 h2 __attribute__((ext_vector_type(2)));
 typedef _Float16 h8 __attribute__((ext_vector_type(8)));
@@ -163,6 +165,8 @@ struct MoeParams {
     uint8_t* h;              // [T*k][2][I] bf16: the hidden rows as high and low halves
     void* out;               // [T][H]
     int T, k, E, H, I;
+    int ring;                // bytes of each wave's ring
+    int unit_rows;           // 4, 8, 16 or 32: most pairs of a unit
     int ks;                  // down projection: waves that split an expert's I
 };
 
@@ -205,7 +209,7 @@ __device__ __forceinline__ float e8m0(uint32_t b) {
 }
 
 // The pairs of every expert, side by side: list[] holds the pair indices
-// (t * k + j) expert by expert, unit[] the stretches of at most kUnitRows of
+// (t * k + j) expert by expert, unit[] the stretches of at most unit_rows of
 // them: expert | first << 10 | (rows - 1) << 20.  Ids outside [0, E) are in no
 // unit.  Every workgroup builds its own copy, so the copies have to agree on
 // which pairs a unit holds: an expert of one unit may list its pairs in the
@@ -213,14 +217,16 @@ __device__ __forceinline__ float e8m0(uint32_t b) {
 // of several lists them in their own order.
 struct Routing {
     int16_t list[kMaxPairs];
-    int16_t expert[kMaxPairs];
     uint32_t unit[kMaxPairs];
-    int cnt[kMaxExperts];
     int tmp[NW];
     int units, most;         // units, and the largest unit's rows
 };
+constexpr int kBuildBytes = kMaxExperts * 4 + kMaxPairs * 2;    // scratch of the build
 
-__device__ __forceinline__ void build_routing(GFG_LDS Routing* r, const int32_t* ids, int P, int E) {
+__device__ __forceinline__ void build_routing(GFG_LDS Routing* r, GFG_LDS uint8_t* scratch, const int32_t* ids, int P, int E,
+                                              int unit_rows) {
+    GFG_LDS int* const cnt = reinterpret_cast<GFG_LDS int*>(scratch);                    // [kMaxExperts]
+    GFG_LDS int16_t* const expert = reinterpret_cast<GFG_LDS int16_t*>(cnt + kMaxExperts);   // [kMaxPairs]
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     constexpr int PPT = kMaxPairs / NT_THREADS, EPT = kMaxExperts / NT_THREADS;
     int e[PPT], slot[PPT];
@@ -231,31 +237,31 @@ __device__ __forceinline__ void build_routing(GFG_LDS Routing* r, const int32_t*
     }
     if (tid == 0) r->most = 0;
 #pragma unroll
-    for (int i = 0; i < EPT; ++i) r->cnt[tid * EPT + i] = 0;
+    for (int i = 0; i < EPT; ++i) cnt[tid * EPT + i] = 0;
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < PPT; ++i) {
         slot[i] = -1;
         if (e[i] < 0 || e[i] >= E) e[i] = -1;
-        r->expert[tid + i * NT_THREADS] = int16_t(e[i]);
-        if (e[i] >= 0) slot[i] = __hip_atomic_fetch_add(&r->cnt[e[i]], 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+        expert[tid + i * NT_THREADS] = int16_t(e[i]);
+        if (e[i] >= 0) slot[i] = __hip_atomic_fetch_add(&cnt[e[i]], 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
     }
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < PPT; ++i)
-        if (slot[i] >= 0 && r->cnt[e[i]] > kUnitRows) {
+        if (slot[i] >= 0 && cnt[e[i]] > unit_rows) {
             const int p = tid + i * NT_THREADS;
             int before = 0;
-            for (int q = 0; q < p; ++q) before += int(r->expert[q]) == e[i];
+            for (int q = 0; q < p; ++q) before += int(expert[q]) == e[i];
             slot[i] = before;
         }
     int c[EPT], mine = 0;                      // pairs | units << 16 of this thread's experts
     int most = 0;
 #pragma unroll
     for (int i = 0; i < EPT; ++i) {
-        c[i] = r->cnt[tid * EPT + i];
+        c[i] = cnt[tid * EPT + i];
         most = max(most, c[i]);
-        mine += c[i] | ((c[i] + kUnitRows - 1) / kUnitRows) << 16;
+        mine += c[i] | ((c[i] + unit_rows - 1) / unit_rows) << 16;
     }
     int x = mine;
 #pragma unroll
@@ -264,7 +270,7 @@ __device__ __forceinline__ void build_routing(GFG_LDS Routing* r, const int32_t*
         if (lane >= d) x += y;
     }
     if (lane == 63) r->tmp[wave] = x;
-    __hip_atomic_fetch_max(&r->most, min(most, kUnitRows), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+    __hip_atomic_fetch_max(&r->most, min(most, unit_rows), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
     __syncthreads();
     int before = x - mine;
 #pragma unroll
@@ -274,16 +280,16 @@ __device__ __forceinline__ void build_routing(GFG_LDS Routing* r, const int32_t*
 #pragma unroll
     for (int i = 0; i < EPT; ++i) {
         const int ex = tid * EPT + i;
-        r->cnt[ex] = first;
-        for (int done = 0; done < c[i]; done += kUnitRows)
-            r->unit[u++] = uint32_t(ex) | uint32_t(first + done) << 10 | uint32_t(min(c[i] - done, kUnitRows) - 1) << 20;
+        cnt[ex] = first;
+        for (int done = 0; done < c[i]; done += unit_rows)
+            r->unit[u++] = uint32_t(ex) | uint32_t(first + done) << 10 | uint32_t(min(c[i] - done, unit_rows) - 1) << 20;
         first += c[i];
     }
     if (tid == NT_THREADS - 1) r->units = u;
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < PPT; ++i)
-        if (slot[i] >= 0) r->list[r->cnt[e[i]] + slot[i]] = int16_t(tid + i * NT_THREADS);
+        if (slot[i] >= 0) r->list[cnt[e[i]] + slot[i]] = int16_t(tid + i * NT_THREADS);
     __syncthreads();
 }
 
@@ -293,314 +299,414 @@ __device__ __forceinline__ Unit unit_of(const GFG_LDS Routing* r, int u) {
     return Unit{int(w & 0x3FF), int((w >> 10) & 0x3FF), int(w >> 20) + 1};
 }
 
-__device__ __forceinline__ u32x4 load16(__amdgpu_buffer_rsrc_t r, uint32_t off) {
-    return __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0);
+// ---- what both kernels share: a wave's ring.
+//
+// A wave streams 128-byte blocks of 16 or 32 weight rows, with the tokens' (or
+// hidden rows') elements of the same columns, through its own ring of LDS
+// stages filled by direct-to-LDS loads, up to kMaxDepth stages ahead and across
+// the ends of experts and tiles; no barrier stands between a load and its
+// MFMAs.  Whole 128-byte lines by adjacent lanes: loaded straight into MFMA
+// fragments, adjacent lanes are adjacent rows, and the load path passes a
+// quarter of its 64 bytes a cycle.  The fragments are read from LDS in inline
+// assembly, each group together with its wait: the stage index is a run-time
+// value, so the compiler, which cannot tell the stages apart, would make its
+// own LDS reads wait for every load in flight.
+
+// Wait until at most (depth - 1) * PER vector-memory operations are in flight:
+// the stage loaded depth - 1 stages ago has landed.  (The counter has six bits:
+// callers keep (depth - 1) * PER at most 63.)
+template <int PER>
+__device__ __forceinline__ void wait_stage(int depth) {
+#define GFG_AHEAD(D) ((D) * PER < 63 ? (D) * PER : 63)
+    switch (depth) {
+        case 1: GFG_WAITCNT(0, 15); break;
+        case 2: GFG_WAITCNT(GFG_AHEAD(1), 15); break;
+        case 3: GFG_WAITCNT(GFG_AHEAD(2), 15); break;
+        case 4: GFG_WAITCNT(GFG_AHEAD(3), 15); break;
+        case 5: GFG_WAITCNT(GFG_AHEAD(4), 15); break;
+        default: GFG_WAITCNT(GFG_AHEAD(5), 15); break;
+    }
+#undef GFG_AHEAD
 }
 
-// ---- hidden rows: h = silu(g) * u for 16 columns of I and one unit.
+__device__ __forceinline__ void dma(__amdgpu_buffer_rsrc_t r, GFG_LDS uint8_t* dst, uint32_t off) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (GFG_LDS void*)dst, 16, off, 0, 0, 0);
+}
+
+// Elements 4 q .. 4 q + 3 of the 16 floats at p (wave-uniform, 4-byte aligned),
+// through the scalar cache: a vector load here would be younger than the loads
+// in flight, and waiting for it would wait for all of them.
+__device__ __forceinline__ v4f quad_of(const float* p, int q) {
+    typedef const __attribute__((address_space(4))) float sfloat_t;
+    sfloat_t* const s = reinterpret_cast<sfloat_t*>(reinterpret_cast<uintptr_t>(uniform_ptr(reinterpret_cast<const uint8_t*>(p))));
+    v4f o;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) o[c] = q == 0 ? s[c] : q == 1 ? s[4 + c] : q == 2 ? s[8 + c] : s[12 + c];
+    return o;
+}
+
+// Token (or hidden) rows staged for a block: the most that any unit has,
+// rounded up to one of these.  A 16-column MFMA with fewer rows repeats them;
+// the columns past a unit's rows are never stored.
+template <int NR> constexpr int kTiles = NR <= 16 ? 1 : NR / 16;
+
+// Four fragments of one 16-column tile at the addresses a[0..3] plus OFS.
+template <int OFS>
+__device__ __forceinline__ void read4(u32x4 (&f)[4], const uint32_t (&a)[4]) {
+    asm volatile(
+        "ds_read_b128 %0, %4 offset:%c8\n\tds_read_b128 %1, %5 offset:%c8\n\t"
+        "ds_read_b128 %2, %6 offset:%c8\n\tds_read_b128 %3, %7 offset:%c8\n\ts_waitcnt lgkmcnt(0)"
+        : "=&v"(f[0]), "=&v"(f[1]), "=&v"(f[2]), "=&v"(f[3])
+        : "v"(a[0]), "v"(a[1]), "v"(a[2]), "v"(a[3]), "i"(OFS)
+        : "memory");
+}
+
+// Weight rows (two 64-byte halves at w0, w1; GATE_UP: and 16 rows further on)
+// and four fragments of a tile, with one wait.
+template <int OFS>
+__device__ __forceinline__ void read_weights(u32x4 (&w)[2], u32x4 (&f)[4], uint32_t w0, uint32_t w1, const uint32_t (&a)[4]) {
+    asm volatile(
+        "ds_read_b128 %0, %6\n\tds_read_b128 %2, %8 offset:%c12\n\tds_read_b128 %3, %9 offset:%c12\n\tds_read_b128 %1, %7\n\t"
+        "ds_read_b128 %4, %10 offset:%c12\n\tds_read_b128 %5, %11 offset:%c12\n\ts_waitcnt lgkmcnt(0)"
+        : "=&v"(w[0]), "=&v"(w[1]), "=&v"(f[0]), "=&v"(f[1]), "=&v"(f[2]), "=&v"(f[3])
+        : "v"(w0), "v"(w1), "v"(a[0]), "v"(a[1]), "v"(a[2]), "v"(a[3]), "i"(OFS)
+        : "memory");
+}
+template <int OFS>
+__device__ __forceinline__ void read_weights(u32x4 (&w)[4], u32x4 (&f)[4], uint32_t w0, uint32_t w1, const uint32_t (&a)[4]) {
+    asm volatile(
+        "ds_read_b128 %0, %8\n\tds_read_b128 %1, %9\n\tds_read_b128 %2, %8 offset:2048\n\tds_read_b128 %3, %9 offset:2048\n\t"
+        "ds_read_b128 %4, %10 offset:%c14\n\tds_read_b128 %5, %11 offset:%c14\n\tds_read_b128 %6, %12 offset:%c14\n\t"
+        "ds_read_b128 %7, %13 offset:%c14\n\ts_waitcnt lgkmcnt(0)"
+        : "=&v"(w[0]), "=&v"(w[1]), "=&v"(w[2]), "=&v"(w[3]), "=&v"(f[0]), "=&v"(f[1]), "=&v"(f[2]), "=&v"(f[3])
+        : "v"(w0), "v"(w1), "v"(a[0]), "v"(a[1]), "v"(a[2]), "v"(a[3]), "i"(OFS)
+        : "memory");
+}
+
+__device__ __forceinline__ uint32_t lds_addr(GFG_LDS uint8_t* p) { return uint32_t(reinterpret_cast<uintptr_t>(p)); }
+
+// ---- hidden rows: h = silu(g) * u.
 //
-// A tile is the 16 gate rows and the 16 up rows of those columns.  The four
-// waves split H; a lane reads 16 bytes of a weight row (K chunk 16 lq of a
-// 64-byte half) and the token's elements of the same chunk, so the MFMA's K
-// order is a permutation that both operands share.
-template <int NT> constexpr int kUpDepth = NT == 1 ? 4 : NT == 2 ? 3 : 2;
-
-template <int W, int NT>
-struct UpStage {
-    u32x4 w[2][2];           // [gate, up][64-byte half]
-    u32x4 x[NT][2][2];       // [token tile][half][8 elements]
-    uint32_t s[2];           // E8M0 bytes
-};
-
-template <int W, typename A, int NT>
-__device__ __forceinline__ void up_tile(const MoeParams& p, const GFG_LDS Routing* r, GFG_LDS v4f* red, Unit un, int it) {
+// A work item is 16 columns of I for one unit: the 16 gate rows and the 16 up
+// rows of W1.  The four waves split H: wave w takes blocks w, w + 4, ...  LDS
+// stage: 32 weight rows of 128 bytes, 16-byte chunks XOR-swizzled by row & 7,
+// then NR token rows of 256 bytes, chunks XOR-swizzled by row & 15.  Weight
+// chunk c of a row (16 k's) meets the token chunks 2 c and 2 c + 1: the MFMA's
+// k order is a permutation that both operands share.
+template <int W, typename A, int NR>
+__device__ __forceinline__ void up_items(const MoeParams& p, const GFG_LDS Routing* r, GFG_LDS uint8_t* ring, GFG_LDS v4f* red) {
     typedef typename Vec<A>::v8 v8;
+    constexpr int NT = kTiles<NR>, XL = NR / 4, PER = 4 + XL, STAGE = PER * 1024;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int l16 = lane & 15, lq = lane >> 4;
-    const int KB = p.H / 128;
-    const int kb0 = wave * KB / NW, kb1 = (wave + 1) * KB / NW;
-    const uint8_t* const base = p.w1 + (int64_t(un.e) * 2 * p.I + it * 16) * p.H;
-    const __amdgpu_buffer_rsrc_t rw[2] = {make_rsrc(base, 16u * uint32_t(p.H)),
-                                          make_rsrc(base + int64_t(p.I) * p.H, 16u * uint32_t(p.H))};
+    const int KB = p.H / 128, IT = p.I / 16;
+    const int items = __builtin_amdgcn_readfirstlane(r->units) * IT;
+    const int depth = min(p.ring / STAGE, kMaxDepth);
+    ring += wave * p.ring;
     const auto rx = make_rsrc(p.x, uint32_t(p.T) * uint32_t(p.H) * 2u);
-    const int sb = p.I / 128;                  // 128-row scale blocks of the gate half
-    const uint8_t* const sbase = static_cast<const uint8_t*>(p.s1) + (int64_t(un.e) * 2 * sb + it / 8) * KB;
-    const __amdgpu_buffer_rsrc_t rs[2] = {make_rsrc(sbase, uint32_t(KB)), make_rsrc(sbase + int64_t(sb) * KB, uint32_t(KB))};
-    const uint32_t woff = uint32_t(l16) * uint32_t(p.H) + uint32_t(lq * 16);
-    uint32_t xoff[NT];
+
+    // ---- the loads' cursor: item, block, stage
+    const uint32_t woff = uint32_t(lane >> 3) * uint32_t(p.H) + uint32_t(((lane & 7) ^ (lane >> 3)) * 16);
+    uint32_t xoff[XL];
+    __amdgpu_buffer_rsrc_t rg = make_rsrc(p.w1, 0), ru = make_rsrc(p.w1, 0);
+    int li = wave < KB ? int(blockIdx.x) : items, lk = wave, ls = 0;
+    // past the last item the windows are empty: the loads stay in the stream,
+    // so that every wait counts alike, and touch nothing
+    auto enter = [&]() {
+        uint32_t window = 0;
+        const uint8_t* base = p.w1;
+        Unit un{0, 0, 0};
+        if (li < items) {
+            const int u = li / IT, it = li - u * IT;
+            un = unit_of(r, u);
+            base += (int64_t(un.e) * 2 * p.I + it * 16) * p.H;
+            window = 16u * uint32_t(p.H);
+        }
+        rg = make_rsrc(base, window);
+        ru = make_rsrc(base + int64_t(p.I) * p.H, window);
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-        const int i = 16 * t + l16;
-        xoff[t] = i < un.rows ? uint32_t(r->list[un.first + i] / p.k) * uint32_t(p.H) * 2u + uint32_t(lq * 32) : kOutside;
-    }
-    constexpr int D = kUpDepth<NT>;
-    UpStage<W, NT> st[D];
-    auto load = [&](UpStage<W, NT>& s, int kb) {
-        const bool in = kb < kb1;
-        const uint32_t ko = in ? uint32_t(kb) * 128u : 0x40000000u;
+        for (int j = 0; j < XL; ++j) {
+            const int row = 4 * j + (lane >> 4);
+            xoff[j] = row < un.rows ? uint32_t(r->list[un.first + row] / p.k) * uint32_t(p.H) * 2u + uint32_t(((lane & 15) ^ (row & 15)) * 16)
+                                    : kOutside;
+        }
+    };
+    enter();
+    auto issue = [&]() {
+        GFG_LDS uint8_t* const dst = ring + ls * STAGE;
+        const uint32_t kw = uint32_t(lk) * 128u, kx = uint32_t(lk) * 256u;
 #pragma unroll
-        for (int f = 0; f < 2; ++f)
+        for (int j = 0; j < 4; ++j) dma(j < 2 ? rg : ru, dst + j * 1024, woff + kw + uint32_t(8 * (j & 1)) * uint32_t(p.H));
 #pragma unroll
-            for (int j = 0; j < 2; ++j) s.w[f][j] = load16(rw[f], woff + ko + 64u * j);
+        for (int j = 0; j < XL; ++j) dma(rx, dst + (4 + j) * 1024, xoff[j] + kx);
+        ls = ls + 1 == depth ? 0 : ls + 1;
+        lk += NW;
+        if (lk >= KB) {
+            lk = wave;
+            li += gridDim.x;
+            enter();
+        }
+    };
+    for (int d = 0; d < depth; ++d) issue();
+
+    // fragment addresses in stage 0
+    const uint32_t w0 = lds_addr(ring) + uint32_t(l16 * 128 + ((lq ^ (l16 & 7)) << 4)), w1 = w0 ^ 64u;
+    const int xr = l16 & (NR - 1) & 15;
+    const uint32_t x0 = lds_addr(ring) + 4096u + uint32_t(xr * 256) + uint32_t(((2 * lq) ^ xr) << 4);
+    int cs = 0;
+    for (int item = blockIdx.x; item < items; item += gridDim.x) {
+        const int u = item / IT, it = item - u * IT;
+        const Unit un = unit_of(r, u);
+        const int sb = p.I / 128;              // 128-row scale blocks of the gate half
+        const uint8_t* const sg = uniform_ptr(static_cast<const uint8_t*>(p.s1) + (int64_t(un.e) * 2 * sb + it / 8) * KB);
+        const uint8_t* const su = uniform_ptr(sg + int64_t(sb) * KB);
+        v4f acc[2][NT] = {};
+        for (int kb = wave; kb < KB; kb += NW) {
+            int bg = 0, bu = 0;
+            if constexpr (W == FP8) {
+                bg = load_scale_word(sg, kb);
+                bu = load_scale_word(su, kb);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            wait_stage<PER>(depth);
+            const uint32_t so = uint32_t(cs * STAGE);
+            const uint32_t xa[4] = {x0 + so, (x0 ^ 16u) + so, (x0 ^ 128u) + so, (x0 ^ 144u) + so};   // [64-byte half][8 elements]
+            u32x4 w[4], x[NT][4];
+            read_weights<0>(w, x[0], w0 + so, w1 + so, xa);
+            if constexpr (NT > 1) read4<4096>(x[1], xa);
+            __builtin_amdgcn_sched_barrier(0);
+            issue();                           // into the stage just read
+            __builtin_amdgcn_sched_barrier(0);
+            cs = cs + 1 == depth ? 0 : cs + 1;
+            v4f part[2][NT];
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+            for (int f = 0; f < 2; ++f)
+#pragma unroll
+                for (int t = 0; t < NT; ++t) part[f][t] = W == FP8 ? v4f{} : acc[f][t];
 #pragma unroll
             for (int j = 0; j < 2; ++j)
 #pragma unroll
                 for (int q = 0; q < 2; ++q)
-                    s.x[t][j][q] = load16(rx, xoff[t] + (in ? uint32_t(kb) * 256u : 0x40000000u) + 128u * j + 16u * q);
-        if constexpr (W == FP8) {
+#pragma unroll
+                    for (int f = 0; f < 2; ++f) {
+                        const v8 a = widen<W, A>(w[2 * f + j][2 * q], w[2 * f + j][2 * q + 1]);
+#pragma unroll
+                        for (int t = 0; t < NT; ++t) part[f][t] = mma(a, __builtin_bit_cast(v8, x[t][2 * j + q]), part[f][t]);
+                    }
+            const float sc[2] = {e8m0(uint32_t(scale_byte(bg, sg, kb))), e8m0(uint32_t(scale_byte(bu, su, kb)))};
 #pragma unroll
             for (int f = 0; f < 2; ++f)
-                s.s[f] = __builtin_amdgcn_raw_buffer_load_b8(rs[f], in ? uint32_t(kb) : kOutside, 0, 0);
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    if constexpr (W == FP8) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) acc[f][t][i] = fmaf(part[f][t][i], sc[f], acc[f][t][i]);
+                    } else {
+                        acc[f][t] = part[f][t];
+                    }
+                }
         }
-    };
-    v4f acc[2][NT] = {};
-    auto consume = [&](const UpStage<W, NT>& s) {
-        v4f part[2][NT];
+        // the waves' sums meet in LDS; wave t finishes token tile t
+        GFG_WAITCNT(63, 0);
+        __builtin_amdgcn_s_barrier();          // the previous item's sums have been read
 #pragma unroll
         for (int f = 0; f < 2; ++f)
 #pragma unroll
-            for (int t = 0; t < NT; ++t) part[f][t] = W == FP8 ? v4f{} : acc[f][t];
+            for (int t = 0; t < NT; ++t) red[((wave * 2 + f) * NT + t) * 64 + lane] = acc[f][t];
+        GFG_WAITCNT(63, 0);
+        __builtin_amdgcn_s_barrier();
+        const int i = 16 * wave + l16;
+        if (wave >= NT || i >= un.rows) continue;
+        v4f g = {}, v = {};
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int w = 0; w < NW; ++w) {
+            g += red[((w * 2) * NT + wave) * 64 + lane];
+            v += red[((w * 2 + 1) * NT + wave) * 64 + lane];
+        }
+        const int col = it * 16 + lq * 4;
+        if constexpr (W == INT8) {
+            const float* sc = static_cast<const float*>(p.s1) + int64_t(un.e) * 2 * p.I + it * 16;
+            const v4f cg = quad_of(sc, lq), cu = quad_of(sc + p.I, lq);
 #pragma unroll
-            for (int q = 0; q < 2; ++q)
-#pragma unroll
-                for (int f = 0; f < 2; ++f) {
-                    const v8 a = widen<W, A>(s.w[f][j][2 * q], s.w[f][j][2 * q + 1]);
-#pragma unroll
-                    for (int t = 0; t < NT; ++t) part[f][t] = mma(a, __builtin_bit_cast(v8, s.x[t][j][q]), part[f][t]);
-                }
-#pragma unroll
-        for (int f = 0; f < 2; ++f)
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                if constexpr (W == FP8) {
-                    const float sc = e8m0(s.s[f]);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[f][t][i] = fmaf(part[f][t][i], sc, acc[f][t][i]);
-                } else {
-                    acc[f][t] = part[f][t];
-                }
+            for (int c = 0; c < 4; ++c) {
+                g[c] *= cg[c];
+                v[c] *= cu[c];
             }
-    };
-#pragma unroll
-    for (int d = 0; d < D; ++d) {
-        load(st[d], kb0 + d);
-        __builtin_amdgcn_sched_barrier(0);
-    }
-    // the barriers keep the order as written: consume a block, load the one
-    // that takes its registers, D blocks ahead
-    for (int kb = kb0; kb < kb1; kb += D) {
-#pragma unroll
-        for (int d = 0; d < D; ++d) {
-            if (kb + d < kb1) consume(st[d]);
-            __builtin_amdgcn_sched_barrier(0);
-            load(st[d], kb + d + D);
-            __builtin_amdgcn_sched_barrier(0);
         }
-    }
-    // the waves' sums meet in LDS; wave t finishes token tile t
-    __syncthreads();                           // the previous tile's sums have been read
-#pragma unroll
-    for (int f = 0; f < 2; ++f)
-#pragma unroll
-        for (int t = 0; t < NT; ++t) red[((wave * 2 + f) * NT + t) * 64 + lane] = acc[f][t];
-    __syncthreads();
-    const int i = 16 * wave + l16;
-    if (wave >= NT || i >= un.rows) return;
-    v4f g = {}, u = {};
-#pragma unroll
-    for (int w = 0; w < NW; ++w) {
-        g += red[((w * 2) * NT + wave) * 64 + lane];
-        u += red[((w * 2 + 1) * NT + wave) * 64 + lane];
-    }
-    const int col = it * 16 + lq * 4;
-    if constexpr (W == INT8) {
-        const float* sc = static_cast<const float*>(p.s1) + int64_t(un.e) * 2 * p.I + col;
+        // h in two bf16 halves, high and low: 16 significant bits with fp32's
+        // range, so that the only rounding to 16 bits is the output's
+        bf4 hi, lo;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-            g[c] *= sc[c];
-            u[c] *= sc[p.I + c];
+            const float h = g[c] / (1.0f + expf(-g[c])) * v[c];
+            hi[c] = __bf16(h);
+            const float rest = h - float(hi[c]);
+            lo[c] = __bf16(rest == rest ? rest : 0.0f);   // an infinite h has no low half
         }
+        uint8_t* const row = p.h + int64_t(r->list[un.first + i]) * 4 * p.I + col * 2;
+        *reinterpret_cast<bf4*>(row) = hi;
+        *reinterpret_cast<bf4*>(row + 2 * p.I) = lo;
     }
-    // h in two bf16 halves, high and low: 16 significant bits with fp32's
-    // range, so that the only rounding to 16 bits is the output's
-    typedef __bf16 b4 __attribute__((ext_vector_type(4)));
-    b4 hi, lo;
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        const float v = g[c] / (1.0f + expf(-g[c])) * u[c];
-        hi[c] = __bf16(v);
-        const float rest = v - float(hi[c]);
-        lo[c] = __bf16(rest == rest ? rest : 0.0f);   // an infinite v has no low half
-    }
-    uint8_t* const row = p.h + int64_t(r->list[un.first + i]) * 4 * p.I + col * 2;
-    *reinterpret_cast<b4*>(row) = hi;
-    *reinterpret_cast<b4*>(row + 2 * p.I) = lo;
 }
 
 template <int W, typename A>
-__global__ __launch_bounds__(NT_THREADS, 2) void moe_up_kernel(MoeParams p) {
+__global__ __launch_bounds__(NT_THREADS) void moe_up_kernel(MoeParams p) {
     __shared__ Routing routing;
-    __shared__ v4f red_mem[NW * 2 * 4 * 64];
+    __shared__ v4f red_mem[NW * 2 * kTiles<kUnitRows> * 64];
+    extern __shared__ __attribute__((aligned(1024))) uint8_t ring_mem[];      // [NW][ring]
     GFG_LDS Routing* const r = (GFG_LDS Routing*)&routing;
     GFG_LDS v4f* const red = (GFG_LDS v4f*)red_mem;
-    build_routing(r, p.ids, p.T * p.k, p.E);
-    const int IT = p.I / 16;
-    const int items = __builtin_amdgcn_readfirstlane(r->units) * IT;
-    for (int item = blockIdx.x; item < items; item += gridDim.x) {
-        const int u = item / IT, it = item - u * IT;
-        const Unit un = unit_of(r, u);
-        if (un.rows <= 16) up_tile<W, A, 1>(p, r, red, un, it);
-        else if (un.rows <= 32) up_tile<W, A, 2>(p, r, red, un, it);
-        else up_tile<W, A, 4>(p, r, red, un, it);
-    }
+    GFG_LDS uint8_t* const ring = (GFG_LDS uint8_t*)ring_mem;
+    build_routing(r, ring, p.ids, p.T * p.k, p.E, p.unit_rows);
+    const int most = __builtin_amdgcn_readfirstlane(r->most);
+    if (most <= 4) up_items<W, A, 4>(p, r, ring, red);
+    else if (most <= 8) up_items<W, A, 8>(p, r, ring, red);
+    else if (most <= 16) up_items<W, A, 16>(p, r, ring, red);
+    else up_items<W, A, 32>(p, r, ring, red);
+    GFG_WAITCNT(0, 0);                         // the last loads land before the workgroup ends
 }
 
 // ---- down projection: 16 output columns (rows of W2) for all tokens.
 //
 // A workgroup walks all units; wave w takes units (w / ks), + NW / ks, ... and
-// part w % ks of their I.  Every (part, pair) sum goes to its own place in
-// LDS, and the tokens' weighted sums are taken from there in the order of j:
-// no atomics, and the result does not depend on the routing's list order.
-template <int NT> constexpr int kDownDepth = NT == 1 ? 4 : NT == 2 ? 2 : 1;
-
-template <int NT>
-struct DownStage {
-    u32x4 w[2];              // [64-byte half]
-    u32x4 h[NT][2][2][2];    // [pair tile][high, low][half][8 elements]
-    uint32_t s;
-    int unit;                // the unit this block belongs to, or -1
-    bool last;               // its last block of this wave's part
-};
-
-template <int W, int NT>
-__device__ __forceinline__ void down_tile(const MoeParams& p, const GFG_LDS Routing* r, GFG_LDS v4f* y, int tile) {
+// of their I the blocks w % ks, + ks, ...  Every (part, pair) sum goes to its
+// own place in LDS, and the tokens' weighted sums are taken from there in the
+// order of j: no atomics, and the result does not depend on the routing's list
+// order.  LDS stage: 16 weight rows of 128 bytes, then the high halves of NR
+// hidden rows of 256 bytes, then their low halves.
+template <int W, int NR>
+__device__ __forceinline__ void down_tile(const MoeParams& p, const GFG_LDS Routing* r, GFG_LDS uint8_t* ring, uint32_t y, int tile) {
+    constexpr int NT = kTiles<NR>, HL = NR / 4, PER = 2 + 2 * HL, STAGE = PER * 1024;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int l16 = lane & 15, lq = lane >> 4;
     const int KB = p.I / 128, P = p.T * p.k;
     const int part = wave % p.ks, stride = NW / p.ks;
-    const int kb0 = part * KB / p.ks, kb1 = (part + 1) * KB / p.ks;     // never empty: ks <= KB
     const int units = __builtin_amdgcn_readfirstlane(r->units);
+    const int depth = min(min(p.ring / STAGE, kMaxDepth), 63 / PER + 1);
+    ring += wave * p.ring;
     const auto rh = make_rsrc(p.h, uint32_t(P) * 4u * uint32_t(p.I));
-    const uint32_t woff = uint32_t(l16) * uint32_t(p.I) + uint32_t(lq * 16);
-    // the cursor of the loads, one unit's block after the other
-    int cu = wave / p.ks, ck = kb0;
-    Unit un{};
-    uint32_t hoff[NT];
-    __amdgpu_buffer_rsrc_t rw = make_rsrc(p.w2, 0), rs = make_rsrc(p.w2, 0);
-#pragma unroll
-    for (int t = 0; t < NT; ++t) hoff[t] = kOutside;
-    // past the last unit the windows are empty: the loads stay in the stream,
-    // so that the compiler's waits count the same on every path, and touch nothing
+
+    const uint32_t woff = uint32_t(lane >> 3) * uint32_t(p.I) + uint32_t(((lane & 7) ^ (lane >> 3)) * 16);
+    uint32_t hoff[HL];
+    __amdgpu_buffer_rsrc_t rw = make_rsrc(p.w2, 0);
+    int lu = wave / p.ks, lk = part, ls = 0;
     auto enter = [&]() {
-        if (cu >= units) {
-            rw = make_rsrc(p.w2, 0);
-            rs = make_rsrc(p.w2, 0);
-#pragma unroll
-            for (int t = 0; t < NT; ++t) hoff[t] = kOutside;
-            return;
+        uint32_t window = 0;
+        const uint8_t* base = p.w2;
+        Unit un{0, 0, 0};
+        if (lu < units) {
+            un = unit_of(r, lu);
+            base += (int64_t(un.e) * p.H + tile * 16) * p.I;
+            window = 16u * uint32_t(p.I);
         }
-        un = unit_of(r, cu);
-        rw = make_rsrc(p.w2 + (int64_t(un.e) * p.H + tile * 16) * p.I, 16u * uint32_t(p.I));
-        rs = make_rsrc(static_cast<const uint8_t*>(p.s2) + (int64_t(un.e) * (p.H / 128) + tile / 8) * KB, uint32_t(KB));
+        rw = make_rsrc(base, window);
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            const int i = 16 * t + l16;
-            hoff[t] = i < un.rows ? uint32_t(r->list[un.first + i]) * 4u * uint32_t(p.I) + uint32_t(lq * 32) : kOutside;
+        for (int j = 0; j < HL; ++j) {
+            const int row = 4 * j + (lane >> 4);
+            hoff[j] = row < un.rows ? uint32_t(r->list[un.first + row]) * 4u * uint32_t(p.I) + uint32_t(((lane & 15) ^ (row & 15)) * 16)
+                                    : kOutside;
         }
     };
     enter();
-    constexpr int D = kDownDepth<NT>;
-    DownStage<NT> st[D];
-    auto load = [&](DownStage<NT>& s) {
-        s.unit = cu < units ? cu : -1;
+    auto issue = [&]() {
+        GFG_LDS uint8_t* const dst = ring + ls * STAGE;
+        const uint32_t kw = uint32_t(lk) * 128u, kh = uint32_t(lk) * 256u;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) s.w[j] = load16(rw, woff + uint32_t(ck) * 128u + 64u * j);
+        for (int j = 0; j < 2; ++j) dma(rw, dst + j * 1024, woff + kw + uint32_t(8 * j) * uint32_t(p.I));
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+        for (int pl = 0; pl < 2; ++pl)
 #pragma unroll
-            for (int pl = 0; pl < 2; ++pl)
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-#pragma unroll
-                    for (int q = 0; q < 2; ++q)
-                        s.h[t][pl][j][q] = load16(rh, hoff[t] + uint32_t(pl) * 2u * uint32_t(p.I) + uint32_t(ck) * 256u + 128u * j + 16u * q);
-        if constexpr (W == FP8) s.s = __builtin_amdgcn_raw_buffer_load_b8(rs, uint32_t(ck), 0, 0);
-        s.last = ++ck == kb1;
-        if (s.last) {
-            ck = kb0;
-            cu += stride;
+            for (int j = 0; j < HL; ++j) dma(rh, dst + (2 + pl * HL + j) * 1024, hoff[j] + kh + uint32_t(pl) * 2u * uint32_t(p.I));
+        ls = ls + 1 == depth ? 0 : ls + 1;
+        lk += p.ks;
+        if (lk >= KB) {
+            lk = part;
+            lu += stride;
             enter();
         }
     };
-    v4f acc[NT] = {};
-    auto consume = [&](const DownStage<NT>& s) {
-        v4f sum[NT];
-#pragma unroll
-        for (int t = 0; t < NT; ++t) sum[t] = W == FP8 ? v4f{} : acc[t];
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                const bf8 a = widen<W, __bf16>(s.w[j][2 * q], s.w[j][2 * q + 1]);
-#pragma unroll
-                for (int t = 0; t < NT; ++t)
-#pragma unroll
-                    for (int pl = 0; pl < 2; ++pl) sum[t] = mma(a, __builtin_bit_cast(bf8, s.h[t][pl][j][q]), sum[t]);
+    for (int d = 0; d < depth; ++d) issue();
+
+    const uint32_t w0 = lds_addr(ring) + uint32_t(l16 * 128 + ((lq ^ (l16 & 7)) << 4)), w1 = w0 ^ 64u;
+    const int hr = l16 & (NR - 1) & 15;
+    const uint32_t h0 = lds_addr(ring) + 2048u + uint32_t(hr * 256) + uint32_t(((2 * lq) ^ hr) << 4);
+    int cs = 0;
+    for (int u = wave / p.ks; u < units; u += stride) {
+        const Unit un = unit_of(r, u);
+        const uint8_t* const srow = uniform_ptr(static_cast<const uint8_t*>(p.s2) + (int64_t(un.e) * (p.H / 128) + tile / 8) * KB);
+        v4f acc[NT] = {};
+        for (int kb = part; kb < KB; kb += p.ks) {
+            int b = 0;
+            if constexpr (W == FP8) b = load_scale_word(srow, kb);
+            __builtin_amdgcn_sched_barrier(0);
+            wait_stage<PER>(depth);
+            const uint32_t so = uint32_t(cs * STAGE);
+            const uint32_t ha[4] = {h0 + so, (h0 ^ 16u) + so, (h0 ^ 128u) + so, (h0 ^ 144u) + so};   // [64-byte half][8 elements]
+            u32x4 w[2], h[NT][2][4];           // [tile][high, low][half, 8 elements]
+            read_weights<0>(w, h[0][0], w0 + so, w1 + so, ha);
+            read4<HL * 1024>(h[0][1], ha);
+            if constexpr (NT > 1) {
+                read4<4096>(h[1][0], ha);
+                read4<HL * 1024 + 4096>(h[1][1], ha);
             }
+            __builtin_amdgcn_sched_barrier(0);
+            issue();                           // into the stage just read
+            __builtin_amdgcn_sched_barrier(0);
+            cs = cs + 1 == depth ? 0 : cs + 1;
+            v4f sum[NT];
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            if constexpr (W == FP8) {
-                const float sc = e8m0(s.s);
+            for (int t = 0; t < NT; ++t) sum[t] = W == FP8 ? v4f{} : acc[t];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) acc[t][i] = fmaf(sum[t][i], sc, acc[t][i]);
-            } else {
-                acc[t] = sum[t];
-            }
-        }
-        if (s.last) {
-            const Unit of = unit_of(r, s.unit);
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const bf8 a = widen<W, __bf16>(w[j][2 * q], w[j][2 * q + 1]);
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+#pragma unroll
+                        for (int pl = 0; pl < 2; ++pl) sum[t] = mma(a, __builtin_bit_cast(bf8, h[t][pl][2 * j + q]), sum[t]);
+                }
+            const float sc = e8m0(uint32_t(scale_byte(b, srow, kb)));
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-                const int i = 16 * t + l16;
-                if (i < of.rows) y[(part * P + r->list[of.first + i]) * 4 + lq] = acc[t];
-                acc[t] = v4f{};
+                if constexpr (W == FP8) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[t][i] = fmaf(sum[t][i], sc, acc[t][i]);
+                } else {
+                    acc[t] = sum[t];
+                }
             }
         }
-    };
+        // (in assembly for the same reason as the reads: no wait for the loads in flight)
 #pragma unroll
-    for (int d = 0; d < D; ++d) {
-        load(st[d]);
-        __builtin_amdgcn_sched_barrier(0);
-    }
-    while (st[0].unit >= 0) {
-#pragma unroll
-        for (int d = 0; d < D; ++d) {
-            if (st[d].unit >= 0) consume(st[d]);
-            __builtin_amdgcn_sched_barrier(0);
-            load(st[d]);
-            __builtin_amdgcn_sched_barrier(0);
+        for (int t = 0; t < NT; ++t) {
+            const int i = 16 * t + l16;
+            if (i < un.rows) {
+                const uint32_t at = y + uint32_t((part * P + r->list[un.first + i]) * 64 + lq * 16);
+                asm volatile("ds_write_b128 %0, %1" : : "v"(at), "v"(acc[t]) : "memory");
+            }
         }
     }
 }
 
 template <int W, typename OutT>
-__global__ __launch_bounds__(NT_THREADS, 2) void moe_down_kernel(MoeParams p) {
+__global__ __launch_bounds__(NT_THREADS) void moe_down_kernel(MoeParams p) {
     __shared__ Routing routing;
-    extern __shared__ v4f y_mem[];             // [ks][T * k][16 columns]
+    extern __shared__ __attribute__((aligned(1024))) uint8_t ring_mem[];      // [NW][ring], then sums [ks][T * k][16 columns]
     GFG_LDS Routing* const r = (GFG_LDS Routing*)&routing;
-    GFG_LDS v4f* const y = (GFG_LDS v4f*)y_mem;
+    GFG_LDS uint8_t* const ring = (GFG_LDS uint8_t*)ring_mem;
+    GFG_LDS v4f* const y = (GFG_LDS v4f*)(ring + NW * p.ring);
     const int P = p.T * p.k;
-    build_routing(r, p.ids, P, p.E);
+    build_routing(r, ring, p.ids, P, p.E, p.unit_rows);
     const int most = __builtin_amdgcn_readfirstlane(r->most);
     typedef OutT o4 __attribute__((ext_vector_type(4)));
     for (int tile = blockIdx.x; tile < p.H / 16; tile += gridDim.x) {
-        if (most <= 16) down_tile<W, 1>(p, r, y, tile);
-        else if (most <= 32) down_tile<W, 2>(p, r, y, tile);
-        else down_tile<W, 4>(p, r, y, tile);
+        const uint32_t ya = lds_addr((GFG_LDS uint8_t*)y);
+        if (most <= 4) down_tile<W, 4>(p, r, ring, ya, tile);
+        else if (most <= 8) down_tile<W, 8>(p, r, ring, ya, tile);
+        else if (most <= 16) down_tile<W, 16>(p, r, ring, ya, tile);
+        else down_tile<W, 32>(p, r, ring, ya, tile);
+        GFG_WAITCNT(0, 0);                     // the last loads have landed, the sums are written
         __syncthreads();
         for (int i = threadIdx.x; i < p.T * 4; i += NT_THREADS) {
             const int t = i >> 2, quad = i & 3, col = tile * 16 + quad * 4;
@@ -627,15 +733,22 @@ __global__ __launch_bounds__(NT_THREADS, 2) void moe_down_kernel(MoeParams p) {
 }
 
 template <int W, typename A>
-int launch_layer(const MoeParams& p, hipStream_t s) {
+int launch_layer(MoeParams p, hipStream_t s) {
     int cus = 0;
     if (int rc = device_cus(&cus)) return rc;
     const int P = p.T * p.k;
-    const int64_t up_items = int64_t(P < p.E ? P : p.E) * (p.I / 16) + int64_t(P / kUnitRows) * (p.I / 16);
-    const int up_grid = int(up_items < 2 * cus ? up_items : 2 * cus);
-    hipLaunchKernelGGL((moe_up_kernel<W, A>), dim3(up_grid), dim3(NT_THREADS), 0, s, p);
-    const int tiles = p.H / 16, down_grid = tiles < 2 * cus ? tiles : 2 * cus;
-    hipLaunchKernelGGL((moe_down_kernel<W, A>), dim3(down_grid), dim3(NT_THREADS), unsigned(p.ks * P * 64), s, p);
+    static const char* v1 = getenv("MOE_UP"); static const char* v2 = getenv("MOE_DN");
+    const int r1 = v1 ? atoi(v1) : 14, r2 = v2 ? atoi(v2) : 14;
+    p.ring = r1 * 1024;
+    p.unit_rows = p.T <= 4 ? 4 : p.T <= 8 ? 8 : p.T <= 16 ? 16 : 32;
+    const int64_t up_items = int64_t(P < p.E ? P : p.E) * (p.I / 16) + int64_t(P / p.unit_rows) * (p.I / 16);
+    const int per = r1 > 16 ? 1 : 2, per2 = r2 > 16 ? 1 : 2;
+    const int up_grid = int(up_items < per * cus ? up_items : per * cus);
+    hipLaunchKernelGGL((moe_up_kernel<W, A>), dim3(up_grid), dim3(NT_THREADS), unsigned(NW * p.ring), s, p);
+    const int tiles = p.H / 16, down_grid = tiles < per2 * cus ? tiles : per2 * cus;
+    p.ring = r2 * 1024;
+    if (p.unit_rows == 32 && p.ring < 18 * 1024) p.ring = 18 * 1024;
+    hipLaunchKernelGGL((moe_down_kernel<W, A>), dim3(down_grid), dim3(NT_THREADS), unsigned(NW * p.ring + p.ks * P * 64), s, p);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return fail(GFG_EHIP, "kernel launch failed: %s", hipGetErrorString(e));
     return GFG_OK;
@@ -670,7 +783,7 @@ int layer(const char* fn, int weight, const void* x, int32_t x_dtype, const int3
         return fail(GFG_EINVAL, "%s: workspace of %lld bytes, %lld are needed", fn, (long long)bytes,
                     (long long)workspace_bytes(T, k, I));
     MoeParams p{x, ids, weights, static_cast<const uint8_t*>(w1), s1, static_cast<const uint8_t*>(w2), s2,
-                static_cast<uint8_t*>(workspace), out, int(T), int(k), int(E), int(H), int(I), 1};
+                static_cast<uint8_t*>(workspace), out, int(T), int(k), int(E), int(H), int(I), 0, kUnitRows, 1};
     while (p.ks < NW && p.ks * 2 <= I / 128 && p.ks * 2 * T * k <= 512) p.ks *= 2;
     hipStream_t s = static_cast<hipStream_t>(stream);
     if (weight == FP8) return x_dtype == GFG_OUT_BF16 ? launch_layer<FP8, __bf16>(p, s) : launch_layer<FP8, _Float16>(p, s);
