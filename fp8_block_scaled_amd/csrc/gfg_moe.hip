@@ -19,7 +19,6 @@
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
-#include <cstdlib>
 
 #include "gfg.h"
 #include "gfg_device.h"
@@ -140,9 +139,11 @@ void launch_topk(const void* logits, const float* bias, int32_t* ids, float* wei
 }
 
 // ------------------------------------------------------------------ layer
-constexpr int NT_THREADS = 256, NW = 4;
+constexpr int kWaves = 8;
 constexpr int kMaxPairs = 1024;
-constexpr int kUnitRows = 32;                  // most pairs of one expert that share a pass over its weights
+constexpr int kSmallPairs = 32;                // up to these the routing is built by a wave alone
+constexpr int kScaleBytes = 512;               // scales of a stage (see below)
+constexpr int kMaxDim = 252 * 128;             // H and I: the words of a scale row fit a wave's lanes
 constexpr int kMaxDepth = 6;                   // LDS stages of a wave's ring
 constexpr uint32_t kOutside = 0x80000000u;     // past every buffer window used here (all below 2^30 bytes)
 
@@ -166,8 +167,8 @@ struct MoeParams {
     void* out;               // [T][H]
     int T, k, E, H, I;
     int ring;                // bytes of each wave's ring
-    int unit_rows;           // 4, 8, 16 or 32: most pairs of a unit
-    int ks;                  // down projection: waves that split an expert's I
+    int resident;            // bytes of the rows that stay in LDS, in whole loads; 0: they go through the ring
+    int ks_most;             // down projection: most waves that may split an expert's I
 };
 
 template <typename A> struct Vec;
@@ -209,7 +210,7 @@ __device__ __forceinline__ float e8m0(uint32_t b) {
 }
 
 // The pairs of every expert, side by side: list[] holds the pair indices
-// (t * k + j) expert by expert, unit[] the stretches of at most unit_rows of
+// (t * k + j) expert by expert, unit[] the stretches of at most `rows` of
 // them: expert | first << 10 | (rows - 1) << 20.  Ids outside [0, E) are in no
 // unit.  Every workgroup builds its own copy, so the copies have to agree on
 // which pairs a unit holds: an expert of one unit may list its pairs in the
@@ -218,24 +219,86 @@ __device__ __forceinline__ float e8m0(uint32_t b) {
 struct Routing {
     int16_t list[kMaxPairs];
     uint32_t unit[kMaxPairs];
-    int tmp[NW];
-    int units, most;         // units, and the largest unit's rows
+    int tmp[8];
+    int total[4];            // units if they had at most 2, 4, 8, 16 pairs
+    int units;
 };
 constexpr int kBuildBytes = kMaxExperts * 4 + kMaxPairs * 2;    // scratch of the build
 
-__device__ __forceinline__ void build_routing(GFG_LDS Routing* r, GFG_LDS uint8_t* scratch, const int32_t* ids, int P, int E,
-                                              int unit_rows) {
+// Units of at most LO .. HI pairs (powers of two): the largest size that leaves
+// room for two stages in the ring reads an expert's weights the fewest times;
+// of the sizes that make hardly more units (1/64), the smallest stages the
+// fewest rows that do not exist.  A stage: `fixed` KB of weights, `per4` KB for
+// every four rows.
+template <int LO, int HI>
+__device__ __forceinline__ int choose_rows(const int (&total)[4], int fixed, int per4, int ring) {
+    int rows = LO, fewest = 0;
+#pragma unroll
+    for (int i = 3; i >= 0; --i) {
+        const int r = 2 << i;
+        if (r < LO || r > HI || (r > LO && 2 * ((fixed + per4 * r / 4) * 1024 + kScaleBytes) > ring)) continue;
+        if (fewest == 0) fewest = total[i] + total[i] / 64;
+        if (total[i] <= fewest) rows = r;
+    }
+    return rows;
+}
+
+// Up to kSmallPairs pairs: lane p of every wave holds pair p, and no barrier
+// but the last is needed.  Returns the unit size.
+template <int LO, int HI>
+__device__ __forceinline__ int build_small(GFG_LDS Routing* r, const int32_t* ids, int P, int E, int fixed, int per4, int ring) {
+    const int lane = threadIdx.x & 63;
+    int e = lane < P ? ids[lane] : -1;
+    const bool live = e >= 0 && e < E;
+    if (!live) e = -1;
+    uint64_t same = 0;                         // the pairs of this lane's expert
+    for (int q = 0; q < P; ++q) {
+        const uint64_t m = __ballot(__builtin_amdgcn_readlane(e, q) == e);
+        same = lane == q ? m : same;
+    }
+    const int lead = __builtin_ctzll(same | 1ull << 63), count = __popcll(same);
+    const int before = __popcll(same & ((1ull << lane) - 1));
+    int total[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) total[i] = __popcll(__ballot(live && (before & ((2 << i) - 1)) == 0));
+    const int rows = choose_rows<LO, HI>(total, fixed, per4, ring);
+    // pairs | units << 16 of the experts whose first pair lies before this lane
+    const int own = live && lane == lead ? count | ((count + rows - 1) / rows) << 16 : 0;
+    int x = own;
+#pragma unroll
+    for (int d = 1; d < kSmallPairs; d <<= 1) {
+        const int y = __shfl_up(x, d, 64);
+        if (lane >= d) x += y;
+    }
+    const int base = __shfl(x - own, lead, 64);
+    const int units = __shfl(x, kSmallPairs - 1, 64) >> 16;
+    if (threadIdx.x < 64) {
+        const int first = base & 0xFFFF;
+        if (live) r->list[first + before] = int16_t(lane);
+        if (live && before % rows == 0)
+            r->unit[(base >> 16) + before / rows] =
+                uint32_t(e) | uint32_t(first + before) << 10 | uint32_t(min(count - before, rows) - 1) << 20;
+        if (lane == 0) r->units = units;
+    }
+    __syncthreads();
+    return rows;
+}
+
+template <int WAVES, int LO, int HI>
+__device__ __forceinline__ int build_routing(GFG_LDS Routing* r, GFG_LDS uint8_t* scratch, const int32_t* ids, int P, int E,
+                                             int fixed, int per4, int ring) {
+    if (P <= kSmallPairs) return build_small<LO, HI>(r, ids, P, E, fixed, per4, ring);
     GFG_LDS int* const cnt = reinterpret_cast<GFG_LDS int*>(scratch);                    // [kMaxExperts]
     GFG_LDS int16_t* const expert = reinterpret_cast<GFG_LDS int16_t*>(cnt + kMaxExperts);   // [kMaxPairs]
+    constexpr int THREADS = WAVES * 64, PPT = kMaxPairs / THREADS, EPT = kMaxExperts / THREADS;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    constexpr int PPT = kMaxPairs / NT_THREADS, EPT = kMaxExperts / NT_THREADS;
     int e[PPT], slot[PPT];
 #pragma unroll
     for (int i = 0; i < PPT; ++i) {
-        const int p = tid + i * NT_THREADS;
+        const int p = tid + i * THREADS;
         e[i] = p < P ? ids[p] : -1;
     }
-    if (tid == 0) r->most = 0;
+    if (tid < 4) r->total[tid] = 0;
 #pragma unroll
     for (int i = 0; i < EPT; ++i) cnt[tid * EPT + i] = 0;
     __syncthreads();
@@ -243,26 +306,39 @@ __device__ __forceinline__ void build_routing(GFG_LDS Routing* r, GFG_LDS uint8_
     for (int i = 0; i < PPT; ++i) {
         slot[i] = -1;
         if (e[i] < 0 || e[i] >= E) e[i] = -1;
-        expert[tid + i * NT_THREADS] = int16_t(e[i]);
+        expert[tid + i * THREADS] = int16_t(e[i]);
         if (e[i] >= 0) slot[i] = __hip_atomic_fetch_add(&cnt[e[i]], 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
     }
     __syncthreads();
+    int c[EPT];
+    uint64_t sums = 0;                         // units of at most 2, 4, 8, 16 pairs, 16 bits each
+#pragma unroll
+    for (int i = 0; i < EPT; ++i) {
+        c[i] = cnt[tid * EPT + i];
+#pragma unroll
+        for (int z = 0; z < 4; ++z) sums += uint64_t((c[i] + (2 << z) - 1) >> (1 + z)) << (16 * z);
+    }
+    if (sums) {
+#pragma unroll
+        for (int z = 0; z < 4; ++z)
+            __hip_atomic_fetch_add(&r->total[z], int(sums >> (16 * z)) & 0xFFFF, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+    }
+    __syncthreads();
+    int total[4];
+#pragma unroll
+    for (int z = 0; z < 4; ++z) total[z] = __builtin_amdgcn_readfirstlane(r->total[z]);
+    const int rows = choose_rows<LO, HI>(total, fixed, per4, ring);
 #pragma unroll
     for (int i = 0; i < PPT; ++i)
-        if (slot[i] >= 0 && cnt[e[i]] > unit_rows) {
-            const int p = tid + i * NT_THREADS;
+        if (slot[i] >= 0 && cnt[e[i]] > rows) {
+            const int p = tid + i * THREADS;
             int before = 0;
             for (int q = 0; q < p; ++q) before += int(expert[q]) == e[i];
             slot[i] = before;
         }
-    int c[EPT], mine = 0;                      // pairs | units << 16 of this thread's experts
-    int most = 0;
+    int mine = 0;                              // pairs | units << 16 of this thread's experts
 #pragma unroll
-    for (int i = 0; i < EPT; ++i) {
-        c[i] = cnt[tid * EPT + i];
-        most = max(most, c[i]);
-        mine += c[i] | ((c[i] + unit_rows - 1) / unit_rows) << 16;
-    }
+    for (int i = 0; i < EPT; ++i) mine += c[i] | ((c[i] + rows - 1) / rows) << 16;
     int x = mine;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
@@ -270,27 +346,27 @@ __device__ __forceinline__ void build_routing(GFG_LDS Routing* r, GFG_LDS uint8_
         if (lane >= d) x += y;
     }
     if (lane == 63) r->tmp[wave] = x;
-    __hip_atomic_fetch_max(&r->most, min(most, unit_rows), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
     __syncthreads();
     int before = x - mine;
 #pragma unroll
-    for (int w = 0; w < NW; ++w)
+    for (int w = 0; w < WAVES; ++w)
         if (w < wave) before += r->tmp[w];
     int first = before & 0xFFFF, u = before >> 16;
 #pragma unroll
     for (int i = 0; i < EPT; ++i) {
         const int ex = tid * EPT + i;
         cnt[ex] = first;
-        for (int done = 0; done < c[i]; done += unit_rows)
-            r->unit[u++] = uint32_t(ex) | uint32_t(first + done) << 10 | uint32_t(min(c[i] - done, unit_rows) - 1) << 20;
+        for (int done = 0; done < c[i]; done += rows)
+            r->unit[u++] = uint32_t(ex) | uint32_t(first + done) << 10 | uint32_t(min(c[i] - done, rows) - 1) << 20;
         first += c[i];
     }
-    if (tid == NT_THREADS - 1) r->units = u;
+    if (tid == THREADS - 1) r->units = u;
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < PPT; ++i)
-        if (slot[i] >= 0) r->list[cnt[e[i]] + slot[i]] = int16_t(tid + i * NT_THREADS);
+        if (slot[i] >= 0) r->list[cnt[e[i]] + slot[i]] = int16_t(tid + i * THREADS);
     __syncthreads();
+    return rows;
 }
 
 struct Unit { int e, first, rows; };
@@ -301,20 +377,25 @@ __device__ __forceinline__ Unit unit_of(const GFG_LDS Routing* r, int u) {
 
 // ---- what both kernels share: a wave's ring.
 //
-// A wave streams 128-byte blocks of 16 or 32 weight rows, with the tokens' (or
-// hidden rows') elements of the same columns, through its own ring of LDS
-// stages filled by direct-to-LDS loads, up to kMaxDepth stages ahead and across
-// the ends of experts and tiles; no barrier stands between a load and its
-// MFMAs.  Whole 128-byte lines by adjacent lanes: loaded straight into MFMA
-// fragments, adjacent lanes are adjacent rows, and the load path passes a
-// quarter of its 64 bytes a cycle.  The fragments are read from LDS in inline
-// assembly, each group together with its wait: the stage index is a run-time
-// value, so the compiler, which cannot tell the stages apart, would make its
-// own LDS reads wait for every load in flight.
+// A wave streams 128-byte blocks of 16 or 32 weight rows through its own ring
+// of LDS stages filled by direct-to-LDS loads, up to kMaxDepth stages ahead
+// and across the ends of experts and tiles; no barrier stands between a load
+// and its MFMAs.  Whole 128-byte lines by adjacent lanes: loaded straight into
+// MFMA fragments, adjacent lanes are adjacent rows, and a load takes four times
+// as long.  A CU passes one such load (1 KB, full or not) about every 48
+// cycles, and that, with 256 CUs HBM's rate, bounds the kernels, so what goes
+// beside the weights is kept to few loads: the tokens' (hidden) rows stay in
+// LDS for the whole launch where they are small, else the stage holds only as
+// many of them as units have; an expert's scales come once for a unit.
+//
+// The fragments are read from LDS in inline assembly, each group together with
+// its wait: the stage index is a run-time value, so the compiler, which cannot
+// tell the stages apart, would make its own LDS reads wait for every load in
+// flight.
 
 // Wait until at most (depth - 1) * PER vector-memory operations are in flight:
-// the stage loaded depth - 1 stages ago has landed.  (The counter has six bits:
-// callers keep (depth - 1) * PER at most 63.)
+// the stage loaded depth - 1 stages ago has landed.  (Loads beside the PER of a
+// stage only make the wait stricter.)
 template <int PER>
 __device__ __forceinline__ void wait_stage(int depth) {
 #define GFG_AHEAD(D) ((D) * PER < 63 ? (D) * PER : 63)
@@ -324,7 +405,8 @@ __device__ __forceinline__ void wait_stage(int depth) {
         case 3: GFG_WAITCNT(GFG_AHEAD(2), 15); break;
         case 4: GFG_WAITCNT(GFG_AHEAD(3), 15); break;
         case 5: GFG_WAITCNT(GFG_AHEAD(4), 15); break;
-        default: GFG_WAITCNT(GFG_AHEAD(5), 15); break;
+        case 6: GFG_WAITCNT(GFG_AHEAD(5), 15); break;
+        default: GFG_WAITCNT(GFG_AHEAD(6), 15); break;
     }
 #undef GFG_AHEAD
 }
@@ -332,84 +414,104 @@ __device__ __forceinline__ void wait_stage(int depth) {
 __device__ __forceinline__ void dma(__amdgpu_buffer_rsrc_t r, GFG_LDS uint8_t* dst, uint32_t off) {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (GFG_LDS void*)dst, 16, off, 0, 0, 0);
 }
+__device__ __forceinline__ void dma4(__amdgpu_buffer_rsrc_t r, GFG_LDS uint8_t* dst, uint32_t off) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (GFG_LDS void*)dst, 4, off, 0, 0, 0);
+}
+__device__ __forceinline__ uint32_t lds_addr(GFG_LDS uint8_t* p) { return uint32_t(reinterpret_cast<uintptr_t>(p)); }
 
-// Elements 4 q .. 4 q + 3 of the 16 floats at p (wave-uniform, 4-byte aligned),
-// through the scalar cache: a vector load here would be younger than the loads
-// in flight, and waiting for it would wait for all of them.
-__device__ __forceinline__ v4f quad_of(const float* p, int q) {
-    typedef const __attribute__((address_space(4))) float sfloat_t;
-    sfloat_t* const s = reinterpret_cast<sfloat_t*>(reinterpret_cast<uintptr_t>(uniform_ptr(reinterpret_cast<const uint8_t*>(p))));
-    v4f o;
-#pragma unroll
-    for (int c = 0; c < 4; ++c) o[c] = q == 0 ? s[c] : q == 1 ? s[4 + c] : q == 2 ? s[8 + c] : s[12 + c];
-    return o;
+// Scales.  A unit's first stage also carries them, behind its rows.  FP8: the
+// aligned words of the whole scale row (all K blocks of a 128-row block), one a
+// lane, read into a register and picked by lane when their block comes.  INT8:
+// a float for each output channel.
+//
+// A window over the whole scale tensor that starts on a word; `shift` is what
+// that adds to the tensor's byte offsets.  (An aligned word that holds a byte
+// of an allocation lies in that byte's page.)
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t scale_rsrc(const void* s, uint32_t bytes, uint32_t* shift) {
+    const uintptr_t v = reinterpret_cast<uintptr_t>(s);
+    *shift = uint32_t(v & 3);
+    return make_rsrc(reinterpret_cast<const void*>(v & ~uintptr_t(3)), (bytes + *shift + 3) & ~3u);
+}
+// The scale of block kb of the row that starts at byte offset `row`, from the
+// row's words (lane i: word i).
+__device__ __forceinline__ float picked_scale(uint32_t words, uint32_t row, int kb) {
+    const uint32_t at = row + uint32_t(kb);
+    const uint32_t w = uint32_t(__builtin_amdgcn_readlane(int(words), int((at >> 2) - (row >> 2))));
+    return e8m0((w >> (8 * (at & 3))) & 0xFF);
+}
+__device__ __forceinline__ uint32_t read_word(uint32_t at) {
+    uint32_t v;
+    asm volatile("ds_read_b32 %0, %1\n\ts_waitcnt lgkmcnt(0)" : "=&v"(v) : "v"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ v4f read_quad(uint32_t at) {
+    v4f v;
+    asm volatile("ds_read_b128 %0, %1\n\ts_waitcnt lgkmcnt(0)" : "=&v"(v) : "v"(at) : "memory");
+    return v;
 }
 
-// Token (or hidden) rows staged for a block: the most that any unit has,
-// rounded up to one of these.  A 16-column MFMA with fewer rows repeats them;
-// the columns past a unit's rows are never stored.
-template <int NR> constexpr int kTiles = NR <= 16 ? 1 : NR / 16;
-
-// Four fragments of one 16-column tile at the addresses a[0..3] plus OFS.
-template <int OFS>
-__device__ __forceinline__ void read4(u32x4 (&f)[4], const uint32_t (&a)[4]) {
+// 16 or 32 weight rows (their 64-byte halves at w0 and w1) and the four
+// fragments of the 16 columns beside them, with one wait.
+__device__ __forceinline__ void read_block(u32x4 (&w)[2], u32x4 (&f)[4], uint32_t w0, uint32_t w1, const uint32_t (&a)[4]) {
     asm volatile(
-        "ds_read_b128 %0, %4 offset:%c8\n\tds_read_b128 %1, %5 offset:%c8\n\t"
-        "ds_read_b128 %2, %6 offset:%c8\n\tds_read_b128 %3, %7 offset:%c8\n\ts_waitcnt lgkmcnt(0)"
-        : "=&v"(f[0]), "=&v"(f[1]), "=&v"(f[2]), "=&v"(f[3])
-        : "v"(a[0]), "v"(a[1]), "v"(a[2]), "v"(a[3]), "i"(OFS)
-        : "memory");
-}
-
-// Weight rows (two 64-byte halves at w0, w1; GATE_UP: and 16 rows further on)
-// and four fragments of a tile, with one wait.
-template <int OFS>
-__device__ __forceinline__ void read_weights(u32x4 (&w)[2], u32x4 (&f)[4], uint32_t w0, uint32_t w1, const uint32_t (&a)[4]) {
-    asm volatile(
-        "ds_read_b128 %0, %6\n\tds_read_b128 %2, %8 offset:%c12\n\tds_read_b128 %3, %9 offset:%c12\n\tds_read_b128 %1, %7\n\t"
-        "ds_read_b128 %4, %10 offset:%c12\n\tds_read_b128 %5, %11 offset:%c12\n\ts_waitcnt lgkmcnt(0)"
+        "ds_read_b128 %0, %6\n\tds_read_b128 %1, %7\n\tds_read_b128 %2, %8\n\tds_read_b128 %3, %9\n\t"
+        "ds_read_b128 %4, %10\n\tds_read_b128 %5, %11\n\ts_waitcnt lgkmcnt(0)"
         : "=&v"(w[0]), "=&v"(w[1]), "=&v"(f[0]), "=&v"(f[1]), "=&v"(f[2]), "=&v"(f[3])
-        : "v"(w0), "v"(w1), "v"(a[0]), "v"(a[1]), "v"(a[2]), "v"(a[3]), "i"(OFS)
+        : "v"(w0), "v"(w1), "v"(a[0]), "v"(a[1]), "v"(a[2]), "v"(a[3])
         : "memory");
 }
-template <int OFS>
-__device__ __forceinline__ void read_weights(u32x4 (&w)[4], u32x4 (&f)[4], uint32_t w0, uint32_t w1, const uint32_t (&a)[4]) {
+__device__ __forceinline__ void read_block(u32x4 (&w)[4], u32x4 (&f)[4], uint32_t w0, uint32_t w1, const uint32_t (&a)[4]) {
     asm volatile(
         "ds_read_b128 %0, %8\n\tds_read_b128 %1, %9\n\tds_read_b128 %2, %8 offset:2048\n\tds_read_b128 %3, %9 offset:2048\n\t"
-        "ds_read_b128 %4, %10 offset:%c14\n\tds_read_b128 %5, %11 offset:%c14\n\tds_read_b128 %6, %12 offset:%c14\n\t"
-        "ds_read_b128 %7, %13 offset:%c14\n\ts_waitcnt lgkmcnt(0)"
+        "ds_read_b128 %4, %10\n\tds_read_b128 %5, %11\n\tds_read_b128 %6, %12\n\tds_read_b128 %7, %13\n\ts_waitcnt lgkmcnt(0)"
         : "=&v"(w[0]), "=&v"(w[1]), "=&v"(w[2]), "=&v"(w[3]), "=&v"(f[0]), "=&v"(f[1]), "=&v"(f[2]), "=&v"(f[3])
-        : "v"(w0), "v"(w1), "v"(a[0]), "v"(a[1]), "v"(a[2]), "v"(a[3]), "i"(OFS)
+        : "v"(w0), "v"(w1), "v"(a[0]), "v"(a[1]), "v"(a[2]), "v"(a[3])
         : "memory");
 }
 
-__device__ __forceinline__ uint32_t lds_addr(GFG_LDS uint8_t* p) { return uint32_t(reinterpret_cast<uintptr_t>(p)); }
+// Token rows of `bytes` (a multiple of 256) that stay in LDS, as they lie in
+// memory, loaded by all waves; 16-byte chunks XOR-swizzled by row & 15.
+__device__ __forceinline__ void load_resident(GFG_LDS uint8_t* dst, __amdgpu_buffer_rsrc_t r, int bytes, int total) {
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    for (int at = wave * 1024; at < total; at += kWaves * 1024) {
+        const int b = at + lane * 16;
+        dma(r, dst + at, uint32_t(b ^ (((b / bytes) & 15) << 4)));
+    }
+}
 
 // ---- hidden rows: h = silu(g) * u.
 //
-// A work item is 16 columns of I for one unit: the 16 gate rows and the 16 up
-// rows of W1.  The four waves split H: wave w takes blocks w, w + 4, ...  LDS
-// stage: 32 weight rows of 128 bytes, 16-byte chunks XOR-swizzled by row & 7,
-// then NR token rows of 256 bytes, chunks XOR-swizzled by row & 15.  Weight
-// chunk c of a row (16 k's) meets the token chunks 2 c and 2 c + 1: the MFMA's
-// k order is a permutation that both operands share.
-template <int W, typename A, int NR>
-__device__ __forceinline__ void up_items(const MoeParams& p, const GFG_LDS Routing* r, GFG_LDS uint8_t* ring, GFG_LDS v4f* red) {
+// A work item is C (16 or 8) columns of I for one unit: the C gate rows and the
+// C up rows of W1, which make C / 8 fragments of 16 rows.  The eight waves
+// split H: wave w takes blocks w, w + 8, ...  LDS stage: 2 C weight rows of 128
+// bytes, 16-byte chunks XOR-swizzled by row & 7, then (unless they are
+// resident) NR token rows of 256 bytes, chunks XOR-swizzled by row & 15.
+// Weight chunk c of a row (16 k's) meets the token chunks 2 c and 2 c + 1: the
+// MFMA's k order is a permutation that both operands share.  A unit has at most
+// NR rows; the MFMA's other columns repeat them, and their sums are not stored.
+template <int W, typename A, int NR, int C, bool RES>
+__device__ __forceinline__ void up_items(const MoeParams& p, const GFG_LDS Routing* r, GFG_LDS uint8_t* ring, GFG_LDS uint8_t* rows_mem,
+                                         GFG_LDS v4f* red) {
     typedef typename Vec<A>::v8 v8;
-    constexpr int NT = kTiles<NR>, XL = NR / 4, PER = 4 + XL, STAGE = PER * 1024;
+    constexpr int F = C / 8, WL = C / 4, XL = RES ? 0 : NR / 4, PER = WL + XL, STAGE = PER * 1024 + kScaleBytes;
+    constexpr bool TWICE = NR <= 8;            // the waves' sums have room for two items
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int l16 = lane & 15, lq = lane >> 4;
-    const int KB = p.H / 128, IT = p.I / 16;
+    const int KB = p.H / 128, IT = p.I / C;
     const int items = __builtin_amdgcn_readfirstlane(r->units) * IT;
-    const int depth = min(p.ring / STAGE, kMaxDepth);
+    const int depth = min(min(p.ring / STAGE, kMaxDepth), 63 / PER);
     ring += wave * p.ring;
     const auto rx = make_rsrc(p.x, uint32_t(p.T) * uint32_t(p.H) * 2u);
 
     // ---- the loads' cursor: item, block, stage
     const uint32_t woff = uint32_t(lane >> 3) * uint32_t(p.H) + uint32_t(((lane & 7) ^ (lane >> 3)) * 16);
-    uint32_t xoff[XL];
+    uint32_t xoff[XL ? XL : 1], soff[2] = {0, 0};
+    uint32_t shift;
+    const int sb = p.I / 128;                  // 128-row scale blocks of the gate half
+    const auto rs = scale_rsrc(p.s1, W == FP8 ? uint32_t(p.E) * 2u * uint32_t(sb) * uint32_t(KB) : uint32_t(p.E) * 8u * uint32_t(p.I), &shift);
     __amdgpu_buffer_rsrc_t rg = make_rsrc(p.w1, 0), ru = make_rsrc(p.w1, 0);
     int li = wave < KB ? int(blockIdx.x) : items, lk = wave, ls = 0;
+    bool fresh = true;                         // the next block is its item's first
     // past the last item the windows are empty: the loads stay in the stream,
     // so that every wait counts alike, and touch nothing
     auto enter = [&]() {
@@ -419,8 +521,17 @@ __device__ __forceinline__ void up_items(const MoeParams& p, const GFG_LDS Routi
         if (li < items) {
             const int u = li / IT, it = li - u * IT;
             un = unit_of(r, u);
-            base += (int64_t(un.e) * 2 * p.I + it * 16) * p.H;
-            window = 16u * uint32_t(p.H);
+            base += (int64_t(un.e) * 2 * p.I + it * C) * p.H;
+            window = uint32_t(C) * uint32_t(p.H);
+#pragma unroll
+            for (int f = 0; f < 2; ++f) {
+                if constexpr (W == FP8)
+                    soff[f] = ((uint32_t(un.e * 2 * sb + it * C / 128 + f * sb) * uint32_t(KB) + shift) & ~3u) + 4u * uint32_t(lane);
+                else
+                    soff[f] = lane < C ? uint32_t((un.e * 2 + f) * p.I + it * C + lane) * 4u : kOutside;
+            }
+        } else {
+            soff[0] = soff[1] = kOutside;
         }
         rg = make_rsrc(base, window);
         ru = make_rsrc(base + int64_t(p.I) * p.H, window);
@@ -430,17 +541,24 @@ __device__ __forceinline__ void up_items(const MoeParams& p, const GFG_LDS Routi
             xoff[j] = row < un.rows ? uint32_t(r->list[un.first + row] / p.k) * uint32_t(p.H) * 2u + uint32_t(((lane & 15) ^ (row & 15)) * 16)
                                     : kOutside;
         }
+        fresh = true;
     };
     enter();
     auto issue = [&]() {
         GFG_LDS uint8_t* const dst = ring + ls * STAGE;
         const uint32_t kw = uint32_t(lk) * 128u, kx = uint32_t(lk) * 256u;
+        if (fresh) {
+            dma4(rs, dst + PER * 1024, soff[0]);
+            dma4(rs, dst + PER * 1024 + 256, soff[1]);
+            fresh = false;
+        }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) dma(j < 2 ? rg : ru, dst + j * 1024, woff + kw + uint32_t(8 * (j & 1)) * uint32_t(p.H));
+        for (int j = 0; j < WL; ++j)
+            dma(j < WL / 2 ? rg : ru, dst + j * 1024, woff + kw + uint32_t(8 * (j % (WL / 2))) * uint32_t(p.H));
 #pragma unroll
-        for (int j = 0; j < XL; ++j) dma(rx, dst + (4 + j) * 1024, xoff[j] + kx);
+        for (int j = 0; j < XL; ++j) dma(rx, dst + (WL + j) * 1024, xoff[j] + kx);
         ls = ls + 1 == depth ? 0 : ls + 1;
-        lk += NW;
+        lk += kWaves;
         if (lk >= KB) {
             lk = wave;
             li += gridDim.x;
@@ -448,91 +566,117 @@ __device__ __forceinline__ void up_items(const MoeParams& p, const GFG_LDS Routi
         }
     };
     for (int d = 0; d < depth; ++d) issue();
+    if constexpr (RES) {                       // the resident rows, loaded before the stages, have landed
+        wait_stage<PER>(depth + 1);
+        __builtin_amdgcn_s_barrier();
+    }
 
     // fragment addresses in stage 0
     const uint32_t w0 = lds_addr(ring) + uint32_t(l16 * 128 + ((lq ^ (l16 & 7)) << 4)), w1 = w0 ^ 64u;
-    const int xr = l16 & (NR - 1) & 15;
-    const uint32_t x0 = lds_addr(ring) + 4096u + uint32_t(xr * 256) + uint32_t(((2 * lq) ^ xr) << 4);
-    int cs = 0;
-    for (int item = blockIdx.x; item < items; item += gridDim.x) {
+    const int xr = l16 & (NR - 1);
+    const uint32_t x0 = lds_addr(ring) + uint32_t(WL * 1024 + xr * 256) + uint32_t(((2 * lq) ^ xr) << 4);
+    int cs = 0, done = 0;
+    for (int item = blockIdx.x; item < items; item += gridDim.x, ++done) {
         const int u = item / IT, it = item - u * IT;
         const Unit un = unit_of(r, u);
-        const int sb = p.I / 128;              // 128-row scale blocks of the gate half
-        const uint8_t* const sg = uniform_ptr(static_cast<const uint8_t*>(p.s1) + (int64_t(un.e) * 2 * sb + it / 8) * KB);
-        const uint8_t* const su = uniform_ptr(sg + int64_t(sb) * KB);
-        v4f acc[2][NT] = {};
-        for (int kb = wave; kb < KB; kb += NW) {
-            int bg = 0, bu = 0;
-            if constexpr (W == FP8) {
-                bg = load_scale_word(sg, kb);
-                bu = load_scale_word(su, kb);
+        // byte offsets of the item's gate and up scale rows
+        const uint32_t sg = uint32_t(un.e * 2 * sb + it * C / 128) * uint32_t(KB) + shift, su = sg + uint32_t(sb) * uint32_t(KB);
+        uint32_t wg = 0, wu = 0;               // FP8: their words
+        v4f cg = {}, cu = {};                  // INT8: the channels' scales
+        uint32_t xres = 0;                     // resident: this column's token row
+        if constexpr (RES) {
+            const int tok = r->list[un.first + min(xr, un.rows - 1)] / p.k;
+            xres = lds_addr(rows_mem) + uint32_t(tok) * uint32_t(p.H) * 2u + uint32_t(((2 * lq) ^ (tok & 15)) << 4);
+        }
+        v4f acc[F] = {};
+        // FP8: a block's sums take its scales when the next block's fragments
+        // have been read, so that its MFMAs run under those reads
+        v4f part[F] = {};
+        float sc[2] = {0.0f, 0.0f};
+        auto apply = [&]() {
+#pragma unroll
+            for (int f = 0; f < F; ++f) {
+                const float s = F == 2 ? sc[f] : lq < 2 ? sc[0] : sc[1];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[f][i] = fmaf(part[f][i], s, acc[f][i]);
             }
+        };
+        for (int kb = wave; kb < KB; kb += kWaves) {
             __builtin_amdgcn_sched_barrier(0);
             wait_stage<PER>(depth);
             const uint32_t so = uint32_t(cs * STAGE);
-            const uint32_t xa[4] = {x0 + so, (x0 ^ 16u) + so, (x0 ^ 128u) + so, (x0 ^ 144u) + so};   // [64-byte half][8 elements]
-            u32x4 w[4], x[NT][4];
-            read_weights<0>(w, x[0], w0 + so, w1 + so, xa);
-            if constexpr (NT > 1) read4<4096>(x[1], xa);
+            const uint32_t xb = RES ? xres + uint32_t(kb) * 256u : x0 + so;
+            const uint32_t xa[4] = {xb, xb ^ 16u, xb ^ 128u, xb ^ 144u};    // [64-byte half][8 elements]
+            u32x4 w[WL], x[4];
+            if (kb == wave) {                  // the item's scales
+                const uint32_t sa = lds_addr(ring) + so + PER * 1024u;
+                if constexpr (W == FP8) {
+                    wg = read_word(sa + uint32_t(lane * 4));
+                    wu = read_word(sa + 256u + uint32_t(lane * 4));
+                } else {                       // lanes of the finishing step's rows: see there
+                    cg = read_quad(sa + uint32_t((lq & (C / 4 - 1)) * 16));
+                    cu = read_quad(sa + 256u + uint32_t((lq & (C / 4 - 1)) * 16));
+                }
+            }
+            read_block(w, x, w0 + so, w1 + so, xa);
             __builtin_amdgcn_sched_barrier(0);
             issue();                           // into the stage just read
             __builtin_amdgcn_sched_barrier(0);
             cs = cs + 1 == depth ? 0 : cs + 1;
-            v4f part[2][NT];
+            if constexpr (W == FP8) {
+                apply();
+                sc[0] = picked_scale(wg, sg, kb);
+                sc[1] = picked_scale(wu, su, kb);
 #pragma unroll
-            for (int f = 0; f < 2; ++f)
-#pragma unroll
-                for (int t = 0; t < NT; ++t) part[f][t] = W == FP8 ? v4f{} : acc[f][t];
+                for (int f = 0; f < F; ++f) part[f] = v4f{};
+            }
+            v4f(&to)[F] = W == FP8 ? part : acc;
 #pragma unroll
             for (int j = 0; j < 2; ++j)
 #pragma unroll
                 for (int q = 0; q < 2; ++q)
 #pragma unroll
-                    for (int f = 0; f < 2; ++f) {
+                    for (int f = 0; f < F; ++f) {
                         const v8 a = widen<W, A>(w[2 * f + j][2 * q], w[2 * f + j][2 * q + 1]);
-#pragma unroll
-                        for (int t = 0; t < NT; ++t) part[f][t] = mma(a, __builtin_bit_cast(v8, x[t][2 * j + q]), part[f][t]);
+                        to[f] = mma(a, __builtin_bit_cast(v8, x[2 * j + q]), to[f]);
                     }
-            const float sc[2] = {e8m0(uint32_t(scale_byte(bg, sg, kb))), e8m0(uint32_t(scale_byte(bu, su, kb)))};
-#pragma unroll
-            for (int f = 0; f < 2; ++f)
-#pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    if constexpr (W == FP8) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) acc[f][t][i] = fmaf(part[f][t][i], sc[f], acc[f][t][i]);
-                    } else {
-                        acc[f][t] = part[f][t];
-                    }
-                }
         }
-        // the waves' sums meet in LDS; wave t finishes token tile t
-        GFG_WAITCNT(63, 0);
-        __builtin_amdgcn_s_barrier();          // the previous item's sums have been read
+        if constexpr (W == FP8) apply();
+        // The waves' sums meet in LDS, and the waves with blocks finish items in turn; the
+        // sums of two items have room where units are small, so one barrier an
+        // item is enough (a wave that passes it has finished the item before
+        // the last).  Fragment f, column l16 of row quad lq: place lq * NR + l16.
+        const int last = done % min(KB, kWaves), mine = wave - (wave > last);
+        GFG_LDS v4f* const sums = red + (TWICE && (done & 1) ? (kWaves - 1) * F * 4 * NR : 0);
+        if (!TWICE) {
+            GFG_WAITCNT(63, 0);
+            __builtin_amdgcn_s_barrier();
+        }
+        if (wave != last && l16 < NR) {
 #pragma unroll
-        for (int f = 0; f < 2; ++f)
-#pragma unroll
-            for (int t = 0; t < NT; ++t) red[((wave * 2 + f) * NT + t) * 64 + lane] = acc[f][t];
+            for (int f = 0; f < F; ++f) sums[(mine * F + f) * 4 * NR + lq * NR + l16] = acc[f];
+        }
         GFG_WAITCNT(63, 0);
         __builtin_amdgcn_s_barrier();
-        const int i = 16 * wave + l16;
-        if (wave >= NT || i >= un.rows) continue;
-        v4f g = {}, v = {};
+        if (wave != last) continue;
+        const int lr = l16 & (NR - 1);
 #pragma unroll
-        for (int w = 0; w < NW; ++w) {
-            g += red[((w * 2) * NT + wave) * 64 + lane];
-            v += red[((w * 2 + 1) * NT + wave) * 64 + lane];
+        for (int w = 0; w < kWaves - 1; ++w)
+#pragma unroll
+            for (int f = 0; f < F; ++f) acc[f] += sums[(w * F + f) * 4 * NR + lq * NR + lr];
+        v4f g = acc[0], v;
+        if constexpr (F == 2) {
+            v = acc[F - 1];
+        } else {                               // quads 0, 1 hold the gate rows, quads 2, 3 the up rows
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = __shfl_xor(acc[0][i], 32, 64);
         }
-        const int col = it * 16 + lq * 4;
         if constexpr (W == INT8) {
-            const float* sc = static_cast<const float*>(p.s1) + int64_t(un.e) * 2 * p.I + it * 16;
-            const v4f cg = quad_of(sc, lq), cu = quad_of(sc + p.I, lq);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                g[c] *= cg[c];
-                v[c] *= cu[c];
-            }
+            g *= cg;
+            v *= cu;
         }
+        if (l16 >= un.rows || lq >= C / 4) continue;
+        const int col = it * C + lq * 4;
         // h in two bf16 halves, high and low: 16 significant bits with fp32's
         // range, so that the only rounding to 16 bits is the output's
         bf4 hi, lo;
@@ -543,82 +687,113 @@ __device__ __forceinline__ void up_items(const MoeParams& p, const GFG_LDS Routi
             const float rest = h - float(hi[c]);
             lo[c] = __bf16(rest == rest ? rest : 0.0f);   // an infinite h has no low half
         }
-        uint8_t* const row = p.h + int64_t(r->list[un.first + i]) * 4 * p.I + col * 2;
+        uint8_t* const row = p.h + int64_t(r->list[un.first + l16]) * 4 * p.I + col * 2;
         *reinterpret_cast<bf4*>(row) = hi;
         *reinterpret_cast<bf4*>(row + 2 * p.I) = lo;
     }
 }
 
-template <int W, typename A>
-__global__ __launch_bounds__(NT_THREADS) void moe_up_kernel(MoeParams p) {
+template <int W, typename A, bool RES>
+__global__ __launch_bounds__(kWaves * 64) void moe_up_kernel(MoeParams p) {
     __shared__ Routing routing;
-    __shared__ v4f red_mem[NW * 2 * kTiles<kUnitRows> * 64];
-    extern __shared__ __attribute__((aligned(1024))) uint8_t ring_mem[];      // [NW][ring]
+    __shared__ v4f red_mem[(kWaves - 1) * 2 * 64];
+    extern __shared__ __attribute__((aligned(256))) uint8_t ring_mem[];       // [waves][ring], then the resident rows
     GFG_LDS Routing* const r = (GFG_LDS Routing*)&routing;
     GFG_LDS v4f* const red = (GFG_LDS v4f*)red_mem;
     GFG_LDS uint8_t* const ring = (GFG_LDS uint8_t*)ring_mem;
-    build_routing(r, ring, p.ids, p.T * p.k, p.E, p.unit_rows);
-    const int most = __builtin_amdgcn_readfirstlane(r->most);
-    if (most <= 4) up_items<W, A, 4>(p, r, ring, red);
-    else if (most <= 8) up_items<W, A, 8>(p, r, ring, red);
-    else if (most <= 16) up_items<W, A, 16>(p, r, ring, red);
-    else up_items<W, A, 32>(p, r, ring, red);
+    GFG_LDS uint8_t* const rows_mem = ring + kWaves * p.ring;
+    if constexpr (RES) {
+        load_resident(rows_mem, make_rsrc(p.x, uint32_t(p.T) * uint32_t(p.H) * 2u), p.H * 2, p.resident);
+        const int rows = build_routing<kWaves, 4, 8>(r, ring, p.ids, p.T * p.k, p.E, 4, 0, p.ring);
+        // items of 8 columns where they spread better over the workgroups
+        const int n = __builtin_amdgcn_readfirstlane(r->units) * (p.I / 16), grid = int(gridDim.x);
+        const int walk16 = (n + grid - 1) / grid * 2, walk8 = (2 * n + grid - 1) / grid;
+        if (walk8 * 8 < walk16 * 7) {
+            if (rows <= 4) up_items<W, A, 4, 8, true>(p, r, ring, rows_mem, red);
+            else up_items<W, A, 8, 8, true>(p, r, ring, rows_mem, red);
+        } else {
+            if (rows <= 4) up_items<W, A, 4, 16, true>(p, r, ring, rows_mem, red);
+            else up_items<W, A, 8, 16, true>(p, r, ring, rows_mem, red);
+        }
+    } else {
+        const int rows = build_routing<kWaves, 4, 16>(r, ring, p.ids, p.T * p.k, p.E, 4, 1, p.ring);
+        if (rows <= 4) up_items<W, A, 4, 16, false>(p, r, ring, rows_mem, red);
+        else if (rows <= 8) up_items<W, A, 8, 16, false>(p, r, ring, rows_mem, red);
+        else up_items<W, A, 16, 16, false>(p, r, ring, rows_mem, red);
+    }
     GFG_WAITCNT(0, 0);                         // the last loads land before the workgroup ends
 }
 
-// ---- down projection: 16 output columns (rows of W2) for all tokens.
+// ---- down projection: 16 RT output columns (rows of W2) for all tokens.
 //
-// A workgroup walks all units; wave w takes units (w / ks), + NW / ks, ... and
-// of their I the blocks w % ks, + ks, ...  Every (part, pair) sum goes to its
-// own place in LDS, and the tokens' weighted sums are taken from there in the
-// order of j: no atomics, and the result does not depend on the routing's list
-// order.  LDS stage: 16 weight rows of 128 bytes, then the high halves of NR
-// hidden rows of 256 bytes, then their low halves.
-template <int W, int NR>
-__device__ __forceinline__ void down_tile(const MoeParams& p, const GFG_LDS Routing* r, GFG_LDS uint8_t* ring, uint32_t y, int tile) {
-    constexpr int NT = kTiles<NR>, HL = NR / 4, PER = 2 + 2 * HL, STAGE = PER * 1024;
+// A workgroup walks all units; ks waves share one: wave w takes the units
+// w / ks, + 8 / ks, ... and of their I the blocks w % ks, + ks, ...  Every
+// (part, pair) sum goes to its own place in LDS, and the tokens' weighted sums
+// are taken from there in the order of j: no atomics, and the result does not
+// depend on the routing's list order.  LDS stage: 16 RT weight rows of 128
+// bytes, then (unless they are resident) the high halves of NR hidden rows of
+// 256 bytes, then their low halves (chunks XOR-swizzled by the row, those of
+// the low halves by 8 more).  A unit has at most 8 rows, so one MFMA takes both
+// halves: the high ones in columns 0..7, the low ones in columns 8..15.
+template <int W, int NR, int RT>
+__device__ __forceinline__ void down_tile(const MoeParams& p, const GFG_LDS Routing* r, GFG_LDS uint8_t* ring, uint32_t y, int ks,
+                                          int tile) {
+    constexpr int HL = NR / 2, WL = 2 * RT, PER = WL + HL, STAGE = PER * 1024 + kScaleBytes;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int l16 = lane & 15, lq = lane >> 4;
     const int KB = p.I / 128, P = p.T * p.k;
-    const int part = wave % p.ks, stride = NW / p.ks;
+    const int part = wave % ks, stride = kWaves / ks;
     const int units = __builtin_amdgcn_readfirstlane(r->units);
-    const int depth = min(min(p.ring / STAGE, kMaxDepth), 63 / PER + 1);
+    const int depth = min(min(p.ring / STAGE, kMaxDepth), 63 / PER);
     ring += wave * p.ring;
     const auto rh = make_rsrc(p.h, uint32_t(P) * 4u * uint32_t(p.I));
 
     const uint32_t woff = uint32_t(lane >> 3) * uint32_t(p.I) + uint32_t(((lane & 7) ^ (lane >> 3)) * 16);
-    uint32_t hoff[HL];
+    uint32_t hoff[HL], soff = 0, shift;
+    const auto rs = scale_rsrc(p.s2, W == FP8 ? uint32_t(p.E) * uint32_t(p.H / 128) * uint32_t(KB) : uint32_t(p.E) * uint32_t(p.H) * 4u, &shift);
     __amdgpu_buffer_rsrc_t rw = make_rsrc(p.w2, 0);
-    int lu = wave / p.ks, lk = part, ls = 0;
+    int lu = wave / ks, lk = part, ls = 0;
+    bool fresh = true;
     auto enter = [&]() {
         uint32_t window = 0;
         const uint8_t* base = p.w2;
         Unit un{0, 0, 0};
         if (lu < units) {
             un = unit_of(r, lu);
-            base += (int64_t(un.e) * p.H + tile * 16) * p.I;
-            window = 16u * uint32_t(p.I);
+            base += (int64_t(un.e) * p.H + tile * 16 * RT) * p.I;
+            window = 16u * RT * uint32_t(p.I);
+            if constexpr (W == FP8)
+                soff = ((uint32_t(un.e * (p.H / 128) + tile * RT / 8) * uint32_t(KB) + shift) & ~3u) + 4u * uint32_t(lane);
+            else
+                soff = lane < 16 * RT ? uint32_t(un.e * p.H + tile * RT * 16 + lane) * 4u : kOutside;
+        } else {
+            soff = kOutside;
         }
         rw = make_rsrc(base, window);
+        // staged row 4 j + (lane >> 4): the high halves of the unit's rows, then the low ones
 #pragma unroll
         for (int j = 0; j < HL; ++j) {
-            const int row = 4 * j + (lane >> 4);
-            hoff[j] = row < un.rows ? uint32_t(r->list[un.first + row]) * 4u * uint32_t(p.I) + uint32_t(((lane & 15) ^ (row & 15)) * 16)
+            const int at = 4 * j + (lane >> 4), row = at & (NR - 1), low = at / NR;
+            hoff[j] = row < un.rows ? uint32_t(r->list[un.first + row]) * 4u * uint32_t(p.I) + uint32_t(low) * 2u * uint32_t(p.I) +
+                                          uint32_t(((lane & 15) ^ row ^ (8 * low)) * 16)
                                     : kOutside;
         }
+        fresh = true;
     };
     enter();
     auto issue = [&]() {
         GFG_LDS uint8_t* const dst = ring + ls * STAGE;
         const uint32_t kw = uint32_t(lk) * 128u, kh = uint32_t(lk) * 256u;
+        if (fresh) {
+            dma4(rs, dst + PER * 1024, soff);
+            fresh = false;
+        }
 #pragma unroll
-        for (int j = 0; j < 2; ++j) dma(rw, dst + j * 1024, woff + kw + uint32_t(8 * j) * uint32_t(p.I));
+        for (int j = 0; j < WL; ++j) dma(rw, dst + j * 1024, woff + kw + uint32_t(8 * j) * uint32_t(p.I));
 #pragma unroll
-        for (int pl = 0; pl < 2; ++pl)
-#pragma unroll
-            for (int j = 0; j < HL; ++j) dma(rh, dst + (2 + pl * HL + j) * 1024, hoff[j] + kh + uint32_t(pl) * 2u * uint32_t(p.I));
+        for (int j = 0; j < HL; ++j) dma(rh, dst + (WL + j) * 1024, hoff[j] + kh);
         ls = ls + 1 == depth ? 0 : ls + 1;
-        lk += p.ks;
+        lk += ks;
         if (lk >= KB) {
             lk = part;
             lu += stride;
@@ -628,127 +803,161 @@ __device__ __forceinline__ void down_tile(const MoeParams& p, const GFG_LDS Rout
     for (int d = 0; d < depth; ++d) issue();
 
     const uint32_t w0 = lds_addr(ring) + uint32_t(l16 * 128 + ((lq ^ (l16 & 7)) << 4)), w1 = w0 ^ 64u;
-    const int hr = l16 & (NR - 1) & 15;
-    const uint32_t h0 = lds_addr(ring) + 2048u + uint32_t(hr * 256) + uint32_t(((2 * lq) ^ hr) << 4);
+    const int low = l16 >> 3, hr = l16 & (NR - 1);             // the half and the row of this lane's column
+    const uint32_t h0 = lds_addr(ring) + uint32_t(WL * 1024 + (low * NR + hr) * 256) + uint32_t(((2 * lq) ^ hr ^ (8 * low)) << 4);
     int cs = 0;
-    for (int u = wave / p.ks; u < units; u += stride) {
+    for (int u = wave / ks; u < units; u += stride) {
         const Unit un = unit_of(r, u);
-        const uint8_t* const srow = uniform_ptr(static_cast<const uint8_t*>(p.s2) + (int64_t(un.e) * (p.H / 128) + tile / 8) * KB);
-        v4f acc[NT] = {};
-        for (int kb = part; kb < KB; kb += p.ks) {
-            int b = 0;
-            if constexpr (W == FP8) b = load_scale_word(srow, kb);
+        const uint32_t srow = uint32_t(un.e * (p.H / 128) + tile * RT / 8) * uint32_t(KB) + shift;
+        uint32_t words = 0;                    // FP8: the scale row's words
+        v4f channel[RT] = {};                  // INT8: the channels' scales
+        v4f acc[RT] = {};
+        v4f sum[RT] = {};                      // FP8: the last block's sums, before its scale
+        float sc = 0.0f;
+        auto apply = [&]() {
+#pragma unroll
+            for (int f = 0; f < RT; ++f)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[f][i] = fmaf(sum[f][i], sc, acc[f][i]);
+        };
+        for (int kb = part; kb < KB; kb += ks) {
             __builtin_amdgcn_sched_barrier(0);
             wait_stage<PER>(depth);
             const uint32_t so = uint32_t(cs * STAGE);
-            const uint32_t ha[4] = {h0 + so, (h0 ^ 16u) + so, (h0 ^ 128u) + so, (h0 ^ 144u) + so};   // [64-byte half][8 elements]
-            u32x4 w[2], h[NT][2][4];           // [tile][high, low][half, 8 elements]
-            read_weights<0>(w, h[0][0], w0 + so, w1 + so, ha);
-            read4<HL * 1024>(h[0][1], ha);
-            if constexpr (NT > 1) {
-                read4<4096>(h[1][0], ha);
-                read4<HL * 1024 + 4096>(h[1][1], ha);
+            const uint32_t hb = h0 + so;
+            const uint32_t ha[4] = {hb, hb ^ 16u, hb ^ 128u, hb ^ 144u};    // [64-byte half][8 elements]
+            u32x4 w[WL], h[4];
+            if (kb == part) {                  // the unit's scales
+                const uint32_t sa = lds_addr(ring) + so + PER * 1024u;
+                if constexpr (W == FP8) {
+                    words = read_word(sa + uint32_t(lane * 4));
+                } else {
+#pragma unroll
+                    for (int f = 0; f < RT; ++f) channel[f] = read_quad(sa + uint32_t(64 * f + lq * 16));
+                }
             }
+            read_block(w, h, w0 + so, w1 + so, ha);
             __builtin_amdgcn_sched_barrier(0);
             issue();                           // into the stage just read
             __builtin_amdgcn_sched_barrier(0);
             cs = cs + 1 == depth ? 0 : cs + 1;
-            v4f sum[NT];
+            if constexpr (W == FP8) {
+                apply();
+                sc = picked_scale(words, srow, kb);
 #pragma unroll
-            for (int t = 0; t < NT; ++t) sum[t] = W == FP8 ? v4f{} : acc[t];
+                for (int f = 0; f < RT; ++f) sum[f] = v4f{};
+            }
+            v4f(&to)[RT] = W == FP8 ? sum : acc;
 #pragma unroll
             for (int j = 0; j < 2; ++j)
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const bf8 a = widen<W, __bf16>(w[j][2 * q], w[j][2 * q + 1]);
+                for (int q = 0; q < 2; ++q)
 #pragma unroll
-                    for (int t = 0; t < NT; ++t)
-#pragma unroll
-                        for (int pl = 0; pl < 2; ++pl) sum[t] = mma(a, __builtin_bit_cast(bf8, h[t][pl][2 * j + q]), sum[t]);
-                }
-            const float sc = e8m0(uint32_t(scale_byte(b, srow, kb)));
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                if constexpr (W == FP8) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[t][i] = fmaf(sum[t][i], sc, acc[t][i]);
-                } else {
-                    acc[t] = sum[t];
-                }
-            }
+                    for (int f = 0; f < RT; ++f) {
+                        const bf8 a = widen<W, __bf16>(w[2 * f + j][2 * q], w[2 * f + j][2 * q + 1]);
+                        to[f] = mma(a, __builtin_bit_cast(bf8, h[2 * j + q]), to[f]);
+                    }
         }
-        // (in assembly for the same reason as the reads: no wait for the loads in flight)
+        if constexpr (W == FP8) apply();
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            const int i = 16 * t + l16;
-            if (i < un.rows) {
-                const uint32_t at = y + uint32_t((part * P + r->list[un.first + i]) * 64 + lq * 16);
-                asm volatile("ds_write_b128 %0, %1" : : "v"(at), "v"(acc[t]) : "memory");
+        for (int f = 0; f < RT; ++f) {
+            v4f v = acc[f];                    // column c takes its low half from column c + 8
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                v[i] += __uint_as_float(uint32_t(__builtin_amdgcn_update_dpp(0, int(__float_as_uint(v[i])), 0x128, 0xF, 0xF, false)));
+            if constexpr (W == INT8) v *= channel[f];
+            if (l16 < un.rows) {
+                // (in assembly for the same reason as the reads: no wait for the loads in flight)
+                const uint32_t at = y + uint32_t(((part * P + r->list[un.first + l16]) * RT + f) * 64 + lq * 16);
+                asm volatile("ds_write_b128 %0, %1" : : "v"(at), "v"(v) : "memory");
             }
         }
     }
 }
 
-template <int W, typename OutT>
-__global__ __launch_bounds__(NT_THREADS) void moe_down_kernel(MoeParams p) {
+template <int W, typename OutT, int RT>
+__global__ __launch_bounds__(kWaves * 64) void moe_down_kernel(MoeParams p) {
+    constexpr int THREADS = kWaves * 64;
     __shared__ Routing routing;
-    extern __shared__ __attribute__((aligned(1024))) uint8_t ring_mem[];      // [NW][ring], then sums [ks][T * k][16 columns]
+    __shared__ float wt[kMaxPairs];            // the pairs' weights
+    __shared__ uint64_t live[kMaxPairs / 64];  // bit p: pair p has an expert here
+    // [waves][ring], then the sums [ks][T * k][16 RT columns]
+    extern __shared__ __attribute__((aligned(256))) uint8_t ring_mem[];
     GFG_LDS Routing* const r = (GFG_LDS Routing*)&routing;
     GFG_LDS uint8_t* const ring = (GFG_LDS uint8_t*)ring_mem;
-    GFG_LDS v4f* const y = (GFG_LDS v4f*)(ring + NW * p.ring);
+    GFG_LDS v4f* const y = (GFG_LDS v4f*)(ring + kWaves * p.ring);
     const int P = p.T * p.k;
-    build_routing(r, ring, p.ids, P, p.E, p.unit_rows);
-    const int most = __builtin_amdgcn_readfirstlane(r->most);
+    for (int i = threadIdx.x; i < (P + 63) / 64 * 64; i += THREADS) {
+        const int e = i < P ? p.ids[i] : -1;
+        const uint64_t m = __ballot(e >= 0 && e < p.E);
+        if ((i & 63) == 0) live[i / 64] = m;
+        if (i < P) wt[i] = p.weights[i];
+    }
+    const int rows = build_routing<kWaves, 2, 8>(r, ring, p.ids, P, p.E, 2 * RT, 2, p.ring);
+    const int units = __builtin_amdgcn_readfirstlane(r->units), KB = p.I / 128;
+    // the waves that share a unit: the split with the shortest longest walk
+    int ks = 1, best = (units + kWaves - 1) / kWaves * KB;
+    for (int c = 2; c <= p.ks_most; c *= 2) {
+        const int walk = (units * c + kWaves - 1) / kWaves * ((KB + c - 1) / c);
+        if (walk < best) {
+            best = walk;
+            ks = c;
+        }
+    }
+    const uint32_t ya = lds_addr((GFG_LDS uint8_t*)y);
     typedef OutT o4 __attribute__((ext_vector_type(4)));
-    for (int tile = blockIdx.x; tile < p.H / 16; tile += gridDim.x) {
-        const uint32_t ya = lds_addr((GFG_LDS uint8_t*)y);
-        if (most <= 4) down_tile<W, 4>(p, r, ring, ya, tile);
-        else if (most <= 8) down_tile<W, 8>(p, r, ring, ya, tile);
-        else if (most <= 16) down_tile<W, 16>(p, r, ring, ya, tile);
-        else down_tile<W, 32>(p, r, ring, ya, tile);
+    for (int tile = blockIdx.x; tile < p.H / (16 * RT); tile += gridDim.x) {
+        if (rows <= 2) down_tile<W, 2, RT>(p, r, ring, ya, ks, tile);
+        else if (rows <= 4) down_tile<W, 4, RT>(p, r, ring, ya, ks, tile);
+        else down_tile<W, 8, RT>(p, r, ring, ya, ks, tile);
         GFG_WAITCNT(0, 0);                     // the last loads have landed, the sums are written
         __syncthreads();
-        for (int i = threadIdx.x; i < p.T * 4; i += NT_THREADS) {
-            const int t = i >> 2, quad = i & 3, col = tile * 16 + quad * 4;
+        for (int i = threadIdx.x; i < p.T * 4 * RT; i += THREADS) {
+            const int t = i / (4 * RT), quad = i % (4 * RT);
             v4f sum = {};
             for (int j = 0; j < p.k; ++j) {
-                const int e = p.ids[t * p.k + j];
-                if (e < 0 || e >= p.E) continue;
-                v4f v = {};
-                for (int s = 0; s < p.ks; ++s) v += y[(s * P + t * p.k + j) * 4 + quad];
-                if constexpr (W == INT8) {
-                    const float* sc = static_cast<const float*>(p.s2) + int64_t(e) * p.H + col;
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) v[c] *= sc[c];
-                }
-                const float w = p.weights[t * p.k + j];
+                const int pair = t * p.k + j;
+                if (!((live[pair / 64] >> (pair % 64)) & 1)) continue;
+                v4f v = y[pair * 4 * RT + quad];
+                for (int s = 1; s < ks; ++s) v += y[(s * P + pair) * 4 * RT + quad];
+                const float w = wt[pair];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) sum[c] = fmaf(w, v[c], sum[c]);
             }
-            *reinterpret_cast<o4*>(static_cast<OutT*>(p.out) + int64_t(t) * p.H + col) =
+            *reinterpret_cast<o4*>(static_cast<OutT*>(p.out) + int64_t(t) * p.H + (tile * RT * 16 + quad * 4)) =
                 o4{OutT(sum[0]), OutT(sum[1]), OutT(sum[2]), OutT(sum[3])};
         }
         __syncthreads();
     }
 }
 
+constexpr int kLds = 160 * 1024;
+
 template <int W, typename A>
 int launch_layer(MoeParams p, hipStream_t s) {
     int cus = 0;
     if (int rc = device_cus(&cus)) return rc;
     const int P = p.T * p.k;
-    static const char* v1 = getenv("MOE_UP"); static const char* v2 = getenv("MOE_DN");
-    const int r1 = v1 ? atoi(v1) : 14, r2 = v2 ? atoi(v2) : 14;
-    p.ring = r1 * 1024;
-    p.unit_rows = p.T <= 4 ? 4 : p.T <= 8 ? 8 : p.T <= 16 ? 16 : 32;
-    const int64_t up_items = int64_t(P < p.E ? P : p.E) * (p.I / 16) + int64_t(P / p.unit_rows) * (p.I / 16);
-    const int per = r1 > 16 ? 1 : 2, per2 = r2 > 16 ? 1 : 2;
-    const int up_grid = int(up_items < per * cus ? up_items : per * cus);
-    hipLaunchKernelGGL((moe_up_kernel<W, A>), dim3(up_grid), dim3(NT_THREADS), unsigned(NW * p.ring), s, p);
-    const int tiles = p.H / 16, down_grid = tiles < per2 * cus ? tiles : per2 * cus;
-    p.ring = r2 * 1024;
-    if (p.unit_rows == 32 && p.ring < 18 * 1024) p.ring = 18 * 1024;
-    hipLaunchKernelGGL((moe_down_kernel<W, A>), dim3(down_grid), dim3(NT_THREADS), unsigned(NW * p.ring + p.ks * P * 64), s, p);
+    const dim3 block(kWaves * 64);
+    // one workgroup a CU: what its LDS has left after the fixed parts and the
+    // resident rows goes to the rings
+    const int64_t up_items = (int64_t(P < p.E ? P : p.E) + P / 4) * (p.I / 8);
+    const int up_grid = int(up_items < cus ? up_items : cus);
+    const int x_bytes = p.T * p.H * 2;
+    p.resident = x_bytes <= 32 * 1024 ? (x_bytes + 1023) & ~1023 : 0;
+    p.ring = ((kLds - int(sizeof(Routing)) - (kWaves - 1) * 2048 - 512 - p.resident) / kWaves) & ~255;
+    const unsigned up_lds = unsigned(kWaves * p.ring + p.resident);
+    if (p.resident) hipLaunchKernelGGL((moe_up_kernel<W, A, true>), dim3(up_grid), block, up_lds, s, p);
+    else hipLaunchKernelGGL((moe_up_kernel<W, A, false>), dim3(up_grid), block, up_lds, s, p);
+    // down: 32 columns a workgroup where they fill three quarters of the CUs and the sums stay small
+    const int rt = p.H % 32 == 0 && p.H / 32 >= cus * 3 / 4 && P * 128 <= 40 * 1024 ? 2 : 1;
+    while (p.ks_most < kWaves && p.ks_most * 2 <= p.I / 128 && p.ks_most * 2 * P * 64 * rt <= 24 * 1024) p.ks_most *= 2;
+    const int y_bytes = p.ks_most * P * 64 * rt;
+    const int tiles = p.H / (16 * rt), down_grid = tiles < cus ? tiles : cus;
+    p.ring = ((kLds - int(sizeof(Routing)) - kMaxPairs * 4 - 512 - y_bytes) / kWaves) & ~255;
+    const unsigned lds = unsigned(kWaves * p.ring + y_bytes);
+    if (rt == 2) hipLaunchKernelGGL((moe_down_kernel<W, A, 2>), dim3(down_grid), block, lds, s, p);
+    else hipLaunchKernelGGL((moe_down_kernel<W, A, 1>), dim3(down_grid), block, lds, s, p);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return fail(GFG_EHIP, "kernel launch failed: %s", hipGetErrorString(e));
     return GFG_OK;
@@ -768,8 +977,8 @@ int layer(const char* fn, int weight, const void* x, int32_t x_dtype, const int3
     if (E > kMaxExperts || T > kMaxPairs || k > kMaxPairs || T * k > kMaxPairs)
         return fail(GFG_EUNSUPPORTED, "%s: E=%lld above %d or T*k=%lld above %d", fn, (long long)E, kMaxExperts,
                     (long long)(T * k), kMaxPairs);
-    if (H % 128 || I % 128 || H > 65536 || I > 65536)
-        return fail(GFG_EUNSUPPORTED, "%s: H=%lld and I=%lld must be multiples of 128 up to 65536", fn, (long long)H, (long long)I);
+    if (H % 128 || I % 128 || H > kMaxDim || I > kMaxDim)
+        return fail(GFG_EUNSUPPORTED, "%s: H=%lld and I=%lld must be multiples of 128 up to %d", fn, (long long)H, (long long)I, kMaxDim);
     if (T == 0) return GFG_OK;
     if (!x || !ids || !weights || !w1 || !s1 || !w2 || !s2 || !out) return fail(GFG_EINVAL, "%s: null pointer argument", fn);
     if ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(w1) | reinterpret_cast<uintptr_t>(w2) |
@@ -783,8 +992,7 @@ int layer(const char* fn, int weight, const void* x, int32_t x_dtype, const int3
         return fail(GFG_EINVAL, "%s: workspace of %lld bytes, %lld are needed", fn, (long long)bytes,
                     (long long)workspace_bytes(T, k, I));
     MoeParams p{x, ids, weights, static_cast<const uint8_t*>(w1), s1, static_cast<const uint8_t*>(w2), s2,
-                static_cast<uint8_t*>(workspace), out, int(T), int(k), int(E), int(H), int(I), 0, kUnitRows, 1};
-    while (p.ks < NW && p.ks * 2 <= I / 128 && p.ks * 2 * T * k <= 512) p.ks *= 2;
+                static_cast<uint8_t*>(workspace), out, int(T), int(k), int(E), int(H), int(I), 0, 0, 1};
     hipStream_t s = static_cast<hipStream_t>(stream);
     if (weight == FP8) return x_dtype == GFG_OUT_BF16 ? launch_layer<FP8, __bf16>(p, s) : launch_layer<FP8, _Float16>(p, s);
     return x_dtype == GFG_OUT_BF16 ? launch_layer<INT8, __bf16>(p, s) : launch_layer<INT8, _Float16>(p, s);

@@ -414,7 +414,7 @@ GFG_API int moe_topk(const void* logits, int32_t in_dtype, const float* bias, in
  *                   moe_layer_workspace_bytes(T, k, I) bytes, uninitialized
  *
  * Sizes: T >= 0 (0 is a no-op), T * k <= 1024, E <= 1024, H and I multiples of
- * 128 up to 65536 (else GFG_EUNSUPPORTED).
+ * 128 up to 32256 (else GFG_EUNSUPPORTED).
  */
 GFG_API int64_t moe_layer_workspace_bytes(int64_t T, int64_t k, int64_t I);
 GFG_API int moe_fp8_layer(const void* x, int32_t dtype, const int32_t* topk_ids, const float* topk_weights,
