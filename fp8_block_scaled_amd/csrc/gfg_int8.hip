@@ -518,6 +518,152 @@ int launch_ring(I8Params p, int out_dtype, hipStream_t s) {
     return GFG_OK;
 }
 
+// ------------------------------------------------------------------ a few tokens, quantized on the way
+//
+// At most kFewTokens rows of x in 16 or 32 bits: every workgroup quantizes them
+// itself, into LDS, while its first weights are on the way (the codes and
+// scales are those of the token quantizer, bit for bit), then streams its 32
+// weight rows like the kernel above.  One launch instead of two.
+constexpr int kFewTokens = 4;
+constexpr int kFewCodes = 32 * 1024;           // bytes of LDS for the codes
+
+template <typename X, typename OutT>
+__global__ __launch_bounds__(256) void int8_few_kernel(const X* __restrict__ xs, I8Params p) {
+    constexpr int NW = 4, D = 4, TN = 32, UNIT = TN * TK, PER = UNIT / 1024;
+    __shared__ __attribute__((aligned(1024))) uint8_t s0[NW * UNIT], s1[NW * UNIT], s2[NW * UNIT], s3[NW * UNIT];
+    __shared__ __attribute__((aligned(1024))) uint8_t codes[kFewCodes];   // [M][K rounded up to 128], chunks swizzled like a stage's
+    __shared__ uint32_t amax[kFewTokens][NW];
+    __shared__ v4i sums[NW][2][64];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int l16 = lane & 15, lq = lane >> 4;
+    GFG_LDS uint8_t* const ring[D] = {(GFG_LDS uint8_t*)s0 + wave * UNIT, (GFG_LDS uint8_t*)s1 + wave * UNIT,
+                                      (GFG_LDS uint8_t*)s2 + wave * UNIT, (GFG_LDS uint8_t*)s3 + wave * UNIT};
+    const int M = int(p.rows), n0 = int(blockIdx.x) * TN, ncols = min(TN, p.N - n0);
+    const auto rb = make_rsrc(p.b + int64_t(n0) * p.K, uint32_t(ncols) * uint32_t(p.K));
+    const int kc = ((lane & 7) ^ (lane >> 3)) * 16;
+    const uint32_t src0 = uint32_t(lane >> 3) * uint32_t(p.K) + uint32_t(kc);
+    auto load = [&](GFG_LDS uint8_t* dst, int k) {
+        const uint32_t base = k + kc < p.K ? src0 + uint32_t(k) : kOutside;
+#pragma unroll
+        for (int j = 0; j < PER; ++j)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (GFG_LDS void*)(dst + j * 1024), 16, base + uint32_t(8 * j) * uint32_t(p.K), 0, 0, 0);
+    };
+    constexpr int STEP = NW * TK;
+#pragma unroll
+    for (int d = 0; d < D; ++d) load(ring[d], wave * TK + d * STEP);
+
+    const int chunks = p.K / 8, KP = (p.K + TK - 1) / TK * TK;
+    // the rows' first 8192 elements stay in registers between the maximum and
+    // the encoding, and all of them are loaded before any is used
+    constexpr int HELD = 4;
+    Chunk<X> held[kFewTokens][HELD];
+    auto each = [&](int m, auto&& use) {       // the chunks past them
+        for (int c = threadIdx.x + 256 * HELD; c < KP / 8; c += 256) {
+            Chunk<X> t{};
+            if (c < chunks) t.load(xs + int64_t(m) * p.K + c * 8);
+            use(c, t);
+        }
+    };
+#pragma unroll
+    for (int m = 0; m < kFewTokens; ++m)
+#pragma unroll
+        for (int i = 0; i < HELD; ++i) {
+            const int c = int(threadIdx.x) + 256 * i;
+            held[m][i] = Chunk<X>{};
+            if (m < M && c < chunks) held[m][i].load(xs + int64_t(m) * p.K + c * 8);
+        }
+#pragma unroll
+    for (int m = 0; m < kFewTokens; ++m) {
+        if (m >= M) break;
+        uint32_t ab = 0;
+#pragma unroll
+        for (int i = 0; i < HELD; ++i) ab = max(ab, chunk_amax(held[m][i]));
+        each(m, [&](int, const Chunk<X>& t) { ab = max(ab, chunk_amax(t)); });
+#pragma unroll
+        for (int w = 32; w >= 1; w >>= 1) ab = max(ab, uint32_t(__shfl_xor(int(ab), w, 64)));
+        if (lane == 0) amax[m][wave] = ab;
+    }
+    __syncthreads();
+    float scale = 0.0f;                        // of row l16
+#pragma unroll
+    for (int m = 0; m < kFewTokens; ++m) {
+        if (m >= M) break;
+        float s, r;
+        row_scale(max(max(amax[m][0], amax[m][1]), max(amax[m][2], amax[m][3])), &s, &r);
+        if (l16 == m) scale = s;
+        auto put = [&](int c, const Chunk<X>& t) {     // past K the chunk is zeros; a row without a scale is
+            const int k = c * 8, chunk = (k >> 4) & 7;
+            *reinterpret_cast<u32x2*>(codes + m * KP + (k & ~127) + ((chunk ^ (m & 7)) << 4) + (k & 15)) =
+                r == 0.0f ? u32x2{0u, 0u} : chunk_encode(t, r);
+        };
+#pragma unroll
+        for (int i = 0; i < HELD; ++i)
+            if (int(threadIdx.x) + 256 * i < KP / 8) put(int(threadIdx.x) + 256 * i, held[m][i]);
+        each(m, put);
+    }
+    __syncthreads();
+
+    v4i acc[2] = {};
+    const int row = min(l16, M - 1);           // columns past M repeat the last row and are not stored
+    auto frag = [&](GFG_LDS uint8_t* src, int rw, int chunk) {
+        return *reinterpret_cast<GFG_LDS v4i*>(src + (rw + l16) * TK + ((chunk ^ (l16 & 7)) << 4));
+    };
+    auto step = [&](GFG_LDS uint8_t* cur, int k) {
+        __builtin_amdgcn_sched_barrier(0);
+        GFG_WAITCNT((D - 1) * PER, 15);
+        v4i af[2], bf[2][2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            af[h] = *reinterpret_cast<GFG_LDS v4i*>((GFG_LDS uint8_t*)codes + row * KP + k + (((4 * h + lq) ^ (row & 7)) << 4));
+#pragma unroll
+            for (int f = 0; f < 2; ++f) bf[h][f] = frag(cur, 16 * f, 4 * h + lq);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) acc[c] = __builtin_amdgcn_mfma_i32_16x16x64_i8(bf[h][c], af[h], acc[c], 0, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
+        load(cur, k + D * STEP);               // past K: zeros
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    for (int k = wave * TK; k < p.K; k += D * STEP) {
+        step(ring[0], k);
+        if (k + STEP >= p.K) break;
+        step(ring[1], k + STEP);
+        if (k + 2 * STEP >= p.K) break;
+        step(ring[2], k + 2 * STEP);
+        if (k + 3 * STEP >= p.K) break;
+        step(ring[3], k + 3 * STEP);
+    }
+    GFG_WAITCNT(0, 15);                        // the last loads land before the workgroup ends
+    sums[wave][0][lane] = acc[0];
+    sums[wave][1][lane] = acc[1];
+    __syncthreads();
+    if (wave >= 2 || l16 >= M) return;
+    const v4i total = sums[0][wave][lane] + sums[1][wave][lane] + sums[2][wave][lane] + sums[3][wave][lane];
+    const int n = n0 + 16 * wave + 4 * lq;
+    float v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int nn = min(n + i, p.N - 1);
+        v[i] = fmaf(float(total[i]) * scale, p.b_scale[nn], p.bias ? p.bias[nn] : -0.0f);
+    }
+    store4(static_cast<OutT*>(p.d) + int64_t(l16) * p.N, n, p.N, (p.N & 3) == 0, v);
+}
+
+template <typename X>
+int launch_few(const void* x, const I8Params& p, int out_dtype, hipStream_t s) {
+    const dim3 grid(unsigned((p.N + 31) / 32)), block(256);
+    if (out_dtype == GFG_OUT_BF16)
+        hipLaunchKernelGGL((int8_few_kernel<X, __bf16>), grid, block, 0, s, static_cast<const X*>(x), p);
+    else
+        hipLaunchKernelGGL((int8_few_kernel<X, _Float16>), grid, block, 0, s, static_cast<const X*>(x), p);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return fail(GFG_EHIP, "kernel launch failed: %s", hipGetErrorString(e));
+    return GFG_OK;
+}
+
 // The launches with too few 256 x 256 tiles, by how many tiles of each size
 // there are (one sweep of M x N x K, us, the chosen tile first):
 //  * few rows: the streamed 16 x 32 tile (1 x 7168 x 2304: 5.9, 32 x 32 6.2,
@@ -695,6 +841,12 @@ extern "C" int int8_linear(const void* x, int32_t in_dtype, const int8_t* b, con
     const int64_t tiles = (M + 127) / 128;
     if (tiles > kMaxRowTiles) return fail(GFG_EUNSUPPORTED, "%s: M=%lld above %lld", fn, (long long)M, (long long)(kMaxRowTiles * 128));
     hipStream_t s = static_cast<hipStream_t>(stream);
+    if (M <= kFewTokens && M * ((K + TK - 1) / TK * TK) <= kFewCodes) {
+        const I8Params p = product(nullptr, nullptr, b, b_scale, bias, nullptr, d, M, N, K, 1);
+        if (in_dtype == GFG_IN_F32) return launch_few<float>(x, p, out_dtype, s);
+        if (in_dtype == GFG_IN_BF16) return launch_few<__bf16>(x, p, out_dtype, s);
+        return launch_few<_Float16>(x, p, out_dtype, s);
+    }
     if (int rc = quantize(x, in_dtype, M, K, q, scale, s)) return rc;
     return launch_i8(fn, product(reinterpret_cast<const int8_t*>(q), scale, b, b_scale, bias, nullptr, d, M, N, K, 1), DENSE,
                      out_dtype, s);

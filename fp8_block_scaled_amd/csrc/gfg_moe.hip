@@ -34,21 +34,28 @@ __device__ __forceinline__ float as_f32(float v) { return v; }
 __device__ __forceinline__ float as_f32(__bf16 v) { return float(v); }
 __device__ __forceinline__ float as_f32(_Float16 v) { return float(v); }
 
-__device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-    for (int w = 32; w >= 1; w >>= 1) v = fmaxf(v, __shfl_xor(v, w, 64));
-    return v;
+// Reductions over a wave: rotations inside the rows of 16 lanes (DPP), then the
+// four rows through scalar registers; about a quarter of the time of shuffles
+// through LDS.
+template <int CTRL>
+__device__ __forceinline__ int dpp(int v) {
+    return __builtin_amdgcn_update_dpp(0, v, CTRL, 0xF, 0xF, false);
 }
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-    for (int w = 32; w >= 1; w >>= 1) v += __shfl_xor(v, w, 64);
-    return v;
+template <typename T, typename Op>
+__device__ __forceinline__ T wave_reduce(T v, Op op) {
+    static_assert(sizeof(T) == 4, "one register");
+#define GFG_ROT(C) v = op(v, __builtin_bit_cast(T, dpp<0x120 + C>(__builtin_bit_cast(int, v))))
+    GFG_ROT(8);
+    GFG_ROT(4);
+    GFG_ROT(2);
+    GFG_ROT(1);
+#undef GFG_ROT
+    auto row = [&](int l) { return __builtin_bit_cast(T, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), l)); };
+    return op(op(row(0), row(16)), op(row(32), row(48)));
 }
-__device__ __forceinline__ int wave_min(int v) {
-#pragma unroll
-    for (int w = 32; w >= 1; w >>= 1) v = min(v, __shfl_xor(v, w, 64));
-    return v;
-}
+__device__ __forceinline__ float wave_max(float v) { return wave_reduce(v, [](float a, float b) { return fmaxf(a, b); }); }
+__device__ __forceinline__ float wave_sum(float v) { return wave_reduce(v, [](float a, float b) { return a + b; }); }
+__device__ __forceinline__ int wave_min(int v) { return wave_reduce(v, [](int a, int b) { return min(a, b); }); }
 
 // One wave a token; lane l holds experts l, l + 64, ... (EPL of them).  A round
 // takes the largest remaining selection value and, among its holders, the
@@ -93,24 +100,27 @@ __global__ __launch_bounds__(256) void moe_topk_kernel(const T* __restrict__ log
         }
     }
     int mine = -1;
+    float logit = ninf;
     for (int j = 0; j < k; ++j) {
-        float best = ninf;
+        float best = ninf, held = ninf;
         int at = 0x7FFFFFFF;
 #pragma unroll
         for (int i = 0; i < EPL; ++i)
-            if (s[i] > best) { best = s[i]; at = lane + 64 * i; }
+            if (s[i] > best) { best = s[i]; held = l[i]; at = lane + 64 * i; }
         const float top = wave_max(best);
-        const int e = wave_min(best == top ? at : 0x7FFFFFFF);
-        if (e == 0x7FFFFFFF) break;            // nothing above -infinity is left
+        if (top == ninf) break;                // nothing above -infinity is left
+        const uint64_t holders = __ballot(best == top);
+        const int e = __popcll(holders) == 1 ? __builtin_amdgcn_readlane(at, __builtin_ctzll(holders))
+                                             : wave_min(best == top ? at : 0x7FFFFFFF);
 #pragma unroll
         for (int i = 0; i < EPL; ++i)
             if (e == lane + 64 * i) s[i] = ninf;
-        if (lane == j) mine = e;
+        const float v = __uint_as_float(uint32_t(__builtin_amdgcn_readlane(int(__float_as_uint(held)), e & 63)));
+        if (lane == j) { mine = e; logit = v; }
     }
     float w = 0.0f;
     if (mine >= 0) {
-        const float v = as_f32(row[mine]);
-        w = sigmoid ? sig(v) : expo(v) / total;
+        w = sigmoid ? sig(logit) : expo(logit) / total;
     }
     if (renorm) {
         const float sum = wave_sum(w);
