@@ -127,7 +127,7 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     lib.grouped_int8_gemm_masked.restype = ctypes.c_int
     lib.moe_topk.argtypes = [vp, i32, vp, vp, vp, i64, i64, i64, i32, i32, f32, vp]
     lib.moe_topk.restype = ctypes.c_int
-    lib.moe_layer_workspace_bytes.argtypes = [i64, i64, i64]
+    lib.moe_layer_workspace_bytes.argtypes = [i64, i64, i64, i64]
     lib.moe_layer_workspace_bytes.restype = i64
     for layer in (lib.moe_fp8_layer, lib.moe_int8_layer):
         layer.argtypes = [vp, i32, vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, i64, vp, i64, vp]

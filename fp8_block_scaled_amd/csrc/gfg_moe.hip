@@ -19,6 +19,7 @@
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
+#include <cmath>
 
 #include "gfg.h"
 #include "gfg_device.h"
@@ -174,6 +175,7 @@ struct MoeParams {
     const uint8_t* w2;       // [E][H][I]
     const void* s2;          // FP8: [E][H/128][I/128] bytes; INT8: [E][H] float
     uint8_t* h;              // [T*k][2][I] bf16: the hidden rows as high and low halves
+    float* y;                // [T*k][H]: the pairs' outputs, where they are summed by a launch of their own
     void* out;               // [T][H]
     int T, k, E, H, I;
     int ring;                // bytes of each wave's ring
@@ -230,7 +232,7 @@ struct Routing {
     int16_t list[kMaxPairs];
     uint32_t unit[kMaxPairs];
     int tmp[8];
-    int total[4];            // units if they had at most 2, 4, 8, 16 pairs
+    int total[6];            // units if they had at most 2, 4, 8, 16, 32, 64 pairs
     int units;
 };
 constexpr int kBuildBytes = kMaxExperts * 4 + kMaxPairs * 2;    // scratch of the build
@@ -241,10 +243,10 @@ constexpr int kBuildBytes = kMaxExperts * 4 + kMaxPairs * 2;    // scratch of th
 // fewest rows that do not exist.  A stage: `fixed` KB of weights, `per4` KB for
 // every four rows.
 template <int LO, int HI>
-__device__ __forceinline__ int choose_rows(const int (&total)[4], int fixed, int per4, int ring) {
+__device__ __forceinline__ int choose_rows(const int (&total)[6], int fixed, int per4, int ring) {
     int rows = LO, fewest = 0;
 #pragma unroll
-    for (int i = 3; i >= 0; --i) {
+    for (int i = 5; i >= 0; --i) {
         const int r = 2 << i;
         if (r < LO || r > HI || (r > LO && 2 * ((fixed + per4 * r / 4) * 1024 + kScaleBytes) > ring)) continue;
         if (fewest == 0) fewest = total[i] + total[i] / 64;
@@ -254,9 +256,9 @@ __device__ __forceinline__ int choose_rows(const int (&total)[4], int fixed, int
 }
 
 // Up to kSmallPairs pairs: lane p of every wave holds pair p, and no barrier
-// but the last is needed.  Returns the unit size.
-template <int LO, int HI>
-__device__ __forceinline__ int build_small(GFG_LDS Routing* r, const int32_t* ids, int P, int E, int fixed, int per4, int ring) {
+// but the last is needed.  choose(total) gives the unit size, which is returned.
+template <typename Choose>
+__device__ __forceinline__ int build_small(GFG_LDS Routing* r, const int32_t* ids, int P, int E, Choose choose) {
     const int lane = threadIdx.x & 63;
     int e = lane < P ? ids[lane] : -1;
     const bool live = e >= 0 && e < E;
@@ -268,10 +270,10 @@ __device__ __forceinline__ int build_small(GFG_LDS Routing* r, const int32_t* id
     }
     const int lead = __builtin_ctzll(same | 1ull << 63), count = __popcll(same);
     const int before = __popcll(same & ((1ull << lane) - 1));
-    int total[4];
+    int total[6];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) total[i] = __popcll(__ballot(live && (before & ((2 << i) - 1)) == 0));
-    const int rows = choose_rows<LO, HI>(total, fixed, per4, ring);
+    for (int i = 0; i < 6; ++i) total[i] = __popcll(__ballot(live && (before & ((2 << i) - 1)) == 0));
+    const int rows = choose(total);
     // pairs | units << 16 of the experts whose first pair lies before this lane
     const int own = live && lane == lead ? count | ((count + rows - 1) / rows) << 16 : 0;
     int x = own;
@@ -294,13 +296,13 @@ __device__ __forceinline__ int build_small(GFG_LDS Routing* r, const int32_t* id
     return rows;
 }
 
-template <int WAVES, int LO, int HI>
+template <typename Choose>
 __device__ __forceinline__ int build_routing(GFG_LDS Routing* r, GFG_LDS uint8_t* scratch, const int32_t* ids, int P, int E,
-                                             int fixed, int per4, int ring) {
-    if (P <= kSmallPairs) return build_small<LO, HI>(r, ids, P, E, fixed, per4, ring);
+                                             Choose choose) {
+    if (P <= kSmallPairs) return build_small(r, ids, P, E, choose);
     GFG_LDS int* const cnt = reinterpret_cast<GFG_LDS int*>(scratch);                    // [kMaxExperts]
     GFG_LDS int16_t* const expert = reinterpret_cast<GFG_LDS int16_t*>(cnt + kMaxExperts);   // [kMaxPairs]
-    constexpr int THREADS = WAVES * 64, PPT = kMaxPairs / THREADS, EPT = kMaxExperts / THREADS;
+    constexpr int THREADS = kWaves * 64, PPT = kMaxPairs / THREADS, EPT = kMaxExperts / THREADS;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     int e[PPT], slot[PPT];
 #pragma unroll
@@ -308,7 +310,7 @@ __device__ __forceinline__ int build_routing(GFG_LDS Routing* r, GFG_LDS uint8_t
         const int p = tid + i * THREADS;
         e[i] = p < P ? ids[p] : -1;
     }
-    if (tid < 4) r->total[tid] = 0;
+    if (tid < 6) r->total[tid] = 0;
 #pragma unroll
     for (int i = 0; i < EPT; ++i) cnt[tid * EPT + i] = 0;
     __syncthreads();
@@ -321,29 +323,33 @@ __device__ __forceinline__ int build_routing(GFG_LDS Routing* r, GFG_LDS uint8_t
     }
     __syncthreads();
     int c[EPT];
-    uint64_t sums = 0;                         // units of at most 2, 4, 8, 16 pairs, 16 bits each
+    int sums[6] = {};                          // units of at most 2, 4, ... 64 pairs
 #pragma unroll
     for (int i = 0; i < EPT; ++i) {
         c[i] = cnt[tid * EPT + i];
 #pragma unroll
-        for (int z = 0; z < 4; ++z) sums += uint64_t((c[i] + (2 << z) - 1) >> (1 + z)) << (16 * z);
+        for (int z = 0; z < 6; ++z) sums[z] += (c[i] + (2 << z) - 1) >> (1 + z);
     }
-    if (sums) {
+    if (sums[5]) {
 #pragma unroll
-        for (int z = 0; z < 4; ++z)
-            __hip_atomic_fetch_add(&r->total[z], int(sums >> (16 * z)) & 0xFFFF, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+        for (int z = 0; z < 6; ++z)
+            __hip_atomic_fetch_add(&r->total[z], sums[z], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
     }
     __syncthreads();
-    int total[4];
+    int total[6];
 #pragma unroll
-    for (int z = 0; z < 4; ++z) total[z] = __builtin_amdgcn_readfirstlane(r->total[z]);
-    const int rows = choose_rows<LO, HI>(total, fixed, per4, ring);
+    for (int z = 0; z < 6; ++z) total[z] = __builtin_amdgcn_readfirstlane(r->total[z]);
+    const int rows = choose(total);
 #pragma unroll
     for (int i = 0; i < PPT; ++i)
         if (slot[i] >= 0 && cnt[e[i]] > rows) {
             const int p = tid + i * THREADS;
-            int before = 0;
-            for (int q = 0; q < p; ++q) before += int(expert[q]) == e[i];
+            int before = 0;                    // earlier pairs of the expert, eight at a time
+            for (int q = 0; q < p; q += 8) {
+                const u32x4 v = *reinterpret_cast<GFG_LDS u32x4*>(expert + q);
+#pragma unroll
+                for (int c = 0; c < 8; ++c) before += q + c < p && int(v[c >> 1] >> (16 * (c & 1)) & 0xFFFF) == e[i];
+            }
             slot[i] = before;
         }
     int mine = 0;                              // pairs | units << 16 of this thread's experts
@@ -359,7 +365,7 @@ __device__ __forceinline__ int build_routing(GFG_LDS Routing* r, GFG_LDS uint8_t
     __syncthreads();
     int before = x - mine;
 #pragma unroll
-    for (int w = 0; w < WAVES; ++w)
+    for (int w = 0; w < kWaves; ++w)
         if (w < wave) before += r->tmp[w];
     int first = before & 0xFFFF, u = before >> 16;
 #pragma unroll
@@ -479,6 +485,17 @@ __device__ __forceinline__ void read_block(u32x4 (&w)[4], u32x4 (&f)[4], uint32_
         : "memory");
 }
 
+// Four more fragments, OFS bytes further on.
+template <int OFS>
+__device__ __forceinline__ void read4(u32x4 (&f)[4], const uint32_t (&a)[4]) {
+    asm volatile(
+        "ds_read_b128 %0, %4 offset:%c8\n\tds_read_b128 %1, %5 offset:%c8\n\t"
+        "ds_read_b128 %2, %6 offset:%c8\n\tds_read_b128 %3, %7 offset:%c8\n\ts_waitcnt lgkmcnt(0)"
+        : "=&v"(f[0]), "=&v"(f[1]), "=&v"(f[2]), "=&v"(f[3])
+        : "v"(a[0]), "v"(a[1]), "v"(a[2]), "v"(a[3]), "i"(OFS)
+        : "memory");
+}
+
 // Token rows of `bytes` (a multiple of 256) that stay in LDS, as they lie in
 // memory, loaded by all waves; 16-byte chunks XOR-swizzled by row & 15.
 __device__ __forceinline__ void load_resident(GFG_LDS uint8_t* dst, __amdgpu_buffer_rsrc_t r, int bytes, int total) {
@@ -487,6 +504,23 @@ __device__ __forceinline__ void load_resident(GFG_LDS uint8_t* dst, __amdgpu_buf
         const int b = at + lane * 16;
         dma(r, dst + at, uint32_t(b ^ (((b / bytes) & 15) << 4)));
     }
+}
+
+// h = silu(g) * u for four columns of a pair, in two bf16 halves, high and low:
+// 16 significant bits with fp32's range, so that the only rounding to 16 bits
+// is the output's.
+__device__ __forceinline__ void store_hidden(const MoeParams& p, int pair, int col, const v4f& g, const v4f& u) {
+    bf4 hi, lo;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        const float h = g[c] / (1.0f + expf(-g[c])) * u[c];
+        hi[c] = __bf16(h);
+        const float rest = h - float(hi[c]);
+        lo[c] = __bf16(rest == rest ? rest : 0.0f);       // an infinite h has no low half
+    }
+    uint8_t* const row = p.h + int64_t(pair) * 4 * p.I + col * 2;
+    *reinterpret_cast<bf4*>(row) = hi;
+    *reinterpret_cast<bf4*>(row + 2 * p.I) = lo;
 }
 
 // ---- hidden rows: h = silu(g) * u.
@@ -685,22 +719,213 @@ __device__ __forceinline__ void up_items(const MoeParams& p, const GFG_LDS Routi
             g *= cg;
             v *= cu;
         }
-        if (l16 >= un.rows || lq >= C / 4) continue;
-        const int col = it * C + lq * 4;
-        // h in two bf16 halves, high and low: 16 significant bits with fp32's
-        // range, so that the only rounding to 16 bits is the output's
-        bf4 hi, lo;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            const float h = g[c] / (1.0f + expf(-g[c])) * v[c];
-            hi[c] = __bf16(h);
-            const float rest = h - float(hi[c]);
-            lo[c] = __bf16(rest == rest ? rest : 0.0f);   // an infinite h has no low half
-        }
-        uint8_t* const row = p.h + int64_t(r->list[un.first + l16]) * 4 * p.I + col * 2;
-        *reinterpret_cast<bf4*>(row) = hi;
-        *reinterpret_cast<bf4*>(row + 2 * p.I) = lo;
+        if (l16 < un.rows && lq < C / 4) store_hidden(p, r->list[un.first + l16], it * C + lq * 4, g, v);
     }
+}
+
+// ---- experts with many rows: the waves share them.
+//
+// Where units are large, staging their rows for every 16 columns costs more
+// than the weights.  Here a work item is 128 weight rows for one unit of up to
+// 32 or 64 rows: each of the eight waves has 16 of the weight rows, and all of
+// them read the unit's rows from one LDS stage.  One barrier a block: a wave that passes it has
+// seen every wave finish the block before, whose stage the new loads go to.
+// The items run on without a break, as above.
+//
+// UP: the weight rows are 64 gate and 64 up rows, eight of each to a wave, so
+// that gate and up meet in a wave.  DOWN: 128 rows of W2; sums go to y.
+template <int N> __device__ __forceinline__ void wait_shared() { GFG_WAITCNT(N, 0); }
+
+// Units of 64 rows where that saves a round of items over the workgroups: a few
+// experts with slightly more than 32 rows would otherwise cost a second pass
+// over their weights.  (Smaller stages leave room for one more of them.)
+__device__ __forceinline__ int shared_rows(const int (&total)[6], int tiles) {
+    const int grid = int(gridDim.x);
+    return (total[5] * tiles + grid - 1) / grid < (total[4] * tiles + grid - 1) / grid ? 64 : 32;
+}
+
+constexpr int shared_stage(int rows, bool up) { return 16 * 1024 + rows * 256 * (up ? 1 : 2) + kScaleBytes; }
+constexpr int shared_depth(int rows, bool up) { return rows == 32 ? (up ? 5 : 4) : (up ? 4 : 3); }
+constexpr int kSharedLds = 3 * shared_stage(64, false);    // the largest ring of the down projection
+static_assert(4 * shared_stage(32, false) <= kSharedLds, "the rings of either unit size fit");
+
+template <int W, typename A, int NR, bool UP>
+__device__ __forceinline__ void shared_items(const MoeParams& p, const GFG_LDS Routing* r, GFG_LDS uint8_t* ring) {
+    typedef typename Vec<A>::v8 v8;
+    constexpr int HALVES = UP ? 1 : 2, RL = NR / 32, NT = NR / 16, S = shared_depth(NR, UP), PER = 2 + HALVES * RL;
+    constexpr int ROWS_AT = 16 * 1024, STAGE = shared_stage(NR, UP), SCALES_AT = STAGE - kScaleBytes;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int l16 = lane & 15, lq = lane >> 4;
+    const int K = UP ? p.H : p.I, N = UP ? 2 * p.I : p.H;      // the weight matrix of an expert is [N][K]
+    const int KB = K / 128, IT = N / 128;
+    const int items = __builtin_amdgcn_readfirstlane(r->units) * IT;
+    const uint8_t* const weights = UP ? p.w1 : p.w2;
+    const auto rx = UP ? make_rsrc(p.x, uint32_t(p.T) * uint32_t(p.H) * 2u) : make_rsrc(p.h, uint32_t(p.T * p.k) * 4u * uint32_t(p.I));
+    uint32_t shift;
+    const auto rs = scale_rsrc(UP ? p.s1 : p.s2, W == FP8 ? uint32_t(p.E) * uint32_t(N / 128) * uint32_t(KB) : uint32_t(p.E) * uint32_t(N) * 4u, &shift);
+    // (UP: blocks it / 2 of the gate and of the up half; DOWN: block it)
+    auto scale_row = [&](int e, int it, int f) {
+        return uint32_t(e * (N / 128) + (UP ? it / 2 + f * (p.I / 128) : it)) * uint32_t(KB) + shift;
+    };
+
+    const uint32_t woff = uint32_t(lane >> 3) * uint32_t(K) + uint32_t(((lane & 7) ^ (lane >> 3)) * 16);
+    uint32_t xoff[RL], soff[2] = {0, 0};       // rows 32 j + 4 wave + (lane >> 4) of the unit's
+    __amdgpu_buffer_rsrc_t rw[2] = {make_rsrc(weights, 0), make_rsrc(weights, 0)};
+    int li = blockIdx.x, lk = 0, ls = 0;
+    auto enter = [&]() {
+        uint32_t window = 0;
+        const uint8_t* base = weights;
+        Unit un{0, 0, 0};
+        if (li < items) {
+            const int u = li / IT, it = li - u * IT;
+            un = unit_of(r, u);
+            base += (int64_t(un.e) * N + (UP ? it * 64 + wave * 8 : it * 128 + wave * 16)) * K;
+            window = 8u * uint32_t(K);
+#pragma unroll
+            for (int f = 0; f < 2; ++f) {
+                if constexpr (W == FP8)
+                    soff[f] = (UP || f == 0) ? (scale_row(un.e, it, f) & ~3u) + 4u * uint32_t(lane) : kOutside;
+                else
+                    soff[f] = uint32_t(un.e * N + (UP ? f * p.I + it * 64 : it * 128 + f * 64) + lane) * 4u;
+            }
+        } else {
+            soff[0] = soff[1] = kOutside;
+        }
+        rw[0] = make_rsrc(base, window);
+        rw[1] = make_rsrc(base + int64_t(UP ? p.I : 8) * K, window);
+#pragma unroll
+        for (int j = 0; j < RL; ++j) {
+            const int row = 32 * j + 4 * wave + (lane >> 4);
+            xoff[j] = kOutside;
+            if (row < un.rows) {
+                const int pair = r->list[un.first + row];
+                xoff[j] = (UP ? uint32_t(pair / p.k) * 2u : uint32_t(pair) * 4u) * uint32_t(K) + uint32_t(((lane & 15) ^ (row & 15)) * 16);
+            }
+        }
+    };
+    enter();
+    auto issue = [&]() {
+        GFG_LDS uint8_t* const dst = ring + ls * STAGE;
+        const uint32_t kw = uint32_t(lk) * 128u, kx = uint32_t(lk) * 256u;
+        if (lk == 0 && wave == 0) {            // the item's scales, for all waves
+            dma4(rs, dst + SCALES_AT, soff[0]);
+            dma4(rs, dst + SCALES_AT + 256, soff[1]);
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) dma(rw[j], dst + wave * 2048 + j * 1024, woff + kw);
+#pragma unroll
+        for (int f = 0; f < HALVES; ++f)       // the low halves' chunks swizzled by 8 more
+#pragma unroll
+            for (int j = 0; j < RL; ++j)
+                dma(rx, dst + ROWS_AT + f * NR * 256 + j * 8192 + wave * 1024, (xoff[j] ^ uint32_t(f * 128)) + kx + uint32_t(f) * 2u * uint32_t(K));
+        ls = ls + 1 == S ? 0 : ls + 1;
+        if (++lk == KB) {
+            lk = 0;
+            li += gridDim.x;
+            enter();
+        }
+    };
+#pragma unroll
+    for (int d = 0; d < S - 1; ++d) issue();
+
+    const uint32_t base = lds_addr(ring);
+    const uint32_t w0 = base + uint32_t(wave * 2048 + l16 * 128 + ((lq ^ (l16 & 7)) << 4)), w1 = w0 ^ 64u;
+    const uint32_t x0 = base + uint32_t(ROWS_AT + l16 * 256) + uint32_t(((2 * lq) ^ l16) << 4);
+    int cs = 0;
+    for (int item = blockIdx.x; item < items; item += gridDim.x) {
+        const int u = item / IT, it = item - u * IT;
+        const Unit un = unit_of(r, u);
+        const int tiles = (un.rows + 15) / 16;
+        uint32_t words[2] = {0, 0};
+        v4f channel = {};                      // INT8: the scales of this lane's rows
+        v4f acc[NT] = {}, part[NT] = {};       // [16 rows of the unit]
+        float sc = 0.0f;                       // FP8: the scale of this lane's rows in the last block
+        auto apply = [&]() {
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[t][i] = fmaf(part[t][i], sc, acc[t][i]);
+        };
+        for (int kb = 0; kb < KB; ++kb) {
+            __builtin_amdgcn_sched_barrier(0);
+            wait_shared<(S - 2) * PER>();
+            __builtin_amdgcn_s_barrier();
+            __builtin_amdgcn_sched_barrier(0);
+            const uint32_t so = uint32_t(cs * STAGE);
+            cs = cs + 1 == S ? 0 : cs + 1;
+            issue();                           // into the stage read a block ago
+            __builtin_amdgcn_sched_barrier(0);
+            if (kb == 0) {
+                const uint32_t sa = base + so + SCALES_AT;
+                if constexpr (W == FP8) {
+                    words[0] = read_word(sa + uint32_t(lane * 4));
+                    words[1] = read_word(sa + 256u + uint32_t(lane * 4));
+                } else {
+                    channel = read_quad(sa + uint32_t(UP ? (lq >> 1) * 256 + (wave * 8 + (lq & 1) * 4) * 4 : (wave * 16 + lq * 4) * 4));
+                }
+            }
+            const uint32_t xb = x0 + so, xa[4] = {xb, xb ^ 16u, xb ^ 128u, xb ^ 144u};     // [64-byte half][8 elements]
+            const uint32_t xl[4] = {xa[2], xa[3], xa[0], xa[1]};                           // ... of the low halves
+            u32x4 w[2], x[HALVES][4];
+            read_block(w, x[0], w0 + so, w1 + so, xa);
+            if constexpr (!UP) read4<NR * 256>(x[HALVES - 1], xl);
+            if constexpr (W == FP8) {
+                apply();
+                sc = picked_scale(words[0], scale_row(un.e, it, 0), kb);
+                if constexpr (UP) {
+                    const float su = picked_scale(words[1], scale_row(un.e, it, 1), kb);
+                    sc = lq < 2 ? sc : su;
+                }
+#pragma unroll
+                for (int t = 0; t < NT; ++t) part[t] = v4f{};
+            }
+            v4f(&to)[NT] = W == FP8 ? part : acc;
+            v8 a[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) a[c] = widen<W, A>(w[c >> 1][2 * (c & 1)], w[c >> 1][2 * (c & 1) + 1]);
+            auto multiply = [&](v4f& sum) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                    for (int f = 0; f < HALVES; ++f) sum = mma(a[c], __builtin_bit_cast(v8, x[f][c]), sum);
+            };
+            multiply(to[0]);
+            if (tiles > 1) {
+                read4<4096>(x[0], xa);
+                if constexpr (!UP) read4<NR * 256 + 4096>(x[HALVES - 1], xl);
+                multiply(to[1]);
+            }
+            if constexpr (NT > 2) {
+                if (tiles > 2) {
+                    read4<8192>(x[0], xa);
+                    if constexpr (!UP) read4<NR * 256 + 8192>(x[HALVES - 1], xl);
+                    multiply(to[NT - 2]);
+                }
+                if (tiles > 3) {
+                    read4<12288>(x[0], xa);
+                    if constexpr (!UP) read4<NR * 256 + 12288>(x[HALVES - 1], xl);
+                    multiply(to[NT - 1]);
+                }
+            }
+        }
+        if constexpr (W == FP8) apply();
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            v4f v = acc[t];
+            if constexpr (W == INT8) v *= channel;
+            const bool live = 16 * t + l16 < un.rows;
+            const int pair = r->list[un.first + min(16 * t + l16, un.rows - 1)];
+            if constexpr (UP) {                // quads 0, 1 hold the gate rows, quads 2, 3 the up rows
+                v4f up;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) up[i] = __shfl_xor(v[i], 32, 64);
+                if (live && lq < 2) store_hidden(p, pair, it * 64 + wave * 8 + lq * 4, v, up);
+            } else {
+                if (live) *reinterpret_cast<v4f*>(p.y + int64_t(pair) * p.H + it * 128 + wave * 16 + lq * 4) = v;
+            }
+        }
+    }
+    GFG_WAITCNT(0, 0);                         // the last loads land before the workgroup ends
 }
 
 template <int W, typename A, bool RES>
@@ -714,7 +939,7 @@ __global__ __launch_bounds__(kWaves * 64) void moe_up_kernel(MoeParams p) {
     GFG_LDS uint8_t* const rows_mem = ring + kWaves * p.ring;
     if constexpr (RES) {
         load_resident(rows_mem, make_rsrc(p.x, uint32_t(p.T) * uint32_t(p.H) * 2u), p.H * 2, p.resident);
-        const int rows = build_routing<kWaves, 4, 8>(r, ring, p.ids, p.T * p.k, p.E, 4, 0, p.ring);
+        const int rows = build_routing(r, ring, p.ids, p.T * p.k, p.E, [&](const int (&total)[6]) { return choose_rows<4, 8>(total, 4, 0, p.ring); });
         // items of 8 columns where they spread better over the workgroups
         const int n = __builtin_amdgcn_readfirstlane(r->units) * (p.I / 16), grid = int(gridDim.x);
         const int walk16 = (n + grid - 1) / grid * 2, walk8 = (2 * n + grid - 1) / grid;
@@ -726,8 +951,17 @@ __global__ __launch_bounds__(kWaves * 64) void moe_up_kernel(MoeParams p) {
             else up_items<W, A, 8, 16, true>(p, r, ring, rows_mem, red);
         }
     } else {
-        const int rows = build_routing<kWaves, 4, 16>(r, ring, p.ids, p.T * p.k, p.E, 4, 1, p.ring);
-        if (rows <= 4) up_items<W, A, 4, 16, false>(p, r, ring, rows_mem, red);
+        const int rows = build_routing(r, ring, p.ids, p.T * p.k, p.E, [&](const int (&total)[6]) {
+            const int few = choose_rows<4, 16>(total, 4, 1, p.ring), rows = shared_rows(total, p.I / 64);
+            // loads a block of K for 16 columns: streamed, and shared; the
+            // latter's coarser items have to fill the launch too
+            const int units = total[rows == 32 ? 4 : 5];
+            const int streamed = total[few == 4 ? 1 : few == 8 ? 2 : 3] * (4 + few / 4), shared = units * 6;
+            return shared * 10 < streamed * 9 && units * (p.I / 64) * 4 >= int(gridDim.x) * 3 ? rows : few;
+        });
+        if (rows == 64) shared_items<W, A, 64, true>(p, r, ring);
+        else if (rows == 32) shared_items<W, A, 32, true>(p, r, ring);
+        else if (rows <= 4) up_items<W, A, 4, 16, false>(p, r, ring, rows_mem, red);
         else if (rows <= 8) up_items<W, A, 8, 16, false>(p, r, ring, rows_mem, red);
         else up_items<W, A, 16, 16, false>(p, r, ring, rows_mem, red);
     }
@@ -903,7 +1137,7 @@ __global__ __launch_bounds__(kWaves * 64) void moe_down_kernel(MoeParams p) {
         if ((i & 63) == 0) live[i / 64] = m;
         if (i < P) wt[i] = p.weights[i];
     }
-    const int rows = build_routing<kWaves, 2, 8>(r, ring, p.ids, P, p.E, 2 * RT, 2, p.ring);
+    const int rows = build_routing(r, ring, p.ids, P, p.E, [&](const int (&total)[6]) { return choose_rows<2, 8>(total, 2 * RT, 2, p.ring); });
     const int units = __builtin_amdgcn_readfirstlane(r->units), KB = p.I / 128;
     // the waves that share a unit: the split with the shortest longest walk
     int ks = 1, best = (units + kWaves - 1) / kWaves * KB;
@@ -941,7 +1175,63 @@ __global__ __launch_bounds__(kWaves * 64) void moe_down_kernel(MoeParams p) {
     }
 }
 
+// The down projection by shared items, and the sums over a token's pairs.
+template <int W>
+__global__ __launch_bounds__(kWaves * 64) void moe_down_shared_kernel(MoeParams p) {
+    __shared__ Routing routing;
+    extern __shared__ __attribute__((aligned(256))) uint8_t ring_mem[];       // the stages
+    GFG_LDS Routing* const r = (GFG_LDS Routing*)&routing;
+    GFG_LDS uint8_t* const ring = (GFG_LDS uint8_t*)ring_mem;
+    const int rows = build_routing(r, ring, p.ids, p.T * p.k, p.E, [&](const int (&total)[6]) { return shared_rows(total, p.H / 128); });
+    if (rows == 32) shared_items<W, __bf16, 32, false>(p, r, ring);
+    else shared_items<W, __bf16, 64, false>(p, r, ring);
+}
+
+// Four columns of a token a thread.  The pairs' sums are loaded eight at a time,
+// also those of pairs without an expert (whose places hold anything), and only
+// then picked, so that no load waits for an id.
+template <typename OutT>
+__global__ __launch_bounds__(256) void moe_combine_kernel(MoeParams p) {
+    const int t = blockIdx.y, col = (int(blockIdx.x) * 256 + int(threadIdx.x)) * 4;
+    if (col >= p.H) return;
+    const float* const y = p.y + int64_t(t) * p.k * p.H + col;
+    v4f sum = {};
+    for (int j0 = 0; j0 < p.k; j0 += 8) {
+        v4f v[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) v[c] = *reinterpret_cast<const v4f*>(y + int64_t(min(j0 + c, p.k - 1)) * p.H);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            if (j0 + c >= p.k) break;
+            const int e = p.ids[t * p.k + j0 + c];
+            if (e < 0 || e >= p.E) continue;
+            const float w = p.weights[t * p.k + j0 + c];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sum[i] = fmaf(w, v[c][i], sum[i]);
+        }
+    }
+    typedef OutT o4 __attribute__((ext_vector_type(4)));
+    *reinterpret_cast<o4*>(static_cast<OutT*>(p.out) + int64_t(t) * p.H + col) = o4{OutT(sum[0]), OutT(sum[1]), OutT(sum[2]), OutT(sum[3])};
+}
+
 constexpr int kLds = 160 * 1024;
+
+// Whether the down projection goes by shared items and a launch that combines
+// them, from the KB that the busiest CU would read either way if the pairs
+// spread evenly over min(T * k, E) experts.  (A CU reads about 37 KB a
+// microsecond; the second launch counts as 180 KB.)  Walking all units for 16
+// or 32 columns leaves CUs idle where H is small and reads the rows again for
+// every 16 columns where experts have many.  Measured, us, walked / shared with
+// its second launch: 5 tokens, k = 6, E = 64, H = 2048, I = 1408: 31 / 25; 100
+// tokens, k = 2, E = 8, H = 4096, I = 1792: 42 / 32; one token, k = 9, E = 385,
+// H = 7168, I = 512: 13.6 / 14.0; 32 tokens of the same: 127 / 137.
+bool shared_down(const MoeParams& p, int cus, int rt) {
+    const float P = float(p.T) * float(p.k), experts = P < float(p.E) ? P : float(p.E), rows = P / experts;
+    const float split8 = ceilf(rows / 8), split32 = ceilf(rows / 32), blocks = float(p.I / 128);
+    const float walked = ceilf(float(p.H / (16 * rt)) / float(cus)) * experts * split8 * blocks * (2.0f * float(rt) + 0.5f * rows / split8);
+    const float shared = ceilf(experts * split32 * float(p.H / 128) / float(cus)) * blocks * (16.0f + 0.5f * rows / split32);
+    return shared + 180.0f < 0.7f * walked;
+}
 
 template <int W, typename A>
 int launch_layer(MoeParams p, hipStream_t s) {
@@ -959,8 +1249,16 @@ int launch_layer(MoeParams p, hipStream_t s) {
     const unsigned up_lds = unsigned(kWaves * p.ring + p.resident);
     if (p.resident) hipLaunchKernelGGL((moe_up_kernel<W, A, true>), dim3(up_grid), block, up_lds, s, p);
     else hipLaunchKernelGGL((moe_up_kernel<W, A, false>), dim3(up_grid), block, up_lds, s, p);
-    // down: 32 columns a workgroup where they fill three quarters of the CUs and the sums stay small
     const int rt = p.H % 32 == 0 && p.H / 32 >= cus * 3 / 4 && P * 128 <= 40 * 1024 ? 2 : 1;
+    if (shared_down(p, cus, rt)) {
+        const int items = ((P < p.E ? P : p.E) + P / 32) * (p.H / 128);
+        hipLaunchKernelGGL((moe_down_shared_kernel<W>), dim3(items < cus ? items : cus), block, kSharedLds, s, p);
+        hipLaunchKernelGGL((moe_combine_kernel<A>), dim3((p.H + 1023) / 1024, p.T), dim3(256), 0, s, p);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return fail(GFG_EHIP, "kernel launch failed: %s", hipGetErrorString(e));
+        return GFG_OK;
+    }
+    // 32 columns a workgroup where they fill three quarters of the CUs and the sums stay small
     while (p.ks_most < kWaves && p.ks_most * 2 <= p.I / 128 && p.ks_most * 2 * P * 64 * rt <= 24 * 1024) p.ks_most *= 2;
     const int y_bytes = p.ks_most * P * 64 * rt;
     const int tiles = p.H / (16 * rt), down_grid = tiles < cus ? tiles : cus;
@@ -973,7 +1271,7 @@ int launch_layer(MoeParams p, hipStream_t s) {
     return GFG_OK;
 }
 
-int64_t workspace_bytes(int64_t T, int64_t k, int64_t I) { return T > 0 && k > 0 && I > 0 ? T * k * I * 4 : 0; }
+int64_t workspace_bytes(int64_t T, int64_t k, int64_t H, int64_t I) { return T > 0 && k > 0 && H > 0 && I > 0 ? T * k * (H + I) * 4 : 0; }
 
 int layer(const char* fn, int weight, const void* x, int32_t x_dtype, const int32_t* ids, const float* weights,
           const void* w1, const void* s1, const void* w2, const void* s2, void* out, int64_t T, int64_t k, int64_t E,
@@ -998,11 +1296,11 @@ int layer(const char* fn, int weight, const void* x, int32_t x_dtype, const int3
         return fail(GFG_EINVAL, "%s: x, w1, w2 and out must be 16-byte aligned, the other operands to their element", fn);
     if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 16)
         return fail(GFG_EINVAL, "%s: workspace must be a 16-byte aligned device pointer", fn);
-    if (bytes < workspace_bytes(T, k, I))
+    if (bytes < workspace_bytes(T, k, H, I))
         return fail(GFG_EINVAL, "%s: workspace of %lld bytes, %lld are needed", fn, (long long)bytes,
-                    (long long)workspace_bytes(T, k, I));
+                    (long long)workspace_bytes(T, k, H, I));
     MoeParams p{x, ids, weights, static_cast<const uint8_t*>(w1), s1, static_cast<const uint8_t*>(w2), s2,
-                static_cast<uint8_t*>(workspace), out, int(T), int(k), int(E), int(H), int(I), 0, 0, 1};
+                static_cast<uint8_t*>(workspace), reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + T * k * I * 4), out, int(T), int(k), int(E), int(H), int(I), 0, 0, 1};
     hipStream_t s = static_cast<hipStream_t>(stream);
     if (weight == FP8) return x_dtype == GFG_OUT_BF16 ? launch_layer<FP8, __bf16>(p, s) : launch_layer<FP8, _Float16>(p, s);
     return x_dtype == GFG_OUT_BF16 ? launch_layer<INT8, __bf16>(p, s) : launch_layer<INT8, _Float16>(p, s);
@@ -1042,7 +1340,7 @@ extern "C" int moe_topk(const void* logits, int32_t in_dtype, const float* bias,
     return GFG_OK;
 }
 
-extern "C" int64_t moe_layer_workspace_bytes(int64_t T, int64_t k, int64_t I) { return workspace_bytes(T, k, I); }
+extern "C" int64_t moe_layer_workspace_bytes(int64_t T, int64_t k, int64_t H, int64_t I) { return workspace_bytes(T, k, H, I); }
 
 extern "C" int moe_fp8_layer(const void* x, int32_t dtype, const int32_t* topk_ids, const float* topk_weights,
                              const void* w1, const uint8_t* w1_scale, const void* w2, const uint8_t* w2_scale, void* out,

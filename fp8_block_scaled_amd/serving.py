@@ -180,9 +180,9 @@ def moe_topk(logits, ids, weights, score="softmax", bias=None, renormalize=True,
     return ids, weights
 
 
-def moe_layer_workspace_bytes(T, k, I):
+def moe_layer_workspace_bytes(T, k, H, I):
     """Bytes of workspace that the layers need for T tokens of k experts each."""
-    return int(load_library().moe_layer_workspace_bytes(T, k, I))
+    return int(load_library().moe_layer_workspace_bytes(T, k, H, I))
 
 
 def _layer(entry, x, topk_ids, topk_weights, w1, w1_scale, w2, w2_scale, out, workspace, stream, wtypes, stype, block):
@@ -191,7 +191,7 @@ def _layer(entry, x, topk_ids, topk_weights, w1, w1_scale, w2, w2_scale, out, wo
     k = _dims(topk_ids, "topk_ids", 2)[1]
     E, _, I = _dims(w2, "w2", 3)
     s1, s2 = ((E, 2 * I // block, H // block), (E, H // block, I // block)) if block else ((E, 2 * I), (E, H))
-    keep, ws, nbytes = _scratch(workspace, T * k * I * 4, dev)
+    keep, ws, nbytes = _scratch(workspace, T * k * (H + I) * 4, dev)
     _check(entry(
         _ptr(x, "x", _OUT, (T, H), dev), _OUT[x.dtype], _ptr(topk_ids, "topk_ids", _I32, (T, k), dev),
         _ptr(topk_weights, "topk_weights", _F32, (T, k), dev), _ptr(w1, "w1", wtypes, (E, 2 * I, H), dev),
@@ -206,7 +206,7 @@ def moe_fp8_layer(x, topk_ids, topk_weights, w1, w1_scale, w2, w2_scale, out, wo
 
     x and out [T, H] bfloat16 or float16; topk_ids [T, k] int32 (outside [0, E): no contribution); w1 [E, 2I, H]
     and w2 [E, H, I] e4m3 with E8M0 scales [E, 2I/128, H/128] and [E, H/128, I/128], as in the grouped FP8 GEMMs.
-    At most 1024 pairs T * k.  ``workspace``: a uint8 tensor of ``moe_layer_workspace_bytes(T, k, I)`` bytes
+    At most 1024 pairs T * k.  ``workspace``: a uint8 tensor of ``moe_layer_workspace_bytes(T, k, H, I)`` bytes
     (allocated if None); calls on different streams need workspaces of their own.
     """
     return _layer(load_library().moe_fp8_layer, x, topk_ids, topk_weights, w1, w1_scale, w2, w2_scale, out, workspace,

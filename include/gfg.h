@@ -411,12 +411,12 @@ GFG_API int moe_topk(const void* logits, int32_t in_dtype, const float* bias, in
  *   moe_int8_layer: w1 [E][2*I][H] int8, w1_scale [E][2*I] float ; w2
  *                   [E][H][I], w2_scale [E][H]: those of the int8 products
  *   workspace       16-byte aligned device memory, at least
- *                   moe_layer_workspace_bytes(T, k, I) bytes, uninitialized
+ *                   moe_layer_workspace_bytes(T, k, H, I) bytes, uninitialized
  *
  * Sizes: T >= 0 (0 is a no-op), T * k <= 1024, E <= 1024, H and I multiples of
  * 128 up to 32256 (else GFG_EUNSUPPORTED).
  */
-GFG_API int64_t moe_layer_workspace_bytes(int64_t T, int64_t k, int64_t I);
+GFG_API int64_t moe_layer_workspace_bytes(int64_t T, int64_t k, int64_t H, int64_t I);
 GFG_API int moe_fp8_layer(const void* x, int32_t dtype, const int32_t* topk_ids, const float* topk_weights,
                           const void* w1, const uint8_t* w1_scale, const void* w2, const uint8_t* w2_scale, void* out,
                           int64_t T, int64_t k, int64_t E, int64_t H, int64_t I, void* workspace,

@@ -145,6 +145,7 @@ def choose(rng, T, E, k):
     (5, 6, 1, 128, 384, "bf16"), (17, 4, 2, 256, 256, "bf16"), (40, 3, 2, 640, 128, "f16"), (64, 40, 8, 128, 256, "bf16"),
     (100, 2, 1, 128, 128, "bf16"), (150, 2, 2, 256, 128, "f16"), (128, 8, 8, 128, 128, "bf16"), (1024, 1, 1, 128, 128, "bf16"),
     (16, 64, 64, 128, 128, "bf16"), (33, 5, 3, 2048, 1024, "f16"), (2, 1024, 6, 128, 128, "bf16"),
+    (200, 4, 2, 256, 2048, "bf16"), (150, 6, 2, 384, 1536, "f16"), (90, 9, 3, 1152, 1408, "bf16"), (100, 8, 1, 128, 2048, "f16"),
 ])
 def test_layer(weight, T, E, k, H, I, dt):
     what = f"{weight} T={T} E={E} k={k} H={H} I={I} {dt}"
@@ -154,7 +155,7 @@ def test_layer(weight, T, E, k, H, I, dt):
     x = torch.from_numpy(rng.standard_normal((T, H))).to(torch_dtype(dt)).cuda()
     ids = choose(rng, T, E, k)
     w = rng.uniform(0.05, 1.0, (T, k)).astype(np.float32)
-    need = gfg.moe_layer_workspace_bytes(T, k, I)
+    need = gfg.moe_layer_workspace_bytes(T, k, H, I)
     flat = torch.full((need + 256,), 0xFF, dtype=torch.uint8, device="cuda")      # NaNs, if any were read
     out = call(weight, x, to_dev(ids), to_dev(w), ops, workspace=flat[128:128 + need])
     assert bool((flat[:128] == 0xFF).all()) and bool((flat[128 + need:] == 0xFF).all())
@@ -256,7 +257,7 @@ def test_layer_and_router_in_a_graph_on_a_stream():
     ids = torch.zeros(T, k, dtype=torch.int32, device="cuda")
     w = torch.zeros(T, k, device="cuda")
     out = torch.zeros_like(x)
-    ws = torch.empty(gfg.moe_layer_workspace_bytes(T, k, I), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(gfg.moe_layer_workspace_bytes(T, k, H, I), dtype=torch.uint8, device="cuda")
     s = torch.cuda.Stream()
     s.wait_stream(torch.cuda.current_stream())
 

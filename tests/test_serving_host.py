@@ -94,7 +94,7 @@ def test_topk_refuses(change, code):
     assert "moe_topk" in last()
 
 
-LAYER = dict(x=P, dt=0, ids=P, w=P, w1=P, s1=P, w2=P, s2=P, out=P, T=2, k=3, E=4, H=256, I=128, ws=P, bytes=2 * 3 * 128 * 4)
+LAYER = dict(x=P, dt=0, ids=P, w=P, w1=P, s1=P, w2=P, s2=P, out=P, T=2, k=3, E=4, H=256, I=128, ws=P, bytes=2 * 3 * 384 * 4)
 
 
 @pytest.mark.parametrize("change,code", [
@@ -103,7 +103,7 @@ LAYER = dict(x=P, dt=0, ids=P, w=P, w1=P, s1=P, w2=P, s2=P, out=P, T=2, k=3, E=4
     (dict(I=64), EUNSUPPORTED), (dict(H=65664), EUNSUPPORTED), (dict(x=None), EINVAL), (dict(ids=None), EINVAL), (dict(w=None), EINVAL),
     (dict(w1=None), EINVAL), (dict(s1=None), EINVAL), (dict(w2=None), EINVAL), (dict(s2=None), EINVAL), (dict(out=None), EINVAL),
     (dict(x=P + 8), EINVAL), (dict(w1=P + 8), EINVAL), (dict(out=P + 2), EINVAL), (dict(ids=P + 2), EINVAL), (dict(ws=None), EINVAL),
-    (dict(ws=P + 4), EINVAL), (dict(bytes=2 * 3 * 128 * 4 - 1), EINVAL),
+    (dict(ws=P + 4), EINVAL), (dict(bytes=2 * 3 * 384 * 4 - 1), EINVAL),
 ])
 @pytest.mark.parametrize("weight", ["fp8", "int8"])
 def test_layer_refuses(change, code, weight):
@@ -128,7 +128,7 @@ def test_nothing_to_do_is_no_error():
 
 def test_workspace_sizes():
     assert gfg.int8_linear_workspace_bytes(7, 64) == 7 * 68 and gfg.int8_linear_workspace_bytes(0, 64) == 0
-    assert gfg.moe_layer_workspace_bytes(2, 3, 128) == 2 * 3 * 128 * 4 and gfg.moe_layer_workspace_bytes(0, 3, 128) == 0
+    assert gfg.moe_layer_workspace_bytes(2, 3, 256, 128) == 2 * 3 * 384 * 4 and gfg.moe_layer_workspace_bytes(0, 3, 256, 128) == 0
 
 
 def test_bindings_refuse_what_is_not_on_a_gpu():
