@@ -34,6 +34,16 @@ struct Params {
 #define GFG_WAITCNT(VM, LG) \
     __builtin_amdgcn_s_waitcnt(((VM) & 15) | ((((VM) >> 4) & 3) << 14) | (7 << 4) | (((LG) & 15) << 8))
 
+// Barrier of a workgroup for LDS data: this wave's LDS operations are done, and
+// the compiler moves no memory operation across (the barrier builtin alone
+// does not say that it touches memory).  Vector-memory operations stay in flight.
+__device__ __forceinline__ void lds_barrier() {
+    asm volatile("" ::: "memory");
+    GFG_WAITCNT(63, 0);
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
 // Raw buffer resource over [base, base + bytes): stride 0, 32-bit data format.
 // The hardware returns zero for loads, and drops stores, at offsets past `bytes`.
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base, uint32_t bytes) {

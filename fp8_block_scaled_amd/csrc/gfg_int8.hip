@@ -94,61 +94,59 @@ template <typename T, int LPR>
 __global__ __launch_bounds__(QT) void quant_token_kernel(const T* __restrict__ x, uint8_t* __restrict__ q,
                                                          float* __restrict__ scale, int64_t M, int K) {
     constexpr int RPB = QT / LPR;              // rows per workgroup
-    __shared__ uint32_t part[QT / 64];
-    const int lane = threadIdx.x % LPR;
-    const int64_t m = int64_t(blockIdx.x) * RPB + threadIdx.x / LPR;
-    const bool live = m < M;                   // a whole wave (LPR >= 64) is live or not
-    const T* row = x + (live ? m : 0) * K;
-    const int chunks = K / 8;
-    Chunk<T> held[kHeld];
-    uint32_t ab = 0;
+    __shared__ uint32_t part[2][QT / 64];      // in turn: a row's maxima are read while the next row's are written
+    const int lane = threadIdx.x % LPR, chunks = K / 8;
+    int turn = 0;
+    for (int64_t m = int64_t(blockIdx.x) * RPB + threadIdx.x / LPR; m < M; m += int64_t(gridDim.x) * RPB, turn ^= 1) {
+        const T* row = x + m * K;
+        Chunk<T> held[kHeld];
+        uint32_t ab = 0;
 #pragma unroll
-    for (int j = 0; j < kHeld; ++j)
-        if (lane + j * LPR < chunks) {
-            held[j].load(row + (lane + j * LPR) * 8);
+        for (int j = 0; j < kHeld; ++j)
+            if (lane + j * LPR < chunks) held[j].load(row + (lane + j * LPR) * 8);
+#pragma unroll
+        for (int j = 0; j < kHeld; ++j)
+            if (lane + j * LPR < chunks) ab = max(ab, chunk_amax(held[j]));
+        for (int c = lane + kHeld * LPR; c < chunks; c += LPR) {
+            Chunk<T> t;
+            t.load(row + c * 8);
+            ab = max(ab, chunk_amax(t));
         }
 #pragma unroll
-    for (int j = 0; j < kHeld; ++j)
-        if (lane + j * LPR < chunks) ab = max(ab, chunk_amax(held[j]));
-    for (int c = lane + kHeld * LPR; c < chunks; c += LPR) {
-        Chunk<T> t;
-        t.load(row + c * 8);
-        ab = max(ab, chunk_amax(t));
-    }
+        for (int w = 32; w >= 1; w >>= 1) ab = max(ab, uint32_t(__shfl_xor(int(ab), w, 64)));
+        if constexpr (LPR > 64) {              // (the workgroup's lanes share the row: all of them are here)
+            if ((threadIdx.x & 63) == 0) part[turn][threadIdx.x >> 6] = ab;
+            __syncthreads();
 #pragma unroll
-    for (int w = 32; w >= 1; w >>= 1) ab = max(ab, uint32_t(__shfl_xor(int(ab), w, 64)));
-    if constexpr (LPR > 64) {
-        if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = ab;
-        __syncthreads();
+            for (int w = 0; w < QT / 64; ++w) ab = max(ab, part[turn][w]);
+        }
+        float s, r;
+        row_scale(ab, &s, &r);
+        if (lane == 0) scale[m] = s;
+        uint8_t* out = q + m * K;
+        const bool bad = r == 0.0f;            // 0 * infinity would be NaN
 #pragma unroll
-        for (int w = 0; w < QT / 64; ++w) ab = max(ab, part[w]);
-    }
-    if (!live) return;
-    float s, r;
-    row_scale(ab, &s, &r);
-    if (lane == 0) scale[m] = s;
-    uint8_t* out = q + m * K;
-    const bool bad = r == 0.0f;                // 0 * infinity would be NaN
-#pragma unroll
-    for (int j = 0; j < kHeld; ++j)
-        if (lane + j * LPR < chunks)
-            *reinterpret_cast<u32x2*>(out + (lane + j * LPR) * 8) = bad ? u32x2{0u, 0u} : chunk_encode(held[j], r);
-    for (int c = lane + kHeld * LPR; c < chunks; c += LPR) {
-        Chunk<T> t;
-        t.load(row + c * 8);
-        *reinterpret_cast<u32x2*>(out + c * 8) = bad ? u32x2{0u, 0u} : chunk_encode(t, r);
+        for (int j = 0; j < kHeld; ++j)
+            if (lane + j * LPR < chunks)
+                *reinterpret_cast<u32x2*>(out + (lane + j * LPR) * 8) = bad ? u32x2{0u, 0u} : chunk_encode(held[j], r);
+        for (int c = lane + kHeld * LPR; c < chunks; c += LPR) {
+            Chunk<T> t;
+            t.load(row + c * 8);
+            *reinterpret_cast<u32x2*>(out + c * 8) = bad ? u32x2{0u, 0u} : chunk_encode(t, r);
+        }
     }
 }
 
 template <typename T>
 void launch_quant(const void* x, uint8_t* q, float* scale, int64_t M, int K, hipStream_t s) {
     // a wave for rows that it holds in registers (2048 elements), else a workgroup
+    constexpr int64_t most = 1 << 22;          // workgroups; each walks on where there are more rows
+    const int64_t wgs = K <= 64 * 8 * kHeld ? (M + 3) / 4 : M;
+    const dim3 grid(unsigned(wgs < most ? wgs : most));
     if (K <= 64 * 8 * kHeld)
-        hipLaunchKernelGGL((quant_token_kernel<T, 64>), dim3(unsigned((M + 3) / 4)), dim3(QT), 0, s,
-                           static_cast<const T*>(x), q, scale, M, K);
+        hipLaunchKernelGGL((quant_token_kernel<T, 64>), grid, dim3(QT), 0, s, static_cast<const T*>(x), q, scale, M, K);
     else
-        hipLaunchKernelGGL((quant_token_kernel<T, QT>), dim3(unsigned(M)), dim3(QT), 0, s, static_cast<const T*>(x), q,
-                           scale, M, K);
+        hipLaunchKernelGGL((quant_token_kernel<T, QT>), grid, dim3(QT), 0, s, static_cast<const T*>(x), q, scale, M, K);
 }
 
 // ------------------------------------------------------------------ tiled product
@@ -254,8 +252,8 @@ __global__ __launch_bounds__(WM * WN * 64) void int8_gemm_kernel(I8Params p) {
     // reads of the stage before it are done; after the barrier, everyone's
     auto step = [&](GFG_LDS uint8_t* cur, GFG_LDS uint8_t* freed, int kb) {
         __builtin_amdgcn_sched_barrier(0);
-        GFG_WAITCNT((S - 2) * PER, 0);
-        __builtin_amdgcn_s_barrier();
+        GFG_WAITCNT((S - 2) * PER, 15);
+        lds_barrier();
         __builtin_amdgcn_sched_barrier(0);
         issue(freed, kb + S - 1);                  // a stage past K loads zeros
         __builtin_amdgcn_sched_barrier(0);
@@ -492,6 +490,7 @@ int launch_stream(I8Params p, int out_dtype, hipStream_t s) {
     p.tiles_per_group = int((p.rows + 16 * RB - 1) / (16 * RB));
     p.m_tiles = p.tiles_per_group * groups;
     const int64_t tiles = int64_t(p.m_tiles) * ((p.N + 16 * CB - 1) / (16 * CB));
+    if (tiles * (NW * 64) >= int64_t(1) << 32) return fail(GFG_EUNSUPPORTED, "the output has too many tiles for one launch");
     const dim3 grid{unsigned(tiles)}, block(NW * 64);
     if (out_dtype == GFG_OUT_BF16)
         hipLaunchKernelGGL((int8_stream_kernel<LAYOUT, RB, CB, NW, D, __bf16>), grid, block, 0, s, p);
@@ -508,6 +507,7 @@ int launch_ring(I8Params p, int out_dtype, hipStream_t s) {
     p.tiles_per_group = int((p.rows + TM - 1) / TM);
     p.m_tiles = p.tiles_per_group * groups;
     const int64_t tiles = int64_t(p.m_tiles) * ((p.N + TN - 1) / TN);
+    if (tiles * (WM * WN * 64) >= int64_t(1) << 32) return fail(GFG_EUNSUPPORTED, "the output has too many tiles for one launch");
     const dim3 grid{unsigned(tiles)}, block(WM * WN * 64);
     if (out_dtype == GFG_OUT_BF16)
         hipLaunchKernelGGL((int8_gemm_kernel<LAYOUT, TM, TN, S, WM, WN, __bf16>), grid, block, 0, s, p);
@@ -693,8 +693,6 @@ int launch_small(const I8Params& p, int out_dtype, hipStream_t s) {
 // 128; 2048 x 4096 x 4096, 128 tiles: 48.6, 50.7; but 2048^3, 64 tiles: 26.8,
 // 16.0).  `p` holds everything but the tile counts.
 int launch_i8(const char* fn, I8Params p, int layout, int out_dtype, hipStream_t s) {
-    int cus = 0;
-    if (int rc = device_cus(&cus)) return rc;
     const int groups = layout == MASKED ? p.G : 1;
     const int64_t t128 = (p.rows + 127) / 128 * groups, t256 = (p.rows + 255) / 256 * groups;
     const int64_t n256 = (int64_t(p.N) + 255) / 256;
@@ -702,6 +700,8 @@ int launch_i8(const char* fn, I8Params p, int layout, int out_dtype, hipStream_t
     const int choice = tile_shape_choice();
     if (choice == GFG_TILE_256x256 && !fits)
         return fail(GFG_EUNSUPPORTED, "%s: the 256 x 256 tile needs N=%d at most 2^22", fn, p.N);
+    int cus = 0;
+    if (int rc = device_cus(&cus)) return rc;
     if (choice == GFG_TILE_256x256 || (choice == GFG_TILE_AUTO && fits && t256 * n256 * 16 >= cus * 7)) {
         p.m_tiles = int(layout == CONTIG ? t128 : t256);
         p.tiles_per_group = int(t256 / groups);
@@ -733,6 +733,8 @@ I8Params product(const int8_t* a, const float* a_scale, const int8_t* b, const f
 
 // ------------------------------------------------------------------ argument checks
 constexpr int64_t kMaxK = (int64_t(1) << 17) - 16;     // |sum| <= 2^14 K stays below 2^31
+constexpr int64_t kMaxN = int64_t(1) << 28;
+constexpr int64_t kMaxRowTiles = 65535;                // of 128 rows
 
 int check_quant(const char* fn, const void* x, int32_t in_dtype, int64_t M, int64_t K, const void* q, const void* scale) {
     if (in_dtype != GFG_IN_F32 && in_dtype != GFG_IN_BF16 && in_dtype != GFG_IN_F16)
@@ -760,7 +762,9 @@ int check_product(const char* fn, int64_t rows, int64_t N, int64_t K, int64_t G,
     if (K % 16 || K > kMaxK)
         return fail(GFG_EUNSUPPORTED, "%s: K=%lld must be a multiple of 16 and at most %lld", fn, (long long)K,
                     (long long)kMaxK);
-    if (N > int64_t(1) << 30) return fail(GFG_EUNSUPPORTED, "%s: N=%lld above 2^30", fn, (long long)N);
+    if (N > kMaxN) return fail(GFG_EUNSUPPORTED, "%s: N=%lld above 2^28", fn, (long long)N);
+    if (rows > kMaxRowTiles * 128)
+        return fail(GFG_EUNSUPPORTED, "%s: %lld rows, at most %lld", fn, (long long)rows, (long long)(kMaxRowTiles * 128));
     *empty = rows == 0;
     return GFG_OK;
 }
@@ -786,8 +790,6 @@ int quantize(const void* x, int32_t in_dtype, int64_t M, int64_t K, uint8_t* q, 
     return GFG_OK;
 }
 
-constexpr int64_t kMaxRowTiles = 65535;        // the grid's second dimension
-
 }  // namespace
 }  // namespace gfg
 
@@ -809,8 +811,6 @@ extern "C" int int8_gemm(const int8_t* a, const float* a_scale, const int8_t* b,
     if (int rc = check_product(fn, M, N, K, 1, out_dtype, &empty)) return rc;
     if (empty) return GFG_OK;
     if (int rc = check_operands(fn, a, a_scale, b, b_scale, bias, false, d)) return rc;
-    const int64_t tiles = (M + 127) / 128;
-    if (tiles > kMaxRowTiles) return fail(GFG_EUNSUPPORTED, "%s: M=%lld above %lld", fn, (long long)M, (long long)(kMaxRowTiles * 128));
     return launch_i8(fn, product(a, a_scale, b, b_scale, bias, nullptr, d, M, N, K, 1), DENSE, out_dtype,
                      static_cast<hipStream_t>(stream));
 }
@@ -838,8 +838,6 @@ extern "C" int int8_linear(const void* x, int32_t in_dtype, const int8_t* b, con
     float* const scale = reinterpret_cast<float*>(q + M * K);
     if (int rc = check_quant(fn, x, in_dtype, M, K, q, scale)) return rc;
     if (int rc = check_operands(fn, q, scale, b, b_scale, bias, false, d)) return rc;
-    const int64_t tiles = (M + 127) / 128;
-    if (tiles > kMaxRowTiles) return fail(GFG_EUNSUPPORTED, "%s: M=%lld above %lld", fn, (long long)M, (long long)(kMaxRowTiles * 128));
     hipStream_t s = static_cast<hipStream_t>(stream);
     if (M <= kFewTokens && M * ((K + TK - 1) / TK * TK) <= kFewCodes) {
         const I8Params p = product(nullptr, nullptr, b, b_scale, bias, nullptr, d, M, N, K, 1);

@@ -30,6 +30,7 @@ namespace {
 
 // ------------------------------------------------------------------ router
 constexpr int kMaxExperts = 1024;
+constexpr int64_t kMostWorkgroups = 1 << 20;   // of the router; each walks on where there are more tokens
 
 __device__ __forceinline__ float as_f32(float v) { return v; }
 __device__ __forceinline__ float as_f32(__bf16 v) { return float(v); }
@@ -62,15 +63,10 @@ __device__ __forceinline__ int wave_min(int v) { return wave_reduce(v, [](int a,
 // takes the largest remaining selection value and, among its holders, the
 // lowest index; lane j keeps the result of round j.
 template <typename T, int EPL>
-__global__ __launch_bounds__(256) void moe_topk_kernel(const T* __restrict__ logits, const float* __restrict__ bias,
-                                                       int32_t* __restrict__ ids, float* __restrict__ weights,
-                                                       int64_t tokens, int E, int k, bool sigmoid, bool renorm,
-                                                       float scale) {
-    const int lane = threadIdx.x & 63;
-    const int64_t t = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6);
-    if (t >= tokens) return;
+__device__ __forceinline__ void topk_row(const T* __restrict__ row, const float* __restrict__ bias, int32_t* __restrict__ ids,
+                                         float* __restrict__ weights, int lane, int E, int k, bool sigmoid, bool renorm,
+                                         float scale) {
     const float ninf = -__builtin_inff();
-    const T* row = logits + t * E;
     float l[EPL], s[EPL];
     float m = ninf;
 #pragma unroll
@@ -128,15 +124,26 @@ __global__ __launch_bounds__(256) void moe_topk_kernel(const T* __restrict__ log
         w = sum > 0.0f ? w / sum : 0.0f;
     }
     if (lane < k) {
-        ids[t * k + lane] = mine;
-        weights[t * k + lane] = w * scale;
+        ids[lane] = mine;
+        weights[lane] = w * scale;
     }
+}
+
+template <typename T, int EPL>
+__global__ __launch_bounds__(256) void moe_topk_kernel(const T* __restrict__ logits, const float* __restrict__ bias,
+                                                       int32_t* __restrict__ ids, float* __restrict__ weights,
+                                                       int64_t tokens, int E, int k, bool sigmoid, bool renorm,
+                                                       float scale) {
+    const int lane = threadIdx.x & 63;
+    for (int64_t t = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6); t < tokens; t += int64_t(gridDim.x) * 4)
+        topk_row<T, EPL>(logits + t * E, bias, ids + t * k, weights + t * k, lane, E, k, sigmoid, renorm, scale);
 }
 
 template <typename T>
 void launch_topk(const void* logits, const float* bias, int32_t* ids, float* weights, int64_t tokens, int E, int k,
                  bool sigmoid, bool renorm, float scale, hipStream_t s) {
-    const dim3 grid(unsigned((tokens + 3) / 4));
+    const int64_t wgs = (tokens + 3) / 4;
+    const dim3 grid(unsigned(wgs < kMostWorkgroups ? wgs : kMostWorkgroups));
     const T* l = static_cast<const T*>(logits);
 #define GFG_TOPK(EPL)                                                                                              \
     hipLaunchKernelGGL((moe_topk_kernel<T, EPL>), grid, dim3(256), 0, s, l, bias, ids, weights, tokens, E, k, sigmoid, \
@@ -612,7 +619,7 @@ __device__ __forceinline__ void up_items(const MoeParams& p, const GFG_LDS Routi
     for (int d = 0; d < depth; ++d) issue();
     if constexpr (RES) {                       // the resident rows, loaded before the stages, have landed
         wait_stage<PER>(depth + 1);
-        __builtin_amdgcn_s_barrier();
+        lds_barrier();
     }
 
     // fragment addresses in stage 0
@@ -692,16 +699,12 @@ __device__ __forceinline__ void up_items(const MoeParams& p, const GFG_LDS Routi
         // the last).  Fragment f, column l16 of row quad lq: place lq * NR + l16.
         const int last = done % min(KB, kWaves), mine = wave - (wave > last);
         GFG_LDS v4f* const sums = red + (TWICE && (done & 1) ? (kWaves - 1) * F * 4 * NR : 0);
-        if (!TWICE) {
-            GFG_WAITCNT(63, 0);
-            __builtin_amdgcn_s_barrier();
-        }
+        if (!TWICE) lds_barrier();
         if (wave != last && l16 < NR) {
 #pragma unroll
             for (int f = 0; f < F; ++f) sums[(mine * F + f) * 4 * NR + lq * NR + l16] = acc[f];
         }
-        GFG_WAITCNT(63, 0);
-        __builtin_amdgcn_s_barrier();
+        lds_barrier();
         if (wave != last) continue;
         const int lr = l16 & (NR - 1);
 #pragma unroll
@@ -734,8 +737,6 @@ __device__ __forceinline__ void up_items(const MoeParams& p, const GFG_LDS Routi
 //
 // UP: the weight rows are 64 gate and 64 up rows, eight of each to a wave, so
 // that gate and up meet in a wave.  DOWN: 128 rows of W2; sums go to y.
-template <int N> __device__ __forceinline__ void wait_shared() { GFG_WAITCNT(N, 0); }
-
 // Units of 64 rows where that saves a round of items over the workgroups: a few
 // experts with slightly more than 32 rows would otherwise cost a second pass
 // over their weights.  (Smaller stages leave room for one more of them.)
@@ -848,8 +849,8 @@ __device__ __forceinline__ void shared_items(const MoeParams& p, const GFG_LDS R
         };
         for (int kb = 0; kb < KB; ++kb) {
             __builtin_amdgcn_sched_barrier(0);
-            wait_shared<(S - 2) * PER>();
-            __builtin_amdgcn_s_barrier();
+            GFG_WAITCNT((S - 2) * PER, 15);
+            lds_barrier();
             __builtin_amdgcn_sched_barrier(0);
             const uint32_t so = uint32_t(cs * STAGE);
             cs = cs + 1 == S ? 0 : cs + 1;
@@ -1283,8 +1284,8 @@ int layer(const char* fn, int weight, const void* x, int32_t x_dtype, const int3
         return fail(GFG_EINVAL, "%s: bad sizes T=%lld k=%lld E=%lld H=%lld I=%lld", fn, (long long)T, (long long)k,
                     (long long)E, (long long)H, (long long)I);
     if (E > kMaxExperts || T > kMaxPairs || k > kMaxPairs || T * k > kMaxPairs)
-        return fail(GFG_EUNSUPPORTED, "%s: E=%lld above %d or T*k=%lld above %d", fn, (long long)E, kMaxExperts,
-                    (long long)(T * k), kMaxPairs);
+        return fail(GFG_EUNSUPPORTED, "%s: E=%lld above %d, or T=%lld times k=%lld above %d", fn, (long long)E, kMaxExperts,
+                    (long long)T, (long long)k, kMaxPairs);
     if (H % 128 || I % 128 || H > kMaxDim || I > kMaxDim)
         return fail(GFG_EUNSUPPORTED, "%s: H=%lld and I=%lld must be multiples of 128 up to %d", fn, (long long)H, (long long)I, kMaxDim);
     if (T == 0) return GFG_OK;

@@ -63,10 +63,20 @@ def _handle(stream, device):
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _scratch(workspace, needed, device):
-    """Address and size of the workspace; a new one where the caller keeps none."""
+def _empty(shape, dtype, device, stream):
+    """A new tensor that belongs to the stream that the call runs on (so that its memory is not reused too early)."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(_handle(stream, device), device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _scratch(workspace, needed, device, stream):
+    """The workspace with its address and size; a new one where the caller keeps none."""
     if workspace is None:
-        workspace = torch.empty(max(needed, 16), dtype=torch.uint8, device=device)
+        workspace = _empty(max(needed, 16), torch.uint8, device, stream)
     elif not isinstance(workspace, torch.Tensor) or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
         raise TypeError("workspace must be a contiguous uint8 tensor")
     elif workspace.device != device:
@@ -85,9 +95,9 @@ def int8_quantize_token_device(x, q=None, scale=None, stream=None):
     if x.dim() < 1:
         raise ValueError("x must have at least one dimension")
     if q is None:
-        q = torch.empty(x.shape, dtype=torch.int8, device=dev)
+        q = _empty(x.shape, torch.int8, dev, stream)
     if scale is None:
-        scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
+        scale = _empty(x.shape[:-1], torch.float32, dev, stream)
     K = x.shape[-1]
     M = x.numel() // K if K else 0
     _check(load_library().int8_quantize_token_device(
@@ -124,7 +134,7 @@ def int8_linear(x, b, b_scale, d, bias=None, workspace=None, stream=None):
     M, K = _dims(x, "x", 2)
     N = _dims(b, "b", 2)[0]
     lib = load_library()
-    keep, ws, nbytes = _scratch(workspace, M * (K + 4), dev)
+    keep, ws, nbytes = _scratch(workspace, M * (K + 4), dev, stream)
     _check(lib.int8_linear(
         _ptr(x, "x", _IN, (M, K), dev), _IN[x.dtype], _ptr(b, "b", _I8, (N, K), dev),
         _ptr(b_scale, "b_scale", _F32, (N,), dev), None if bias is None else _ptr(bias, "bias", _F32, (N,), dev),
@@ -191,7 +201,7 @@ def _layer(entry, x, topk_ids, topk_weights, w1, w1_scale, w2, w2_scale, out, wo
     k = _dims(topk_ids, "topk_ids", 2)[1]
     E, _, I = _dims(w2, "w2", 3)
     s1, s2 = ((E, 2 * I // block, H // block), (E, H // block, I // block)) if block else ((E, 2 * I), (E, H))
-    keep, ws, nbytes = _scratch(workspace, T * k * (H + I) * 4, dev)
+    keep, ws, nbytes = _scratch(workspace, T * k * (H + I) * 4, dev, stream)
     _check(entry(
         _ptr(x, "x", _OUT, (T, H), dev), _OUT[x.dtype], _ptr(topk_ids, "topk_ids", _I32, (T, k), dev),
         _ptr(topk_weights, "topk_weights", _F32, (T, k), dev), _ptr(w1, "w1", wtypes, (E, 2 * I, H), dev),

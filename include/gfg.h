@@ -333,8 +333,9 @@ GFG_API int int8_quantize_token_device(const void* x, int32_t in_dtype, int64_t 
  *   (a and b 16-byte aligned, d 8-byte aligned, the rest 4-byte aligned, else
  *   GFG_EINVAL)
  *
- * Sizes: M >= 0 (0 is a no-op), M <= 128 * 65535, any N in [1, 2^30], K a
- * multiple of 16 up to 2^17 - 16 (else GFG_EUNSUPPORTED).
+ * Sizes: M >= 0 (0 is a no-op), M <= 128 * 65535, any N in [1, 2^28], K a
+ * multiple of 16 up to 2^17 - 16, and few enough output tiles for one launch
+ * (M * N below 2^36 always has; else GFG_EUNSUPPORTED).
  *
  * int8_linear is the token quantizer and this product in one call, from
  * x [M][K] in 32 or 16 bits: a 16-byte aligned device workspace of at least

@@ -233,6 +233,41 @@ def test_layer_extreme_scale_bytes():
     assert np.all(np.abs(out - ref) <= 2.0 ** -8 * np.abs(ref) * 1.01 + 2.0 ** -12 * np.abs(ref).max(1, keepdims=True) + 2.0 ** -126)
 
 
+@pytest.mark.parametrize("T,E,k,H,I", [(2, 6, 3, 512, 384), (90, 9, 3, 1152, 1408)])
+@pytest.mark.parametrize("offset", [1, 2, 3])
+def test_layer_scale_bytes_at_any_alignment(T, E, k, H, I, offset):
+    """E8M0 scales are bytes and may start anywhere; the kernels read them in words."""
+    rng = np.random.default_rng(T + offset)
+    (w1, s1, w2, s2), (d1, d2) = make(rng, "fp8", E, H, I)
+
+    def moved(s):
+        flat = torch.full((s.numel() + 8,), 200, dtype=torch.uint8, device="cuda")
+        flat[offset:offset + s.numel()] = s.reshape(-1)
+        return flat[offset:offset + s.numel()].view(s.shape)
+
+    x = torch.from_numpy(rng.standard_normal((T, H))).to(torch.bfloat16).cuda()
+    ids, w = choose(rng, T, E, k), rng.uniform(0.1, 1.0, (T, k)).astype(np.float32)
+    out = call("fp8", x, to_dev(ids), to_dev(w), (w1, moved(s1), w2, moved(s2)))
+    check_layer(out, so.layer(x.float().cpu().numpy(), ids, w, d1, d2), "bf16", f"scales at {offset}")
+
+
+def test_layer_on_a_stream_without_a_workspace():
+    rng = np.random.default_rng(31)
+    T, E, k, H, I = 3, 5, 2, 256, 256
+    ops, (d1, d2) = make(rng, "int8", E, H, I)
+    x = torch.from_numpy(rng.standard_normal((T, H))).to(torch.bfloat16).cuda()
+    ids, w = choose(rng, T, E, k), rng.uniform(0.1, 1.0, (T, k)).astype(np.float32)
+    di, dw = to_dev(ids), to_dev(w)
+    outs = [torch.zeros_like(x) for _ in range(2)]
+    torch.cuda.synchronize()
+    ref = so.layer(x.float().cpu().numpy(), ids, w, d1, d2)
+    s = torch.cuda.Stream()
+    for stream, out in zip((s, s.cuda_stream), outs):     # a Stream, and its handle
+        call("int8", x, di, dw, ops, out=out, stream=stream)
+        s.synchronize()
+        check_layer(out, ref, "bf16", "on a stream")
+
+
 def test_layer_hidden_values_beyond_half_precision():
     """float16 tokens whose hidden rows pass 65504 and come back into range."""
     rng = np.random.default_rng(12)

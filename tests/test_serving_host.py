@@ -53,8 +53,16 @@ def test_product_refuses(change, code):
     assert "int8_gemm" in last()
 
 
+def test_large_tile_refuses_wide_outputs():
+    gfg.set_tile_shape(gfg.TILE_256x256)
+    try:
+        assert lib().int8_gemm(P, P, P, P, None, P, 4, (1 << 22) + 8, 64, 0, None) == EUNSUPPORTED
+    finally:
+        gfg.set_tile_shape(gfg.TILE_AUTO)
+
+
 @pytest.mark.parametrize("change,code", [
-    (dict(dt=5), EINVAL), (dict(ws=None), EINVAL), (dict(ws=P + 8), EINVAL), (dict(bytes=4 * 68 - 1), EINVAL), (dict(x=None), EINVAL),
+    (dict(M=1 << 62), EUNSUPPORTED), (dict(dt=5), EINVAL), (dict(ws=None), EINVAL), (dict(ws=P + 8), EINVAL), (dict(bytes=4 * 68 - 1), EINVAL), (dict(x=None), EINVAL),
     (dict(K=24), EUNSUPPORTED), (dict(out=9), EINVAL), (dict(b=None), EINVAL), (dict(d=P + 2), EINVAL), (dict(x=P + 4), EINVAL),
 ])
 def test_linear_refuses(change, code):
