@@ -183,14 +183,11 @@ __global__ __launch_bounds__(WM * WN * 64) void int8_gemm_kernel(I8Params p) {
     constexpr int WAVES = WM * WN, BYTES = (TM + TN) * TK;
     constexpr int PER = BYTES / 1024 / WAVES;      // 1 KB loads per wave and stage
     constexpr int RB = TM / WM / 16, CB = TN / WN / 16;
-    static_assert(S >= 3 && S <= 8 && BYTES % (1024 * WAVES) == 0 && TM % (8 * WAVES) == 0, "stage shape");
+    static_assert(S == 4 && BYTES % (1024 * WAVES) == 0 && TM % (8 * WAVES) == 0, "stage shape");
     // an array for each stage: the compiler then knows that reading one need
     // not wait for the loads into another
-    __shared__ __attribute__((aligned(1024))) uint8_t s0[BYTES], s1[BYTES], s2[BYTES];
-    __shared__ __attribute__((aligned(1024))) uint8_t s3[S > 3 ? BYTES : 1024], s4[S > 4 ? BYTES : 1024],
-        s5[S > 5 ? BYTES : 1024], s6[S > 6 ? BYTES : 1024], s7[S > 7 ? BYTES : 1024];
-    GFG_LDS uint8_t* const buf[8] = {(GFG_LDS uint8_t*)s0, (GFG_LDS uint8_t*)s1, (GFG_LDS uint8_t*)s2, (GFG_LDS uint8_t*)s3,
-                                     (GFG_LDS uint8_t*)s4, (GFG_LDS uint8_t*)s5, (GFG_LDS uint8_t*)s6, (GFG_LDS uint8_t*)s7};
+    __shared__ __attribute__((aligned(1024))) uint8_t s0[BYTES], s1[BYTES], s2[BYTES], s3[BYTES];
+    GFG_LDS uint8_t* const buf[S] = {(GFG_LDS uint8_t*)s0, (GFG_LDS uint8_t*)s1, (GFG_LDS uint8_t*)s2, (GFG_LDS uint8_t*)s3};
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int l16 = lane & 15, lq = lane >> 4;
@@ -282,26 +279,8 @@ __global__ __launch_bounds__(WM * WN * 64) void int8_gemm_kernel(I8Params p) {
         if (kb + 2 >= KB) break;
         step(buf[2], buf[1], kb + 2);
         if (kb + 3 >= KB) break;
-        if constexpr (S > 3) {
-            step(buf[3], buf[2], kb + 3);
-            if (kb + 4 >= KB) break;
-        }
-        if constexpr (S > 4) {
-            step(buf[4], buf[3], kb + 4);
-            if (kb + 5 >= KB) break;
-        }
-        if constexpr (S > 5) {
-            step(buf[5], buf[4], kb + 5);
-            if (kb + 6 >= KB) break;
-        }
-        if constexpr (S > 6) {
-            step(buf[6], buf[5], kb + 6);
-            if (kb + 7 >= KB) break;
-        }
-        if constexpr (S > 7) {
-            step(buf[7], buf[6], kb + 7);
-            if (kb + 8 >= KB) break;
-        }
+        step(buf[3], buf[2], kb + 3);
+        if (kb + 4 >= KB) break;
     }
     GFG_WAITCNT(0, 15);                            // the last loads land before the workgroup ends
 
@@ -346,18 +325,16 @@ __global__ __launch_bounds__(NW * 64) void int8_stream_kernel(I8Params p) {
     constexpr int TM = 16 * RB, TN = 16 * CB;
     constexpr int UNIT = (TM + TN) * TK;           // bytes of a stage: A's rows, then B's
     constexpr int PER = UNIT / 1024;               // loads per stage
-    static_assert(D >= 2 && D <= 6 && PER * D < 64, "ring depth");
+    static_assert((D == 2 || D == 4) && PER * D < 64, "ring depth");
     // an array for each stage: the compiler then knows that reading one need
     // not wait for the loads into another
     __shared__ __attribute__((aligned(1024))) uint8_t s0[NW * UNIT], s1[NW * UNIT];
-    __shared__ __attribute__((aligned(1024))) uint8_t s2[D > 2 ? NW * UNIT : 1024], s3[D > 3 ? NW * UNIT : 1024],
-        s4[D > 4 ? NW * UNIT : 1024], s5[D > 5 ? NW * UNIT : 1024];
+    __shared__ __attribute__((aligned(1024))) uint8_t s2[D > 2 ? NW * UNIT : 1024], s3[D > 2 ? NW * UNIT : 1024];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int l16 = lane & 15, lq = lane >> 4;
-    GFG_LDS uint8_t* const ring[6] = {(GFG_LDS uint8_t*)s0 + wave * UNIT, (GFG_LDS uint8_t*)s1 + wave * UNIT,
-                                      (GFG_LDS uint8_t*)s2 + (D > 2 ? wave * UNIT : 0), (GFG_LDS uint8_t*)s3 + (D > 3 ? wave * UNIT : 0),
-                                      (GFG_LDS uint8_t*)s4 + (D > 4 ? wave * UNIT : 0), (GFG_LDS uint8_t*)s5 + (D > 5 ? wave * UNIT : 0)};
+    GFG_LDS uint8_t* const ring[4] = {(GFG_LDS uint8_t*)s0 + wave * UNIT, (GFG_LDS uint8_t*)s1 + wave * UNIT,
+                                      (GFG_LDS uint8_t*)s2 + (D > 2 ? wave * UNIT : 0), (GFG_LDS uint8_t*)s3 + (D > 2 ? wave * UNIT : 0)};
     const unsigned nx = unsigned(p.num_xcd), T = gridDim.x;
     const unsigned x = blockIdx.x % nx, per = T / nx, rem = T % nx;
     const unsigned item = x * per + min(x, rem) + blockIdx.x / nx;
@@ -437,18 +414,8 @@ __global__ __launch_bounds__(NW * 64) void int8_stream_kernel(I8Params p) {
         if constexpr (D > 2) {
             if (k + 2 * STEP >= p.K) break;
             step(ring[2], k + 2 * STEP);
-        }
-        if constexpr (D > 3) {
             if (k + 3 * STEP >= p.K) break;
             step(ring[3], k + 3 * STEP);
-        }
-        if constexpr (D > 4) {
-            if (k + 4 * STEP >= p.K) break;
-            step(ring[4], k + 4 * STEP);
-        }
-        if constexpr (D > 5) {
-            if (k + 5 * STEP >= p.K) break;
-            step(ring[5], k + 5 * STEP);
         }
     }
     GFG_WAITCNT(0, 15);                            // the last loads land before the workgroup ends

@@ -293,3 +293,73 @@ def test_graph_replays_match_eager():
             g.replay()
         torch.cuda.synchronize()
         assert torch.equal(d, want[0]) and torch.equal(one, want[1]), f"replay {r}"
+
+
+# ------------------------------------------------------------------ offsets past 32 bits
+def some_codes(seed, *shape):
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(seed)
+    return torch.randint(-127, 128, shape, dtype=torch.int8, device="cuda", generator=gen)
+
+
+def check_rows(d, a, sa, b, sb, rows, out, what):
+    rows = torch.tensor(rows, device="cuda")
+    got, pa, ps = d[rows], a[rows].cpu().numpy(), sa[rows].cpu().numpy()
+    ref = so.int8_product(pa, ps, b.cpu().numpy(), sb.cpu().numpy())
+    check(got, ref, out, np.abs(ref), what)
+
+
+def test_dense_operands_past_4_gib(tile):
+    M, N, K = 530_001, 72, 8208                           # A has 4.35e9 bytes
+    a, b = some_codes(1, M, K), some_codes(2, N, K)
+    sa, sb = torch.rand(M, device="cuda") + 0.5, (torch.rand(N, device="cuda") + 0.5) / 4096
+    d = torch.empty(M, N, dtype=torch.bfloat16, device="cuda")
+    print(f"[int8] A past 4 GiB, tile {tile}", flush=True)
+    gfg.int8_gemm(a, sa, b, sb, d)
+    check_rows(d, a, sa, b, sb, [0, 1, 261_632, 523_263, 523_264, 523_500, M - 1], "bf16", "A past 4 GiB")
+
+
+def test_outputs_past_4_gib(tile):
+    M, N, K = 33_000, 70_000, 32                          # D has 4.6e9 bytes
+    a, b = some_codes(3, M, K), some_codes(4, N, K)
+    sa, sb = torch.rand(M, device="cuda") + 0.5, (torch.rand(N, device="cuda") + 0.5) / 256
+    d = torch.empty(M, N, dtype=torch.float16, device="cuda")
+    print(f"[int8] D past 4 GiB, tile {tile}", flush=True)
+    gfg.int8_gemm(a, sa, b, sb, d)
+    check_rows(d, a, sa, b, sb, [0, 15_339, 15_340, 30_678, 30_679, M - 1], "f16", "D past 4 GiB")
+
+
+@pytest.mark.parametrize("rows", [3, 300])
+def test_grouped_weights_past_4_gib(rows, tile):
+    G, N, K = 36, 8192, 16384                             # 134 MB an expert, 4.8e9 bytes
+    b = some_codes(5, G, N, K)
+    sb = (torch.rand(G, N, device="cuda") + 0.5) / 8192
+    a, sa = some_codes(6, rows, K), torch.rand(rows, device="cuda") + 0.5
+    print(f"[int8] B past 4 GiB, {rows} rows, tile {tile}", flush=True)
+    for g in (0, 17, G - 1):
+        d = torch.empty(rows, N, dtype=torch.bfloat16, device="cuda")
+        gfg.grouped_int8_gemm_contiguous(a, sa, b, sb, torch.full((rows,), g, dtype=torch.int32, device="cuda"), d)
+        ref = so.int8_product(a[:8].cpu().numpy(), sa[:8].cpu().numpy(), b[g].cpu().numpy(), sb[g].cpu().numpy())
+        check(d[:8], ref, "bf16", np.abs(ref), f"expert {g}")
+        assert torch.equal(d, gfg.int8_gemm(a, sa, b[g], sb[g], torch.empty_like(d)))
+
+
+def test_quantizer_past_4_gib():
+    M, K = 280_001, 8208                                  # x has 4.6e9 bytes
+    x = (some_codes(7, M, K).to(torch.bfloat16) * 0.125)
+    q, s = gfg.int8_quantize_token_device(x)
+    rows = torch.tensor([0, 130_800, 261_632, 261_700, M - 1], device="cuda")
+    ref_q, ref_s = so.quantize_token(x[rows].float().cpu().numpy())
+    assert np.array_equal(q[rows].cpu().numpy(), ref_q) and np.array_equal(s[rows].cpu().numpy(), ref_s)
+
+
+def test_quantizer_many_rows():
+    """More rows than one launch has workgroups for, in both of the quantizer's forms."""
+    for M, K in ((1 << 24) + 9, 16), ((1 << 22) + 3, 2064):
+        x = some_codes(M, M, K).to(torch.float16)
+        q, s = gfg.int8_quantize_token_device(x)
+        rows = torch.tensor([0, 1 << 20, (1 << 22) - 1, 1 << 22, M - 1], device="cuda")
+        ref_q, ref_s = so.quantize_token(x[rows].float().cpu().numpy())
+        assert np.array_equal(q[rows].cpu().numpy(), ref_q) and np.array_equal(s[rows].cpu().numpy(), ref_s)
+        del x, q, s
+        torch.cuda.empty_cache()

@@ -327,3 +327,104 @@ def test_layer_no_tokens():
     x = torch.empty(0, 128, dtype=torch.bfloat16, device="cuda")
     out = call("fp8", x, torch.empty(0, 2, dtype=torch.int32, device="cuda"), torch.empty(0, 2, device="cuda"), ops)
     assert out.shape == (0, 128)
+
+
+# ------------------------------------------------------------------ limits and offsets
+@pytest.mark.parametrize("weight,T,E,k,H,I", [("fp8", 2, 3, 2, 32256, 128), ("int8", 2, 3, 2, 32256, 128), ("fp8", 3, 3, 1, 128, 32256),
+                                              ("int8", 70, 2, 1, 128, 32256), ("fp8", 70, 2, 2, 16512, 128)])
+def test_layer_long_rows(weight, T, E, k, H, I):
+    what = f"{weight} long rows T={T} H={H} I={I}"
+    print(f"[moe] {what}", flush=True)
+    rng = np.random.default_rng(H + I + T)
+    ops, (d1, d2) = make(rng, weight, E, H, I)
+    x = torch.from_numpy(rng.standard_normal((T, H))).to(torch.bfloat16).cuda()
+    ids, w = choose(rng, T, E, k), rng.uniform(0.1, 1.0, (T, k)).astype(np.float32)
+    out = call(weight, x, to_dev(ids), to_dev(w), ops)
+    check_layer(out, so.layer(x.float().cpu().numpy(), ids, w, d1, d2), "bf16", what)
+
+
+@pytest.mark.parametrize("T", [2, 70])
+def test_layer_largest_experts(T):
+    """The longest rows both ways: an expert of 2.08 + 1.04 GB, the second one past 32-bit offsets."""
+    E, k, H, I = 2, 1, 32256, 32256
+    print(f"[moe] largest experts T={T}", flush=True)
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(T)
+
+    def weight(N, K):
+        q = torch.randint(-96, 97, (E, N, K), dtype=torch.int8, device="cuda", generator=gen)
+        return q, (torch.rand(E, N, device="cuda", generator=gen) + 0.5) / (56 * K ** 0.5)
+
+    def times(v, q, s):                                   # v [R, K] . (q s)^T in float64, a few rows of q at a time
+        return torch.cat([v @ (a.double() * b.double()[:, None]).T.contiguous() for a, b in zip(q.split(2016), s.split(2016))], 1)
+
+    (w1, s1), (w2, s2) = weight(2 * I, H), weight(H, I)
+    x = torch.randn(T, H, device="cuda", generator=gen).to(torch.bfloat16)
+    ids = (torch.arange(T, device="cuda") % E).int().view(T, 1)
+    w = torch.rand(T, 1, device="cuda", generator=gen) + 0.1
+    out = call("int8", x, ids, w, (w1, s1, w2, s2))
+    ref = torch.empty(T, H, dtype=torch.float64, device="cuda")
+    for e in range(E):
+        rows = ids[:, 0] == e
+        gu = times(x[rows].double(), w1[e], s1[e])
+        g, u = gu.chunk(2, 1)
+        ref[rows] = w[rows].double() * times(g * torch.sigmoid(g) * u, w2[e], s2[e])
+    check_layer(out, ref.cpu().numpy(), "bf16", f"largest experts T={T}")
+
+
+def test_layer_on_two_streams_at_once():
+    rng = np.random.default_rng(41)
+    E, k, H, I = 24, 4, 1024, 512
+    ops, (d1, d2) = make(rng, "fp8", E, H, I)
+    work = []
+    for T in (40, 3):
+        x = torch.from_numpy(rng.standard_normal((T, H))).to(torch.bfloat16).cuda()
+        ids, w = choose(rng, T, E, k), rng.uniform(0.1, 1.0, (T, k)).astype(np.float32)
+        ws = torch.empty(gfg.moe_layer_workspace_bytes(T, k, H, I), dtype=torch.uint8, device="cuda")
+        work.append((x, to_dev(ids), to_dev(w), ws, torch.zeros(8, T, H, dtype=torch.bfloat16, device="cuda"),
+                     so.layer(x.float().cpu().numpy(), ids, w, d1, d2), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for i in range(8):
+        for x, ids, w, ws, outs, _, s in work:
+            call("fp8", x, ids, w, ops, out=outs[i], workspace=ws, stream=s)
+    torch.cuda.synchronize()
+    for x, _, _, _, outs, ref, _ in work:
+        check_layer(outs[0], ref, "bf16", f"two streams T={x.shape[0]}")
+        assert all(torch.equal(outs[0], o) for o in outs)
+
+
+def test_calls_refuse_tensors_that_do_not_fit():
+    T, E, k, H, I = 2, 4, 2, 256, 128
+    ops, _ = make(np.random.default_rng(5), "fp8", E, H, I)
+    x, out = (torch.zeros(T, H, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    ids, w = torch.zeros(T, k, dtype=torch.int32, device="cuda"), torch.zeros(T, k, device="cuda")
+    wide = torch.zeros(T, 2 * H, dtype=torch.bfloat16, device="cuda")
+    for bad in (dict(x=wide[:, ::2]), dict(x=x.float()), dict(x=x[:1]), dict(ids=ids.long()), dict(ids=ids[:, :1].expand(T, k)),
+                dict(w=w.half()), dict(w=w[:, :1]), dict(out=out.half()), dict(out=out.cpu()), dict(w=w.cpu())):
+        a = dict(x=x, ids=ids, w=w, out=out) | bad
+        with pytest.raises((TypeError, ValueError)):
+            gfg.moe_fp8_layer(a["x"], a["ids"], a["w"], *ops, a["out"])
+    with pytest.raises(ValueError):
+        gfg.moe_fp8_layer(x, ids, w, ops[0], ops[1][:, :1], ops[2], ops[3], out)
+    with pytest.raises(TypeError):
+        gfg.moe_fp8_layer(x, ids, w, *ops, out, workspace=torch.empty(1 << 20, device="cuda"))
+    with pytest.raises(Exception, match="workspace"):
+        gfg.moe_fp8_layer(x, ids, w, *ops, out, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(ValueError):
+        gfg.moe_topk(torch.zeros(T, E, device="cuda"), ids, w, score="softplus")
+    with pytest.raises(ValueError):
+        gfg.moe_topk(torch.zeros(E, T, device="cuda").T, ids, w)
+
+
+def test_topk_many_tokens():
+    """More tokens than one launch has workgroups for; the last ones count."""
+    T, E, k = (1 << 22) + 5, 8, 2
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(8)
+    logits = torch.randn(T, E, device="cuda", generator=gen)
+    ids = torch.full((T, k), -7, dtype=torch.int32, device="cuda")
+    w = torch.full((T, k), -7.0, device="cuda")
+    gfg.moe_topk(logits, ids, w)
+    top, idx = logits.topk(k, dim=1)
+    assert torch.equal(ids, idx.int())
+    assert torch.allclose(w, torch.softmax(top, 1), atol=1e-6, rtol=0)

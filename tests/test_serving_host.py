@@ -108,7 +108,7 @@ LAYER = dict(x=P, dt=0, ids=P, w=P, w1=P, s1=P, w2=P, s2=P, out=P, T=2, k=3, E=4
 @pytest.mark.parametrize("change,code", [
     (dict(dt=2), EINVAL), (dict(T=-1), EINVAL), (dict(k=0), EINVAL), (dict(E=0), EINVAL), (dict(H=0), EINVAL), (dict(I=-128), EINVAL),
     (dict(E=1025), EUNSUPPORTED), (dict(T=342), EUNSUPPORTED), (dict(T=1 << 40, k=1 << 40), EUNSUPPORTED), (dict(H=192), EUNSUPPORTED),
-    (dict(I=64), EUNSUPPORTED), (dict(H=65664), EUNSUPPORTED), (dict(x=None), EINVAL), (dict(ids=None), EINVAL), (dict(w=None), EINVAL),
+    (dict(I=64), EUNSUPPORTED), (dict(H=65664), EUNSUPPORTED), (dict(H=32384), EUNSUPPORTED), (dict(I=32384), EUNSUPPORTED), (dict(x=None), EINVAL), (dict(ids=None), EINVAL), (dict(w=None), EINVAL),
     (dict(w1=None), EINVAL), (dict(s1=None), EINVAL), (dict(w2=None), EINVAL), (dict(s2=None), EINVAL), (dict(out=None), EINVAL),
     (dict(x=P + 8), EINVAL), (dict(w1=P + 8), EINVAL), (dict(out=P + 2), EINVAL), (dict(ids=P + 2), EINVAL), (dict(ws=None), EINVAL),
     (dict(ws=P + 4), EINVAL), (dict(bytes=2 * 3 * 384 * 4 - 1), EINVAL),
