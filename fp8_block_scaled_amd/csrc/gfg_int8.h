@@ -23,15 +23,14 @@ struct I8Params {
     void* d;                 // [rows][N] (masked: [G][rows][N])
     int64_t rows;            // masked: rows per group
     int N, K, G;
-    int m_tiles;             // candidate row tiles of the kernel's tile height, over all groups
-    int tiles_per_group;     // masked: candidates per group
+    int m_tiles;             // row tiles of the kernel's tile height, over all groups (the 256 x 256 kernel: of 128 rows)
+    int tiles_per_group;     // masked: row tiles per group (not the 256 x 256 kernel)
     int group_m, num_xcd;    // tile order of the 256 x 256 kernel
 };
 
-// The 256 x 256-tile kernel (gfg_int8_gemm256.hip).  m_tiles: 128-row
-// candidates for the contiguous layout, 256-row ones for the others.  The
-// caller has checked: N at most 2^22, and for the grouped layouts at most 4096
-// candidates.
+// The 256 x 256-tile kernel (gfg_int8_gemm256.hip).  The caller has
+// checked: N at most 2^22, and for the grouped layouts at most 4096 tiles of
+// 128 rows.
 int launch_int8_256(const I8Params& p, int layout, int out_dtype, hipStream_t s);
 
 }  // namespace gfg

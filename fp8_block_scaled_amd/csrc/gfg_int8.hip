@@ -167,9 +167,9 @@ constexpr uint32_t kOutside = 0x80000000u;     // past every buffer window used 
 
 // One output element row piece: columns n .. n+3 of a row, from the integer sums.
 template <typename OutT>
-__device__ __forceinline__ void store4(OutT* row, int n, int N, bool vec, const float (&v)[4]) {
-    typedef OutT o4 __attribute__((ext_vector_type(4)));
-    if (vec && n + 4 <= N) {
+__device__ __forceinline__ void store4(OutT* row, int n, int N, const float (&v)[4]) {
+    typedef OutT o4 __attribute__((ext_vector_type(4), aligned(2)));      // (rows start anywhere where N is odd)
+    if (n + 4 <= N) {
         *reinterpret_cast<o4*>(row + n) = o4{OutT(v[0]), OutT(v[1]), OutT(v[2]), OutT(v[3])};
     } else {
 #pragma unroll
@@ -285,7 +285,6 @@ __global__ __launch_bounds__(WM * WN * 64) void int8_gemm_kernel(I8Params p) {
     GFG_WAITCNT(0, 15);                            // the last loads land before the workgroup ends
 
     // acc[y][c] of lane (l16, lq): row 16 y + l16, columns 16 c + 4 lq .. +3
-    const bool vec = (p.N & 3) == 0;
     OutT* const d = static_cast<OutT*>(p.d);
 #pragma unroll
     for (int y = 0; y < RB; ++y) {
@@ -305,7 +304,7 @@ __global__ __launch_bounds__(WM * WN * 64) void int8_gemm_kernel(I8Params p) {
                 v[i] = fmaf(float(acc[y][c][i]) * sa, p.b_scale[int64_t(g) * p.N + nn],
                             LAYOUT == DENSE && p.bias ? p.bias[nn] : -0.0f);
             }
-            store4(d + (arow + r) * p.N, n, p.N, vec, v);
+            store4(d + (arow + r) * p.N, n, p.N, v);
         }
     }
 }
@@ -427,7 +426,6 @@ __global__ __launch_bounds__(NW * 64) void int8_stream_kernel(I8Params p) {
 #pragma unroll
         for (int c = 0; c < CB; ++c) sums(wave, y * CB + c) = acc[y][c];
     __syncthreads();
-    const bool vec = (p.N & 3) == 0;
     OutT* const d = static_cast<OutT*>(p.d);
 #pragma unroll
     for (int i0 = 0; i0 < RB * CB; i0 += NW) {
@@ -447,7 +445,7 @@ __global__ __launch_bounds__(NW * 64) void int8_stream_kernel(I8Params p) {
             const int nn = min(n + q, p.N - 1);
             v[q] = fmaf(float(v4[q]) * sa, p.b_scale[int64_t(g) * p.N + nn], LAYOUT == DENSE && p.bias ? p.bias[nn] : -0.0f);
         }
-        store4(d + (arow + r) * p.N, n, p.N, vec, v);
+        store4(d + (arow + r) * p.N, n, p.N, v);
     }
 }
 
@@ -616,7 +614,7 @@ __global__ __launch_bounds__(256) void int8_few_kernel(const X* __restrict__ xs,
         const int nn = min(n + i, p.N - 1);
         v[i] = fmaf(float(total[i]) * scale, p.b_scale[nn], p.bias ? p.bias[nn] : -0.0f);
     }
-    store4(static_cast<OutT*>(p.d) + int64_t(l16) * p.N, n, p.N, (p.N & 3) == 0, v);
+    store4(static_cast<OutT*>(p.d) + int64_t(l16) * p.N, n, p.N, v);
 }
 
 template <typename X>
@@ -655,23 +653,24 @@ int launch_small(const I8Params& p, int out_dtype, hipStream_t s) {
     return launch_stream<LAYOUT, 4, 4, 4, 2>(p, out_dtype, s);
 }
 
-// Launch the product on the tile that suits it: 256 x 256 from 7/16 as many
-// such tiles as CUs on (1024 x 7168 x 2304, 112 tiles: 31.5 us, 35.2 on 128 x
-// 128; 2048 x 4096 x 4096, 128 tiles: 48.6, 50.7; but 2048^3, 64 tiles: 26.8,
-// 16.0).  `p` holds everything but the tile counts.
+// Launch the product on the tile that suits it: the 256 x 256 kernel (whose
+// tiles have 192 rows where that fills the CUs better) wherever tiles of
+// 128 x 128 would need a second round over the CUs.  Measured, us, the 256
+// kernel and the smaller tiles: 768 x 7168 x 2304 (336 tiles of 128 x 128) 25.7,
+// 28.3; 700 x 6144 x 4096 (288) 37.5, 40.7; 2048 x 2104 x 1024 (272) 17.1, 18.5;
+// but 1024 x 4096 x 4096 (256) 37.4, 22.3; 1920 x 2048 x 7168 (240) 61.6, 35.2.
+// `p` holds everything but the tile counts.
 int launch_i8(const char* fn, I8Params p, int layout, int out_dtype, hipStream_t s) {
     const int groups = layout == MASKED ? p.G : 1;
-    const int64_t t128 = (p.rows + 127) / 128 * groups, t256 = (p.rows + 255) / 256 * groups;
-    const int64_t n256 = (int64_t(p.N) + 255) / 256;
+    const int64_t t128 = (p.rows + 127) / 128 * groups, n128 = (int64_t(p.N) + 127) / 128;
     const bool fits = p.N <= 1 << 22;
     const int choice = tile_shape_choice();
     if (choice == GFG_TILE_256x256 && !fits)
         return fail(GFG_EUNSUPPORTED, "%s: the 256 x 256 tile needs N=%d at most 2^22", fn, p.N);
     int cus = 0;
     if (int rc = device_cus(&cus)) return rc;
-    if (choice == GFG_TILE_256x256 || (choice == GFG_TILE_AUTO && fits && t256 * n256 * 16 >= cus * 7)) {
-        p.m_tiles = int(layout == CONTIG ? t128 : t256);
-        p.tiles_per_group = int(t256 / groups);
+    if (choice == GFG_TILE_256x256 || (choice == GFG_TILE_AUTO && fits && t128 * n128 > cus)) {
+        p.m_tiles = int(t128);                 // (read for the contiguous layout: the 128-row candidates)
         return launch_int8_256(p, layout, out_dtype, s);
     }
     if (layout == DENSE) return launch_small<DENSE>(p, out_dtype, s);

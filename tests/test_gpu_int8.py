@@ -295,6 +295,46 @@ def test_graph_replays_match_eager():
         assert torch.equal(d, want[0]) and torch.equal(one, want[1]), f"replay {r}"
 
 
+# ------------------------------------------------------------------ rows of the large tile
+@pytest.fixture
+def eight_workgroups():
+    """Eight workgroups on the large tile: a few tiles are several rounds, which decide the tile's rows."""
+    gfg.set_tile_shape(gfg.TILE_256x256)
+    gfg.set_grid_limit(8)
+    yield
+    gfg.set_grid_limit(0)
+    gfg.set_tile_shape(gfg.TILE_AUTO)
+
+
+# 8 tiles of 256 rows are one round where 16 of 192 are two; 8 of 192 (rows up to 192) are as good as 8 of 256
+@pytest.mark.parametrize("M,N,K", [(256, 2048, 272), (255, 2047, 272), (193, 2042, 400), (192, 2048, 400), (160, 1999, 144),
+                                   (97, 1030, 2064), (700, 1500, 656), (510, 1028, 144), (576, 769, 1296)])
+def test_dense_rows_of_the_large_tile(M, N, K, eight_workgroups):
+    rng = np.random.default_rng(M + N + K)
+    a, b, sa, sb = codes(rng, (M, K)), codes(rng, (N, K)), scales(rng, M, 1), scales(rng, N, K)
+    bias = rng.standard_normal(N).astype(np.float32)
+    flat = torch.full((M * N + 128,), SENTINEL, dtype=torch.float16, device="cuda")
+    d = flat[64:64 + M * N].view(M, N)
+    gfg.int8_gemm(to_dev(a), to_dev(sa), to_dev(b), to_dev(sb), d, bias=to_dev(bias))
+    prod = so.int8_product(a, sa, b, sb)
+    check(d, prod + bias, "f16", np.abs(prod) + np.abs(bias), f"rows of the large tile {M} {N} {K}")
+    assert np.all(bits(torch.cat([flat[:64], flat[-64:]])) == sentinel_bits("f16"))
+
+
+@pytest.mark.parametrize("masked_m,Mmax,N,K", [([256, 0, 256], 256, 1024, 272), ([192, 10, 0, 150], 400, 517, 400), ([600, 1, 193], 600, 770, 144),
+                                               ([0, 0], 300, 256, 128), ([256] * 5, 256, 1000, 528), ([383, 385, 384], 385, 511, 272)])
+def test_masked_rows_of_the_large_tile(masked_m, Mmax, N, K, eight_workgroups):
+    rng = np.random.default_rng(sum(masked_m) + N + K)
+    G = len(masked_m)
+    a, b, sa, sb = codes(rng, (G, Mmax, K)), codes(rng, (G, N, K)), scales(rng, (G, Mmax), 1), scales(rng, (G, N), K)
+    d = torch.full((G, Mmax, N), SENTINEL, dtype=torch.bfloat16, device="cuda")
+    gfg.grouped_int8_gemm_masked(to_dev(a), to_dev(sa), to_dev(b), to_dev(sb), torch.tensor(masked_m, dtype=torch.int32, device="cuda"), d)
+    for g, m in enumerate(masked_m):
+        ref = so.int8_product(a[g, :m], sa[g, :m], b[g], sb[g])
+        check(d[g, :m], ref, "bf16", np.abs(ref), f"masked rows of the large tile {g} {m}")
+        assert np.all(bits(d[g, m:]) == sentinel_bits("bf16"))
+
+
 # ------------------------------------------------------------------ offsets past 32 bits
 def some_codes(seed, *shape):
     gen = torch.Generator(device="cuda")
