@@ -26,12 +26,14 @@ typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
 // ------------------------------------------------------------------ token quantizer
 //
 // One pass over memory: a row's 16-byte chunks stay in registers between the
-// maximum and the encoding (rows longer than kHeld chunks a lane read the rest
-// again, from the cache).  LPR lanes share a row: a wave for short rows, a
-// workgroup for long ones, whose maximum then crosses the waves through LDS.
-constexpr int QT = 256;
-constexpr int kHeld = 4;
-
+// maximum and the encoding, HELD a lane (longer rows read the rest again, from
+// the cache).  LPR lanes share a row: a wave up to 2048 elements, two waves up
+// to 3 * 1024, four past that; with more than one, the maximum crosses the waves
+// through LDS.  Bound by the copy rate (5.0 TB/s).  Measured, bf16, us and TB/s
+// of reads and writes: 32768 x 2048 41, 4.9; 8192 x 7168 35.5, 5.0; 4096 x 16384
+// 41.3, 4.9 (with half of the row held: 44.7; f32 70.4 and 80.1); 32768 x 2304
+// 48.3, 4.7 on two waves, 55.4 on four, whose second pass has few lanes; f32
+// 16384 x 3584 53.9 on two, 49.7 on four.
 template <typename T> struct Chunk;            // 8 elements of a row
 template <> struct Chunk<__bf16> {
     u32x4 w;
@@ -90,24 +92,24 @@ __device__ __forceinline__ void row_scale(uint32_t ab, float* scale, float* r) {
     }
 }
 
-template <typename T, int LPR>
-__global__ __launch_bounds__(QT) void quant_token_kernel(const T* __restrict__ x, uint8_t* __restrict__ q,
+template <typename T, int LPR, int HELD>
+__global__ __launch_bounds__(LPR == 64 ? 256 : LPR) void quant_token_kernel(const T* __restrict__ x, uint8_t* __restrict__ q,
                                                          float* __restrict__ scale, int64_t M, int K) {
-    constexpr int RPB = QT / LPR;              // rows per workgroup
-    __shared__ uint32_t part[2][QT / 64];      // in turn: a row's maxima are read while the next row's are written
+    constexpr int RPB = LPR == 64 ? 4 : 1;      // rows per workgroup
+    __shared__ uint32_t part[2][LPR / 64];     // in turn: a row's maxima are read while the next row's are written
     const int lane = threadIdx.x % LPR, chunks = K / 8;
     int turn = 0;
     for (int64_t m = int64_t(blockIdx.x) * RPB + threadIdx.x / LPR; m < M; m += int64_t(gridDim.x) * RPB, turn ^= 1) {
         const T* row = x + m * K;
-        Chunk<T> held[kHeld];
+        Chunk<T> held[HELD];
         uint32_t ab = 0;
 #pragma unroll
-        for (int j = 0; j < kHeld; ++j)
+        for (int j = 0; j < HELD; ++j)
             if (lane + j * LPR < chunks) held[j].load(row + (lane + j * LPR) * 8);
 #pragma unroll
-        for (int j = 0; j < kHeld; ++j)
+        for (int j = 0; j < HELD; ++j)
             if (lane + j * LPR < chunks) ab = max(ab, chunk_amax(held[j]));
-        for (int c = lane + kHeld * LPR; c < chunks; c += LPR) {
+        for (int c = lane + HELD * LPR; c < chunks; c += LPR) {
             Chunk<T> t;
             t.load(row + c * 8);
             ab = max(ab, chunk_amax(t));
@@ -118,7 +120,7 @@ __global__ __launch_bounds__(QT) void quant_token_kernel(const T* __restrict__ x
             if ((threadIdx.x & 63) == 0) part[turn][threadIdx.x >> 6] = ab;
             __syncthreads();
 #pragma unroll
-            for (int w = 0; w < QT / 64; ++w) ab = max(ab, part[turn][w]);
+            for (int w = 0; w < LPR / 64; ++w) ab = max(ab, part[turn][w]);
         }
         float s, r;
         row_scale(ab, &s, &r);
@@ -126,10 +128,10 @@ __global__ __launch_bounds__(QT) void quant_token_kernel(const T* __restrict__ x
         uint8_t* out = q + m * K;
         const bool bad = r == 0.0f;            // 0 * infinity would be NaN
 #pragma unroll
-        for (int j = 0; j < kHeld; ++j)
+        for (int j = 0; j < HELD; ++j)
             if (lane + j * LPR < chunks)
                 *reinterpret_cast<u32x2*>(out + (lane + j * LPR) * 8) = bad ? u32x2{0u, 0u} : chunk_encode(held[j], r);
-        for (int c = lane + kHeld * LPR; c < chunks; c += LPR) {
+        for (int c = lane + HELD * LPR; c < chunks; c += LPR) {
             Chunk<T> t;
             t.load(row + c * 8);
             *reinterpret_cast<u32x2*>(out + c * 8) = bad ? u32x2{0u, 0u} : chunk_encode(t, r);
@@ -137,16 +139,21 @@ __global__ __launch_bounds__(QT) void quant_token_kernel(const T* __restrict__ x
     }
 }
 
+template <typename T, int LPR, int HELD>
+void launch_quant_rows(const void* x, uint8_t* q, float* scale, int64_t M, int K, hipStream_t s) {
+    constexpr int64_t most = 1 << 22;          // workgroups; each walks on where there are more rows
+    constexpr int threads = LPR == 64 ? 256 : LPR;
+    const int64_t wgs = (M * LPR + threads - 1) / threads;
+    hipLaunchKernelGGL((quant_token_kernel<T, LPR, HELD>), dim3(unsigned(wgs < most ? wgs : most)), dim3(threads), 0, s,
+                       static_cast<const T*>(x), q, scale, M, K);
+}
+
 template <typename T>
 void launch_quant(const void* x, uint8_t* q, float* scale, int64_t M, int K, hipStream_t s) {
-    // a wave for rows that it holds in registers (2048 elements), else a workgroup
-    constexpr int64_t most = 1 << 22;          // workgroups; each walks on where there are more rows
-    const int64_t wgs = K <= 64 * 8 * kHeld ? (M + 3) / 4 : M;
-    const dim3 grid(unsigned(wgs < most ? wgs : most));
-    if (K <= 64 * 8 * kHeld)
-        hipLaunchKernelGGL((quant_token_kernel<T, 64>), grid, dim3(QT), 0, s, static_cast<const T*>(x), q, scale, M, K);
-    else
-        hipLaunchKernelGGL((quant_token_kernel<T, QT>), grid, dim3(QT), 0, s, static_cast<const T*>(x), q, scale, M, K);
+    if (K <= 64 * 8 * 4) launch_quant_rows<T, 64, 4>(x, q, scale, M, K, s);
+    else if (K <= 128 * 8 * 3) launch_quant_rows<T, 128, 3>(x, q, scale, M, K, s);
+    else if (K <= 256 * 8 * 4) launch_quant_rows<T, 256, 4>(x, q, scale, M, K, s);
+    else launch_quant_rows<T, 256, 8>(x, q, scale, M, K, s);
 }
 
 // ------------------------------------------------------------------ tiled product
@@ -157,9 +164,10 @@ void launch_quant(const void* x, uint8_t* q, float* scale, int64_t M, int K, hip
 // every wave finish the previous step, whose buffer the new loads go to).
 // These are the launches with too few 256 x 256 tiles, whose time is the
 // latency of a tile's first loads plus a chain of steps, so depth matters
-// more than the bytes per step.  LDS row R (128 bytes) holds its 16-byte chunks
-// XOR-swizzled by R & 7, so that the 16 rows that a fragment read touches
-// spread over all banks.  Rows past the operand's end and chunks past K lie
+// more than the bytes per step (1024 x 4096 x 4096: 37.9 us with one stage ahead,
+// 22.5 with three; 512 x 4096 x 4096 on 64 x 64: 34, 21).  LDS row R (128 bytes)
+// holds its 16-byte chunks XOR-swizzled by R & 7, so that the 16 rows that a
+// fragment read touches spread over all banks.  Rows past the operand's end and chunks past K lie
 // outside the buffer window, where the hardware returns zeros, so no size
 // needs its own path: zeros add nothing to an integer sum.
 constexpr int TK = 128;
@@ -318,7 +326,10 @@ __global__ __launch_bounds__(WM * WN * 64) void int8_gemm_kernel(I8Params p) {
 // once; the waves' sums meet in LDS at the end (integers: exact in any order).
 // (Loading the fragments straight into registers instead is slower: a
 // fragment's adjacent lanes are adjacent rows, so four lanes touch four cache
-// lines, and the load path then passes 16 bytes a cycle, not 64.)
+// lines, and the load path then passes 16 bytes a cycle, not 64: 1 x 7168 x 2304
+// took 13.7 us that way, 5.9 this way.)  Bound by the launch and the way of the
+// first loads, then by what a CU takes in, about 37 GB/s: 128 x 4096 x 4096 in 10.0
+// us.
 template <int LAYOUT, int RB, int CB, int NW, int D, typename OutT>
 __global__ __launch_bounds__(NW * 64) void int8_stream_kernel(I8Params p) {
     constexpr int TM = 16 * RB, TN = 16 * CB;
@@ -488,7 +499,9 @@ int launch_ring(I8Params p, int out_dtype, hipStream_t s) {
 // At most kFewTokens rows of x in 16 or 32 bits: every workgroup quantizes them
 // itself, into LDS, while its first weights are on the way (the codes and
 // scales are those of the token quantizer, bit for bit), then streams its 32
-// weight rows like the kernel above.  One launch instead of two.
+// weight rows like the kernel above.  One launch instead of two: 7168 x 2304 with
+// cold weights (16.5 MB), 1 token 7.3 us, 10.2 in two launches; 4 tokens 9.8, 10.5
+// (every workgroup encodes all rows, so more of them would gain nothing).
 constexpr int kFewTokens = 4;
 constexpr int kFewCodes = 32 * 1024;           // bytes of LDS for the codes
 

@@ -15,7 +15,12 @@
 // widened in registers (exactly: E4M3 and int8 fit bf16 and f16), and the
 // products run on 16x16x32 MFMAs whose 16 rows are weight rows and whose 16
 // columns are tokens.  Two launches: the experts' hidden rows, and the
-// weighted sum of their down projections.
+// weighted sum of their down projections; where the experts' items are shared
+// out over the CUs (shared_down), that sum is a launch of its own.  Measured, us
+// up / down (/ sum): one token, k = 9, E = 385, H = 7168, I = 512, FP8: 18.5 /
+// 12 (99 MB); 32 tokens of it: 250 / 134 (2.25 GB, 5.6 TB/s); 100 tokens, k = 2,
+// E = 8, H = 4096, I = 1792, FP8: 34 / 19 / 4 (178 MB); 5 tokens, k = 6, E = 64,
+// H = 2048, I = 1408, int8: 32 / 20 / 4 (216 MB).
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -61,7 +66,11 @@ __device__ __forceinline__ int wave_min(int v) { return wave_reduce(v, [](int a,
 
 // One wave a token; lane l holds experts l, l + 64, ... (EPL of them).  A round
 // takes the largest remaining selection value and, among its holders, the
-// lowest index; lane j keeps the result of round j.
+// lowest index; lane j keeps the result of round j.  The rounds are a chain of
+// wave reductions, which stay in registers (DPP rotations; through LDS they cost
+// twice as much): 3.8 us for one token of 256 experts, k = 8, of which 2.5 are the
+// launch; 8.3 us for 4096 tokens of 385 in fp32, k = 9 (6.6 MB: 0.8 TB/s), bound
+// by those chains.
 template <typename T, int EPL>
 __device__ __forceinline__ void topk_row(const T* __restrict__ row, const float* __restrict__ bias, int32_t* __restrict__ ids,
                                          float* __restrict__ weights, int lane, int E, int k, bool sigmoid, bool renorm,
@@ -405,11 +414,13 @@ __device__ __forceinline__ Unit unit_of(const GFG_LDS Routing* r, int u) {
 // and across the ends of experts and tiles; no barrier stands between a load
 // and its MFMAs.  Whole 128-byte lines by adjacent lanes: loaded straight into
 // MFMA fragments, adjacent lanes are adjacent rows, and a load takes four times
-// as long.  A CU passes one such load (1 KB, full or not) about every 48
-// cycles, and that, with 256 CUs HBM's rate, bounds the kernels, so what goes
-// beside the weights is kept to few loads: the tokens' (hidden) rows stay in
-// LDS for the whole launch where they are small, else the stage holds only as
-// many of them as units have; an expert's scales come once for a unit.
+// as long.  What bounds the kernels: HBM, 5.0-5.6 TB/s where the launch is long
+// (32 tokens, k = 9, E = 385, H = 7168, I = 512: 2.25 GB in 400 us), and for
+// short ones what a CU takes in, about 37 GB/s, after some 5 us of launch,
+// routing and the first loads' way (an up launch of 16 items takes 7.5 us).  So
+// what goes beside the weights is kept small: the tokens' rows stay in LDS for
+// the whole launch where they are small, else the stage holds only as many of
+// them as units have; an expert's scales come once for a unit.
 //
 // The fragments are read from LDS in inline assembly, each group together with
 // its wait: the stage index is a run-time value, so the compiler, which cannot
@@ -739,7 +750,9 @@ __device__ __forceinline__ void up_items(const MoeParams& p, const GFG_LDS Routi
 // that gate and up meet in a wave.  DOWN: 128 rows of W2; sums go to y.
 // Units of 64 rows where that saves a round of items over the workgroups: a few
 // experts with slightly more than 32 rows would otherwise cost a second pass
-// over their weights.  (Smaller stages leave room for one more of them.)
+// over their weights (100 tokens, k = 2, E = 8, H = 4096, I = 1792: 64 us a layer,
+// 70 with units of 32 alone; 130 tokens: 64, 92).  (Smaller stages leave room for
+// one more of them.)  Units of 8, two MFMA halves in one, measured no faster.
 __device__ __forceinline__ int shared_rows(const int (&total)[6], int tiles) {
     const int grid = int(gridDim.x);
     return (total[5] * tiles + grid - 1) / grid < (total[4] * tiles + grid - 1) / grid ? 64 : 32;
@@ -763,7 +776,8 @@ __device__ __forceinline__ void shared_items(const MoeParams& p, const GFG_LDS R
     const uint8_t* const weights = UP ? p.w1 : p.w2;
     const auto rx = UP ? make_rsrc(p.x, uint32_t(p.T) * uint32_t(p.H) * 2u) : make_rsrc(p.h, uint32_t(p.T * p.k) * 4u * uint32_t(p.I));
     uint32_t shift;
-    const auto rs = scale_rsrc(UP ? p.s1 : p.s2, W == FP8 ? uint32_t(p.E) * uint32_t(N / 128) * uint32_t(KB) : uint32_t(p.E) * uint32_t(N) * 4u, &shift);
+    const auto rs = scale_rsrc(UP ? p.s1 : p.s2,
+                               W == FP8 ? uint32_t(p.E) * uint32_t(N / 128) * uint32_t(KB) : uint32_t(p.E) * uint32_t(N) * 4u, &shift);
     // (UP: blocks it / 2 of the gate and of the up half; DOWN: block it)
     auto scale_row = [&](int e, int it, int f) {
         return uint32_t(e * (N / 128) + (UP ? it / 2 + f * (p.I / 128) : it)) * uint32_t(KB) + shift;
@@ -940,8 +954,11 @@ __global__ __launch_bounds__(kWaves * 64) void moe_up_kernel(MoeParams p) {
     GFG_LDS uint8_t* const rows_mem = ring + kWaves * p.ring;
     if constexpr (RES) {
         load_resident(rows_mem, make_rsrc(p.x, uint32_t(p.T) * uint32_t(p.H) * 2u), p.H * 2, p.resident);
-        const int rows = build_routing(r, ring, p.ids, p.T * p.k, p.E, [&](const int (&total)[6]) { return choose_rows<4, 8>(total, 4, 0, p.ring); });
-        // items of 8 columns where they spread better over the workgroups
+        const int rows = build_routing(r, ring, p.ids, p.T * p.k, p.E,
+                                       [&](const int (&total)[6]) { return choose_rows<4, 8>(total, 4, 0, p.ring); });
+        // items of 8 columns where they spread better over the workgroups (one
+        // token, k = 9, I = 512: 288 items of 16 or 576 of 8 over 256: the layer
+        // takes 34.2 us with 8, 35.4 with 16)
         const int n = __builtin_amdgcn_readfirstlane(r->units) * (p.I / 16), grid = int(gridDim.x);
         const int walk16 = (n + grid - 1) / grid * 2, walk8 = (2 * n + grid - 1) / grid;
         if (walk8 * 8 < walk16 * 7) {
@@ -954,8 +971,11 @@ __global__ __launch_bounds__(kWaves * 64) void moe_up_kernel(MoeParams p) {
     } else {
         const int rows = build_routing(r, ring, p.ids, p.T * p.k, p.E, [&](const int (&total)[6]) {
             const int few = choose_rows<4, 16>(total, 4, 1, p.ring), rows = shared_rows(total, p.I / 64);
-            // loads a block of K for 16 columns: streamed, and shared; the
-            // latter's coarser items have to fill the launch too
+            // KB a block of K for 16 columns: streamed, and shared; the latter's
+            // coarser items have to fill the launch too.  Measured, us a layer,
+            // shared and streamed: 100 tokens, k = 2, E = 8, H = 4096, I = 1792: 64,
+            // 75; 130 tokens: 64, 86; but 48 tokens with one or two rows an expert,
+            // H = 4096, I = 1024: 106, 96.
             const int units = total[rows == 32 ? 4 : 5];
             const int streamed = total[few == 4 ? 1 : few == 8 ? 2 : 3] * (4 + few / 4), shared = units * 6;
             return shared * 10 < streamed * 9 && units * (p.I / 64) * 4 >= int(gridDim.x) * 3 ? rows : few;
@@ -1140,10 +1160,14 @@ __global__ __launch_bounds__(kWaves * 64) void moe_down_kernel(MoeParams p) {
     }
     const int rows = build_routing(r, ring, p.ids, P, p.E, [&](const int (&total)[6]) { return choose_rows<2, 8>(total, 2 * RT, 2, p.ring); });
     const int units = __builtin_amdgcn_readfirstlane(r->units), KB = p.I / 128;
-    // the waves that share a unit: the split with the shortest longest walk
-    int ks = 1, best = (units + kWaves - 1) / kWaves * KB;
+    // the waves that share a unit: the split with the shortest longest walk, in
+    // blocks of I; entering a unit costs about three.  Measured, us a layer of one
+    // token, H = 7168: k = 9, I = 512: 31.8 unsplit, 34.0 split; k = 2, I = 2048:
+    // 27.4 unsplit, 25.0 split.
+    constexpr int kEnter = 3;
+    int ks = 1, best = (units + kWaves - 1) / kWaves * (KB + kEnter);
     for (int c = 2; c <= p.ks_most; c *= 2) {
-        const int walk = (units * c + kWaves - 1) / kWaves * ((KB + c - 1) / c);
+        const int walk = (units * c + kWaves - 1) / kWaves * ((KB + c - 1) / c + kEnter);
         if (walk < best) {
             best = walk;
             ks = c;
@@ -1177,6 +1201,7 @@ __global__ __launch_bounds__(kWaves * 64) void moe_down_kernel(MoeParams p) {
 }
 
 // The down projection by shared items, and the sums over a token's pairs.
+// (A round of 256 items, 128 x 1408 each, takes 10.5 us: 4.4 TB/s of weights.)
 template <int W>
 __global__ __launch_bounds__(kWaves * 64) void moe_down_shared_kernel(MoeParams p) {
     __shared__ Routing routing;
@@ -1241,7 +1266,9 @@ int launch_layer(MoeParams p, hipStream_t s) {
     const int P = p.T * p.k;
     const dim3 block(kWaves * 64);
     // one workgroup a CU: what its LDS has left after the fixed parts and the
-    // resident rows goes to the rings
+    // resident rows goes to the rings.  (One token, H = 7168, 14 KB of rows: 34.2 us
+    // a layer, 35.7 with the rows in the stages; 12 tokens, H = 2048, 48 KB: 93.6 and
+    // 94.4, no more than the boxes differ, so larger rows leave the LDS to the rings.)
     const int64_t up_items = (int64_t(P < p.E ? P : p.E) + P / 4) * (p.I / 8);
     const int up_grid = int(up_items < cus ? up_items : cus);
     const int x_bytes = p.T * p.H * 2;
@@ -1250,6 +1277,9 @@ int launch_layer(MoeParams p, hipStream_t s) {
     const unsigned up_lds = unsigned(kWaves * p.ring + p.resident);
     if (p.resident) hipLaunchKernelGGL((moe_up_kernel<W, A, true>), dim3(up_grid), block, up_lds, s, p);
     else hipLaunchKernelGGL((moe_up_kernel<W, A, false>), dim3(up_grid), block, up_lds, s, p);
+    // 32 columns a workgroup of the down projection (one token, H = 7168, I = 512, 224
+    // tiles: 34.2 us a layer, 39.4 with 448 tiles of 16) where they fill three quarters
+    // of the CUs and the sums stay small
     const int rt = p.H % 32 == 0 && p.H / 32 >= cus * 3 / 4 && P * 128 <= 40 * 1024 ? 2 : 1;
     if (shared_down(p, cus, rt)) {
         const int items = ((P < p.E ? P : p.E) + P / 32) * (p.H / 128);
@@ -1259,7 +1289,6 @@ int launch_layer(MoeParams p, hipStream_t s) {
         if (e != hipSuccess) return fail(GFG_EHIP, "kernel launch failed: %s", hipGetErrorString(e));
         return GFG_OK;
     }
-    // 32 columns a workgroup where they fill three quarters of the CUs and the sums stay small
     while (p.ks_most < kWaves && p.ks_most * 2 <= p.I / 128 && p.ks_most * 2 * P * 64 * rt <= 24 * 1024) p.ks_most *= 2;
     const int y_bytes = p.ks_most * P * 64 * rt;
     const int tiles = p.H / (16 * rt), down_grid = tiles < cus ? tiles : cus;

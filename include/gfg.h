@@ -341,6 +341,7 @@ GFG_API int int8_quantize_token_device(const void* x, int32_t in_dtype, int64_t 
  * x [M][K] in 32 or 16 bits: a 16-byte aligned device workspace of at least
  * int8_linear_workspace_bytes(M, K) bytes holds the codes and scales between
  * them (it needs no initialization; a call leaves nothing in it for the next).
+ * Up to 4 rows are quantized inside the product's kernel, in one launch.
  */
 GFG_API int int8_gemm(const int8_t* a, const float* a_scale, const int8_t* b, const float* b_scale,
                       const float* bias, void* d, int64_t M, int64_t N, int64_t K, int32_t out_dtype, void* stream);
@@ -393,7 +394,7 @@ GFG_API int moe_topk(const void* logits, int32_t in_dtype, const float* bias, in
                      int64_t E, int64_t k, int32_t score, int32_t renormalize, float scale, void* stream);
 
 /*
- * A whole mixture-of-experts layer for a few tokens (two launches):
+ * A whole mixture-of-experts layer for a few tokens (two or three launches):
  *
  *   g | u = W1[e] x[t],  h = silu(g) * u,
  *   out[t] = sum over j of topk_weights[t, j] * (W2[e] h),  e = topk_ids[t, j]
@@ -456,9 +457,10 @@ GFG_API int moe_int8_layer(const void* x, int32_t dtype, const int32_t* topk_ids
  * aligned; a call that misses them then returns GFG_EUNSUPPORTED.  Other
  * values: GFG_EINVAL.  Results of the two tiles agree to the parity
  * tolerance; they are not promised to agree bit for bit.  The int8 products
- * follow the setting too: GFG_TILE_AUTO takes 256 x 256 from 7/16 as many such
- * tiles as CUs on, GFG_TILE_128x256 their smaller tiles, GFG_TILE_256x256 needs
- * N at most 2^22; their results do not depend on it.
+ * follow the setting too: GFG_TILE_AUTO takes their large tiles (256 or 192 rows
+ * by 256 columns) where tiles of 128 x 128 would outnumber the CUs,
+ * GFG_TILE_128x256 the smaller ones, GFG_TILE_256x256 the large ones (N at most
+ * 2^22); their results do not depend on it.
  *
  * grouped_fp8_set_grid_limit: at most max_workgroups workgroups per GEMM
  * launch (0, the default: one per CU, fewer when there are fewer tiles).  The

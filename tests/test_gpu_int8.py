@@ -54,6 +54,17 @@ def test_quantizer_bit_exact(M, K, dtype):
     assert np.array_equal(q.cpu().numpy(), ref_q)
 
 
+@pytest.mark.parametrize("M,K", [(9, 2576), (6, 3056), (5, 3088), (3, 8208), (2, 16384)])
+def test_quantizer_of_every_row_split(M, K):
+    for dtype in (torch.bfloat16, torch.float32):
+        x = torch.randn(M, K, generator=torch.Generator().manual_seed(K)).to(dtype)
+        x[0, K - 1] = 9.0                                # the maximum in the row's last chunk
+        x[1, K // 2] = float("nan")
+        q, s = gfg.int8_quantize_token_device(x.cuda())
+        ref_q, ref_s = so.quantize_token(x.float().numpy())
+        assert np.array_equal(q.cpu().numpy(), ref_q) and np.array_equal(s.cpu().numpy(), ref_s, equal_nan=True)
+
+
 def test_quantizer_ties_extremes_and_non_finite_rows():
     K = 64
     x = np.zeros((9, K), np.float32)
