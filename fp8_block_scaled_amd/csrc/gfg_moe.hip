@@ -1213,9 +1213,9 @@ __global__ __launch_bounds__(kWaves * 64) void moe_down_shared_kernel(MoeParams 
     else shared_items<W, __bf16, 64, false>(p, r, ring);
 }
 
-// Four columns of a token a thread.  The pairs' sums are loaded eight at a time,
-// also those of pairs without an expert (whose places hold anything), and only
-// then picked, so that no load waits for an id.
+// Four columns of a token a thread.  The pairs' sums, ids and weights are loaded
+// eight pairs at a time, also the sums of pairs without an expert (whose places
+// hold anything), and only then picked, so that no load waits for another.
 template <typename OutT>
 __global__ __launch_bounds__(256) void moe_combine_kernel(MoeParams p) {
     const int t = blockIdx.y, col = (int(blockIdx.x) * 256 + int(threadIdx.x)) * 4;
@@ -1224,16 +1224,20 @@ __global__ __launch_bounds__(256) void moe_combine_kernel(MoeParams p) {
     v4f sum = {};
     for (int j0 = 0; j0 < p.k; j0 += 8) {
         v4f v[8];
-#pragma unroll
-        for (int c = 0; c < 8; ++c) v[c] = *reinterpret_cast<const v4f*>(y + int64_t(min(j0 + c, p.k - 1)) * p.H);
+        int e[8];
+        float w[8];
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
-            if (j0 + c >= p.k) break;
-            const int e = p.ids[t * p.k + j0 + c];
-            if (e < 0 || e >= p.E) continue;
-            const float w = p.weights[t * p.k + j0 + c];
+            const int j = min(j0 + c, p.k - 1);
+            v[c] = *reinterpret_cast<const v4f*>(y + int64_t(j) * p.H);
+            e[c] = p.ids[t * p.k + j];
+            w[c] = p.weights[t * p.k + j];
+        }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) sum[i] = fmaf(w, v[c][i], sum[i]);
+        for (int c = 0; c < 8; ++c) {
+            const bool live = j0 + c < p.k && e[c] >= 0 && e[c] < p.E;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sum[i] = live ? fmaf(w[c], v[c][i], sum[i]) : sum[i];
         }
     }
     typedef OutT o4 __attribute__((ext_vector_type(4)));
