@@ -44,6 +44,26 @@ __device__ __forceinline__ void lds_barrier() {
     asm volatile("" ::: "memory");
 }
 
+// Reductions over a wave: rotations inside the rows of 16 lanes (DPP), then the
+// four rows through scalar registers; about a quarter of the time of shuffles
+// through LDS.  All lanes take part.
+template <int CTRL>
+__device__ __forceinline__ int dpp(int v) {
+    return __builtin_amdgcn_update_dpp(0, v, CTRL, 0xF, 0xF, false);
+}
+template <typename T, typename Op>
+__device__ __forceinline__ T wave_reduce(T v, Op op) {
+    static_assert(sizeof(T) == 4, "one register");
+#define GFG_ROT(C) v = op(v, __builtin_bit_cast(T, dpp<0x120 + C>(__builtin_bit_cast(int, v))))
+    GFG_ROT(8);
+    GFG_ROT(4);
+    GFG_ROT(2);
+    GFG_ROT(1);
+#undef GFG_ROT
+    auto row = [&](int l) { return __builtin_bit_cast(T, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), l)); };
+    return op(op(row(0), row(16)), op(row(32), row(48)));
+}
+
 // Raw buffer resource over [base, base + bytes): stride 0, 32-bit data format.
 // The hardware returns zero for loads, and drops stores, at offsets past `bytes`.
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base, uint32_t bytes) {

@@ -37,6 +37,7 @@ typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
 template <typename T> struct Chunk;            // 8 elements of a row
 template <> struct Chunk<__bf16> {
     u32x4 w;
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t at) { w = __builtin_amdgcn_raw_buffer_load_b128(r, at, 0, 0); }
     __device__ __forceinline__ void load(const __bf16* p) { w = *reinterpret_cast<const u32x4*>(p); }
     __device__ __forceinline__ float at(int i) const {
         return __uint_as_float((i & 1) ? w[i >> 1] & 0xFFFF0000u : w[i >> 1] << 16);
@@ -44,6 +45,7 @@ template <> struct Chunk<__bf16> {
 };
 template <> struct Chunk<_Float16> {
     u32x4 w;
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t at) { w = __builtin_amdgcn_raw_buffer_load_b128(r, at, 0, 0); }
     __device__ __forceinline__ void load(const _Float16* p) { w = *reinterpret_cast<const u32x4*>(p); }
     __device__ __forceinline__ float at(int i) const {
         return float(__builtin_bit_cast(_Float16, uint16_t(w[i >> 1] >> (16 * (i & 1)))));
@@ -51,6 +53,10 @@ template <> struct Chunk<_Float16> {
 };
 template <> struct Chunk<float> {
     u32x4 w[2];
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t at) {
+        w[0] = __builtin_amdgcn_raw_buffer_load_b128(r, at, 0, 0);
+        w[1] = __builtin_amdgcn_raw_buffer_load_b128(r, at + 16, 0, 0);
+    }
     __device__ __forceinline__ void load(const float* p) {
         w[0] = reinterpret_cast<const u32x4*>(p)[0];
         w[1] = reinterpret_cast<const u32x4*>(p)[1];
@@ -114,8 +120,7 @@ __global__ __launch_bounds__(LPR == 64 ? 256 : LPR) void quant_token_kernel(cons
             t.load(row + c * 8);
             ab = max(ab, chunk_amax(t));
         }
-#pragma unroll
-        for (int w = 32; w >= 1; w >>= 1) ab = max(ab, uint32_t(__shfl_xor(int(ab), w, 64)));
+        ab = wave_reduce(ab, [](uint32_t a, uint32_t b) { return max(a, b); });
         if constexpr (LPR > 64) {              // (the workgroup's lanes share the row: all of them are here)
             if ((threadIdx.x & 63) == 0) part[turn][threadIdx.x >> 6] = ab;
             __syncthreads();
@@ -278,17 +283,20 @@ __global__ __launch_bounds__(WM * WN * 64) void int8_gemm_kernel(I8Params p) {
                 for (int c = 0; c < CB; ++c)
                     acc[y][c] = __builtin_amdgcn_mfma_i32_16x16x64_i8(bf[h][c], af[h][y], acc[y][c], 0, 0, 0);
     };
-    // every step leaves the loop from its own place, so that the order of the
-    // loads is the same on every path and the compiler's own waits stay exact
-    for (int kb = 0;; kb += S) {
-        step(buf[0], buf[S - 1], kb);
-        if (kb + 1 >= KB) break;
-        step(buf[1], buf[0], kb + 1);
-        if (kb + 2 >= KB) break;
-        step(buf[2], buf[1], kb + 2);
-        if (kb + 3 >= KB) break;
-        step(buf[3], buf[2], kb + 3);
-        if (kb + 4 >= KB) break;
+    // whole rounds of the ring, then the rest: a loop with one way out, in which
+    // every path to a stage's reads passes the same loads, so that the compiler's
+    // own waits stay exact
+    int kb = 0;
+    for (; kb + S <= KB; kb += S) {
+#pragma unroll
+        for (int j = 0; j < S; ++j) step(buf[j], buf[(j + S - 1) % S], kb + j);
+    }
+    if (kb < KB) {
+        step(buf[0], buf[3], kb);
+        if (kb + 1 < KB) {
+            step(buf[1], buf[0], kb + 1);
+            if (kb + 2 < KB) step(buf[2], buf[1], kb + 2);
+        }
     }
     GFG_WAITCNT(0, 15);                            // the last loads land before the workgroup ends
 
@@ -415,17 +423,18 @@ __global__ __launch_bounds__(NW * 64) void int8_stream_kernel(I8Params p) {
     constexpr int STEP = NW * TK;
 #pragma unroll
     for (int d = 0; d < D; ++d) load(ring[d], wave * TK + d * STEP);
-    // every step leaves the loop from its own place, so that the order of the
-    // loads is the same on every path and the compiler's own waits stay exact
-    for (int k = wave * TK; k < p.K; k += D * STEP) {
+    int k = wave * TK;                         // (rounds as above)
+    for (; k + (D - 1) * STEP < p.K; k += D * STEP) {
+#pragma unroll
+        for (int d = 0; d < D; ++d) step(ring[d], k + d * STEP);
+    }
+    if (k < p.K) {
         step(ring[0], k);
-        if (k + STEP >= p.K) break;
-        step(ring[1], k + STEP);
         if constexpr (D > 2) {
-            if (k + 2 * STEP >= p.K) break;
-            step(ring[2], k + 2 * STEP);
-            if (k + 3 * STEP >= p.K) break;
-            step(ring[3], k + 3 * STEP);
+            if (k + STEP < p.K) {
+                step(ring[1], k + STEP);
+                if (k + 2 * STEP < p.K) step(ring[2], k + 2 * STEP);
+            }
         }
     }
     GFG_WAITCNT(0, 15);                            // the last loads land before the workgroup ends
@@ -505,12 +514,12 @@ int launch_ring(I8Params p, int out_dtype, hipStream_t s) {
 constexpr int kFewTokens = 4;
 constexpr int kFewCodes = 32 * 1024;           // bytes of LDS for the codes
 
-template <typename X, typename OutT>
+template <int MT, typename X, typename OutT>
 __global__ __launch_bounds__(256) void int8_few_kernel(const X* __restrict__ xs, I8Params p) {
     constexpr int NW = 4, D = 4, TN = 32, UNIT = TN * TK, PER = UNIT / 1024;
     __shared__ __attribute__((aligned(1024))) uint8_t s0[NW * UNIT], s1[NW * UNIT], s2[NW * UNIT], s3[NW * UNIT];
     __shared__ __attribute__((aligned(1024))) uint8_t codes[kFewCodes];   // [M][K rounded up to 128], chunks swizzled like a stage's
-    __shared__ uint32_t amax[kFewTokens][NW];
+    __shared__ uint32_t amax[MT][NW];
     __shared__ v4i sums[NW][2][64];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -527,46 +536,42 @@ __global__ __launch_bounds__(256) void int8_few_kernel(const X* __restrict__ xs,
         for (int j = 0; j < PER; ++j)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (GFG_LDS void*)(dst + j * 1024), 16, base + uint32_t(8 * j) * uint32_t(p.K), 0, 0, 0);
     };
-    constexpr int STEP = NW * TK;
-#pragma unroll
-    for (int d = 0; d < D; ++d) load(ring[d], wave * TK + d * STEP);
-
     const int chunks = p.K / 8, KP = (p.K + TK - 1) / TK * TK;
-    // the rows' first 8192 elements stay in registers between the maximum and
-    // the encoding, and all of them are loaded before any is used
-    constexpr int HELD = 4;
-    Chunk<X> held[kFewTokens][HELD];
-    auto each = [&](int m, auto&& use) {       // the chunks past them
-        for (int c = threadIdx.x + 256 * HELD; c < KP / 8; c += 256) {
-            Chunk<X> t{};
-            if (c < chunks) t.load(xs + int64_t(m) * p.K + c * 8);
-            use(c, t);
-        }
-    };
+    // the rows stay in registers between the maximum and the encoding; they are
+    // loaded before the weights, so that they are not waited for behind those
+    constexpr int HELD = kFewCodes / 8 / 256 / MT, STEP = NW * TK;
+    Chunk<X> held[MT][HELD];
 #pragma unroll
-    for (int m = 0; m < kFewTokens; ++m)
+    for (int m = 0; m < MT; ++m) {
+        const auto rx = make_rsrc(xs + int64_t(min(m, M - 1)) * p.K, uint32_t(p.K) * uint32_t(sizeof(X)));
 #pragma unroll
         for (int i = 0; i < HELD; ++i) {
-            const int c = int(threadIdx.x) + 256 * i;
             held[m][i] = Chunk<X>{};
-            if (m < M && c < chunks) held[m][i].load(xs + int64_t(m) * p.K + c * 8);
+            if (256 * i < chunks) held[m][i].load(rx, (threadIdx.x + 256 * i) * uint32_t(8 * sizeof(X)));   // past K: zeros
         }
+    }
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int m = 0; m < kFewTokens; ++m) {
-        if (m >= M) break;
+    for (int d = 0; d < D; ++d) load(ring[d], wave * TK + d * STEP);
+    __builtin_amdgcn_sched_barrier(0);
+    uint32_t most[MT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
         uint32_t ab = 0;
 #pragma unroll
-        for (int i = 0; i < HELD; ++i) ab = max(ab, chunk_amax(held[m][i]));
-        each(m, [&](int, const Chunk<X>& t) { ab = max(ab, chunk_amax(t)); });
-#pragma unroll
-        for (int w = 32; w >= 1; w >>= 1) ab = max(ab, uint32_t(__shfl_xor(int(ab), w, 64)));
-        if (lane == 0) amax[m][wave] = ab;
+        for (int i = 0; i < HELD; ++i)
+            if (256 * i < chunks) ab = max(ab, chunk_amax(held[m][i]));
+        most[m] = wave_reduce(ab, [](uint32_t a, uint32_t b) { return max(a, b); });
     }
-    __syncthreads();
+    if (lane == 0) {
+#pragma unroll
+        for (int m = 0; m < MT; ++m) amax[m][wave] = most[m];
+    }
+    lds_barrier();                             // (the weights stay in flight)
     float scale = 0.0f;                        // of row l16
 #pragma unroll
-    for (int m = 0; m < kFewTokens; ++m) {
-        if (m >= M) break;
+    for (int m = 0; m < MT; ++m) {
+        if (MT > 1 && m >= M) break;
         float s, r;
         row_scale(max(max(amax[m][0], amax[m][1]), max(amax[m][2], amax[m][3])), &s, &r);
         if (l16 == m) scale = s;
@@ -578,9 +583,8 @@ __global__ __launch_bounds__(256) void int8_few_kernel(const X* __restrict__ xs,
 #pragma unroll
         for (int i = 0; i < HELD; ++i)
             if (int(threadIdx.x) + 256 * i < KP / 8) put(int(threadIdx.x) + 256 * i, held[m][i]);
-        each(m, put);
     }
-    __syncthreads();
+    lds_barrier();
 
     v4i acc[2] = {};
     const int row = min(l16, M - 1);           // columns past M repeat the last row and are not stored
@@ -605,14 +609,17 @@ __global__ __launch_bounds__(256) void int8_few_kernel(const X* __restrict__ xs,
         load(cur, k + D * STEP);               // past K: zeros
         __builtin_amdgcn_sched_barrier(0);
     };
-    for (int k = wave * TK; k < p.K; k += D * STEP) {
+    int k = wave * TK;                         // (rounds as above)
+    for (; k + (D - 1) * STEP < p.K; k += D * STEP) {
+#pragma unroll
+        for (int d = 0; d < D; ++d) step(ring[d], k + d * STEP);
+    }
+    if (k < p.K) {
         step(ring[0], k);
-        if (k + STEP >= p.K) break;
-        step(ring[1], k + STEP);
-        if (k + 2 * STEP >= p.K) break;
-        step(ring[2], k + 2 * STEP);
-        if (k + 3 * STEP >= p.K) break;
-        step(ring[3], k + 3 * STEP);
+        if (k + STEP < p.K) {
+            step(ring[1], k + STEP);
+            if (k + 2 * STEP < p.K) step(ring[2], k + 2 * STEP);
+        }
     }
     GFG_WAITCNT(0, 15);                        // the last loads land before the workgroup ends
     sums[wave][0][lane] = acc[0];
@@ -630,13 +637,20 @@ __global__ __launch_bounds__(256) void int8_few_kernel(const X* __restrict__ xs,
     store4(static_cast<OutT*>(p.d) + int64_t(l16) * p.N, n, p.N, v);
 }
 
-template <typename X>
-int launch_few(const void* x, const I8Params& p, int out_dtype, hipStream_t s) {
+template <int MT, typename X>
+void launch_few_rows(const void* x, const I8Params& p, int out_dtype, hipStream_t s) {
     const dim3 grid(unsigned((p.N + 31) / 32)), block(256);
     if (out_dtype == GFG_OUT_BF16)
-        hipLaunchKernelGGL((int8_few_kernel<X, __bf16>), grid, block, 0, s, static_cast<const X*>(x), p);
+        hipLaunchKernelGGL((int8_few_kernel<MT, X, __bf16>), grid, block, 0, s, static_cast<const X*>(x), p);
     else
-        hipLaunchKernelGGL((int8_few_kernel<X, _Float16>), grid, block, 0, s, static_cast<const X*>(x), p);
+        hipLaunchKernelGGL((int8_few_kernel<MT, X, _Float16>), grid, block, 0, s, static_cast<const X*>(x), p);
+}
+
+template <typename X>
+int launch_few(const void* x, const I8Params& p, int out_dtype, hipStream_t s) {
+    if (p.rows == 1) launch_few_rows<1, X>(x, p, out_dtype, s);
+    else if (p.rows == 2) launch_few_rows<2, X>(x, p, out_dtype, s);
+    else launch_few_rows<kFewTokens, X>(x, p, out_dtype, s);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return fail(GFG_EHIP, "kernel launch failed: %s", hipGetErrorString(e));
     return GFG_OK;
@@ -818,7 +832,7 @@ extern "C" int int8_linear(const void* x, int32_t in_dtype, const int8_t* b, con
     if (int rc = check_quant(fn, x, in_dtype, M, K, q, scale)) return rc;
     if (int rc = check_operands(fn, q, scale, b, b_scale, bias, false, d)) return rc;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    if (M <= kFewTokens && M * ((K + TK - 1) / TK * TK) <= kFewCodes) {
+    if (M <= kFewTokens && (M == 3 ? 4 : M) * ((K + TK - 1) / TK * TK) <= kFewCodes) {      // (three rows run as four)
         const I8Params p = product(nullptr, nullptr, b, b_scale, bias, nullptr, d, M, N, K, 1);
         if (in_dtype == GFG_IN_F32) return launch_few<float>(x, p, out_dtype, s);
         if (in_dtype == GFG_IN_BF16) return launch_few<__bf16>(x, p, out_dtype, s);
