@@ -170,7 +170,7 @@ void launch_quant(const void* x, uint8_t* q, float* scale, int64_t M, int K, hip
 // These are the launches with too few 256 x 256 tiles, whose time is the
 // latency of a tile's first loads plus a chain of steps, so depth matters
 // more than the bytes per step (1024 x 4096 x 4096: 37.9 us with one stage ahead,
-// 22.5 with three; 512 x 4096 x 4096 on 64 x 64: 34, 21).  LDS row R (128 bytes)
+// 26.1 with three; 512 x 4096 x 4096 on 64 x 64: 34, 17.2).  LDS row R (128 bytes)
 // holds its 16-byte chunks XOR-swizzled by R & 7, so that the 16 rows that a
 // fragment read touches spread over all banks.  Rows past the operand's end and chunks past K lie
 // outside the buffer window, where the hardware returns zeros, so no size
@@ -335,9 +335,8 @@ __global__ __launch_bounds__(WM * WN * 64) void int8_gemm_kernel(I8Params p) {
 // (Loading the fragments straight into registers instead is slower: a
 // fragment's adjacent lanes are adjacent rows, so four lanes touch four cache
 // lines, and the load path then passes 16 bytes a cycle, not 64: 1 x 7168 x 2304
-// took 13.7 us that way, 5.9 this way.)  Bound by the launch and the way of the
-// first loads, then by what a CU takes in, about 37 GB/s: 128 x 4096 x 4096 in 10.0
-// us.
+// took twice as long.)  Bound by the launch and the way of the first loads, then
+// by what a CU takes in, about 37 GB/s: 128 x 4096 x 4096 in 8.6 us.
 template <int LAYOUT, int RB, int CB, int NW, int D, typename OutT>
 __global__ __launch_bounds__(NW * 64) void int8_stream_kernel(I8Params p) {
     constexpr int TM = 16 * RB, TN = 16 * CB;
@@ -509,8 +508,9 @@ int launch_ring(I8Params p, int out_dtype, hipStream_t s) {
 // itself, into LDS, while its first weights are on the way (the codes and
 // scales are those of the token quantizer, bit for bit), then streams its 32
 // weight rows like the kernel above.  One launch instead of two: 7168 x 2304 with
-// cold weights (16.5 MB), 1 token 7.3 us, 10.2 in two launches; 4 tokens 9.8, 10.5
-// (every workgroup encodes all rows, so more of them would gain nothing).
+// cold weights (16.5 MB), 1 token 6.5 us, 10.2 in two launches; 4 tokens 8.0, 10.5
+// (every workgroup encodes all rows, half a microsecond each, and 5 tokens take 9.9
+// in two launches, so a few more of them would gain nothing).
 constexpr int kFewTokens = 4;
 constexpr int kFewCodes = 32 * 1024;           // bytes of LDS for the codes
 
@@ -657,16 +657,15 @@ int launch_few(const void* x, const I8Params& p, int out_dtype, hipStream_t s) {
 }
 
 // The launches with too few 256 x 256 tiles, by how many tiles of each size
-// there are (one sweep of M x N x K, us, the chosen tile first):
-//  * few rows: the streamed 16 x 32 tile (1 x 7168 x 2304: 5.9, 32 x 32 6.2,
-//    64 x 64 7.7; 16 x 4096 x 4096: 6.3, 6.8, 11.1), or 32 x 32 up to 32 rows;
-//  * 192 tiles of 128 x 128 or more: those (512 x 7168 x 2304: 18.8, 64 x 64
-//    25.8; 1024 x 4096 x 4096: 26.4, 39.2);
-//  * 256 tiles of 64 x 64 or more: those, in shared stages (512 x 4096 x 4096:
-//    21.2, 128 x 128 24.6; 256 x 7168 x 7168: 36.3, 40.4);
-//  * below, the streamed tiles, 32 x 32 up to 512 of them (128 x 4096 x 4096:
-//    10.0, 64 x 64 12.6; 4096 x 64 x 16384: 24, 44), then 64 x 64 (2000 x 300 x
-//    16384: 37.9, 32 x 32 52).
+// there are (M x N x K, us in a graph with warm operands, the chosen tile first):
+//  * few rows: the streamed 16 x 32 tile (1 x 7168 x 2304: 3.6, 32 x 32 3.8,
+//    64 x 64 5.9; 16 x 4096 x 4096: 4.1, 4.5, 8.5), or 32 x 32 up to 32 rows;
+//  * 192 tiles of 128 x 128 or more: those (512 x 7168 x 2304: 15.8, 64 x 64
+//    18.6; 1024 x 4096 x 4096: 26.1, 33.7);
+//  * up to 512 tiles of 32 x 32: those, streamed (128 x 4096 x 4096: 8.6, 64 x 64
+//    9.6; 4096 x 64 x 16384: 21.8, 27.1);
+//  * else 64 x 64 (2000 x 300 x 16384: 30.0, 32 x 32 52; 512 x 4096 x 4096: 17.2,
+//    30.4, 128 x 128 20.8).
 template <int LAYOUT>
 int launch_small(const I8Params& p, int out_dtype, hipStream_t s) {
     auto tiles = [&](int64_t tm, int64_t tn) {
@@ -675,9 +674,8 @@ int launch_small(const I8Params& p, int out_dtype, hipStream_t s) {
     if (p.rows <= 16) return launch_stream<LAYOUT, 1, 2, 4, 4>(p, out_dtype, s);
     if (p.rows <= 32) return launch_stream<LAYOUT, 2, 2, 4, 2>(p, out_dtype, s);
     if (tiles(128, 128) >= 192) return launch_ring<LAYOUT, 128, 128, 4, 2, 4>(p, out_dtype, s);
-    if (tiles(64, 64) >= 256) return launch_ring<LAYOUT, 64, 64, 4, 2, 2>(p, out_dtype, s);
     if (tiles(32, 32) <= 512) return launch_stream<LAYOUT, 2, 2, 4, 2>(p, out_dtype, s);
-    return launch_stream<LAYOUT, 4, 4, 4, 2>(p, out_dtype, s);
+    return launch_ring<LAYOUT, 64, 64, 4, 2, 2>(p, out_dtype, s);
 }
 
 // Launch the product on the tile that suits it: the 256 x 256 kernel (whose
