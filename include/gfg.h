@@ -341,7 +341,8 @@ GFG_API int int8_quantize_token_device(const void* x, int32_t in_dtype, int64_t 
  * x [M][K] in 32 or 16 bits: a 16-byte aligned device workspace of at least
  * int8_linear_workspace_bytes(M, K) bytes holds the codes and scales between
  * them (it needs no initialization; a call leaves nothing in it for the next).
- * Up to 4 rows are quantized inside the product's kernel, in one launch.
+ * Up to 4 rows (with at most 32 KB of codes) are quantized inside the product's
+ * kernel, in one launch, with the same results.
  */
 GFG_API int int8_gemm(const int8_t* a, const float* a_scale, const int8_t* b, const float* b_scale,
                       const float* bias, void* d, int64_t M, int64_t N, int64_t K, int32_t out_dtype, void* stream);
