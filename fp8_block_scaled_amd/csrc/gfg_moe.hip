@@ -507,15 +507,17 @@ __device__ __forceinline__ void load_resident(GFG_LDS uint8_t* dst, __amdgpu_buf
 
 // h = silu(g) * u for four columns of a pair, in two bf16 halves, high and low:
 // 16 significant bits with fp32's range, so that the only rounding to 16 bits
-// is the output's.
+// is the output's.  A finite h above the largest bf16 keeps that as its high
+// half and the rest as its low one; a NaN or an infinity has no low half.
 __device__ __forceinline__ void store_hidden(const MoeParams& p, int pair, int col, const v4f& g, const v4f& u) {
+    constexpr float kTop = 0x1.FEp127f;        // the largest bf16
     bf4 hi, lo;
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
         const float h = g[c] / (1.0f + expf(-g[c])) * u[c];
-        hi[c] = __bf16(h);
-        const float rest = h - float(hi[c]);
-        lo[c] = __bf16(rest == rest ? rest : 0.0f);       // an infinite h has no low half
+        const bool finite = fabsf(h) < __builtin_inff();
+        hi[c] = __bf16(finite ? fminf(fmaxf(h, -kTop), kTop) : h);
+        lo[c] = __bf16(finite ? h - float(hi[c]) : 0.0f);
     }
     uint8_t* const row = p.h + int64_t(pair) * 4 * p.I + col * 2;
     *reinterpret_cast<bf4*>(row) = hi;
