@@ -311,10 +311,30 @@ def _out_code(d):
     raise TypeError(f"d has dtype {d.dtype}; expected bfloat16 or float16")
 
 
+def _on(device, entry, *args):
+    """Call an entry point with ``device`` current.  A launch goes to the current device, and the handle of a default
+    stream (0) does not name one, so the GPU that holds the tensors is made current for the call."""
+    cuda = _torch().cuda
+    if cuda.current_device() == device.index:
+        rc = entry(*args)
+    else:
+        with cuda.device(device):
+            rc = entry(*args)
+    _check(rc)
+
+
+def _check_stream(stream, device):
+    on = getattr(stream, "device", device)
+    if on != device:
+        raise ValueError(f"stream is on {on}, the tensors are on {device}")
+
+
 def _stream_handle(stream, device):
     torch = _torch()
     if stream is None:
         stream = torch.cuda.current_stream(device)
+    else:
+        _check_stream(stream, device)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -334,12 +354,12 @@ def grouped_fp8_gemm_contiguous(a, a_scale, b, b_scale, grouped_layout, d, strea
         raise ValueError("shape mismatch between a, b, grouped_layout and d")
     if tuple(a_scale.shape) != (-(-K // 128), M) or tuple(b_scale.shape) != (G, -(-N // 128), -(-K // 128)):
         raise ValueError("scale tensor shapes do not match the (1,128)/(128,128) layouts")
-    _check(raw_contiguous(
+    _on(dev, raw_contiguous,
         _dev_ptr(a, "a", f8, dev), _dev_ptr(a_scale, "a_scale", (torch.uint8,), dev),
         _dev_ptr(b, "b", f8, dev), _dev_ptr(b_scale, "b_scale", (torch.uint8,), dev),
         _dev_ptr(grouped_layout, "grouped_layout", (torch.int32,), dev),
         _dev_ptr(d, "d", (torch.bfloat16, torch.float16), dev),
-        M, N, K, G, _out_code(d), _stream_handle(stream, dev)))
+        M, N, K, G, _out_code(d), _stream_handle(stream, dev))
     return d
 
 
@@ -358,12 +378,12 @@ def grouped_fp8_gemm_masked(a, a_scale, b, b_scale, masked_m, d, stream=None):
         raise ValueError("shape mismatch between a, b, masked_m and d")
     if tuple(a_scale.shape) != (G, -(-K // 128), Mmax) or tuple(b_scale.shape) != (G, -(-N // 128), -(-K // 128)):
         raise ValueError("scale tensor shapes do not match the (1,128)/(128,128) layouts")
-    _check(raw_masked(
+    _on(dev, raw_masked,
         _dev_ptr(a, "a", f8, dev), _dev_ptr(a_scale, "a_scale", (torch.uint8,), dev),
         _dev_ptr(b, "b", f8, dev), _dev_ptr(b_scale, "b_scale", (torch.uint8,), dev),
         _dev_ptr(masked_m, "masked_m", (torch.int32,), dev),
         _dev_ptr(d, "d", (torch.bfloat16, torch.float16), dev),
-        G, Mmax, N, K, _out_code(d), _stream_handle(stream, dev)))
+        G, Mmax, N, K, _out_code(d), _stream_handle(stream, dev))
     return d
 
 
@@ -383,12 +403,12 @@ def grouped_fp8_gemm_silu_mul_contiguous(a, a_scale, b, b_scale, grouped_layout,
         raise ValueError("shape mismatch between a, b [G, 2I, K], grouped_layout and d [M, I]")
     if tuple(a_scale.shape) != (-(-K // 128), M) or tuple(b_scale.shape) != (G, -(-N2 // 128), -(-K // 128)):
         raise ValueError("scale tensor shapes do not match the (1,128)/(128,128) layouts")
-    _check(raw_silu_mul_contiguous(
+    _on(dev, raw_silu_mul_contiguous,
         _dev_ptr(a, "a", f8, dev), _dev_ptr(a_scale, "a_scale", (torch.uint8,), dev),
         _dev_ptr(b, "b", f8, dev), _dev_ptr(b_scale, "b_scale", (torch.uint8,), dev),
         _dev_ptr(grouped_layout, "grouped_layout", (torch.int32,), dev),
         _dev_ptr(d, "d", (torch.bfloat16, torch.float16), dev),
-        M, N2 // 2, K, G, _out_code(d), _stream_handle(stream, dev)))
+        M, N2 // 2, K, G, _out_code(d), _stream_handle(stream, dev))
     return d
 
 
@@ -404,12 +424,12 @@ def grouped_fp8_gemm_silu_mul_masked(a, a_scale, b, b_scale, masked_m, d, stream
         raise ValueError("shape mismatch between a, b [G, 2I, K], masked_m and d [G, M_max, I]")
     if tuple(a_scale.shape) != (G, -(-K // 128), Mmax) or tuple(b_scale.shape) != (G, -(-N2 // 128), -(-K // 128)):
         raise ValueError("scale tensor shapes do not match the (1,128)/(128,128) layouts")
-    _check(raw_silu_mul_masked(
+    _on(dev, raw_silu_mul_masked,
         _dev_ptr(a, "a", f8, dev), _dev_ptr(a_scale, "a_scale", (torch.uint8,), dev),
         _dev_ptr(b, "b", f8, dev), _dev_ptr(b_scale, "b_scale", (torch.uint8,), dev),
         _dev_ptr(masked_m, "masked_m", (torch.int32,), dev),
         _dev_ptr(d, "d", (torch.bfloat16, torch.float16), dev),
-        G, Mmax, N2 // 2, K, _out_code(d), _stream_handle(stream, dev)))
+        G, Mmax, N2 // 2, K, _out_code(d), _stream_handle(stream, dev))
     return d
 
 
@@ -425,12 +445,12 @@ def grouped_mxfp8_gemm_contiguous(a, a_scale, b, b_scale, grouped_layout, d, str
         raise ValueError("shape mismatch between a, b, grouped_layout and d")
     if K % 32 or tuple(a_scale.shape) != (K // 32, M) or tuple(b_scale.shape) != (G, K // 32, N):
         raise ValueError("scale tensor shapes do not match the MX (1,32) layouts")
-    _check(raw_mx_contiguous(
+    _on(dev, raw_mx_contiguous,
         _dev_ptr(a, "a", f8, dev), _dev_ptr(a_scale, "a_scale", (torch.uint8,), dev),
         _dev_ptr(b, "b", f8, dev), _dev_ptr(b_scale, "b_scale", (torch.uint8,), dev),
         _dev_ptr(grouped_layout, "grouped_layout", (torch.int32,), dev),
         _dev_ptr(d, "d", (torch.bfloat16, torch.float16), dev),
-        M, N, K, G, _out_code(d), _stream_handle(stream, dev)))
+        M, N, K, G, _out_code(d), _stream_handle(stream, dev))
     return d
 
 
@@ -446,12 +466,12 @@ def grouped_mxfp8_gemm_masked(a, a_scale, b, b_scale, masked_m, d, stream=None):
         raise ValueError("shape mismatch between a, b, masked_m and d")
     if K % 32 or tuple(a_scale.shape) != (G, K // 32, Mmax) or tuple(b_scale.shape) != (G, K // 32, N):
         raise ValueError("scale tensor shapes do not match the MX (1,32) layouts")
-    _check(raw_mx_masked(
+    _on(dev, raw_mx_masked,
         _dev_ptr(a, "a", f8, dev), _dev_ptr(a_scale, "a_scale", (torch.uint8,), dev),
         _dev_ptr(b, "b", f8, dev), _dev_ptr(b_scale, "b_scale", (torch.uint8,), dev),
         _dev_ptr(masked_m, "masked_m", (torch.int32,), dev),
         _dev_ptr(d, "d", (torch.bfloat16, torch.float16), dev),
-        G, Mmax, N, K, _out_code(d), _stream_handle(stream, dev)))
+        G, Mmax, N, K, _out_code(d), _stream_handle(stream, dev))
     return d
 
 
@@ -477,10 +497,10 @@ def fp8_quantize_act_1x128_device(x, q=None, scale_t=None, stream=None):
     if tuple(q.shape) != tuple(x.shape) or tuple(scale_t.shape) != lead + (-(-K // 128), M):
         raise ValueError("q / scale_t shapes do not match x")
     code = IN_F32 if x.dtype == torch.float32 else IN_BF16
-    _check(raw_quantize_act_device(
+    _on(dev, raw_quantize_act_device,
         _dev_ptr(x, "x", (torch.float32, torch.bfloat16), dev), code, G, M, K,
         _dev_ptr(q, "q", (torch.uint8, torch.float8_e4m3fn), dev),
-        _dev_ptr(scale_t, "scale_t", (torch.uint8,), dev), _stream_handle(stream, dev)))
+        _dev_ptr(scale_t, "scale_t", (torch.uint8,), dev), _stream_handle(stream, dev))
     return q, scale_t
 
 
@@ -562,10 +582,10 @@ def grouped_mxfp4_gemm_contiguous(a, a_scale, b, b_scale, grouped_layout, d, str
     if tuple(a_scale.shape) != (K // 32, M) or tuple(b_scale.shape) != (G, K // 32, N):
         raise ValueError("scale tensor shapes do not match the MX (1,32) layouts")
     u8 = (torch.uint8,)
-    _check(raw_mx4_contiguous(
+    _on(dev, raw_mx4_contiguous,
         _dev_ptr(a, "a", u8, dev), _dev_ptr(a_scale, "a_scale", u8, dev), _dev_ptr(b, "b", u8, dev),
         _dev_ptr(b_scale, "b_scale", u8, dev), _dev_ptr(grouped_layout, "grouped_layout", (torch.int32,), dev),
-        _dev_ptr(d, "d", (torch.bfloat16, torch.float16), dev), M, N, K, G, _out_code(d), _stream_handle(stream, dev)))
+        _dev_ptr(d, "d", (torch.bfloat16, torch.float16), dev), M, N, K, G, _out_code(d), _stream_handle(stream, dev))
     return d
 
 
@@ -582,11 +602,11 @@ def grouped_mxfp4_gemm_masked(a, a_scale, b, b_scale, masked_m, d, stream=None):
     if tuple(a_scale.shape) != (G, K // 32, Mmax) or tuple(b_scale.shape) != (G, K // 32, N):
         raise ValueError("scale tensor shapes do not match the MX (1,32) layouts")
     u8 = (torch.uint8,)
-    _check(raw_mx4_masked(
+    _on(dev, raw_mx4_masked,
         _dev_ptr(a, "a", u8, dev), _dev_ptr(a_scale, "a_scale", u8, dev), _dev_ptr(b, "b", u8, dev),
         _dev_ptr(b_scale, "b_scale", u8, dev), _dev_ptr(masked_m, "masked_m", (torch.int32,), dev),
         _dev_ptr(d, "d", (torch.bfloat16, torch.float16), dev), G, Mmax, N, K, _out_code(d),
-        _stream_handle(stream, dev)))
+        _stream_handle(stream, dev))
     return d
 
 
@@ -604,11 +624,11 @@ def grouped_mxfp4_gemm_silu_mul_contiguous(a, a_scale, b, b_scale, grouped_layou
     if tuple(a_scale.shape) != (K // 32, M) or tuple(b_scale.shape) != (G, K // 32, N2):
         raise ValueError("scale tensor shapes do not match the MX (1,32) layouts")
     u8 = (torch.uint8,)
-    _check(raw_mx4_silu_mul_contiguous(
+    _on(dev, raw_mx4_silu_mul_contiguous,
         _dev_ptr(a, "a", u8, dev), _dev_ptr(a_scale, "a_scale", u8, dev), _dev_ptr(b, "b", u8, dev),
         _dev_ptr(b_scale, "b_scale", u8, dev), _dev_ptr(grouped_layout, "grouped_layout", (torch.int32,), dev),
         _dev_ptr(d, "d", (torch.bfloat16, torch.float16), dev), M, N2 // 2, K, G, _out_code(d),
-        _stream_handle(stream, dev)))
+        _stream_handle(stream, dev))
     return d
 
 
@@ -625,9 +645,9 @@ def grouped_mxfp4_gemm_silu_mul_masked(a, a_scale, b, b_scale, masked_m, d, stre
     if tuple(a_scale.shape) != (G, K // 32, Mmax) or tuple(b_scale.shape) != (G, K // 32, N2):
         raise ValueError("scale tensor shapes do not match the MX (1,32) layouts")
     u8 = (torch.uint8,)
-    _check(raw_mx4_silu_mul_masked(
+    _on(dev, raw_mx4_silu_mul_masked,
         _dev_ptr(a, "a", u8, dev), _dev_ptr(a_scale, "a_scale", u8, dev), _dev_ptr(b, "b", u8, dev),
         _dev_ptr(b_scale, "b_scale", u8, dev), _dev_ptr(masked_m, "masked_m", (torch.int32,), dev),
         _dev_ptr(d, "d", (torch.bfloat16, torch.float16), dev), G, Mmax, N2 // 2, K, _out_code(d),
-        _stream_handle(stream, dev)))
+        _stream_handle(stream, dev))
     return d

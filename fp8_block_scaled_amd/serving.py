@@ -12,7 +12,7 @@ from __future__ import annotations
 
 import torch
 
-from . import IN_BF16, IN_F16, IN_F32, OUT_BF16, OUT_F16, _check, load_library
+from . import IN_BF16, IN_F16, IN_F32, OUT_BF16, OUT_F16, _check, _check_stream, _on, load_library
 
 _IN = {torch.float32: IN_F32, torch.bfloat16: IN_BF16, torch.float16: IN_F16}
 _OUT = {torch.bfloat16: OUT_BF16, torch.float16: OUT_F16}
@@ -37,7 +37,7 @@ def _ptr(t, name, dtypes, shape, device):
 
 
 def _device(t, name):
-    """The GPU that a call runs on: that of its output."""
+    """The GPU that a call runs on: that of its output, whichever is current."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
@@ -51,8 +51,10 @@ def _dims(t, name, n):
     return t.shape
 
 
-# the current stream's handle without a Stream object around it (a quarter of a small call's time)
+# the current stream's handle without a Stream object around it (a quarter of a small call's time), and the current
+# device without the check that there is one (its tensors show that)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _handle(stream, device):
@@ -60,15 +62,25 @@ def _handle(stream, device):
         if _raw_stream is not None:
             return _raw_stream(device.index)
         return torch.cuda.current_stream(device).cuda_stream
+    _check_stream(stream, device)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _call(device, entry, *args):
+    """Call an entry point on ``device``: it is current already, or made current for the call."""
+    if _current_device() == device.index:
+        _check(entry(*args))
+    else:
+        _on(device, entry, *args)
 
 
 def _empty(shape, dtype, device, stream):
     """A new tensor that belongs to the stream that the call runs on (so that its memory is not reused too early)."""
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=device)
+    handle = _handle(stream, device)
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(_handle(stream, device), device=device)
+        stream = torch.cuda.ExternalStream(handle, device=device)
     with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
@@ -100,9 +112,9 @@ def int8_quantize_token_device(x, q=None, scale=None, stream=None):
         scale = _empty(x.shape[:-1], torch.float32, dev, stream)
     K = x.shape[-1]
     M = x.numel() // K if K else 0
-    _check(load_library().int8_quantize_token_device(
+    _call(dev, load_library().int8_quantize_token_device,
         _ptr(x, "x", _IN, x.shape, dev), _IN[x.dtype], M, K, _ptr(q, "q", _I8, x.shape, dev),
-        _ptr(scale, "scale", _F32, x.shape[:-1], dev), _handle(stream, dev)))
+        _ptr(scale, "scale", _F32, x.shape[:-1], dev), _handle(stream, dev))
     return q, scale
 
 
@@ -112,10 +124,10 @@ def int8_gemm(a, a_scale, b, b_scale, d, bias=None, stream=None):
     dev = _device(d, "d")
     M, K = _dims(a, "a", 2)
     N = _dims(b, "b", 2)[0]
-    _check(load_library().int8_gemm(
+    _call(dev, load_library().int8_gemm,
         _ptr(a, "a", _I8, (M, K), dev), _ptr(a_scale, "a_scale", _F32, (M,), dev), _ptr(b, "b", _I8, (N, K), dev),
         _ptr(b_scale, "b_scale", _F32, (N,), dev), None if bias is None else _ptr(bias, "bias", _F32, (N,), dev),
-        _ptr(d, "d", _OUT, (M, N), dev), M, N, K, _OUT[d.dtype], _handle(stream, dev)))
+        _ptr(d, "d", _OUT, (M, N), dev), M, N, K, _OUT[d.dtype], _handle(stream, dev))
     return d
 
 
@@ -135,10 +147,10 @@ def int8_linear(x, b, b_scale, d, bias=None, workspace=None, stream=None):
     N = _dims(b, "b", 2)[0]
     lib = load_library()
     keep, ws, nbytes = _scratch(workspace, M * (K + 4), dev, stream)
-    _check(lib.int8_linear(
+    _call(dev, lib.int8_linear,
         _ptr(x, "x", _IN, (M, K), dev), _IN[x.dtype], _ptr(b, "b", _I8, (N, K), dev),
         _ptr(b_scale, "b_scale", _F32, (N,), dev), None if bias is None else _ptr(bias, "bias", _F32, (N,), dev),
-        _ptr(d, "d", _OUT, (M, N), dev), M, N, K, _OUT[d.dtype], ws, nbytes, _handle(stream, dev)))
+        _ptr(d, "d", _OUT, (M, N), dev), M, N, K, _OUT[d.dtype], ws, nbytes, _handle(stream, dev))
     return d
 
 
@@ -148,10 +160,10 @@ def grouped_int8_gemm_contiguous(a, a_scale, b, b_scale, grouped_layout, d, stre
     dev = _device(d, "d")
     M, K = _dims(a, "a", 2)
     G, N = _dims(b, "b", 3)[:2]
-    _check(load_library().grouped_int8_gemm_contiguous(
+    _call(dev, load_library().grouped_int8_gemm_contiguous,
         _ptr(a, "a", _I8, (M, K), dev), _ptr(a_scale, "a_scale", _F32, (M,), dev), _ptr(b, "b", _I8, (G, N, K), dev),
         _ptr(b_scale, "b_scale", _F32, (G, N), dev), _ptr(grouped_layout, "grouped_layout", _I32, (M,), dev),
-        _ptr(d, "d", _OUT, (M, N), dev), M, N, K, G, _OUT[d.dtype], _handle(stream, dev)))
+        _ptr(d, "d", _OUT, (M, N), dev), M, N, K, G, _OUT[d.dtype], _handle(stream, dev))
     return d
 
 
@@ -161,11 +173,11 @@ def grouped_int8_gemm_masked(a, a_scale, b, b_scale, masked_m, d, stream=None):
     dev = _device(d, "d")
     G, Mmax, K = _dims(a, "a", 3)
     N = _dims(b, "b", 3)[1]
-    _check(load_library().grouped_int8_gemm_masked(
+    _call(dev, load_library().grouped_int8_gemm_masked,
         _ptr(a, "a", _I8, (G, Mmax, K), dev), _ptr(a_scale, "a_scale", _F32, (G, Mmax), dev),
         _ptr(b, "b", _I8, (G, N, K), dev), _ptr(b_scale, "b_scale", _F32, (G, N), dev),
         _ptr(masked_m, "masked_m", _I32, (G,), dev), _ptr(d, "d", _OUT, (G, Mmax, N), dev), G, Mmax, N, K,
-        _OUT[d.dtype], _handle(stream, dev)))
+        _OUT[d.dtype], _handle(stream, dev))
     return d
 
 
@@ -182,11 +194,11 @@ def moe_topk(logits, ids, weights, score="softmax", bias=None, renormalize=True,
     k = _dims(ids, "ids", 2)[1]
     if score not in _SCORE:
         raise ValueError(f"score is {score!r}, expected one of {tuple(_SCORE)}")
-    _check(load_library().moe_topk(
+    _call(dev, load_library().moe_topk,
         _ptr(logits, "logits", _IN, (T, E), dev), _IN[logits.dtype],
         None if bias is None else _ptr(bias, "bias", _F32, (E,), dev), _ptr(ids, "ids", _I32, (T, k), dev),
         _ptr(weights, "weights", _F32, (T, k), dev), T, E, k, _SCORE[score], bool(renormalize), scale,
-        _handle(stream, dev)))
+        _handle(stream, dev))
     return ids, weights
 
 
@@ -202,12 +214,12 @@ def _layer(entry, x, topk_ids, topk_weights, w1, w1_scale, w2, w2_scale, out, wo
     E, _, I = _dims(w2, "w2", 3)
     s1, s2 = ((E, 2 * I // block, H // block), (E, H // block, I // block)) if block else ((E, 2 * I), (E, H))
     keep, ws, nbytes = _scratch(workspace, T * k * (H + I) * 4, dev, stream)
-    _check(entry(
+    _call(dev, entry,
         _ptr(x, "x", _OUT, (T, H), dev), _OUT[x.dtype], _ptr(topk_ids, "topk_ids", _I32, (T, k), dev),
         _ptr(topk_weights, "topk_weights", _F32, (T, k), dev), _ptr(w1, "w1", wtypes, (E, 2 * I, H), dev),
         _ptr(w1_scale, "w1_scale", stype, s1, dev), _ptr(w2, "w2", wtypes, (E, H, I), dev),
         _ptr(w2_scale, "w2_scale", stype, s2, dev), _ptr(out, "out", (x.dtype,), (T, H), dev), T, k, E, H, I, ws, nbytes,
-        _handle(stream, dev)))
+        _handle(stream, dev))
     return out
 
 

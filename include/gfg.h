@@ -20,6 +20,9 @@
  *  - GEMM tensor pointers are DEVICE pointers owned by the caller.  The
  *    library never allocates, frees or synchronizes inside a GEMM call; the
  *    call is asynchronous on `stream` (a hipStream_t, NULL = null stream).
+ *    It runs on the calling thread's current device, to which the pointers and
+ *    the stream must belong.  (The torch-facing calls make the tensors' device
+ *    current and refuse a stream of another one.)
  *  - Quantizer pointers are HOST pointers owned by the caller; the quantizers
  *    are synchronous CPU functions.
  *  - Return value: GFG_OK (0) or an error code; no exceptions cross the ABI.
