@@ -25,6 +25,7 @@ struct I8Params {
     int N, K, G;
     int m_tiles;             // row tiles of the kernel's tile height, over all groups (the 256 x 256 kernel: of 128 rows)
     int tiles_per_group;     // masked: row tiles per group (not the 256 x 256 kernel)
+    unsigned tiles;          // output tiles of the launch (not the 256 x 256 kernel)
     int group_m, num_xcd;    // tile order of the 256 x 256 kernel
 };
 

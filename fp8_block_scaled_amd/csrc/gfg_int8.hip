@@ -192,7 +192,7 @@ __device__ __forceinline__ void store4(OutT* row, int n, int N, const float (&v)
 }
 
 template <int LAYOUT, int TM, int TN, int S, int WM, int WN, typename OutT>
-__global__ __launch_bounds__(WM * WN * 64) void int8_gemm_kernel(I8Params p) {
+__device__ __forceinline__ void ring_tile(const I8Params& p, unsigned w) {
     constexpr int WAVES = WM * WN, BYTES = (TM + TN) * TK;
     constexpr int PER = BYTES / 1024 / WAVES;      // 1 KB loads per wave and stage
     constexpr int RB = TM / WM / 16, CB = TN / WN / 16;
@@ -206,9 +206,8 @@ __global__ __launch_bounds__(WM * WN * 64) void int8_gemm_kernel(I8Params p) {
     const int l16 = lane & 15, lq = lane >> 4;
     // tiles in ranges, one for each XCD (the hardware deals workgroup w to XCD
     // w % num_xcd), row tiles first, so that a B panel stays in one L2
-    const unsigned nx = unsigned(p.num_xcd), T = gridDim.x;
-    const unsigned x = blockIdx.x % nx, per = T / nx, rem = T % nx;
-    const unsigned item = x * per + min(x, rem) + blockIdx.x / nx;
+    const unsigned nx = unsigned(p.num_xcd), x = w % nx, per = p.tiles / nx, rem = p.tiles % nx;
+    const unsigned item = x * per + min(x, rem) + w / nx;
     const int mt = int(item % unsigned(p.m_tiles)), n0 = int(item / unsigned(p.m_tiles)) * TN;
     int g = 0, row0, lim;
     int64_t region = 0;
@@ -325,6 +324,22 @@ __global__ __launch_bounds__(WM * WN * 64) void int8_gemm_kernel(I8Params p) {
     }
 }
 
+// The tiles of a workgroup: one, or, under a grid limit, every gridDim.x-th.
+template <typename Tile>
+__device__ __forceinline__ void walk(unsigned tiles, Tile tile) {
+    for (unsigned w = blockIdx.x;;) {
+        tile(w);
+        w += gridDim.x;
+        if (w >= tiles) return;
+        __syncthreads();                           // every wave is done with the tile's LDS
+    }
+}
+
+template <int LAYOUT, int TM, int TN, int S, int WM, int WN, typename OutT>
+__global__ __launch_bounds__(WM * WN * 64) void int8_gemm_kernel(I8Params p) {
+    walk(p.tiles, [&](unsigned w) { ring_tile<LAYOUT, TM, TN, S, WM, WN, OutT>(p, w); });
+}
+
 // ------------------------------------------------------------------ streamed product
 //
 // 16 RB x 16 CB output tiles whose NW waves split K: wave w takes the 128-byte
@@ -338,7 +353,7 @@ __global__ __launch_bounds__(WM * WN * 64) void int8_gemm_kernel(I8Params p) {
 // took twice as long.)  Bound by the launch and the way of the first loads, then
 // by what a CU takes in, about 37 GB/s: 128 x 4096 x 4096 in 8.6 us.
 template <int LAYOUT, int RB, int CB, int NW, int D, typename OutT>
-__global__ __launch_bounds__(NW * 64) void int8_stream_kernel(I8Params p) {
+__device__ __forceinline__ void stream_tile(const I8Params& p, unsigned w) {
     constexpr int TM = 16 * RB, TN = 16 * CB;
     constexpr int UNIT = (TM + TN) * TK;           // bytes of a stage: A's rows, then B's
     constexpr int PER = UNIT / 1024;               // loads per stage
@@ -352,9 +367,8 @@ __global__ __launch_bounds__(NW * 64) void int8_stream_kernel(I8Params p) {
     const int l16 = lane & 15, lq = lane >> 4;
     GFG_LDS uint8_t* const ring[4] = {(GFG_LDS uint8_t*)s0 + wave * UNIT, (GFG_LDS uint8_t*)s1 + wave * UNIT,
                                       (GFG_LDS uint8_t*)s2 + (D > 2 ? wave * UNIT : 0), (GFG_LDS uint8_t*)s3 + (D > 2 ? wave * UNIT : 0)};
-    const unsigned nx = unsigned(p.num_xcd), T = gridDim.x;
-    const unsigned x = blockIdx.x % nx, per = T / nx, rem = T % nx;
-    const unsigned item = x * per + min(x, rem) + blockIdx.x / nx;
+    const unsigned nx = unsigned(p.num_xcd), x = w % nx, per = p.tiles / nx, rem = p.tiles % nx;
+    const unsigned item = x * per + min(x, rem) + w / nx;
     const int mt = int(item % unsigned(p.m_tiles)), n0 = int(item / unsigned(p.m_tiles)) * TN;
     int g = 0, row0, lim;
     int64_t region = 0;
@@ -468,6 +482,19 @@ __global__ __launch_bounds__(NW * 64) void int8_stream_kernel(I8Params p) {
     }
 }
 
+template <int LAYOUT, int RB, int CB, int NW, int D, typename OutT>
+__global__ __launch_bounds__(NW * 64) void int8_stream_kernel(I8Params p) {
+    walk(p.tiles, [&](unsigned w) { stream_tile<LAYOUT, RB, CB, NW, D, OutT>(p, w); });
+}
+
+// Workgroups of a launch over p.tiles tiles: one for each, or as many as the
+// grid limit allows, which is rounded up to whole slots on every XCD.
+unsigned workgroups(const I8Params& p) {
+    const int lim = grid_limit();
+    const unsigned nx = unsigned(p.num_xcd), most = lim > 0 ? (unsigned(lim) + nx - 1) / nx * nx : p.tiles;
+    return p.tiles < most ? p.tiles : most;
+}
+
 template <int LAYOUT, int RB, int CB, int NW, int D>
 int launch_stream(I8Params p, int out_dtype, hipStream_t s) {
     const int groups = LAYOUT == MASKED ? p.G : 1;
@@ -475,7 +502,8 @@ int launch_stream(I8Params p, int out_dtype, hipStream_t s) {
     p.m_tiles = p.tiles_per_group * groups;
     const int64_t tiles = int64_t(p.m_tiles) * ((p.N + 16 * CB - 1) / (16 * CB));
     if (tiles * (NW * 64) >= int64_t(1) << 32) return fail(GFG_EUNSUPPORTED, "the output has too many tiles for one launch");
-    const dim3 grid{unsigned(tiles)}, block(NW * 64);
+    p.tiles = unsigned(tiles);
+    const dim3 grid(workgroups(p)), block(NW * 64);
     if (out_dtype == GFG_OUT_BF16)
         hipLaunchKernelGGL((int8_stream_kernel<LAYOUT, RB, CB, NW, D, __bf16>), grid, block, 0, s, p);
     else
@@ -492,7 +520,8 @@ int launch_ring(I8Params p, int out_dtype, hipStream_t s) {
     p.m_tiles = p.tiles_per_group * groups;
     const int64_t tiles = int64_t(p.m_tiles) * ((p.N + TN - 1) / TN);
     if (tiles * (WM * WN * 64) >= int64_t(1) << 32) return fail(GFG_EUNSUPPORTED, "the output has too many tiles for one launch");
-    const dim3 grid{unsigned(tiles)}, block(WM * WN * 64);
+    p.tiles = unsigned(tiles);
+    const dim3 grid(workgroups(p)), block(WM * WN * 64);
     if (out_dtype == GFG_OUT_BF16)
         hipLaunchKernelGGL((int8_gemm_kernel<LAYOUT, TM, TN, S, WM, WN, __bf16>), grid, block, 0, s, p);
     else
@@ -639,11 +668,20 @@ __global__ __launch_bounds__(256) void int8_few_kernel(const X* __restrict__ xs,
 
 template <int MT, typename X>
 void launch_few_rows(const void* x, const I8Params& p, int out_dtype, hipStream_t s) {
-    const dim3 grid(unsigned((p.N + 31) / 32)), block(256);
+    const dim3 grid(p.tiles), block(256);
     if (out_dtype == GFG_OUT_BF16)
         hipLaunchKernelGGL((int8_few_kernel<MT, X, __bf16>), grid, block, 0, s, static_cast<const X*>(x), p);
     else
         hipLaunchKernelGGL((int8_few_kernel<MT, X, _Float16>), grid, block, 0, s, static_cast<const X*>(x), p);
+}
+
+// Whether M rows of K codes go this way: a workgroup has one tile, so not under
+// a grid limit that is below their number (walking tiles in this kernel costs
+// it 0.5 us where there is no limit).
+bool few(I8Params* p) {
+    p->tiles = unsigned((p->N + 31) / 32);
+    const int64_t rows = p->rows == 3 ? 4 : p->rows;       // (three run as four)
+    return rows <= kFewTokens && rows * ((p->K + TK - 1) / TK * TK) <= kFewCodes && workgroups(*p) == p->tiles;
 }
 
 template <typename X>
@@ -830,8 +868,7 @@ extern "C" int int8_linear(const void* x, int32_t in_dtype, const int8_t* b, con
     if (int rc = check_quant(fn, x, in_dtype, M, K, q, scale)) return rc;
     if (int rc = check_operands(fn, q, scale, b, b_scale, bias, false, d)) return rc;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    if (M <= kFewTokens && (M == 3 ? 4 : M) * ((K + TK - 1) / TK * TK) <= kFewCodes) {      // (three rows run as four)
-        const I8Params p = product(nullptr, nullptr, b, b_scale, bias, nullptr, d, M, N, K, 1);
+    if (I8Params p = product(nullptr, nullptr, b, b_scale, bias, nullptr, d, M, N, K, 1); few(&p)) {
         if (in_dtype == GFG_IN_F32) return launch_few<float>(x, p, out_dtype, s);
         if (in_dtype == GFG_IN_BF16) return launch_few<__bf16>(x, p, out_dtype, s);
         return launch_few<_Float16>(x, p, out_dtype, s);

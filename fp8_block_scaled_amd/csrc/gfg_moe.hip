@@ -1250,6 +1250,8 @@ template <int W, typename A>
 int launch_layer(MoeParams p, hipStream_t s) {
     int cus = 0;
     if (int rc = device_cus(&cus)) return rc;
+    // what a grid limit leaves of the CUs: the kernels walk their items by the grid they get
+    if (const int lim = grid_limit(); lim > 0 && lim < cus) cus = lim;
     const int P = p.T * p.k;
     const dim3 block(kWaves * 64);
     // one workgroup a CU: what its LDS has left after the fixed parts and the

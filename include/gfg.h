@@ -467,9 +467,14 @@ GFG_API int moe_int8_layer(const void* x, int32_t dtype, const int32_t* topk_ids
  * 2^22); their results do not depend on it.
  *
  * grouped_fp8_set_grid_limit: at most max_workgroups workgroups per GEMM
- * launch (0, the default: one per CU, fewer when there are fewer tiles).  The
- * grid is then rounded up to a multiple of num_xcd.  Each workgroup walks
- * more tiles; the results do not change.  Negative: GFG_EINVAL.
+ * launch.  0, the default, is no limit: one per CU, fewer when there are fewer
+ * tiles (the int8 products' smaller tiles: one per tile).  The grid of a GEMM
+ * launch is then rounded up to a multiple of num_xcd.  Each workgroup walks
+ * more tiles; the results do not change.  The limit covers the FP8, MX and int8
+ * products (int8_linear of a few tokens then takes two launches) and, not
+ * rounded up, the expert layer's two products, whose fp32 sums it may reorder;
+ * not the quantizers, the router and the layer's last sum over a token's pairs.
+ * Negative: GFG_EINVAL.
  */
 enum gfg_tile_shape { GFG_TILE_AUTO = 0, GFG_TILE_128x256 = 1, GFG_TILE_256x256 = 2 };
 GFG_API int grouped_fp8_set_tile_order(int32_t num_xcd, int32_t group_m);
