@@ -37,7 +37,7 @@ RIDGE_FLOP_PER_BYTE = PEAK_FP8_TFLOPS * 1e12 / (PEAK_HBM_GBS * 1e9)
 # The largest of the five reference workloads: 8 experts x 4096 rows, N=7168, K=2304.
 DEFAULT_WORKLOAD = "contig_g8_m4096_n7168_k2304_logmag"
 _CSRC = os.path.join(ROOT, "fp8_block_scaled_amd", "csrc")
-KERNEL_SRC = [os.path.join(_CSRC, n) for n in ("gfg_gemm.hip", "gfg_gemm256.hip", "gfg_device.h")]
+KERNEL_SRC = [os.path.join(_CSRC, n) for n in ("gfg_gemm.hip", "gfg_gemm256.hip", "gfg_device.h", "gfg_tile256.h")]
 QUANT_SRC = [os.path.join(_CSRC, "gfg_quant.hip")]
 
 
