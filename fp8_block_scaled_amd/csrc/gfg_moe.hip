@@ -526,19 +526,19 @@ __device__ __forceinline__ void store_hidden(const MoeParams& p, int pair, int c
 
 // ---- hidden rows: h = silu(g) * u.
 //
-// A work item is C (16 or 8) columns of I for one unit: the C gate rows and the
-// C up rows of W1, which make C / 8 fragments of 16 rows.  The eight waves
-// split H: wave w takes blocks w, w + 8, ...  LDS stage: 2 C weight rows of 128
-// bytes, 16-byte chunks XOR-swizzled by row & 7, then (unless they are
-// resident) NR token rows of 256 bytes, chunks XOR-swizzled by row & 15.
+// A work item is 16 columns of I for one unit: the 16 gate rows and the 16 up
+// rows of W1, a fragment each.  The eight waves split H: wave w takes blocks w,
+// w + 8, ...  LDS stage: 32 weight rows of 128 bytes, 16-byte chunks
+// XOR-swizzled by row & 7, then (unless they are resident) NR token rows of 256
+// bytes, chunks XOR-swizzled by row & 15.
 // Weight chunk c of a row (16 k's) meets the token chunks 2 c and 2 c + 1: the
 // MFMA's k order is a permutation that both operands share.  A unit has at most
 // NR rows; the MFMA's other columns repeat them, and their sums are not stored.
-template <int W, typename A, int NR, int C, bool RES>
+template <int W, typename A, int NR, bool RES>
 __device__ __forceinline__ void up_items(const MoeParams& p, const GFG_LDS Routing* r, GFG_LDS uint8_t* ring, GFG_LDS uint8_t* rows_mem,
                                          GFG_LDS v4f* red) {
     typedef typename Vec<A>::v8 v8;
-    constexpr int F = C / 8, WL = C / 4, XL = RES ? 0 : NR / 4, PER = WL + XL, STAGE = PER * 1024 + kScaleBytes;
+    constexpr int C = 16, F = 2, WL = 4, XL = RES ? 0 : NR / 4, PER = WL + XL, STAGE = PER * 1024 + kScaleBytes;
     constexpr bool TWICE = NR <= 8;            // the waves' sums have room for two items
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int l16 = lane & 15, lq = lane >> 4;
@@ -640,11 +640,9 @@ __device__ __forceinline__ void up_items(const MoeParams& p, const GFG_LDS Routi
         float sc[2] = {0.0f, 0.0f};
         auto apply = [&]() {
 #pragma unroll
-            for (int f = 0; f < F; ++f) {
-                const float s = F == 2 ? sc[f] : lq < 2 ? sc[0] : sc[1];
+            for (int f = 0; f < F; ++f)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) acc[f][i] = fmaf(part[f][i], s, acc[f][i]);
-            }
+                for (int i = 0; i < 4; ++i) acc[f][i] = fmaf(part[f][i], sc[f], acc[f][i]);
         };
         for (int kb = wave; kb < KB; kb += kWaves) {
             __builtin_amdgcn_sched_barrier(0);
@@ -659,8 +657,8 @@ __device__ __forceinline__ void up_items(const MoeParams& p, const GFG_LDS Routi
                     wg = read_word(sa + uint32_t(lane * 4));
                     wu = read_word(sa + 256u + uint32_t(lane * 4));
                 } else {                       // lanes of the finishing step's rows: see there
-                    cg = read_quad(sa + uint32_t((lq & (C / 4 - 1)) * 16));
-                    cu = read_quad(sa + 256u + uint32_t((lq & (C / 4 - 1)) * 16));
+                    cg = read_quad(sa + uint32_t(lq * 16));
+                    cu = read_quad(sa + 256u + uint32_t(lq * 16));
                 }
             }
             read_block(w, x, w0 + so, w1 + so, xa);
@@ -705,18 +703,12 @@ __device__ __forceinline__ void up_items(const MoeParams& p, const GFG_LDS Routi
         for (int w = 0; w < kWaves - 1; ++w)
 #pragma unroll
             for (int f = 0; f < F; ++f) acc[f] += sums[(w * F + f) * 4 * NR + lq * NR + lr];
-        v4f g = acc[0], v;
-        if constexpr (F == 2) {
-            v = acc[F - 1];
-        } else {                               // quads 0, 1 hold the gate rows, quads 2, 3 the up rows
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = __shfl_xor(acc[0][i], 32, 64);
-        }
+        v4f g = acc[0], v = acc[1];
         if constexpr (W == INT8) {
             g *= cg;
             v *= cu;
         }
-        if (l16 < un.rows && lq < C / 4) store_hidden(p, r->list[un.first + l16], it * C + lq * 4, g, v);
+        if (l16 < un.rows) store_hidden(p, r->list[un.first + l16], it * C + lq * 4, g, v);
     }
 }
 
@@ -939,18 +931,8 @@ __global__ __launch_bounds__(kWaves * 64) void moe_up_kernel(MoeParams p) {
         load_resident(rows_mem, make_rsrc(p.x, uint32_t(p.T) * uint32_t(p.H) * 2u), p.H * 2, p.resident);
         const int rows = build_routing(r, ring, p.ids, p.T * p.k, p.E,
                                        [&](const int (&total)[6]) { return choose_rows<4, 8>(total, 4, 0, p.ring); });
-        // items of 8 columns where they spread better over the workgroups (one
-        // token, k = 9, I = 512: 288 items of 16 or 576 of 8 over 256: the layer
-        // takes 34.2 us with 8, 35.4 with 16)
-        const int n = __builtin_amdgcn_readfirstlane(r->units) * (p.I / 16), grid = int(gridDim.x);
-        const int walk16 = (n + grid - 1) / grid * 2, walk8 = (2 * n + grid - 1) / grid;
-        if (walk8 * 8 < walk16 * 7) {
-            if (rows <= 4) up_items<W, A, 4, 8, true>(p, r, ring, rows_mem, red);
-            else up_items<W, A, 8, 8, true>(p, r, ring, rows_mem, red);
-        } else {
-            if (rows <= 4) up_items<W, A, 4, 16, true>(p, r, ring, rows_mem, red);
-            else up_items<W, A, 8, 16, true>(p, r, ring, rows_mem, red);
-        }
+        if (rows <= 4) up_items<W, A, 4, true>(p, r, ring, rows_mem, red);
+        else up_items<W, A, 8, true>(p, r, ring, rows_mem, red);
     } else {
         const int rows = build_routing(r, ring, p.ids, p.T * p.k, p.E, [&](const int (&total)[6]) {
             const int few = choose_rows<4, 16>(total, 4, 1, p.ring), rows = shared_rows(total, p.I / 64);
@@ -965,9 +947,9 @@ __global__ __launch_bounds__(kWaves * 64) void moe_up_kernel(MoeParams p) {
         });
         if (rows == 64) shared_items<W, A, 64, true>(p, r, ring);
         else if (rows == 32) shared_items<W, A, 32, true>(p, r, ring);
-        else if (rows <= 4) up_items<W, A, 4, 16, false>(p, r, ring, rows_mem, red);
-        else if (rows <= 8) up_items<W, A, 8, 16, false>(p, r, ring, rows_mem, red);
-        else up_items<W, A, 16, 16, false>(p, r, ring, rows_mem, red);
+        else if (rows <= 4) up_items<W, A, 4, false>(p, r, ring, rows_mem, red);
+        else if (rows <= 8) up_items<W, A, 8, false>(p, r, ring, rows_mem, red);
+        else up_items<W, A, 16, false>(p, r, ring, rows_mem, red);
     }
     GFG_WAITCNT(0, 0);                         // the last loads land before the workgroup ends
 }
@@ -1255,10 +1237,12 @@ int launch_layer(MoeParams p, hipStream_t s) {
     const int P = p.T * p.k;
     const dim3 block(kWaves * 64);
     // one workgroup a CU: what its LDS has left after the fixed parts and the
-    // resident rows goes to the rings.  (One token, H = 7168, 14 KB of rows: 34.2 us
-    // a layer, 35.7 with the rows in the stages; 12 tokens, H = 2048, 48 KB: 93.6 and
-    // 94.4, no more than the boxes differ, so larger rows leave the LDS to the rings.)
-    const int64_t up_items = (int64_t(P < p.E ? P : p.E) + P / 4) * (p.I / 8);
+    // resident rows goes to the rings.  (Rows resident and in the stages: one token,
+    // k = 9, H = 7168, I = 512: 29.4 and 30.2 us a layer; k = 3, H = 4096, I = 1536:
+    // 21.8, 22.5; two tokens of H = 7168, 28 KB: 43.1, 43.6; but 12 of H = 2048, 48 KB:
+    // 91.4 and 92.0, no more than runs differ, so larger rows leave the LDS to the
+    // rings.)
+    const int64_t up_items = (int64_t(P < p.E ? P : p.E) + P / 4) * (p.I / 16);
     const int up_grid = int(up_items < cus ? up_items : cus);
     const int x_bytes = p.T * p.H * 2;
     p.resident = x_bytes <= 32 * 1024 ? (x_bytes + 1023) & ~1023 : 0;
