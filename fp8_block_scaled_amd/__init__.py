@@ -175,12 +175,16 @@ def set_tile_order(num_xcd: int = 8, group_m: int = 0) -> None:
 
 
 def set_tile_shape(shape: int = TILE_AUTO) -> None:
-    """Output tile of the plain FP8 GEMM calls: TILE_AUTO, TILE_128x256 or TILE_256x256."""
+    """Output tile of the plain FP8 GEMM calls: TILE_AUTO, TILE_128x256 or TILE_256x256 (process-wide).
+
+    The int8 products follow it too: TILE_128x256 keeps them on their smaller tiles, TILE_256x256 on their large ones,
+    however few the rows.
+    """
     _check(load_library().grouped_fp8_set_tile_shape(shape))
 
 
 def set_grid_limit(max_workgroups: int = 0) -> None:
-    """Cap the workgroups of a GEMM launch (0: one per CU)."""
+    """Cap the workgroups of a GEMM launch, FP8, MX or int8, and of the expert layer's products (0: no cap)."""
     _check(load_library().grouped_fp8_set_grid_limit(max_workgroups))
 
 

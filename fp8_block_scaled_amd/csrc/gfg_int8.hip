@@ -29,11 +29,11 @@ typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
 // maximum and the encoding, HELD a lane (longer rows read the rest again, from
 // the cache).  LPR lanes share a row: a wave up to 2048 elements, two waves up
 // to 3 * 1024, four past that; with more than one, the maximum crosses the waves
-// through LDS.  Bound by the copy rate (5.0 TB/s).  Measured, bf16, us and TB/s
-// of reads and writes: 32768 x 2048 41, 4.9; 8192 x 7168 35.5, 5.0; 4096 x 16384
-// 41.3, 4.9 (with half of the row held: 44.7; f32 70.4 and 80.1); 32768 x 2304
-// 48.3, 4.7 on two waves, 55.4 on four, whose second pass has few lanes; f32
-// 16384 x 3584 53.9 on two, 49.7 on four.
+// through LDS.  Bound by the copy rate (5.0 TB/s).  Measured, us on one, two and
+// four waves a row: bf16 32768 x 2048 40.8 (4.9 TB/s of reads and writes), 41.1,
+// 49.5; 32768 x 2304 45.6, 47.9, 54.7 (f32 73.0, 68.8, 67.8); 16384 x 3584 38.1, 36.0,
+// 34.3 (f32 66.2, 54.5, 50.0); 8192 x 7168 42.4, 40.9, 33.6 (5.2 TB/s).  4096 x 16384
+// on four: 41.2, with half of the row held 45.0 (f32 70.3 and 80.3).
 template <typename T> struct Chunk;            // 8 elements of a row
 template <> struct Chunk<__bf16> {
     u32x4 w;
@@ -169,8 +169,9 @@ void launch_quant(const void* x, uint8_t* q, float* scale, int64_t M, int K, hip
 // every wave finish the previous step, whose buffer the new loads go to).
 // These are the launches with too few 256 x 256 tiles, whose time is the
 // latency of a tile's first loads plus a chain of steps, so depth matters
-// more than the bytes per step (1024 x 4096 x 4096: 37.9 us with one stage ahead,
-// 26.1 with three; 512 x 4096 x 4096 on 64 x 64: 34, 17.2).  LDS row R (128 bytes)
+// more than the bytes per step (with one stage ahead, the first form of this
+// kernel, 1024 x 4096 x 4096 took 1.6 times as long, 512 x 4096 x 4096 twice; they
+// take 23.5 and 17.5 us).  LDS row R (128 bytes)
 // holds its 16-byte chunks XOR-swizzled by R & 7, so that the 16 rows that a
 // fragment read touches spread over all banks.  Rows past the operand's end and chunks past K lie
 // outside the buffer window, where the hardware returns zeros, so no size
@@ -349,9 +350,9 @@ __global__ __launch_bounds__(WM * WN * 64) void int8_gemm_kernel(I8Params p) {
 // once; the waves' sums meet in LDS at the end (integers: exact in any order).
 // (Loading the fragments straight into registers instead is slower: a
 // fragment's adjacent lanes are adjacent rows, so four lanes touch four cache
-// lines, and the load path then passes 16 bytes a cycle, not 64: 1 x 7168 x 2304
-// took twice as long.)  Bound by the launch and the way of the first loads, then
-// by what a CU takes in, about 37 GB/s: 128 x 4096 x 4096 in 8.6 us.
+// lines: 1 x 7168 x 2304 took twice as long.)  Bound by the launch and the way of
+// the first loads, then by a wave's chain of units: 1 x 7168 x 2304 5.9 us with cold
+// weights (16.5 MB), 3.5 with warm ones; 128 x 4096 x 4096 9.1.
 template <int LAYOUT, int RB, int CB, int NW, int D, typename OutT>
 __device__ __forceinline__ void stream_tile(const I8Params& p, unsigned w) {
     constexpr int TM = 16 * RB, TN = 16 * CB;
@@ -537,9 +538,10 @@ int launch_ring(I8Params p, int out_dtype, hipStream_t s) {
 // itself, into LDS, while its first weights are on the way (the codes and
 // scales are those of the token quantizer, bit for bit), then streams its 32
 // weight rows like the kernel above.  One launch instead of two: 7168 x 2304 with
-// cold weights (16.5 MB), 1 token 6.5 us, 10.2 in two launches; 4 tokens 8.0, 10.5
-// (every workgroup encodes all rows, half a microsecond each, and 5 tokens take 9.9
-// in two launches, so a few more of them would gain nothing).
+// cold weights (16.5 MB), bf16: 1 token 6.5 us, 9.5 in two launches; 2: 7.0, 9.7; 4:
+// 8.0, 9.9 (f32 6.7, 9.0 and 8.1, 9.2).  Every workgroup encodes all rows, half a
+// microsecond each, and 5 tokens take 10.0 in two launches, so a few more of them
+// would gain nothing.
 constexpr int kFewTokens = 4;
 constexpr int kFewCodes = 32 * 1024;           // bytes of LDS for the codes
 
@@ -695,15 +697,17 @@ int launch_few(const void* x, const I8Params& p, int out_dtype, hipStream_t s) {
 }
 
 // The launches with too few 256 x 256 tiles, by how many tiles of each size
-// there are (M x N x K, us in a graph with warm operands, the chosen tile first):
-//  * few rows: the streamed 16 x 32 tile (1 x 7168 x 2304: 3.6, 32 x 32 3.8,
-//    64 x 64 5.9; 16 x 4096 x 4096: 4.1, 4.5, 8.5), or 32 x 32 up to 32 rows;
-//  * 192 tiles of 128 x 128 or more: those (512 x 7168 x 2304: 15.8, 64 x 64
-//    18.6; 1024 x 4096 x 4096: 26.1, 33.7);
-//  * up to 512 tiles of 32 x 32: those, streamed (128 x 4096 x 4096: 8.6, 64 x 64
-//    9.6; 4096 x 64 x 16384: 21.8, 27.1);
-//  * else 64 x 64 (2000 x 300 x 16384: 30.0, 32 x 32 52; 512 x 4096 x 4096: 17.2,
-//    30.4, 128 x 128 20.8).
+// there are (M x N x K, us, the chosen tile first):
+//  * up to 16 rows: the streamed 16 x 32 tile (cold weights, 32 x 32 second: 1 x
+//    1024 x 7168: 5.6, 6.5; 4 x 2048 x 16384: 14.9, 16.1; 1 x 4096 x 4096: 6.6, 7.1; 1 x
+//    7168 x 2304: 5.9, 5.9; but 1 x 28672 x 4096, 896 tiles: 28.7, 25.3), or 32 x 32 up to
+//    32 rows (32 x 4096 x 4096: 5.9, 64 x 64 9.4);
+//  * 192 tiles of 128 x 128 or more: those (512 x 7168 x 2304, 224 of them: 16.0,
+//    64 x 64 20.0; 1024 x 4096 x 4096, 256: 23.5, 30.8);
+//  * up to 512 tiles of 32 x 32: those, streamed (128 x 4096 x 4096: 9.1, 64 x 64
+//    10.0; 300 x 770 x 4096: 5.9, 9.8; 4096 x 64 x 16384: 22.4, 37.6);
+//  * else 64 x 64 (2000 x 300 x 16384: 28.4, 32 x 32 50.4; 128 x 7168 x 2304: 7.6,
+//    11.2; 512 x 4096 x 4096: 17.5, 29.2, 128 x 128 21.0).
 template <int LAYOUT>
 int launch_small(const I8Params& p, int out_dtype, hipStream_t s) {
     auto tiles = [&](int64_t tm, int64_t tn) {
@@ -719,9 +723,14 @@ int launch_small(const I8Params& p, int out_dtype, hipStream_t s) {
 // Launch the product on the tile that suits it: the 256 x 256 kernel (whose
 // tiles have 192 rows where that fills the CUs better) wherever tiles of
 // 128 x 128 would need a second round over the CUs.  Measured, us, the 256
-// kernel and the smaller tiles: 768 x 7168 x 2304 (336 tiles of 128 x 128) 25.7,
-// 28.3; 700 x 6144 x 4096 (288) 37.5, 40.7; 2048 x 2104 x 1024 (272) 17.1, 18.5;
-// but 1024 x 4096 x 4096 (256) 37.4, 22.3; 1920 x 2048 x 7168 (240) 61.6, 35.2.
+// kernel and the smaller tiles' own choice: 2000 x 4096 x 4096 (512 tiles of
+// 128 x 128) 41.5, 48.4; 768 x 7168 x 2304 (336) 26.4, 27.9; 700 x 6144 x 4096 (288) 38.4,
+// 40.0; 2048 x 2104 x 1024 (272) 17.1, 17.9; but 1024 x 4096 x 4096 (256) 38.3, 23.5;
+// 1920 x 2048 x 7168 (240) 61.8, 37.1.  Just past the threshold tiles of 64 x 64 would
+// be faster than both (34.5 and 15.4 at 288 and 272).  The masked layout is counted
+// by its capacity, since the live rows are device data: with 1 to 32 of 1024 rows in
+// each of 8 groups, N = 2048, K = 7168, the 256 kernel takes 69 us where the smaller
+// tiles take 59 to 63; with 128 rows 74 and 85, with 1024 104 and 171.
 // `p` holds everything but the tile counts.
 int launch_i8(const char* fn, I8Params p, int layout, int out_dtype, hipStream_t s) {
     const int groups = layout == MASKED ? p.G : 1;

@@ -18,19 +18,23 @@
 // stage.  The refills of a tile's last two steps load the next tile's first
 // two stages.
 //
-// What bounds it: a CU takes in about 62 GB/s through the direct-to-LDS loads
-// (1.05 us for a step's 64 KB, 0.90 us for the 56 KB of a 192-row tile, with the
-// operands in L2 and idle neighbours), a little less than the MFMAs would use
-// (0.85 us); with every CU busy a step takes 1.4-1.55 us, at a lower clock.
-// 4096 x 4096 x 16384: 203-207 us, 2655-2710 TOP/s; 8 x 4096 x 7168 x 2304: 466
-// us, 2320; a library's product of the first shape: 2408.
+// What bounds it: with every CU busy, a wave alone on its SIMD, whose own loads,
+// LDS reads and barriers hold up its MFMAs, at the clock that the chip holds under
+// this load; between tiles, the epilogue.  8 x 4096 x 7168 at five depths fits 1.58
+// us a step and 6.2 us a tile (the FP8 kernel on the same box: 1.53 and 3.2); a tile
+// alone on the chip takes 1.05 us a step, 0.90 with 192 rows.  Counters: 4096 x 4096 x
+// 16384, 205-219 us, 2510-2680 TOP/s (a library's product: 2408): the matrix pipes are
+// busy 67% of the time at 1.97 GHz, each CU takes in 42 GB/s from L2, no LDS bank
+// conflicts; 8 x 4096 x 7168 x 2304, 470-496 us, 2180-2300: 51% at 2.06 GHz, 34 GB/s; the
+// masked 8 x up to 1024 rows x 2048 x 7168, one round of 192-row tiles, 87-90 us: 37%
+// at 2.4 GHz, 32 GB/s.
 //
 // Rows of a tile: 192 where 7/8 of its rounds over the CUs beat the 256-row
 // tile's (a 192-row tile moves 7/8 of the bytes).  Measured, us, 192 and 256:
-// 2000 x 4096 x 4096 (176, 128 tiles) 42.5, 46.8; 768 x 7168 x 2304 (112, 84)
-// 25.7, 29.1; 5000 x 7168 x 2304 (756, 560: three rounds either way) 78, 88; but
-// 8192 x 7168 x 2304 (1204, 896: 5 and 4) 127, 122; 4096 x 4096 x 16384 (352,
-// 256: 2 and 1) 281, 203.  (The contiguous layout's experts start at 128-row
+// 2000 x 4096 x 4096 (176, 128 tiles) 39.9, 45.1; 768 x 7168 x 2304 (112, 84)
+// 26.3, 30.0; 5000 x 7168 x 2304 (756, 560: three rounds either way) 82.8, 91.1; but
+// 8192 x 7168 x 2304 (1204, 896: 5 and 4) 138.8, 130.1; 4096 x 4096 x 16384 (352,
+// 256: 2 and 1) 281, 205.  (The contiguous layout's experts start at 128-row
 // tiles, which 192 does not divide: 256 there.)
 //
 // Sizes that are no multiple of the tile cost nothing inside the loop: rows

@@ -16,11 +16,11 @@
 // products run on 16x16x32 MFMAs whose 16 rows are weight rows and whose 16
 // columns are tokens.  Two launches: the experts' hidden rows, and the
 // weighted sum of their down projections; where the experts' items are shared
-// out over the CUs (shared_down), that sum is a launch of its own.  Measured, us
-// up / down (/ sum): one token, k = 9, E = 385, H = 7168, I = 512, FP8: 18.5 /
-// 12 (99 MB); 32 tokens of it: 250 / 134 (2.25 GB, 5.6 TB/s); 100 tokens, k = 2,
-// E = 8, H = 4096, I = 1792, FP8: 34 / 19 / 4 (178 MB); 5 tokens, k = 6, E = 64,
-// H = 2048, I = 1408, int8: 32 / 20 / 4 (216 MB).
+// out over the CUs (shared_down), that sum is a launch of its own.  Measured in a
+// trace, us up / down (/ sum): one token, k = 9, E = 385, H = 7168, I = 512, FP8: 18 /
+// 11 (99 MB); 32 tokens of it: 246-274 / 135-148 (2.25 GB, 5.0-5.6 TB/s); 100 tokens,
+// k = 2, E = 8, H = 4096, I = 1792, FP8: 35-37 / 19-22 / 4.5 (178 MB); 5 tokens, k = 6,
+// E = 64, H = 2048, I = 1408, int8: 31-33 / 20 / 4.5 (216 MB).
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -50,8 +50,8 @@ __device__ __forceinline__ int wave_min(int v) { return wave_reduce(v, [](int a,
 // lowest index; lane j keeps the result of round j.  The rounds are a chain of
 // wave reductions, which stay in registers (DPP rotations; through LDS they cost
 // twice as much): 3.8 us for one token of 256 experts, k = 8, of which 2.5 are the
-// launch; 8.3 us for 4096 tokens of 385 in fp32, k = 9 (6.6 MB: 0.8 TB/s), bound
-// by those chains.
+// launch; 8.3-9.2 us for 4096 tokens of 385 in fp32, k = 9 (6.6 MB: 0.7-0.8 TB/s),
+// bound by those chains.
 template <typename T, int EPL>
 __device__ __forceinline__ void topk_row(const T* __restrict__ row, const float* __restrict__ bias, int32_t* __restrict__ ids,
                                          float* __restrict__ weights, int lane, int E, int k, bool sigmoid, bool renorm,
@@ -395,13 +395,15 @@ __device__ __forceinline__ Unit unit_of(const GFG_LDS Routing* r, int u) {
 // and across the ends of experts and tiles; no barrier stands between a load
 // and its MFMAs.  Whole 128-byte lines by adjacent lanes: loaded straight into
 // MFMA fragments, adjacent lanes are adjacent rows, and a load takes four times
-// as long.  What bounds the kernels: HBM, 5.0-5.6 TB/s where the launch is long
-// (32 tokens, k = 9, E = 385, H = 7168, I = 512: 2.25 GB in 400 us), and for
-// short ones what a CU takes in, about 37 GB/s, after some 5 us of launch,
-// routing and the first loads' way (an up launch of 16 items takes 7.5 us).  So
-// what goes beside the weights is kept small: the tokens' rows stay in LDS for
-// the whole launch where they are small, else the stage holds only as many of
-// them as units have; an expert's scales come once for a unit.
+// as long.  What bounds the kernels: HBM where the launch is long (32 tokens, k = 9,
+// E = 385, H = 7168, I = 512: 5.6 TB/s up and 5.1 down by the traffic counters).  The
+// short ones reach 3.0-4.4 TB/s and 12-19 GB/s into each CU, with the matrix pipes 2-11%
+// busy and half of the waves' time spent waiting for memory: some 5 us of
+// launch, routing and the first loads' way (an up launch of 16 items takes 7.5 us),
+// then the latency of each wave's chain of stages.  So what goes beside the weights
+// is kept small: the tokens' rows stay in LDS for the whole launch where they are
+// small, else the stage holds only as many of them as units have; an expert's
+// scales come once for a unit.
 //
 // The fragments are read from LDS in inline assembly, each group together with
 // its wait: the stage index is a run-time value, so the compiler, which cannot
@@ -507,7 +509,7 @@ __device__ __forceinline__ void load_resident(GFG_LDS uint8_t* dst, __amdgpu_buf
 
 // h = silu(g) * u for four columns of a pair, in two bf16 halves, high and low:
 // 16 significant bits with fp32's range, so that the only rounding to 16 bits
-// is the output's.  A finite h above the largest bf16 keeps that as its high
+// is the output's.  (The sums over them are of raw codes, before their scales.)  A finite h above the largest bf16 keeps that as its high
 // half and the rest as its low one; a NaN or an infinity has no low half.
 __device__ __forceinline__ void store_hidden(const MoeParams& p, int pair, int col, const v4f& g, const v4f& u) {
     constexpr float kTop = 0x1.FEp127f;        // the largest bf16
@@ -725,9 +727,11 @@ __device__ __forceinline__ void up_items(const MoeParams& p, const GFG_LDS Routi
 // that gate and up meet in a wave.  DOWN: 128 rows of W2; sums go to y.
 // Units of 64 rows where that saves a round of items over the workgroups: a few
 // experts with slightly more than 32 rows would otherwise cost a second pass
-// over their weights (100 tokens, k = 2, E = 8, H = 4096, I = 1792: 64 us a layer,
-// 70 with units of 32 alone; 130 tokens: 64, 92).  (Smaller stages leave room for
-// one more of them.)  Units of 8, two MFMA halves in one, measured no faster.
+// over their weights (us a layer, units by the rule and of 32 alone: 100 tokens,
+// k = 2, E = 8, H = 4096, I = 1792: 63.7, 69.9; 130 tokens: 66.6, 89.5; of 64 alone: 48
+// tokens with one or two rows an expert 97.1, by the rule 93.3).  (Smaller stages
+// leave room for one more of them.)  Units of 8, two MFMA halves in one, measured
+// no faster.
 __device__ __forceinline__ int shared_rows(const int (&total)[6], int tiles) {
     const int grid = int(gridDim.x);
     return (total[5] * tiles + grid - 1) / grid < (total[4] * tiles + grid - 1) / grid ? 64 : 32;
@@ -938,9 +942,13 @@ __global__ __launch_bounds__(kWaves * 64) void moe_up_kernel(MoeParams p) {
             const int few = choose_rows<4, 16>(total, 4, 1, p.ring), rows = shared_rows(total, p.I / 64);
             // KB a block of K for 16 columns: streamed, and shared; the latter's
             // coarser items have to fill the launch too.  Measured, us a layer,
-            // shared and streamed: 100 tokens, k = 2, E = 8, H = 4096, I = 1792: 64,
-            // 75; 130 tokens: 64, 86; but 48 tokens with one or two rows an expert,
-            // H = 4096, I = 1024: 106, 96.
+            // shared and streamed: 100 tokens, k = 2, E = 8, H = 4096, I = 1792: 63.6,
+            // 72.4; 200 tokens 72.3, 104; 64 tokens, k = 6, E = 64, H = 2048, I = 1408: 125,
+            // 136; the rule streams 48 tokens with one or two rows an expert,
+            // H = 4096, I = 1024: 102, 93.1; 4 tokens, k = 9, E = 385: 94.6, 75.5.  Near
+            // its threshold it shares where streaming is faster: 30 tokens of the
+            // first layer 59.7, 56.1; 40 tokens, k = 4, E = 32, H = 3584, I = 768: 79.3,
+            // 74.6.
             const int units = total[rows == 32 ? 4 : 5];
             const int streamed = total[few == 4 ? 1 : few == 8 ? 2 : 3] * (4 + few / 4), shared = units * 6;
             return shared * 10 < streamed * 9 && units * (p.I / 64) * 4 >= int(gridDim.x) * 3 ? rows : few;
@@ -1127,8 +1135,9 @@ __global__ __launch_bounds__(kWaves * 64) void moe_down_kernel(MoeParams p) {
     const int units = __builtin_amdgcn_readfirstlane(r->units), KB = p.I / 128;
     // the waves that share a unit: the split with the shortest longest walk, in
     // blocks of I; entering a unit costs about three.  Measured, us a layer of one
-    // token, H = 7168: k = 9, I = 512: 31.8 unsplit, 34.0 split; k = 2, I = 2048:
-    // 27.4 unsplit, 25.0 split.
+    // token, unsplit and split as far as there is room: H = 7168, k = 9, I = 512: 29.2,
+    // 31.6 (by the rule unsplit); k = 2, I = 2048: 24.9, 24.5 (by the rule split in
+    // four: 23.8); H = 2048, k = 6, I = 1408: 24.8, 27.7.
     constexpr int kEnter = 3;
     int ks = 1, best = (units + kWaves - 1) / kWaves * (KB + kEnter);
     for (int c = 2; c <= p.ks_most; c *= 2) {
@@ -1166,7 +1175,7 @@ __global__ __launch_bounds__(kWaves * 64) void moe_down_kernel(MoeParams p) {
 }
 
 // The down projection by shared items, and the sums over a token's pairs.
-// (A round of 256 items, 128 x 1408 each, takes 10.5 us: 4.4 TB/s of weights.)
+// (384 items, 128 x 1408 each, 1.5 rounds: 20.5 us, 3.4-3.8 TB/s of weights.)
 template <int W>
 __global__ __launch_bounds__(kWaves * 64) void moe_down_shared_kernel(MoeParams p) {
     __shared__ Routing routing;
@@ -1213,13 +1222,17 @@ constexpr int kLds = 160 * 1024;
 
 // Whether the down projection goes by shared items and a launch that combines
 // them, from the KB that the busiest CU would read either way if the pairs
-// spread evenly over min(T * k, E) experts.  (A CU reads about 37 KB a
-// microsecond; the second launch counts as 180 KB.)  Walking all units for 16
-// or 32 columns leaves CUs idle where H is small and reads the rows again for
-// every 16 columns where experts have many.  Measured, us, walked / shared with
-// its second launch: 5 tokens, k = 6, E = 64, H = 2048, I = 1408: 31 / 25; 100
-// tokens, k = 2, E = 8, H = 4096, I = 1792: 42 / 32; one token, k = 9, E = 385,
-// H = 7168, I = 512: 13.6 / 14.0; 32 tokens of the same: 127 / 137.
+// spread evenly over min(T * k, E) experts.  (The second launch counts as 180 KB.)
+// Walking all units for 16 or 32 columns leaves CUs idle where H is small and reads
+// the rows again for every 16 columns where experts have many.  Measured, us a
+// layer, walked and shared: 5 tokens, k = 6, E = 64, H = 2048, I = 1408: 62.9, 58.1; 12
+// tokens of it 104, 91.9; 100 tokens, k = 2, E = 8, H = 4096, I = 1792: 83.5, 63.8; but
+// one token, k = 9, E = 385, H = 7168, I = 512: 29.6, 31.6; 32 tokens of it 390, 397.
+// Near the threshold it walks where sharing is faster: 30 tokens, k = 2, E = 8
+// 59.8, 53.4; 40 tokens, k = 4, E = 32, H = 3584, I = 768: 79.3, 73.1.  Pairs of other
+// ranks' experts are counted too, since the ids are device data: a rank with an
+// eighth of them (48 tokens, k = 8, E = 48, H = 4096, I = 1024) shares, 93.3, where
+// walking takes 91.3.
 bool shared_down(const MoeParams& p, int cus, int rt) {
     const float P = float(p.T) * float(p.k), experts = P < float(p.E) ? P : float(p.E), rows = P / experts;
     const float split8 = ceilf(rows / 8), split32 = ceilf(rows / 32), blocks = float(p.I / 128);
@@ -1237,11 +1250,11 @@ int launch_layer(MoeParams p, hipStream_t s) {
     const int P = p.T * p.k;
     const dim3 block(kWaves * 64);
     // one workgroup a CU: what its LDS has left after the fixed parts and the
-    // resident rows goes to the rings.  (Rows resident and in the stages: one token,
-    // k = 9, H = 7168, I = 512: 29.4 and 30.2 us a layer; k = 3, H = 4096, I = 1536:
-    // 21.8, 22.5; two tokens of H = 7168, 28 KB: 43.1, 43.6; but 12 of H = 2048, 48 KB:
-    // 91.4 and 92.0, no more than runs differ, so larger rows leave the LDS to the
-    // rings.)
+    // resident rows goes to the rings.  (Us a layer, rows resident and in the stages:
+    // one token, k = 9, H = 7168, I = 512: 29.4, 30.4; k = 2, I = 2048: 23.8, 24.4; H = 4096,
+    // k = 3, I = 1536: 21.8, 22.5; two tokens of H = 7168, 28 KB: 43.1, 43.4; but one of
+    // H = 2048, k = 6, I = 1408: 25.2, 24.9; 12 of H = 2048, 48 KB: 91.0, 91.8, no more
+    // than boxes differ, so larger rows leave the LDS to the rings.)
     const int64_t up_items = (int64_t(P < p.E ? P : p.E) + P / 4) * (p.I / 16);
     const int up_grid = int(up_items < cus ? up_items : cus);
     const int x_bytes = p.T * p.H * 2;
@@ -1250,9 +1263,10 @@ int launch_layer(MoeParams p, hipStream_t s) {
     const unsigned up_lds = unsigned(kWaves * p.ring + p.resident);
     if (p.resident) hipLaunchKernelGGL((moe_up_kernel<W, A, true>), dim3(up_grid), block, up_lds, s, p);
     else hipLaunchKernelGGL((moe_up_kernel<W, A, false>), dim3(up_grid), block, up_lds, s, p);
-    // 32 columns a workgroup of the down projection (one token, H = 7168, I = 512, 224
-    // tiles: 34.2 us a layer, 39.4 with 448 tiles of 16) where they fill three quarters
-    // of the CUs and the sums stay small
+    // 32 columns a workgroup of the down projection where they fill three quarters of
+    // the CUs and the sums stay small (us a layer, 32 and 16 columns: one token, k = 9,
+    // H = 7168, I = 512, 224 tiles: 29.6, 33.6; k = 2, I = 2048: 23.9, 27.0; with H = 4096,
+    // 128 tiles, k = 2, E = 8, I = 1792: 10 tokens 49.8, 44.6, but 30 tokens 54.3, 59.8)
     const int rt = p.H % 32 == 0 && p.H / 32 >= cus * 3 / 4 && P * 128 <= 40 * 1024 ? 2 : 1;
     if (shared_down(p, cus, rt)) {
         const int items = ((P < p.E ? P : p.E) + P / 32) * (p.H / 128);

@@ -329,7 +329,9 @@ GFG_API int int8_quantize_token_device(const void* x, int32_t in_dtype, int64_t 
  *   d[m, n] = (sum_k a[m, k] b[n, k]) * a_scale[m] * b_scale[n] + bias[n]
  *
  * The sum is an exact 32-bit integer; the scales and the bias are applied in
- * fp32 and d is rounded once.
+ * fp32, first a_scale, then b_scale, and d is rounded once.  So sum * a_scale has
+ * to lie in fp32's range itself, also where b_scale would bring it back (it always
+ * does for an a_scale below 2^97).
  *
  *   a [M][K] int8 ; a_scale [M] float ; b [N][K] int8 ; b_scale [N] float
  *   bias [N] float or NULL ; d [M][N] bf16 or f16
@@ -363,8 +365,9 @@ GFG_API int int8_linear(const void* x, int32_t in_dtype, const int8_t* b, const 
  *   masked:     a [G][M_max][K], a_scale [G][M_max], masked_m [G], d [G][M_max][N]
  *   both:       b [G][N][K], b_scale [G][N]
  *
- * Sizes: N and K as in int8_gemm, 1 <= G <= 65535, at most 4096 tiles of 128
- * rows (ceil(M / 128), or G * ceil(M_max / 128)), else GFG_EUNSUPPORTED.
+ * Sizes: N and K as in int8_gemm, 1 <= G <= 65535 (else GFG_EINVAL), at most
+ * 4096 tiles of 128 rows (ceil(M / 128), or G * ceil(M_max / 128); else
+ * GFG_EUNSUPPORTED).
  */
 GFG_API int grouped_int8_gemm_contiguous(const int8_t* a, const float* a_scale, const int8_t* b,
                                          const float* b_scale, const int32_t* grouped_layout, void* d, int64_t M,
@@ -383,9 +386,9 @@ GFG_API int grouped_int8_gemm_masked(const int8_t* a, const float* a_scale, cons
  *   weights   score * scale, or, renormalized, score / (sum of the chosen
  *             scores) * scale (0 where that sum is 0)
  *
- * An expert whose logit is -infinity or NaN is never chosen; where fewer than
- * k are left, the remaining ids are -1 with weight 0 (the layers below skip
- * them).
+ * An expert whose logit (or, with a bias, whose score + bias[e]) is -infinity or
+ * NaN is never chosen; where fewer than k are left, the remaining ids are -1 with
+ * weight 0 (the layers below skip them).
  *
  *   logits [T][E] GFG_IN_F32, _BF16 or _F16 ; bias [E] float or NULL
  *   ids [T][k] int32 ; weights [T][k] float
@@ -405,9 +408,12 @@ GFG_API int moe_topk(const void* logits, int32_t in_dtype, const float* bias, in
  *
  * Ids outside [0, E) (another rank's experts, or none) contribute nothing; a
  * token with no expert here gets zeros.  A token may name an expert twice.
- * The tokens stay in 16 bits, the hidden rows keep 16 significant bits, all
- * sums are fp32 and out is rounded once.  For more than 1024 pairs use the
- * grouped products on the same weights.
+ * The tokens stay in 16 bits, the hidden rows keep 16 significant bits (of any
+ * finite fp32 value), all sums are fp32 and out is rounded once.  Scales multiply
+ * sums of the raw codes (of a 128-block in FP8, of a row in int8), so those sums
+ * have to lie in fp32's range themselves; tokens and hidden values below 2^105
+ * always keep them there.  Two calls with the same operands give the same bytes.
+ * For more than 1024 pairs use the grouped products on the same weights.
  *
  *   x, out [T][H] bf16 or f16 (dtype GFG_OUT_*) ; topk_ids [T][k] int32 ;
  *   topk_weights [T][k] float
