@@ -21,7 +21,7 @@
 // What bounds it: with every CU busy, a wave alone on its SIMD, whose own loads,
 // LDS reads and barriers hold up its MFMAs, at the clock that the chip holds under
 // this load; between tiles, the epilogue.  8 x 4096 x 7168 at five depths fits 1.58
-// us a step and 6.2 us a tile (the FP8 kernel on the same box: 1.53 and 3.2); a tile
+// us a step and 6.2 us a tile (the FP8 kernel beside it: 1.53 and 3.2); a tile
 // alone on the chip takes 1.05 us a step, 0.90 with 192 rows.  Counters: 4096 x 4096 x
 // 16384, 205-219 us, 2510-2680 TOP/s (a library's product: 2408): the matrix pipes are
 // busy 67% of the time at 1.97 GHz, each CU takes in 42 GB/s from L2, no LDS bank

@@ -1254,7 +1254,7 @@ int launch_layer(MoeParams p, hipStream_t s) {
     // one token, k = 9, H = 7168, I = 512: 29.4, 30.4; k = 2, I = 2048: 23.8, 24.4; H = 4096,
     // k = 3, I = 1536: 21.8, 22.5; two tokens of H = 7168, 28 KB: 43.1, 43.4; but one of
     // H = 2048, k = 6, I = 1408: 25.2, 24.9; 12 of H = 2048, 48 KB: 91.0, 91.8, no more
-    // than boxes differ, so larger rows leave the LDS to the rings.)
+    // than runs differ, so larger rows leave the LDS to the rings.)
     const int64_t up_items = (int64_t(P < p.E ? P : p.E) + P / 4) * (p.I / 16);
     const int up_grid = int(up_items < cus ? up_items : cus);
     const int x_bytes = p.T * p.H * 2;
