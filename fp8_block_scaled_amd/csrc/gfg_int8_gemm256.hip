@@ -23,7 +23,7 @@
 // this load; between tiles, the epilogue.  8 x 4096 x 7168 at five depths fits 1.58
 // us a step and 6.2 us a tile (the FP8 kernel beside it: 1.53 and 3.2); a tile
 // alone on the chip takes 1.05 us a step, 0.90 with 192 rows.  Counters: 4096 x 4096 x
-// 16384, 205-219 us, 2510-2680 TOP/s (a library's product: 2408): the matrix pipes are
+// 16384, 199-219 us, 2510-2760 TOP/s (a library's product: 2408): the matrix pipes are
 // busy 67% of the time at 1.97 GHz, each CU takes in 42 GB/s from L2, no LDS bank
 // conflicts; 8 x 4096 x 7168 x 2304, 470-496 us, 2180-2300: 51% at 2.06 GHz, 34 GB/s; the
 // masked 8 x up to 1024 rows x 2048 x 7168, one round of 192-row tiles, 87-90 us: 37%
