@@ -19,6 +19,11 @@ and as an MXFP8 GEMM (one E8M0 scale per 32 K elements of every row of A and B).
 ``serving.py`` adds what decoding from the same weights needs: a top-k router,
 the whole expert layer for a few tokens, and 8-bit integer products with one
 scale per token and per output channel.
+
+``layers.py`` adds the rest of a block on FP8 weights, served and trained: the
+dense FP8 linear layer with its gradients and the device quantizer of its
+weights, the norms around a block with its gate and residual sum, and the
+router's balance loss and gradient.
 """
 from __future__ import annotations
 
@@ -40,14 +45,17 @@ __all__ = [
     "int8_quantize_token_device", "int8_gemm", "int8_linear", "int8_linear_workspace_bytes",
     "grouped_int8_gemm_contiguous", "grouped_int8_gemm_masked",
     "moe_topk", "moe_fp8_layer", "moe_int8_layer", "moe_layer_workspace_bytes",
-    "OUT_BF16", "OUT_F16", "IN_F32", "IN_BF16", "IN_F16",
+    "fp8_gemm", "fp8_linear", "fp8_linear_workspace_bytes", "fp8_linear_backward", "fp8_linear_backward_workspace_bytes",
+    "fp8_quantize_weight_device", "residual_norm", "residual_norm_fp8", "residual_norm_backward",
+    "residual_norm_backward_workspace_bytes", "moe_balance_loss", "moe_balance_workspace_bytes", "moe_router_backward",
+    "OUT_BF16", "OUT_F16", "OUT_F32", "IN_F32", "IN_BF16", "IN_F16",
     "set_tile_order", "set_tile_shape", "set_grid_limit", "TILE_AUTO", "TILE_128x256", "TILE_256x256",
 ]
 
 # GFG_LIBRARY names another build of the library to load (the host-sanitizer
 # build of the CPU tests); by default the in-tree libgfg.so.
 _LIB_PATH = os.environ.get("GFG_LIBRARY") or os.path.join(os.path.dirname(os.path.abspath(__file__)), "libgfg.so")
-OUT_BF16, OUT_F16 = 0, 1
+OUT_BF16, OUT_F16, OUT_F32 = 0, 1, 2
 IN_F32, IN_BF16, IN_F16 = 0, 1, 2
 _STATUS = {0: "GFG_OK", 1: "GFG_EINVAL", 2: "GFG_EUNSUPPORTED", 3: "GFG_EHIP", 4: "GFG_ERANGE"}
 _lib = None
@@ -56,13 +64,21 @@ _lib = None
 _SERVING = ("int8_quantize_token_device", "int8_gemm", "int8_linear", "int8_linear_workspace_bytes",
             "grouped_int8_gemm_contiguous", "grouped_int8_gemm_masked",
             "moe_topk", "moe_fp8_layer", "moe_int8_layer", "moe_layer_workspace_bytes")
+# and those of layers.py
+_LAYERS = ("fp8_gemm", "fp8_linear", "fp8_linear_workspace_bytes", "fp8_linear_backward",
+           "fp8_linear_backward_workspace_bytes", "fp8_quantize_weight_device", "residual_norm", "residual_norm_fp8",
+           "residual_norm_backward", "residual_norm_backward_workspace_bytes", "moe_balance_loss",
+           "moe_balance_workspace_bytes", "moe_router_backward")
 
 
 def __getattr__(name):
-    if name not in _SERVING:
+    if name in _SERVING:
+        from . import serving as module
+    elif name in _LAYERS:
+        from . import layers as module
+    else:
         raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
-    from . import serving
-    globals()[name] = getattr(serving, name)
+    globals()[name] = getattr(module, name)
     return globals()[name]
 
 
@@ -132,6 +148,33 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     for layer in (lib.moe_fp8_layer, lib.moe_int8_layer):
         layer.argtypes = [vp, i32, vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, i64, vp, i64, vp]
         layer.restype = ctypes.c_int
+    lib.fp8_gemm.argtypes = [vp, vp, i64, vp, vp, vp, vp, i64, i64, i64, i32, vp]
+    lib.fp8_gemm.restype = ctypes.c_int
+    lib.fp8_linear_workspace_bytes.argtypes = [i64, i64]
+    lib.fp8_linear_workspace_bytes.restype = i64
+    lib.fp8_linear.argtypes = [vp, i32, vp, vp, vp, vp, i64, i64, i64, i32, vp, i64, vp]
+    lib.fp8_linear.restype = ctypes.c_int
+    lib.fp8_linear_backward_workspace_bytes.argtypes = [i64, i64, i64]
+    lib.fp8_linear_backward_workspace_bytes.restype = i64
+    lib.fp8_linear_backward.argtypes = [vp, vp, i32, vp, vp, vp, vp, vp, i64, i64, i64, i32, i32, i32, vp, i64, vp]
+    lib.fp8_linear_backward.restype = ctypes.c_int
+    lib.fp8_quantize_weight_device.argtypes = [vp, i32, i32, i64, i64, vp, vp, vp, vp, vp]
+    lib.fp8_quantize_weight_device.restype = ctypes.c_int
+    lib.residual_norm.argtypes = [vp, vp, vp, vp, vp, i32, f32, f32, vp, vp, vp, i64, i64, i32, i32, vp]
+    lib.residual_norm.restype = ctypes.c_int
+    lib.residual_norm_fp8.argtypes = [vp, vp, vp, vp, vp, i32, f32, f32, vp, vp, vp, i64, vp, i64, i64, i32, i32, vp]
+    lib.residual_norm_fp8.restype = ctypes.c_int
+    lib.residual_norm_backward_workspace_bytes.argtypes = [i64, i64]
+    lib.residual_norm_backward_workspace_bytes.restype = i64
+    lib.residual_norm_backward.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i32, f32, vp, vp, vp, vp, vp, i32, i64, i64,
+                                           i32, i32, vp, i64, vp]
+    lib.residual_norm_backward.restype = ctypes.c_int
+    lib.moe_balance_workspace_bytes.argtypes = [i64, i64, i64]
+    lib.moe_balance_workspace_bytes.restype = i64
+    lib.moe_balance_loss.argtypes = [vp, i32, vp, vp, vp, vp, vp, i64, i64, i64, i64, i32, f32, f32, vp, i64, vp]
+    lib.moe_balance_loss.restype = ctypes.c_int
+    lib.moe_router_backward.argtypes = [vp, i32, vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, i32, i32, f32, vp]
+    lib.moe_router_backward.restype = ctypes.c_int
     lib.grouped_fp8_last_error.argtypes = []
     lib.grouped_fp8_last_error.restype = ctypes.c_char_p
     lib.grouped_fp8_set_tile_order.argtypes = [i32, i32]

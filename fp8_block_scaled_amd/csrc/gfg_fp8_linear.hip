@@ -1,0 +1,968 @@
+// The FP8 (E4M3) linear layer with one power-of-two scale per 128 channels of a
+// token and per 128 x 128 block of the weight, and its gradients, for gfx950
+// (MI355X).
+//
+//   Q(v)      per block: t = the smallest integer with 448 * 2^t >= max|v| (0
+//             for zeros), codes E4M3(v / 2^t), value code * 2^t
+//   y  = Q(x) W^T + b         x in blocks of 1 x 128 along K
+//   dx = Q(dy) W              dy in blocks of 1 x 128 along N; the product of
+//                             dy and the transposed weight, whose 128 x 128
+//                             blocks are the same blocks
+//   dW = Q(dy^T) Q(x^T)^T     both in blocks of 128 tokens, for the sum runs
+//                             over tokens
+//   db = sum of dy over the tokens, in fp32
+//
+// The products run on v_mfma_scale_f32_16x16x128_f8f6f4, whose 128 k are one
+// scale block, so the E8M0 bytes are its scale operands and a sum over K is a
+// chain of fp32 accumulations.
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "gfg.h"
+#include "gfg_device.h"
+#include "gfg_fp8_linear.h"
+#include "gfg_internal.h"
+
+namespace gfg {
+namespace {
+
+typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+
+constexpr int QB = 128;                        // elements of a scale block
+constexpr uint32_t kOutside = 0x80000000u;     // past every buffer window used here (all below 2^31 bytes)
+
+// ------------------------------------------------------------------ encoding a block
+// Eight elements of a row as they lie in memory.
+template <typename T> struct Eight;
+template <> struct Eight<__bf16> {
+    u32x4 w;
+    __device__ __forceinline__ float at(int i) const {
+        return __uint_as_float((i & 1) ? w[i >> 1] & 0xFFFF0000u : w[i >> 1] << 16);
+    }
+};
+template <> struct Eight<_Float16> {
+    u32x4 w;
+    __device__ __forceinline__ float at(int i) const {
+        return float(__builtin_bit_cast(_Float16, uint16_t(w[i >> 1] >> (16 * (i & 1)))));
+    }
+};
+template <> struct Eight<float> {
+    u32x4 w, w2;
+    __device__ __forceinline__ float at(int i) const { return __uint_as_float(i < 4 ? w[i & 3] : w2[i & 3]); }
+};
+template <typename T>
+__device__ __forceinline__ Eight<T> load8(const T* p) {
+    Eight<T> e;
+    e.w = reinterpret_cast<const u32x4*>(p)[0];
+    if constexpr (sizeof(T) == 4) e.w2 = reinterpret_cast<const u32x4*>(p)[1];
+    return e;
+}
+
+// Magnitude bits: their integer order is that of the magnitudes, with
+// infinities and NaN above every finite value.
+__device__ __forceinline__ uint32_t mag(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+
+// The E8M0 byte of a block with largest magnitude `ab`, and 2^-t in *inv.  With
+// 448 = 1.75 * 2^8 and max|v| = 1.f * 2^e, t is e - 8 where 1.f <= 1.75 and e - 7
+// otherwise, at least -127 (which still keeps |v / 2^t| <= 448).  A block with an
+// infinity or a NaN has byte 255 (NaN) and *inv 0.
+__device__ __forceinline__ uint32_t block_scale(uint32_t ab, float* inv) {
+    if (ab >= 0x7F800000u) {
+        *inv = 0.0f;
+        return 255u;
+    }
+    int e = int(ab >> 23) - 127;
+    uint32_t mant = ab & 0x7FFFFFu;
+    if (e == -127) {                           // subnormal or zero
+        const int lz = __builtin_clz(mant | 1u) - 8;
+        mant = (mant << lz) & 0x7FFFFFu;
+        e = -126 - lz;
+    }
+    int t = mant <= 0x600000u ? e - 8 : e - 7;
+    t = t < -127 ? -127 : t;
+    if (ab == 0) t = 0;
+    *inv = __builtin_ldexpf(1.0f, -t);
+    return uint32_t(t + 127);
+}
+
+// Four codes, rounded to nearest even by the packed conversion; |v * inv| <= 448.
+// A block without a scale gets the codes of NaN.
+__device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d, float inv) {
+    if (inv == 0.0f) return 0x7F7F7F7Fu;
+    uint32_t w = uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(a * inv, b * inv, 0, false));
+    return uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(c * inv, d * inv, int(w), true));
+}
+
+// ------------------------------------------------------------------ token quantizer
+// x [R][C] -> q [R][C], scale [ceil(C/128)][ld]: 16 lanes share a block, a
+// workgroup takes 16 U rows of one column of blocks, so that its scale bytes
+// are neighbours.  C a multiple of 16.
+template <typename T, int U>
+__global__ __launch_bounds__(256) void quant_rows_kernel(const T* __restrict__ x, uint8_t* __restrict__ q,
+                                                         uint8_t* __restrict__ scale, int64_t R, int C, int64_t ld) {
+    const int CB = (C + QB - 1) / QB;
+    const int kb = int(blockIdx.x % unsigned(CB));
+    const int64_t r0 = int64_t(blockIdx.x / unsigned(CB)) * (16 * U) + (threadIdx.x >> 4);
+    const int col = kb * QB + int(threadIdx.x & 15) * 8;
+    Eight<T> v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        v[u] = Eight<T>{};
+        if (r0 + 16 * u < R && col < C) v[u] = load8(x + (r0 + 16 * u) * C + col);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int64_t r = r0 + 16 * u;
+        uint32_t ab = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ab = max(ab, mag(v[u].at(i)));
+#pragma unroll
+        for (int w = 8; w >= 1; w >>= 1) ab = max(ab, uint32_t(__shfl_xor(int(ab), w, 16)));
+        float inv;
+        const uint32_t byte = block_scale(ab, &inv);
+        if (r >= R) continue;
+        if (col < C)
+            *reinterpret_cast<u32x2*>(q + r * C + col) =
+                u32x2{encode4(v[u].at(0), v[u].at(1), v[u].at(2), v[u].at(3), inv),
+                      encode4(v[u].at(4), v[u].at(5), v[u].at(6), v[u].at(7), inv)};
+        if ((threadIdx.x & 15) == 0) scale[kb * ld + r] = uint8_t(byte);
+    }
+}
+
+// ------------------------------------------------------------------ tile quantizer
+// One 128 x 128 tile of x [R][C] a workgroup, read once, for what needs it in
+// both orientations: codes along the rows (q, scale [CB][ld]), codes along the
+// columns, transposed (qt [C][ldt], scale_t [RB][ld_t]), and the columns' sums
+// (sums [RB][C]); each one only where its pointer is given.  BLOCK: one scale
+// for the whole tile in place of both (scale [RB][CB], scale_t [CB][RB]), G
+// matrices one after the other.  Thread (g, l) holds rows 8 g .. +7 and columns
+// 8 l .. +7, so a column's eight codes are one 8-byte word of the transposed
+// tile in LDS, whose words are XOR-swizzled by the column's l.
+template <typename T, bool BLOCK>
+__global__ __launch_bounds__(256) void quant_tile_kernel(const T* __restrict__ x, uint8_t* __restrict__ q,
+                                                         uint8_t* __restrict__ scale, int64_t ld, uint8_t* __restrict__ qt,
+                                                         int64_t ldt, int64_t store_t, uint8_t* __restrict__ scale_t,
+                                                         int64_t ld_t, float* __restrict__ sums, int64_t R, int C) {
+    __shared__ __attribute__((aligned(16))) uint8_t tile[QB * QB];
+    __shared__ uint32_t top[16][QB];
+    __shared__ float part[16][QB];
+    const int l = threadIdx.x & 15, g = threadIdx.x >> 4;
+    const int CB = (C + QB - 1) / QB;
+    const int64_t RB = (R + QB - 1) / QB;
+    int64_t item = blockIdx.x;
+    if (BLOCK) {
+        const int64_t per = RB * CB, gi = item / per;
+        item -= gi * per;
+        x += gi * R * C;
+        q += gi * R * C;
+        scale += gi * per;
+        if (qt) {
+            qt += gi * R * C;
+            scale_t += gi * per;
+        }
+    }
+    const int cb = int(item % CB);
+    const int64_t rb = item / CB, r0 = rb * QB + 8 * g;
+    const int col = cb * QB + 8 * l;
+    Eight<T> v[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+        v[u] = Eight<T>{};
+        if (r0 + u < R && col < C) v[u] = load8(x + (r0 + u) * C + col);
+    }
+    uint32_t whole = 0;
+    float block_inv = 0.0f;
+    uint32_t block_byte = 0;
+    if (BLOCK) {
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) whole = max(whole, mag(v[u].at(i)));
+        whole = wave_reduce(whole, [](uint32_t a, uint32_t b) { return max(a, b); });
+        if ((threadIdx.x & 63) == 0) top[0][threadIdx.x >> 6] = whole;
+        __syncthreads();
+        whole = max(max(top[0][0], top[0][1]), max(top[0][2], top[0][3]));
+        block_byte = block_scale(whole, &block_inv);
+        if (threadIdx.x == 0) {
+            scale[rb * CB + cb] = uint8_t(block_byte);
+            if (qt) scale_t[cb * RB + rb] = uint8_t(block_byte);
+        }
+    }
+    // ---- along the rows
+    if (q) {
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            float inv = block_inv;
+            if (!BLOCK) {
+                uint32_t ab = 0;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) ab = max(ab, mag(v[u].at(i)));
+#pragma unroll
+                for (int w = 8; w >= 1; w >>= 1) ab = max(ab, uint32_t(__shfl_xor(int(ab), w, 16)));
+                const uint32_t byte = block_scale(ab, &inv);
+                if (l == 0 && r0 + u < R) scale[cb * ld + r0 + u] = uint8_t(byte);
+            }
+            if (r0 + u < R && col < C)
+                *reinterpret_cast<u32x2*>(q + (r0 + u) * C + col) =
+                    u32x2{encode4(v[u].at(0), v[u].at(1), v[u].at(2), v[u].at(3), inv),
+                          encode4(v[u].at(4), v[u].at(5), v[u].at(6), v[u].at(7), inv)};
+        }
+    }
+    // ---- the columns' sums, eight rows a thread, then the sixteen parts in order
+    if (!BLOCK && sums) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            float t = 0.0f;
+#pragma unroll
+            for (int u = 0; u < 8; ++u) t += v[u].at(i);
+            part[g][8 * l + i] = t;
+        }
+    }
+    if (!qt && !sums) return;
+    // ---- along the columns
+    if (!BLOCK && qt) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            uint32_t ab = 0;
+#pragma unroll
+            for (int u = 0; u < 8; ++u) ab = max(ab, mag(v[u].at(i)));
+            top[g][8 * l + i] = ab;
+        }
+    }
+    if (!BLOCK) __syncthreads();
+    if (!BLOCK && threadIdx.x < QB) {
+        const int c = threadIdx.x;
+        if (qt) {
+            uint32_t ab = 0;
+#pragma unroll
+            for (int w = 0; w < 16; ++w) ab = max(ab, top[w][c]);
+            float inv;
+            const uint32_t byte = block_scale(ab, &inv);
+            top[0][c] = __float_as_uint(inv);          // (column c's maxima are read by this thread alone)
+            if (cb * QB + c < C) scale_t[rb * ld_t + cb * QB + c] = uint8_t(byte);
+        }
+        if (sums && cb * QB + c < C) {
+            float t = 0.0f;
+#pragma unroll
+            for (int w = 0; w < 16; ++w) t += part[w][c];
+            sums[rb * C + cb * QB + c] = t;
+        }
+    }
+    if (!qt) return;
+    if (!BLOCK) __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float inv = BLOCK ? block_inv : __uint_as_float(top[0][8 * l + i]);
+        *reinterpret_cast<u32x2*>(tile + (8 * l + i) * QB + ((g ^ l) << 3)) =
+            u32x2{encode4(v[0].at(i), v[1].at(i), v[2].at(i), v[3].at(i), inv),
+                  encode4(v[4].at(i), v[5].at(i), v[6].at(i), v[7].at(i), inv)};
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int c = 32 * j + int(threadIdx.x >> 3), ch = threadIdx.x & 7, key = c >> 3;
+        const u32x4 w = *reinterpret_cast<const u32x4*>(tile + c * QB + ((ch ^ (key >> 1)) << 4));
+        const u32x4 o = (key & 1) ? u32x4{w[2], w[3], w[0], w[1]} : w;
+        if (cb * QB + c < C && rb * QB + 16 * ch < store_t)
+            *reinterpret_cast<u32x4*>(qt + (cb * QB + c) * ldt + rb * QB + 16 * ch) = o;
+    }
+}
+
+// db[c] (+)= the sum over the row blocks of sums [RB][C], in a fixed order: 16
+// lanes of partial sums a column, then those.
+__global__ __launch_bounds__(256) void column_sums_kernel(const float* __restrict__ sums, float* __restrict__ out, int64_t RB,
+                                                          int C, int accumulate) {
+    __shared__ float part[16][17];
+    const int c = int(blockIdx.x) * 16 + int(threadIdx.x & 15), g = threadIdx.x >> 4;
+    float t = 0.0f;
+    if (c < C)
+        for (int64_t r = g; r < RB; r += 16) t += sums[r * C + c];
+    part[g][threadIdx.x & 15] = t;
+    __syncthreads();
+    if (g || c >= C) return;
+    t = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 16; ++w) t += part[w][threadIdx.x];
+    out[c] = accumulate ? out[c] + t : t;
+}
+
+template <typename T>
+__global__ __launch_bounds__(256) void zero_kernel(T* __restrict__ p, int64_t n) {
+    for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < n; i += int64_t(gridDim.x) * 256) p[i] = T(0.0f);
+}
+
+// ------------------------------------------------------------------ tiled product
+// N bytes at any address
+template <int N> struct Bytes;
+template <> struct Bytes<1> { typedef uint8_t type; };
+template <> struct Bytes<2> { typedef uint16_t type __attribute__((aligned(1))); };
+template <> struct Bytes<4> { typedef uint32_t type __attribute__((aligned(1))); };
+
+__device__ __forceinline__ v8i join(u32x4 l, u32x4 h) {
+    return __builtin_bit_cast(v8i, __builtin_shufflevector(l, h, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
+// The product of one 16 x 16 block and 128 k; the scale bytes SB of sb and SA
+// of sa (they have to be constants of the instruction).
+template <int SB, int SA>
+__device__ __forceinline__ v4f mfma_at(const v8i& b, const v8i& a, const v4f& c, int sb, int sa) {
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b, a, c, 0, 0, SB, sb, SA, sa);
+}
+template <int SB>
+__device__ __forceinline__ v4f mfma_sa(const v8i& b, const v8i& a, const v4f& c, int sb, int y, int sa) {
+    switch (y) {
+        case 0: return mfma_at<SB, 0>(b, a, c, sb, sa);
+        case 1: return mfma_at<SB, 1>(b, a, c, sb, sa);
+        case 2: return mfma_at<SB, 2>(b, a, c, sb, sa);
+        default: return mfma_at<SB, 3>(b, a, c, sb, sa);
+    }
+}
+__device__ __forceinline__ v4f mfma(const v8i& b, const v8i& a, const v4f& c, int x, int sb, int y, int sa) {
+    switch (x) {
+        case 0: return mfma_sa<0>(b, a, c, sb, y, sa);
+        case 1: return mfma_sa<1>(b, a, c, sb, y, sa);
+        case 2: return mfma_sa<2>(b, a, c, sb, y, sa);
+        default: return mfma_sa<3>(b, a, c, sb, y, sa);
+    }
+}
+
+// Rows of a tile of RB fragments: fragment f of lane l16 is row RB l16 + f, so
+// that a lane's RB scale bytes are neighbours (one load).  LDS row R holds tile
+// row R ^ ((R >> r) & 1), r = log2 RB (R itself for RB = 1), and its 16-byte
+// chunk c the logical chunk c ^ ((R >> r) & 7): the 16 rows of a fragment then
+// lie in both halves of the banks and in all chunks.
+template <int RB> struct Rows {
+    static constexpr int r = RB == 4 ? 2 : RB == 2 ? 1 : 0;
+    __device__ static __forceinline__ int key(int R) { return (R >> r) & 7; }
+    __device__ static __forceinline__ int swap(int R) { return RB == 1 ? R : R ^ ((R >> r) & 1); }
+};
+
+// Where a lane's RB scale bytes of one operand's rows lie: at `at` in a row of
+// `total` bytes, with `shift` to bring them down where the load had to start
+// lower to end inside the row (total >= RB).
+struct ScaleAt { uint32_t at; int shift; };
+template <int RB>
+__device__ __forceinline__ ScaleAt scale_at(int64_t row, int64_t total) {
+    const int64_t at = row < total - RB ? row : total - RB;
+    const int64_t by = row - at;
+    return ScaleAt{uint32_t(at), int(by < RB ? 8 * by : 8 * RB)};
+}
+template <int RB>
+__device__ __forceinline__ int scale_bytes(uint32_t raw, const ScaleAt& s) {
+    return int(s.shift >= 32 ? 0u : raw >> s.shift);
+}
+
+// Columns n .. n + CNT - 1 of a row.
+template <int CNT, typename OutT>
+__device__ __forceinline__ void store_row(OutT* row, int n, int N, const float (&v)[CNT], int accumulate) {
+    typedef OutT vec __attribute__((ext_vector_type(CNT), aligned(sizeof(OutT))));     // (rows start anywhere where N is odd)
+    const bool add = sizeof(OutT) == 4 && accumulate;
+    if (n + CNT <= N) {
+        vec o;
+#pragma unroll
+        for (int i = 0; i < CNT; ++i) o[i] = OutT(v[i]);
+        if (add) o += *reinterpret_cast<const vec*>(row + n);
+        *reinterpret_cast<vec*>(row + n) = o;
+    } else {
+#pragma unroll
+        for (int i = 0; i < CNT; ++i)
+            if (n + i < N) row[n + i] = add ? OutT(row[n + i] + OutT(v[i])) : OutT(v[i]);
+    }
+}
+
+// TM x TN output tiles, WM x WN waves, K in steps of 128 through four LDS
+// stages filled by direct-to-LDS loads: three are in flight while one is
+// consumed, and a step has one barrier (a wave that passes it has seen every
+// wave finish the previous step, whose buffer the new loads go to).  Rows past
+// an operand's end and chunks past K lie outside the buffer window, where the
+// hardware returns zeros; zeros add nothing whatever their scale (which is a
+// clamped one of the operand's own).
+template <int TM, int TN, int WM, int WN, bool BROW, typename OutT>
+__device__ __forceinline__ void ring_tile(const F8Params& p, unsigned w) {
+    constexpr int S = 4, WAVES = WM * WN, BYTES = (TM + TN) * QB;
+    constexpr int PER = BYTES / 1024 / WAVES, A_LOADS = TM / 8 / WAVES;
+    constexpr int RB = TM / WM / 16, CB = TN / WN / 16;
+    constexpr int OPS = PER + 1 + (BROW ? 1 : 0);      // vector-memory operations of a wave and stage
+    static_assert(BYTES % (1024 * WAVES) == 0 && TM % (8 * WAVES) == 0 && WAVES % 4 == 0 && TN <= QB, "stage shape");
+    // an array for each stage: the compiler then knows that reading one need
+    // not wait for the loads into another
+    __shared__ __attribute__((aligned(1024))) uint8_t s0[BYTES], s1[BYTES], s2[BYTES], s3[BYTES];
+    GFG_LDS uint8_t* const buf[S] = {(GFG_LDS uint8_t*)s0, (GFG_LDS uint8_t*)s1, (GFG_LDS uint8_t*)s2, (GFG_LDS uint8_t*)s3};
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int l16 = lane & 15, lq = lane >> 4;
+    // tiles in ranges, one for each XCD (the hardware deals workgroup w to XCD
+    // w % num_xcd), row tiles first, so that a B panel stays in one L2
+    const unsigned nx = unsigned(p.num_xcd), x = w % nx, per = p.tiles / nx, rem = p.tiles % nx;
+    const unsigned item = x * per + min(x, rem) + w / nx;
+    const int mt = int(item % unsigned(p.m_tiles)), n0 = int(item / unsigned(p.m_tiles)) * TN;
+    const int64_t row0 = int64_t(mt) * TM;
+    const int lim = int(p.rows - row0 < TM ? p.rows - row0 : TM), ncols = min(TN, p.N - n0);
+    const auto ra = make_rsrc(p.a + row0 * p.K, uint32_t(lim) * uint32_t(p.K));
+    const auto rb = make_rsrc(p.b + int64_t(n0) * p.K, uint32_t(ncols) * uint32_t(p.K));
+    const int wm = (wave / WN) * (TM / WM), wn = (wave % WN) * (TN / WN);
+
+    // load j of a wave: LDS rows 8 (WAVES j + wave) .. +7 of the stage (A's TM
+    // rows, then B's); lane i writes physical chunk i & 7 of row i >> 3 of them
+    const int R = 8 * wave + (lane >> 3);
+    const int ka = ((lane & 7) ^ Rows<RB>::key(R)) * 16, kbo = ((lane & 7) ^ Rows<CB>::key(R)) * 16;
+    const uint32_t src_a = uint32_t(Rows<RB>::swap(R)) * uint32_t(p.K) + uint32_t(ka);
+    const uint32_t src_b = uint32_t(Rows<CB>::swap(R)) * uint32_t(p.K) + uint32_t(kbo);
+    const ScaleAt at_a = scale_at<RB>(row0 + wm + RB * l16, p.rows);
+    const ScaleAt at_b = BROW ? scale_at<CB>(n0 + wn + CB * l16, p.N) : ScaleAt{};
+    const uint8_t* const sb_row = uniform_ptr(p.b_scale + (BROW ? 0 : int64_t(n0 / QB) * p.KB));
+    uint32_t sa[S], sb[S];
+    auto issue = [&](int j, int kb) {
+        const int ks = min(kb, p.KB - 1);
+        sa[j] = *reinterpret_cast<const typename Bytes<RB>::type*>(p.a_scale + ks * p.ld_a + at_a.at);
+        if (BROW) sb[j] = *reinterpret_cast<const typename Bytes<CB>::type*>(p.b_scale + ks * p.ld_b + at_b.at);
+        else sb[j] = uint32_t(load_scale_word(sb_row, ks));
+        const uint32_t oa = kb * QB + ka < p.K ? src_a + uint32_t(kb) * QB : kOutside;
+        const uint32_t ob = kb * QB + kbo < p.K ? src_b + uint32_t(kb) * QB : kOutside;
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int jr = i < A_LOADS ? i : i - A_LOADS;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(i < A_LOADS ? ra : rb, (GFG_LDS void*)(buf[j] + (WAVES * i + wave) * 1024), 16,
+                                                     (i < A_LOADS ? oa : ob) + uint32_t(8 * WAVES * jr) * uint32_t(p.K), 0, 0, 0);
+        }
+    };
+    auto frag = [&](GFG_LDS uint8_t* src, int row, int key) {
+        auto part = [&](int c) { return *reinterpret_cast<GFG_LDS u32x4*>(src + row * QB + ((c ^ key) << 4)); };
+        return join(part(lq), part(lq + 4));
+    };
+    v4f acc[RB][CB] = {};                          // [row fragment][column fragment]
+#pragma unroll
+    for (int j = 0; j < S - 1; ++j) issue(j, j);
+    auto step = [&](int j, int kb) {
+        __builtin_amdgcn_sched_barrier(0);
+        GFG_WAITCNT((S - 2) * OPS, 15);
+        lds_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+        const int a_bytes = scale_bytes<RB>(sa[j], at_a);
+        const int b_bytes = BROW ? scale_bytes<CB>(sb[j], at_b) : scale_byte(int(sb[j]), sb_row, kb);
+        issue((j + S - 1) % S, kb + S - 1);        // a stage past K loads zeros
+        __builtin_amdgcn_sched_barrier(0);
+        v8i af[RB], bf[CB];
+#pragma unroll
+        for (int f = 0; f < RB; ++f) {
+            const int row = Rows<RB>::swap(wm + RB * l16 + f);
+            af[f] = frag(buf[j], row, Rows<RB>::key(row));
+        }
+#pragma unroll
+        for (int f = 0; f < CB; ++f) {
+            const int row = Rows<CB>::swap(wn + CB * l16 + f);
+            bf[f] = frag(buf[j] + TM * QB, row, Rows<CB>::key(row));
+        }
+#pragma unroll
+        for (int y = 0; y < RB; ++y)
+#pragma unroll
+            for (int c = 0; c < CB; ++c) acc[y][c] = mfma(bf[c], af[y], acc[y][c], BROW ? c : 0, b_bytes, y, a_bytes);
+    };
+    // whole rounds of the ring, then the rest: a loop with one way out, in which
+    // every path to a stage's reads passes the same loads, so that the compiler's
+    // own waits stay exact
+    int kb = 0;
+    for (; kb + S <= p.KB; kb += S) {
+#pragma unroll
+        for (int j = 0; j < S; ++j) step(j, kb + j);
+    }
+    if (kb < p.KB) {
+        step(0, kb);
+        if (kb + 1 < p.KB) {
+            step(1, kb + 1);
+            if (kb + 2 < p.KB) step(2, kb + 2);
+        }
+    }
+    GFG_WAITCNT(0, 15);                            // the last loads land before the workgroup ends
+
+    // acc[y][c][i] of lane (l16, lq): row RB l16 + y, column CB (4 lq + i) + c
+    OutT* const d = static_cast<OutT*>(p.d);
+    const int n = n0 + wn + 4 * CB * lq;
+#pragma unroll
+    for (int y = 0; y < RB; ++y) {
+        const int r = wm + RB * l16 + y;
+        if (r >= lim) continue;
+        float v[4 * CB];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int c = 0; c < CB; ++c) {
+                v[CB * i + c] = acc[y][c][i];
+                if (p.bias) v[CB * i + c] += p.bias[min(n + CB * i + c, p.N - 1)];
+            }
+        store_row<4 * CB>(d + (row0 + r) * p.N, n, p.N, v, p.accumulate);
+    }
+}
+
+// The tiles of a workgroup: one, or, under a grid limit, every gridDim.x-th.
+template <typename Tile>
+__device__ __forceinline__ void walk(unsigned tiles, Tile tile) {
+    for (unsigned w = blockIdx.x;;) {
+        tile(w);
+        w += gridDim.x;
+        if (w >= tiles) return;
+        __syncthreads();                           // every wave is done with the tile's LDS
+    }
+}
+
+template <int TM, int TN, int WM, int WN, bool BROW, typename OutT>
+__global__ __launch_bounds__(WM * WN * 64) void fp8_ring_kernel(F8Params p) {
+    walk(p.tiles, [&](unsigned w) { ring_tile<TM, TN, WM, WN, BROW, OutT>(p, w); });
+}
+
+// ------------------------------------------------------------------ streamed product
+//
+// 16 RB x 16 CB output tiles whose NW waves split K: wave w takes the 128-byte
+// units w, w + NW, ... of the tile's rows through its own ring of D LDS stages,
+// filled by direct-to-LDS loads.  No barrier stands between a load and its
+// MFMAs, every byte of the tile's rows enters the CU once and leaves the LDS
+// once; the waves' sums meet in LDS at the end, in wave order.
+template <int RB, int CB, int NW, int D, bool BROW, typename OutT>
+__device__ __forceinline__ void stream_tile(const F8Params& p, unsigned w) {
+    constexpr int TM = 16 * RB, TN = 16 * CB;
+    constexpr int UNIT = (TM + TN) * QB;           // bytes of a stage: A's rows, then B's
+    constexpr int PER = UNIT / 1024;               // loads per stage
+    constexpr int OPS = PER + 1 + (BROW ? 1 : 0);
+    static_assert((D == 2 || D == 4) && OPS * D < 64, "ring depth");
+    // an array for each stage: the compiler then knows that reading one need
+    // not wait for the loads into another
+    __shared__ __attribute__((aligned(1024))) uint8_t s0[NW * UNIT], s1[NW * UNIT];
+    __shared__ __attribute__((aligned(1024))) uint8_t s2[D > 2 ? NW * UNIT : 1024], s3[D > 2 ? NW * UNIT : 1024];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int l16 = lane & 15, lq = lane >> 4;
+    GFG_LDS uint8_t* const ring[4] = {(GFG_LDS uint8_t*)s0 + wave * UNIT, (GFG_LDS uint8_t*)s1 + wave * UNIT,
+                                      (GFG_LDS uint8_t*)s2 + (D > 2 ? wave * UNIT : 0), (GFG_LDS uint8_t*)s3 + (D > 2 ? wave * UNIT : 0)};
+    const unsigned nx = unsigned(p.num_xcd), x = w % nx, per = p.tiles / nx, rem = p.tiles % nx;
+    const unsigned item = x * per + min(x, rem) + w / nx;
+    const int mt = int(item % unsigned(p.m_tiles)), n0 = int(item / unsigned(p.m_tiles)) * TN;
+    const int64_t row0 = int64_t(mt) * TM;
+    const int lim = int(p.rows - row0 < TM ? p.rows - row0 : TM), ncols = min(TN, p.N - n0);
+    const auto ra = make_rsrc(p.a + row0 * p.K, uint32_t(lim) * uint32_t(p.K));
+    const auto rb = make_rsrc(p.b + int64_t(n0) * p.K, uint32_t(ncols) * uint32_t(p.K));
+
+    // load i: LDS rows 8 i .. +7 of the stage; lane l writes physical chunk
+    // l & 7 of row l >> 3 of them
+    const ScaleAt at_a = scale_at<RB>(row0 + RB * l16, p.rows);
+    const ScaleAt at_b = BROW ? scale_at<CB>(n0 + CB * l16, p.N) : ScaleAt{};
+    const uint8_t* const sb_row = uniform_ptr(p.b_scale + (BROW ? 0 : int64_t(n0 / QB) * p.KB));
+    uint32_t sa[D], sb[D];
+    auto load = [&](int d, int kb) {
+        const int ks = min(kb, p.KB - 1);
+        sa[d] = *reinterpret_cast<const typename Bytes<RB>::type*>(p.a_scale + ks * p.ld_a + at_a.at);
+        if (BROW) sb[d] = *reinterpret_cast<const typename Bytes<CB>::type*>(p.b_scale + ks * p.ld_b + at_b.at);
+        else sb[d] = uint32_t(load_scale_word(sb_row, ks));
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const bool of_a = i < TM / 8;
+            const int R = 8 * (of_a ? i : i - TM / 8) + (lane >> 3);
+            const int k = kb * QB + ((lane & 7) ^ (of_a ? Rows<RB>::key(R) : Rows<CB>::key(R))) * 16;
+            const int row = of_a ? Rows<RB>::swap(R) : Rows<CB>::swap(R);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(of_a ? ra : rb, (GFG_LDS void*)(ring[d] + i * 1024), 16,
+                                                     k < p.K ? uint32_t(row) * uint32_t(p.K) + uint32_t(k) : kOutside, 0, 0, 0);
+        }
+    };
+    v4f acc[RB][CB] = {};
+    auto frag = [&](GFG_LDS uint8_t* src, int row, int key) {
+        auto part = [&](int c) { return *reinterpret_cast<GFG_LDS u32x4*>(src + row * QB + ((c ^ key) << 4)); };
+        return join(part(lq), part(lq + 4));
+    };
+    // consume a unit, then load the one that takes its place, D units ahead
+    auto step = [&](int d, int kb) {
+        __builtin_amdgcn_sched_barrier(0);
+        GFG_WAITCNT((D - 1) * OPS, 15);
+        __builtin_amdgcn_sched_barrier(0);
+        const int a_bytes = scale_bytes<RB>(sa[d], at_a);
+        const int b_bytes = BROW ? scale_bytes<CB>(sb[d], at_b) : scale_byte(int(sb[d]), sb_row, kb);
+        v8i af[RB], bf[CB];
+#pragma unroll
+        for (int f = 0; f < RB; ++f) {
+            const int row = Rows<RB>::swap(RB * l16 + f);
+            af[f] = frag(ring[d], row, Rows<RB>::key(row));
+        }
+#pragma unroll
+        for (int f = 0; f < CB; ++f) {
+            const int row = Rows<CB>::swap(CB * l16 + f);
+            bf[f] = frag(ring[d] + TM * QB, row, Rows<CB>::key(row));
+        }
+#pragma unroll
+        for (int y = 0; y < RB; ++y)
+#pragma unroll
+            for (int c = 0; c < CB; ++c) acc[y][c] = mfma(bf[c], af[y], acc[y][c], BROW ? c : 0, b_bytes, y, a_bytes);
+        __builtin_amdgcn_sched_barrier(0);
+        load(d, kb + D * NW);                      // past K: zeros
+        __builtin_amdgcn_sched_barrier(0);
+    };
+#pragma unroll
+    for (int d = 0; d < D; ++d) load(d, wave + d * NW);
+    int kb = wave;                                 // (rounds as above)
+    for (; kb + (D - 1) * NW < p.KB; kb += D * NW) {
+#pragma unroll
+        for (int d = 0; d < D; ++d) step(d, kb + d * NW);
+    }
+    if (kb < p.KB) {
+        step(0, kb);
+        if constexpr (D > 2) {
+            if (kb + NW < p.KB) {
+                step(1, kb + NW);
+                if (kb + 2 * NW < p.KB) step(2, kb + 2 * NW);
+            }
+        }
+    }
+    GFG_WAITCNT(0, 15);                            // the last loads land before the workgroup ends
+    // a wave's sums go where its first stage was
+    static_assert(RB * CB * 1024 <= UNIT, "the sums fit a stage");
+    auto sums = [&](int v, int i) -> GFG_LDS v4f& { return reinterpret_cast<GFG_LDS v4f*>((GFG_LDS uint8_t*)s0 + v * UNIT)[i * 64 + lane]; };
+#pragma unroll
+    for (int y = 0; y < RB; ++y)
+#pragma unroll
+        for (int c = 0; c < CB; ++c) sums(wave, y * CB + c) = acc[y][c];
+    __syncthreads();
+    // wave y sums and stores the rows of fragment y
+    static_assert(RB <= NW, "a wave for each row fragment");
+    if (wave >= RB) return;
+    const int r = RB * l16 + wave, n = n0 + 4 * CB * lq;
+    if (r >= lim) return;
+    float v[4 * CB];
+#pragma unroll
+    for (int c = 0; c < CB; ++c) {
+        v4f t = sums(0, wave * CB + c);
+#pragma unroll
+        for (int u = 1; u < NW; ++u) t += sums(u, wave * CB + c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[CB * i + c] = t[i];
+            if (p.bias) v[CB * i + c] += p.bias[min(n + CB * i + c, p.N - 1)];
+        }
+    }
+    store_row<4 * CB>(static_cast<OutT*>(p.d) + (row0 + r) * p.N, n, p.N, v, p.accumulate);
+}
+
+template <int RB, int CB, int NW, int D, bool BROW, typename OutT>
+__global__ __launch_bounds__(NW * 64) void fp8_stream_kernel(F8Params p) {
+    walk(p.tiles, [&](unsigned w) { stream_tile<RB, CB, NW, D, BROW, OutT>(p, w); });
+}
+
+// Workgroups of a launch over p.tiles tiles: one for each, or as many as the
+// grid limit allows, which is rounded up to whole slots on every XCD.
+unsigned workgroups(const F8Params& p) {
+    const int lim = grid_limit();
+    const unsigned nx = unsigned(p.num_xcd), most = lim > 0 ? (unsigned(lim) + nx - 1) / nx * nx : p.tiles;
+    return p.tiles < most ? p.tiles : most;
+}
+
+int launched() {
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return fail(GFG_EHIP, "kernel launch failed: %s", hipGetErrorString(e));
+    return GFG_OK;
+}
+
+template <int TM, int TN, int WM, int WN, bool BROW>
+int launch_ring(F8Params p, int out_dtype, hipStream_t s) {
+    p.m_tiles = int((p.rows + TM - 1) / TM);
+    const int64_t tiles = int64_t(p.m_tiles) * ((p.N + TN - 1) / TN);
+    if (tiles * (WM * WN * 64) >= int64_t(1) << 32) return fail(GFG_EUNSUPPORTED, "the output has too many tiles for one launch");
+    p.tiles = unsigned(tiles);
+    const dim3 grid(workgroups(p)), block(WM * WN * 64);
+    if (out_dtype == GFG_OUT_BF16)
+        hipLaunchKernelGGL((fp8_ring_kernel<TM, TN, WM, WN, BROW, __bf16>), grid, block, 0, s, p);
+    else if (out_dtype == GFG_OUT_F16)
+        hipLaunchKernelGGL((fp8_ring_kernel<TM, TN, WM, WN, BROW, _Float16>), grid, block, 0, s, p);
+    else if constexpr (BROW)
+        hipLaunchKernelGGL((fp8_ring_kernel<TM, TN, WM, WN, BROW, float>), grid, block, 0, s, p);
+    return launched();
+}
+
+template <int RB, int CB, int NW, int D, bool BROW>
+int launch_stream(F8Params p, int out_dtype, hipStream_t s) {
+    p.m_tiles = int((p.rows + 16 * RB - 1) / (16 * RB));
+    const int64_t tiles = int64_t(p.m_tiles) * ((p.N + 16 * CB - 1) / (16 * CB));
+    if (tiles * (NW * 64) >= int64_t(1) << 32) return fail(GFG_EUNSUPPORTED, "the output has too many tiles for one launch");
+    p.tiles = unsigned(tiles);
+    const dim3 grid(workgroups(p)), block(NW * 64);
+    if (out_dtype == GFG_OUT_BF16)
+        hipLaunchKernelGGL((fp8_stream_kernel<RB, CB, NW, D, BROW, __bf16>), grid, block, 0, s, p);
+    else if (out_dtype == GFG_OUT_F16)
+        hipLaunchKernelGGL((fp8_stream_kernel<RB, CB, NW, D, BROW, _Float16>), grid, block, 0, s, p);
+    else if constexpr (BROW)
+        hipLaunchKernelGGL((fp8_stream_kernel<RB, CB, NW, D, BROW, float>), grid, block, 0, s, p);
+    return launched();
+}
+
+// A tile's lane loads the scale bytes of its RB (CB) neighbouring rows at once,
+// so an operand has to have that many rows: up to 16 rows of A go to RB = 1,
+// and the gradient of a weight has at least 16 of both.
+template <bool BROW>
+int launch_product(const F8Params& p, int out_dtype, hipStream_t s) {
+    if constexpr (!BROW)
+        if (p.rows <= 16) return launch_stream<1, 2, 4, 4, false>(p, out_dtype, s);
+    if (p.rows <= 32) return launch_stream<2, 2, 4, 2, BROW>(p, out_dtype, s);
+    auto tiles = [&](int64_t tm, int64_t tn) { return (p.rows + tm - 1) / tm * ((p.N + tn - 1) / tn); };
+    if (tiles(128, 128) >= 192) return launch_ring<128, 128, 2, 4, BROW>(p, out_dtype, s);
+    if (tiles(32, 32) <= 512) return launch_stream<2, 2, 4, 2, BROW>(p, out_dtype, s);
+    return launch_ring<64, 64, 2, 2, BROW>(p, out_dtype, s);
+}
+
+F8Params product(const void* a, const uint8_t* a_scale, int64_t ld_a, const void* b, const uint8_t* b_scale, int64_t ld_b,
+                 const float* bias, void* d, int64_t M, int64_t N, int64_t K) {
+    F8Params p{};
+    p.a = static_cast<const uint8_t*>(a);
+    p.a_scale = a_scale;
+    p.b = static_cast<const uint8_t*>(b);
+    p.b_scale = b_scale;
+    p.bias = bias;
+    p.d = d;
+    p.rows = M;
+    p.ld_a = ld_a;
+    p.ld_b = ld_b;
+    p.N = int(N);
+    p.K = int(K);
+    p.KB = int((K + QB - 1) / QB);
+    p.group_m = locality_group_m();
+    p.num_xcd = locality_num_xcd();
+    return p;
+}
+
+template <typename T>
+int launch_quant_rows(const void* x, uint8_t* q, uint8_t* scale, int64_t R, int64_t C, int64_t ld, hipStream_t s) {
+    const int64_t CB = (C + QB - 1) / QB;
+    if (R <= 16) {
+        hipLaunchKernelGGL((quant_rows_kernel<T, 1>), dim3(unsigned(CB)), dim3(256), 0, s, static_cast<const T*>(x), q, scale, R, int(C), ld);
+    } else {
+        const int64_t wgs = (R + 63) / 64 * CB;    // (below 2^31: R * CB is)
+        hipLaunchKernelGGL((quant_rows_kernel<T, 4>), dim3(unsigned(wgs)), dim3(256), 0, s, static_cast<const T*>(x), q, scale, R, int(C), ld);
+    }
+    return launched();
+}
+
+int quantize_rows(const void* x, int32_t in_dtype, uint8_t* q, uint8_t* scale, int64_t R, int64_t C, int64_t ld, hipStream_t s) {
+    if (in_dtype == GFG_IN_F32) return launch_quant_rows<float>(x, q, scale, R, C, ld, s);
+    if (in_dtype == GFG_IN_BF16) return launch_quant_rows<__bf16>(x, q, scale, R, C, ld, s);
+    return launch_quant_rows<_Float16>(x, q, scale, R, C, ld, s);
+}
+
+struct TileOut {
+    uint8_t *q, *scale;
+    int64_t ld;
+    uint8_t* qt;
+    int64_t ldt, store_t;
+    uint8_t* scale_t;
+    int64_t ld_t;
+    float* sums;
+};
+
+template <bool BLOCK>
+int quantize_tiles(const void* x, int32_t in_dtype, int64_t R, int64_t C, int64_t G, const TileOut& o, hipStream_t s) {
+    const dim3 grid(unsigned((R + QB - 1) / QB * ((C + QB - 1) / QB) * G));
+    auto go = [&](auto* kernel, auto* xs) {
+        hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, xs, o.q, o.scale, o.ld, o.qt, o.ldt, o.store_t, o.scale_t, o.ld_t, o.sums, R, int(C));
+    };
+    if (in_dtype == GFG_IN_F32) go(quant_tile_kernel<float, BLOCK>, static_cast<const float*>(x));
+    else if (in_dtype == GFG_IN_BF16) go(quant_tile_kernel<__bf16, BLOCK>, static_cast<const __bf16*>(x));
+    else go(quant_tile_kernel<_Float16, BLOCK>, static_cast<const _Float16*>(x));
+    return launched();
+}
+
+// ------------------------------------------------------------------ argument checks
+constexpr int64_t kMaxK = int64_t(1) << 22;            // 256 rows of K stay below 2^31 bytes
+constexpr int64_t kMaxN = int64_t(1) << 28;
+constexpr int64_t kMaxRows = int64_t(65535) * 128;
+
+bool misaligned(const void* p, uintptr_t by) { return reinterpret_cast<uintptr_t>(p) % by != 0; }
+
+int check_in(const char* fn, int32_t in_dtype) {
+    if (in_dtype != GFG_IN_F32 && in_dtype != GFG_IN_BF16 && in_dtype != GFG_IN_F16)
+        return fail(GFG_EINVAL, "%s: in_dtype %d is not a GFG_IN_* value", fn, in_dtype);
+    return GFG_OK;
+}
+
+// Sizes of a product of M rows; M = 0 passes.
+int check_sizes(const char* fn, int64_t M, int64_t N, int64_t K) {
+    if (M < 0 || N <= 0 || K <= 0)
+        return fail(GFG_EINVAL, "%s: bad sizes M=%lld N=%lld K=%lld", fn, (long long)M, (long long)N, (long long)K);
+    if (K % 16 || K > kMaxK)
+        return fail(GFG_EUNSUPPORTED, "%s: K=%lld must be a multiple of 16 and at most %lld", fn, (long long)K, (long long)kMaxK);
+    if (N > kMaxN) return fail(GFG_EUNSUPPORTED, "%s: N=%lld above 2^28", fn, (long long)N);
+    if (M > kMaxRows) return fail(GFG_EUNSUPPORTED, "%s: M=%lld above %lld", fn, (long long)M, (long long)kMaxRows);
+    if ((M + 3) * ((K + QB - 1) / QB) >= int64_t(1) << 31)
+        return fail(GFG_EUNSUPPORTED, "%s: M=%lld rows of %lld scales are 2^31 bytes or more", fn, (long long)M, (long long)((K + QB - 1) / QB));
+    return GFG_OK;
+}
+
+int check_out(const char* fn, int32_t out_dtype) {
+    if (out_dtype != GFG_OUT_BF16 && out_dtype != GFG_OUT_F16)
+        return fail(GFG_EINVAL, "%s: out_dtype %d is not GFG_OUT_BF16 or GFG_OUT_F16", fn, out_dtype);
+    return GFG_OK;
+}
+
+int check_operands(const char* fn, const void* a, const void* b, const void* b_scale, const void* bias, const void* d) {
+    if (!a || !b || !b_scale || !d) return fail(GFG_EINVAL, "%s: null pointer argument", fn);
+    if (misaligned(a, 16) || misaligned(b, 16) || misaligned(bias, 4) || misaligned(d, 8))
+        return fail(GFG_EINVAL, "%s: the operands must be 16-byte aligned, the output 8-byte, the bias 4-byte", fn);
+    return GFG_OK;
+}
+
+int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
+
+int check_workspace(const char* fn, const void* workspace, int64_t have, int64_t need) {
+    if (!workspace || misaligned(workspace, 16))
+        return fail(GFG_EINVAL, "%s: workspace must be a 16-byte aligned device pointer", fn);
+    if (have < need)
+        return fail(GFG_EINVAL, "%s: workspace of %lld bytes, %lld are needed", fn, (long long)have, (long long)need);
+    return GFG_OK;
+}
+
+// The backward workspace: dy along N with its scales, dy and x along the tokens
+// (padded to whole blocks) with theirs, and the parts of the bias's gradient.
+struct BackwardSpace {
+    int64_t Mp, MB, ldm, ldn, ldk, q, qs, yt, yts, xt, xts, sums, bytes;
+    BackwardSpace(int64_t M, int64_t N, int64_t K) {
+        Mp = up(M, QB);
+        MB = Mp / QB;
+        ldm = up(M, 4);
+        ldn = up(N, 4);
+        ldk = up(K, 4);
+        int64_t at = 0;
+        auto take = [&](int64_t n) {
+            const int64_t v = at;
+            at += up(n, 16);
+            return v;
+        };
+        q = take(M * N);
+        qs = take((N + QB - 1) / QB * ldm);
+        yt = take(N * Mp);
+        yts = take(MB * ldn);
+        xt = take(K * Mp);
+        xts = take(MB * ldk);
+        sums = take(MB * N * 4);
+        bytes = at;
+    }
+};
+
+template <typename T>
+void zero(T* p, int64_t n, hipStream_t s) {
+    const int64_t wgs = (n + 255) / 256;
+    hipLaunchKernelGGL((zero_kernel<T>), dim3(unsigned(wgs < 2048 ? wgs : 2048)), dim3(256), 0, s, p, n);
+}
+
+}  // namespace
+}  // namespace gfg
+
+using namespace gfg;
+
+extern "C" int fp8_quantize_weight_device(const void* w, int32_t in_dtype, int32_t G, int64_t N, int64_t K, uint8_t* q,
+                                          uint8_t* scale, uint8_t* q_t, uint8_t* scale_t, void* stream) {
+    clear_error();
+    const char* fn = "fp8_quantize_weight_device";
+    if (int rc = check_in(fn, in_dtype)) return rc;
+    if (G <= 0 || G > 65535) return fail(GFG_EINVAL, "%s: G=%d outside [1, 65535]", fn, G);
+    if (int rc = check_sizes(fn, 1, N, K)) return rc;
+    if ((N + QB - 1) / QB * ((K + QB - 1) / QB) * G >= int64_t(1) << 24)
+        return fail(GFG_EUNSUPPORTED, "%s: 2^24 blocks of 128 x 128 or more", fn);
+    if (!w || !q || !scale || (!q_t != !scale_t)) return fail(GFG_EINVAL, "%s: null pointer argument", fn);
+    if (misaligned(w, 16) || misaligned(q, 16) || misaligned(q_t, 16))
+        return fail(GFG_EINVAL, "%s: w, q and q_t must be 16-byte aligned", fn);
+    if (q_t && N % 16) return fail(GFG_EUNSUPPORTED, "%s: N=%lld must be a multiple of 16 for the transposed codes", fn, (long long)N);
+    return quantize_tiles<true>(w, in_dtype, N, K, G, TileOut{q, scale, 0, q_t, N, N, scale_t, 0, nullptr}, static_cast<hipStream_t>(stream));
+}
+
+extern "C" int fp8_gemm(const void* a, const uint8_t* a_scale, int64_t a_scale_ld, const void* b, const uint8_t* b_scale,
+                        const float* bias, void* d, int64_t M, int64_t N, int64_t K, int32_t out_dtype, void* stream) {
+    clear_error();
+    const char* fn = "fp8_gemm";
+    if (int rc = check_out(fn, out_dtype)) return rc;
+    if (int rc = check_sizes(fn, M, N, K)) return rc;
+    if (M == 0) return GFG_OK;
+    if (a_scale_ld < M) return fail(GFG_EINVAL, "%s: a_scale_ld=%lld is below M=%lld", fn, (long long)a_scale_ld, (long long)M);
+    if (int rc = check_operands(fn, a, b, b_scale, bias, d)) return rc;
+    if (!a_scale) return fail(GFG_EINVAL, "%s: null pointer argument", fn);
+    return launch_product<false>(product(a, a_scale, a_scale_ld, b, b_scale, 0, bias, d, M, N, K), out_dtype, static_cast<hipStream_t>(stream));
+}
+
+extern "C" int64_t fp8_linear_workspace_bytes(int64_t M, int64_t K) {
+    return M > 0 && K > 0 ? M * up(K, 16) + (K + QB - 1) / QB * up(M, 4) : 0;
+}
+
+extern "C" int fp8_linear(const void* x, int32_t in_dtype, const void* b, const uint8_t* b_scale, const float* bias, void* d,
+                          int64_t M, int64_t N, int64_t K, int32_t out_dtype, void* workspace, int64_t workspace_bytes, void* stream) {
+    clear_error();
+    const char* fn = "fp8_linear";
+    if (int rc = check_in(fn, in_dtype)) return rc;
+    if (int rc = check_out(fn, out_dtype)) return rc;
+    if (int rc = check_sizes(fn, M, N, K)) return rc;
+    if (M == 0) return GFG_OK;
+    if ((M + 63) / 64 * ((K + QB - 1) / QB) >= int64_t(1) << 24)
+        return fail(GFG_EUNSUPPORTED, "%s: x has 2^37 elements or more", fn);
+    if (int rc = check_operands(fn, x, b, b_scale, bias, d)) return rc;
+    if (int rc = check_workspace(fn, workspace, workspace_bytes, fp8_linear_workspace_bytes(M, K))) return rc;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    uint8_t *q = static_cast<uint8_t*>(workspace), *scale = q + M * K;
+    const int64_t ld = up(M, 4);
+    if (int rc = quantize_rows(x, in_dtype, q, scale, M, K, ld, s)) return rc;
+    return launch_product<false>(product(q, scale, ld, b, b_scale, 0, bias, d, M, N, K), out_dtype, s);
+}
+
+extern "C" int64_t fp8_linear_backward_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+    return M > 0 && N > 0 && K > 0 ? BackwardSpace(M, N, K).bytes : 0;
+}
+
+extern "C" int fp8_linear_backward(const void* dy, const void* x, int32_t in_dtype, const void* b_t, const uint8_t* b_t_scale,
+                                   void* dx, void* dw, float* dbias, int64_t M, int64_t N, int64_t K, int32_t dx_dtype,
+                                   int32_t dw_dtype, int32_t accumulate, void* workspace, int64_t workspace_bytes, void* stream) {
+    clear_error();
+    const char* fn = "fp8_linear_backward";
+    if (int rc = check_in(fn, in_dtype)) return rc;
+    if (dx)
+        if (int rc = check_out(fn, dx_dtype)) return rc;
+    if (dw && dw_dtype != GFG_OUT_F32)
+        if (int rc = check_out(fn, dw_dtype)) return rc;
+    if (dw && accumulate && dw_dtype != GFG_OUT_F32)
+        return fail(GFG_EINVAL, "%s: a gradient that is added to has to be GFG_OUT_F32", fn);
+    if (int rc = check_sizes(fn, M, N, K)) return rc;
+    if (N % 16 || N > kMaxK)
+        return fail(GFG_EUNSUPPORTED, "%s: N=%lld must be a multiple of 16 and at most %lld", fn, (long long)N, (long long)kMaxK);
+    if (M > kMaxK) return fail(GFG_EUNSUPPORTED, "%s: M=%lld above %lld", fn, (long long)M, (long long)kMaxK);
+    const int64_t MB = (M + QB - 1) / QB;
+    if (MB * ((N > K ? N : K) + QB) >= int64_t(1) << 31)
+        return fail(GFG_EUNSUPPORTED, "%s: dy or x (M=%lld, N=%lld, K=%lld) has 2^38 elements or more", fn, (long long)M, (long long)N, (long long)K);
+    if (!dx && !dw && !dbias) return fail(GFG_EINVAL, "%s: dx, dw and dbias are all null", fn);
+    if (misaligned(dx, 8) || misaligned(dw, 8) || misaligned(dbias, 4))
+        return fail(GFG_EINVAL, "%s: dx and dw must be 8-byte aligned, dbias 4-byte", fn);
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (M == 0) {                                  // the sums over no tokens
+        if (accumulate) return GFG_OK;
+        if (dw && dw_dtype == GFG_OUT_F32) zero(static_cast<float*>(dw), N * K, s);
+        else if (dw) zero(static_cast<_Float16*>(dw), N * K, s);       // (bf16 and f16 zeros are the same bits)
+        if (dbias) zero(dbias, N, s);
+        return launched();
+    }
+    if (!dy || (dw && !x) || (dx && (!b_t || !b_t_scale))) return fail(GFG_EINVAL, "%s: null pointer argument", fn);
+    if (misaligned(dy, 16) || misaligned(x, 16) || misaligned(b_t, 16))
+        return fail(GFG_EINVAL, "%s: dy, x and b_t must be 16-byte aligned", fn);
+    const BackwardSpace at(M, N, K);
+    if (int rc = check_workspace(fn, workspace, workspace_bytes, at.bytes)) return rc;
+    uint8_t* const ws = static_cast<uint8_t*>(workspace);
+    float* const sums = reinterpret_cast<float*>(ws + at.sums);
+    if (int rc = quantize_tiles<false>(dy, in_dtype, M, N, 1,
+                                       TileOut{dx ? ws + at.q : nullptr, ws + at.qs, at.ldm, dw ? ws + at.yt : nullptr, at.Mp, at.Mp,
+                                               ws + at.yts, at.ldn, dbias ? sums : nullptr}, s))
+        return rc;
+    if (dw) {
+        if (int rc = quantize_tiles<false>(x, in_dtype, M, K, 1,
+                                           TileOut{nullptr, nullptr, 0, ws + at.xt, at.Mp, at.Mp, ws + at.xts, at.ldk, nullptr}, s))
+            return rc;
+    }
+    if (dbias) {
+        hipLaunchKernelGGL(column_sums_kernel, dim3(unsigned((N + 15) / 16)), dim3(256), 0, s, sums, dbias, at.MB, int(N), accumulate);
+        if (int rc = launched()) return rc;
+    }
+    if (dx)
+        if (int rc = launch_product<false>(product(ws + at.q, ws + at.qs, at.ldm, b_t, b_t_scale, 0, nullptr, dx, M, K, N), dx_dtype, s)) return rc;
+    if (!dw) return GFG_OK;
+    F8Params p = product(ws + at.yt, ws + at.yts, at.ldn, ws + at.xt, ws + at.xts, at.ldk, nullptr, dw, N, K, at.Mp);
+    p.accumulate = accumulate;
+    return launch_product<true>(p, dw_dtype, s);
+}

@@ -56,7 +56,7 @@ enum gfg_status {
     GFG_ERANGE = 4        /* quantizer: a block scale falls outside E8M0's range  */
 };
 
-enum gfg_out_dtype { GFG_OUT_BF16 = 0, GFG_OUT_F16 = 1 };
+enum gfg_out_dtype { GFG_OUT_BF16 = 0, GFG_OUT_F16 = 1, GFG_OUT_F32 = 2 /* where a call says so */ };
 enum gfg_in_dtype { GFG_IN_F32 = 0, GFG_IN_BF16 = 1, GFG_IN_F16 = 2 };
 
 /*
@@ -437,6 +437,170 @@ GFG_API int moe_int8_layer(const void* x, int32_t dtype, const int32_t* topk_ids
                            const int8_t* w1, const float* w1_scale, const int8_t* w2, const float* w2_scale, void* out,
                            int64_t T, int64_t k, int64_t E, int64_t H, int64_t I, void* workspace,
                            int64_t workspace_bytes, void* stream);
+
+/*
+ * FP8 linear layer (GPU, asynchronous on `stream`): the dense product on the
+ * grouped GEMMs' operands, from one token on, with its quantizers and its
+ * gradients.  Per block, t = the smallest integer with 448 * 2^t >= max|v| (t = 0
+ * for zeros, at least -127), scale byte t + 127, code E4M3(v / 2^t) to nearest even;
+ * a block with a NaN or an infinity gets byte 255 (NaN) and the codes of NaN, so
+ * whatever it enters is NaN.  A last block of fewer elements has a scale of its own.
+ *
+ * fp8_gemm: d[m, n] = sum_k a[m, k] b[n, k] + bias[n]
+ *   a [M][K] e4m3 ; a_scale [ceil(K/128)][a_scale_ld] E8M0, row m in byte m,
+ *   a_scale_ld >= M (the grouped GEMMs' layout has a_scale_ld = M)
+ *   b [N][K] e4m3 ; b_scale [ceil(N/128)][ceil(K/128)] E8M0
+ *   bias [N] float or NULL ; d [M][N] bf16 or f16
+ * fp8_linear: the same from x [M][K] (GFG_IN_F32, _BF16 or _F16), which it
+ *   quantizes in blocks of 1 x 128 into the workspace (at least
+ *   fp8_linear_workspace_bytes(M, K) bytes of device memory, 16-byte aligned,
+ *   uninitialized; a call leaves nothing in it for the next).
+ *
+ * The sums are fp32 sums of the matrix instruction's products of 128 k, inside
+ * which a product 2^14 times smaller than another of its group of 16 may be
+ * dropped: an error of about 2e-5 of the result's norm.  d is rounded once.
+ *
+ * fp8_linear_backward, for y = x W^T + bias and the gradient dy of y:
+ *   dx = Q(dy) W          dy in blocks of 1 x 128 along N
+ *   dW = Q(dy^T) Q(x^T)^T both in blocks of 128 tokens
+ *   dbias = the sum of dy over the tokens, in fp32
+ *   dy [M][N], x [M][K] (the same in_dtype) ; b_t [K][N] e4m3, b_t_scale
+ *   [ceil(K/128)][ceil(N/128)]: the transposed weight (fp8_quantize_weight_device)
+ *   dx [M][K] bf16 or f16 ; dw [N][K] bf16, f16 or GFG_OUT_F32 ; dbias [N] float
+ *   Each of dx, dw and dbias may be NULL (not all), and is then not computed; x
+ *   is read for dw, b_t for dx.  accumulate: dw (GFG_OUT_F32 only, else
+ *   GFG_EINVAL) and dbias are added to.  M = 0: dw and dbias are zeros, or are
+ *   left as they are.
+ *   workspace: at least fp8_linear_backward_workspace_bytes(M, N, K) bytes, as above.
+ *
+ * fp8_quantize_weight_device: w [G][N][K] (32 or 16 bits) in blocks of 128 x 128:
+ *   q [G][N][K], scale [G][ceil(N/128)][ceil(K/128)], and, unless both are NULL,
+ *   the same codes and bytes transposed, q_t [G][K][N], scale_t
+ *   [G][ceil(K/128)][ceil(N/128)] (N a multiple of 16).  The grouped GEMMs' B
+ *   operand is one of these too.
+ *
+ * Alignment: x, dy, w and all codes 16 bytes, d, dx and dw 8, bias and dbias 4
+ * (else GFG_EINVAL).  Two calls with the same operands give the same bytes.
+ *
+ * Sizes: M >= 0 and at most 128 * 65535 (0 is a no-op, but for the gradients
+ * above), N in [1, 2^28], K a multiple of 16 up to 2^22, fewer than 2^31 scale
+ * bytes, 2^37 elements of x and 2^24 tiles of 128 x 128; backward: also N a multiple of
+ * 16 up to 2^22, and M at most 2^22; else GFG_EUNSUPPORTED.
+ */
+GFG_API int fp8_gemm(const void* a, const uint8_t* a_scale, int64_t a_scale_ld, const void* b, const uint8_t* b_scale,
+                     const float* bias, void* d, int64_t M, int64_t N, int64_t K, int32_t out_dtype, void* stream);
+GFG_API int64_t fp8_linear_workspace_bytes(int64_t M, int64_t K);
+GFG_API int fp8_linear(const void* x, int32_t in_dtype, const void* b, const uint8_t* b_scale, const float* bias, void* d,
+                       int64_t M, int64_t N, int64_t K, int32_t out_dtype, void* workspace, int64_t workspace_bytes,
+                       void* stream);
+GFG_API int64_t fp8_linear_backward_workspace_bytes(int64_t M, int64_t N, int64_t K);
+GFG_API int fp8_linear_backward(const void* dy, const void* x, int32_t in_dtype, const void* b_t, const uint8_t* b_t_scale,
+                                void* dx, void* dw, float* dbias, int64_t M, int64_t N, int64_t K, int32_t dx_dtype,
+                                int32_t dw_dtype, int32_t accumulate, void* workspace, int64_t workspace_bytes,
+                                void* stream);
+GFG_API int fp8_quantize_weight_device(const void* w, int32_t in_dtype, int32_t G, int64_t N, int64_t K, uint8_t* q,
+                                       uint8_t* scale, uint8_t* q_t, uint8_t* scale_t, void* stream);
+
+/*
+ * Between two blocks of a network (GPU, asynchronous on `stream`): the norm after
+ * a block, its gate, the residual sum and the norm before the next block, in one
+ * pass over the rows.  With rstd(v) = 1 / sqrt(mean(v^2) + eps), per row m of H:
+ *
+ *   u      = y * rstd(y) * post_weight     or u = y without post_weight
+ *   out    = alpha * residual + gate * u   (gate 1 where there is none, u = 0 without y)
+ *   normed = out * rstd(out) * weight      of the unrounded out
+ *
+ *   y [M][H] (dtype: GFG_IN_*) or NULL ; residual, out [M][H] (residual_dtype:
+ *   dtype, or GFG_IN_F32) ; normed [M][H] (dtype) ; post_weight, weight [H] float
+ *   gate: GFG_GATE_NONE, GFG_GATE_CHANNEL (float [H]) or GFG_GATE_TOKEN (float [M])
+ *   out may be residual itself, and may be NULL; without weight there is no normed.
+ *   stats [2][M] float or NULL: rstd(y) (1 without y or post_weight) and rstd(out)
+ *   (written where weight is given)
+ *   residual_norm_fp8: normed as the operand of fp8_gemm and the grouped GEMMs, in
+ *   place of 16 bits: q [M][H] e4m3, scale [ceil(H/128)][scale_ld] E8M0 (H a multiple
+ *   of 16, q 8-byte aligned), quantized as in fp8_linear from the unrounded values
+ *
+ * residual_norm_backward: from dout [M][H] (residual_dtype) and dnormed [M][H]
+ * (dtype), either may be NULL, and the forward call's out, y and stats.  With
+ * zh = out * rstd(out), yh = y * rstd(y) (y without post_weight):
+ *
+ *   G  = dout + rstd(out) * (dnormed * weight - zh * mean(dnormed * weight * zh))
+ *   dresidual = alpha * G ; du = gate * G
+ *   dy = rstd(y) * (post_weight * du - yh * mean(post_weight * du * yh))  (du without post_weight)
+ *   dweight = sum_m dnormed * zh ; dpost_weight = sum_m du * yh ; dgate = the sum
+ *   of G * u over m (GFG_GATE_CHANNEL) or over the row (GFG_GATE_TOKEN)
+ *
+ *   Each output may be NULL.  accumulate: dweight, dpost_weight and a channel
+ *   gate's dgate are added to.  M = 0 writes zeros to those (unless accumulated).
+ *   workspace: residual_norm_backward_workspace_bytes(M, H) bytes of device memory,
+ *   16-byte aligned, uninitialized; needed for dweight, dpost_weight and a channel
+ *   gate's dgate.
+ *
+ * All sums and statistics are fp32 (so a row's squares have to sum up within
+ * fp32's range); every output is rounded once.  Two calls give the same bytes.
+ * Rows need no alignment beyond that of their elements.
+ *
+ * Sizes: M >= 0 (0 is a no-op but for the sums) and below 2^31, H in [1, 32768]
+ * (else GFG_EUNSUPPORTED).
+ */
+enum gfg_gate { GFG_GATE_NONE = 0, GFG_GATE_CHANNEL = 1, GFG_GATE_TOKEN = 2 };
+GFG_API int residual_norm(const void* y, const void* residual, const float* weight, const float* post_weight,
+                          const float* gate, int32_t gate_kind, float alpha, float eps, void* out, void* normed,
+                          float* stats, int64_t M, int64_t H, int32_t dtype, int32_t residual_dtype, void* stream);
+GFG_API int residual_norm_fp8(const void* y, const void* residual, const float* weight, const float* post_weight,
+                              const float* gate, int32_t gate_kind, float alpha, float eps, void* out, uint8_t* q,
+                              uint8_t* scale, int64_t scale_ld, float* stats, int64_t M, int64_t H, int32_t dtype,
+                              int32_t residual_dtype, void* stream);
+GFG_API int64_t residual_norm_backward_workspace_bytes(int64_t M, int64_t H);
+GFG_API int residual_norm_backward(const void* dout, const void* dnormed, const void* out, const void* y,
+                                   const float* stats, const float* weight, const float* post_weight,
+                                   const float* gate, int32_t gate_kind, float alpha, void* dresidual, void* dy,
+                                   float* dweight, float* dpost_weight, float* dgate, int32_t accumulate, int64_t M,
+                                   int64_t H, int32_t dtype, int32_t residual_dtype, void* workspace,
+                                   int64_t workspace_bytes, void* stream);
+
+/*
+ * Training of the router (GPU, asynchronous on `stream`).  moe_balance_loss: how
+ * unevenly the tokens of each sequence spread over the experts, with the counts.
+ * A token counts if it has an id in [0, E) (padding has ids -1, say).  For
+ * sequence s with n tokens that count, over those:
+ *
+ *   counts[s, e] = how often e is an id ;  f_e = counts[s, e] * E / (k n)
+ *   P_e = mean of p_e: the softmax of the logits, or the sigmoids over their sum
+ *   loss = 1/S sum_s (alpha * sum_e f_e P_e + z * mean(logsumexp(logits)^2))
+ *
+ * Logits of -infinity or NaN are of masked experts (p = 0).  A sequence without
+ * such tokens adds 0.
+ *
+ *   logits [T][E] (GFG_IN_*) ; ids [T][k] int32 (moe_topk's) ; seq_offsets [S+1]
+ *   int32, rising from 0 to T, or NULL with S = 1 ; tokens outside are in no sequence
+ *   loss [1] float ; counts [S][E] int32
+ *   factors [S][E+1] float: alpha f_e / (S n), then 2 z / (S n), for the gradient
+ *   workspace: moe_balance_workspace_bytes(T, E, S) bytes of device memory, 16-byte
+ *   aligned, uninitialized
+ *
+ * moe_router_backward: dlogits [T][E] (the logits' type) of
+ *
+ *   dloss * loss + sum over t, j of dweights[t, j] * weights[t, j]
+ *
+ * with moe_topk's weights (same score, renormalize and scale; the choice and the
+ * bias have no gradient).  dweights [T][k] float or NULL ; factors (with seq_offsets
+ * and S as above) and dloss [1] float, both or neither NULL.  Ids outside [0, E)
+ * have no weight; an id that stands twice has both.  dlogits is 0 where p is.
+ *
+ * Counts are exact, the sums fp32 in a fixed order: two calls give the same bytes.
+ * Sizes: T >= 0 (0: loss and counts are 0) and below 2^31, E in [1, 1024],
+ * k in [1, 64], S in [1, 65535] (else GFG_EUNSUPPORTED).
+ */
+GFG_API int64_t moe_balance_workspace_bytes(int64_t T, int64_t E, int64_t S);
+GFG_API int moe_balance_loss(const void* logits, int32_t in_dtype, const int32_t* ids, const int32_t* seq_offsets,
+                             float* loss, int32_t* counts, float* factors, int64_t T, int64_t E, int64_t k, int64_t S,
+                             int32_t score, float alpha, float z, void* workspace, int64_t workspace_bytes,
+                             void* stream);
+GFG_API int moe_router_backward(const void* logits, int32_t in_dtype, const int32_t* ids, const float* dweights,
+                                const float* factors, const float* dloss, const int32_t* seq_offsets, void* dlogits,
+                                int64_t T, int64_t E, int64_t k, int64_t S, int32_t score, int32_t renormalize,
+                                float scale, void* stream);
 
 /*
  * Launch settings (process-wide, read at every GEMM call; not synchronized
