@@ -371,6 +371,17 @@ __device__ __forceinline__ void store_row(OutT* row, int n, int N, const float (
     }
 }
 
+// The bias of columns n .. n + CNT - 1; without one -0, which changes nothing, not even a zero's sign.
+template <int CNT>
+__device__ __forceinline__ void load_bias(float (&v)[CNT], const F8Params& p, int n) {
+#pragma unroll
+    for (int i = 0; i < CNT; ++i) v[i] = -0.0f;
+    if (p.bias) {
+#pragma unroll
+        for (int i = 0; i < CNT; ++i) v[i] = p.bias[min(n + i, p.N - 1)];
+    }
+}
+
 // TM x TN output tiles, WM x WN waves, K in steps of 128 through four LDS
 // stages filled by direct-to-LDS loads: three are in flight while one is
 // consumed, and a step has one barrier (a wave that passes it has seen every
@@ -415,6 +426,7 @@ __device__ __forceinline__ void ring_tile(const F8Params& p, unsigned w) {
     uint32_t sa[S], sb[S];
     auto issue = [&](int j, int kb) {
         const int ks = min(kb, p.KB - 1);
+        __builtin_amdgcn_sched_barrier(0);         // (the waits count what was issued after a stage's loads)
         sa[j] = *reinterpret_cast<const typename Bytes<RB>::type*>(p.a_scale + ks * p.ld_a + at_a.at);
         if (BROW) sb[j] = *reinterpret_cast<const typename Bytes<CB>::type*>(p.b_scale + ks * p.ld_b + at_b.at);
         else sb[j] = uint32_t(load_scale_word(sb_row, ks));
@@ -427,6 +439,7 @@ __device__ __forceinline__ void ring_tile(const F8Params& p, unsigned w) {
             __builtin_amdgcn_raw_ptr_buffer_load_lds(i < A_LOADS ? ra : rb, (GFG_LDS void*)(buf[j] + (WAVES * i + wave) * 1024), 16,
                                                      (i < A_LOADS ? oa : ob) + uint32_t(8 * WAVES * jr) * uint32_t(p.K), 0, 0, 0);
         }
+        __builtin_amdgcn_sched_barrier(0);
     };
     auto frag = [&](GFG_LDS uint8_t* src, int row, int key) {
         auto part = [&](int c) { return *reinterpret_cast<GFG_LDS u32x4*>(src + row * QB + ((c ^ key) << 4)); };
@@ -435,9 +448,9 @@ __device__ __forceinline__ void ring_tile(const F8Params& p, unsigned w) {
     v4f acc[RB][CB] = {};                          // [row fragment][column fragment]
 #pragma unroll
     for (int j = 0; j < S - 1; ++j) issue(j, j);
-    auto step = [&](int j, int kb) {
+    auto step = [&](int j, int kb, auto ops) {
         __builtin_amdgcn_sched_barrier(0);
-        GFG_WAITCNT((S - 2) * OPS, 15);
+        GFG_WAITCNT((S - 2) * decltype(ops)::value, 15);
         lds_barrier();
         __builtin_amdgcn_sched_barrier(0);
         const int a_bytes = scale_bytes<RB>(sa[j], at_a);
@@ -462,17 +475,20 @@ __device__ __forceinline__ void ring_tile(const F8Params& p, unsigned w) {
     };
     // whole rounds of the ring, then the rest: a loop with one way out, in which
     // every path to a stage's reads passes the same loads, so that the compiler's
-    // own waits stay exact
+    // own waits stay exact.  (The rest's own scale loads are of use to nobody and
+    // not issued, so its waits count the direct-to-LDS loads alone.)
+    constexpr std::integral_constant<int, OPS> all{};
+    constexpr std::integral_constant<int, PER> least{};
     int kb = 0;
     for (; kb + S <= p.KB; kb += S) {
 #pragma unroll
-        for (int j = 0; j < S; ++j) step(j, kb + j);
+        for (int j = 0; j < S; ++j) step(j, kb + j, all);
     }
     if (kb < p.KB) {
-        step(0, kb);
+        step(0, kb, least);
         if (kb + 1 < p.KB) {
-            step(1, kb + 1);
-            if (kb + 2 < p.KB) step(2, kb + 2);
+            step(1, kb + 1, least);
+            if (kb + 2 < p.KB) step(2, kb + 2, least);
         }
     }
     GFG_WAITCNT(0, 15);                            // the last loads land before the workgroup ends
@@ -480,6 +496,8 @@ __device__ __forceinline__ void ring_tile(const F8Params& p, unsigned w) {
     // acc[y][c][i] of lane (l16, lq): row RB l16 + y, column CB (4 lq + i) + c
     OutT* const d = static_cast<OutT*>(p.d);
     const int n = n0 + wn + 4 * CB * lq;
+    float bias[4 * CB];
+    load_bias(bias, p, n);
 #pragma unroll
     for (int y = 0; y < RB; ++y) {
         const int r = wm + RB * l16 + y;
@@ -488,10 +506,7 @@ __device__ __forceinline__ void ring_tile(const F8Params& p, unsigned w) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int c = 0; c < CB; ++c) {
-                v[CB * i + c] = acc[y][c][i];
-                if (p.bias) v[CB * i + c] += p.bias[min(n + CB * i + c, p.N - 1)];
-            }
+            for (int c = 0; c < CB; ++c) v[CB * i + c] = acc[y][c][i] + bias[CB * i + c];
         store_row<4 * CB>(d + (row0 + r) * p.N, n, p.N, v, p.accumulate);
     }
 }
@@ -551,6 +566,7 @@ __device__ __forceinline__ void stream_tile(const F8Params& p, unsigned w) {
     uint32_t sa[D], sb[D];
     auto load = [&](int d, int kb) {
         const int ks = min(kb, p.KB - 1);
+        __builtin_amdgcn_sched_barrier(0);
         sa[d] = *reinterpret_cast<const typename Bytes<RB>::type*>(p.a_scale + ks * p.ld_a + at_a.at);
         if (BROW) sb[d] = *reinterpret_cast<const typename Bytes<CB>::type*>(p.b_scale + ks * p.ld_b + at_b.at);
         else sb[d] = uint32_t(load_scale_word(sb_row, ks));
@@ -564,6 +580,7 @@ __device__ __forceinline__ void stream_tile(const F8Params& p, unsigned w) {
             __builtin_amdgcn_raw_ptr_buffer_load_lds(of_a ? ra : rb, (GFG_LDS void*)(ring[d] + i * 1024), 16,
                                                      k < p.K ? uint32_t(row) * uint32_t(p.K) + uint32_t(k) : kOutside, 0, 0, 0);
         }
+        __builtin_amdgcn_sched_barrier(0);
     };
     v4f acc[RB][CB] = {};
     auto frag = [&](GFG_LDS uint8_t* src, int row, int key) {
@@ -571,9 +588,9 @@ __device__ __forceinline__ void stream_tile(const F8Params& p, unsigned w) {
         return join(part(lq), part(lq + 4));
     };
     // consume a unit, then load the one that takes its place, D units ahead
-    auto step = [&](int d, int kb) {
+    auto step = [&](int d, int kb, auto ops) {
         __builtin_amdgcn_sched_barrier(0);
-        GFG_WAITCNT((D - 1) * OPS, 15);
+        GFG_WAITCNT((D - 1) * decltype(ops)::value, 15);
         __builtin_amdgcn_sched_barrier(0);
         const int a_bytes = scale_bytes<RB>(sa[d], at_a);
         const int b_bytes = BROW ? scale_bytes<CB>(sb[d], at_b) : scale_byte(int(sb[d]), sb_row, kb);
@@ -592,23 +609,23 @@ __device__ __forceinline__ void stream_tile(const F8Params& p, unsigned w) {
         for (int y = 0; y < RB; ++y)
 #pragma unroll
             for (int c = 0; c < CB; ++c) acc[y][c] = mfma(bf[c], af[y], acc[y][c], BROW ? c : 0, b_bytes, y, a_bytes);
-        __builtin_amdgcn_sched_barrier(0);
         load(d, kb + D * NW);                      // past K: zeros
-        __builtin_amdgcn_sched_barrier(0);
     };
+    constexpr std::integral_constant<int, OPS> all{};
+    constexpr std::integral_constant<int, PER> least{};
 #pragma unroll
     for (int d = 0; d < D; ++d) load(d, wave + d * NW);
     int kb = wave;                                 // (rounds as above)
     for (; kb + (D - 1) * NW < p.KB; kb += D * NW) {
 #pragma unroll
-        for (int d = 0; d < D; ++d) step(d, kb + d * NW);
+        for (int d = 0; d < D; ++d) step(d, kb + d * NW, all);
     }
     if (kb < p.KB) {
-        step(0, kb);
+        step(0, kb, least);
         if constexpr (D > 2) {
             if (kb + NW < p.KB) {
-                step(1, kb + NW);
-                if (kb + 2 * NW < p.KB) step(2, kb + 2 * NW);
+                step(1, kb + NW, least);
+                if (kb + 2 * NW < p.KB) step(2, kb + 2 * NW, least);
             }
         }
     }
@@ -626,17 +643,15 @@ __device__ __forceinline__ void stream_tile(const F8Params& p, unsigned w) {
     if (wave >= RB) return;
     const int r = RB * l16 + wave, n = n0 + 4 * CB * lq;
     if (r >= lim) return;
-    float v[4 * CB];
+    float v[4 * CB], bias[4 * CB];
+    load_bias(bias, p, n);
 #pragma unroll
     for (int c = 0; c < CB; ++c) {
         v4f t = sums(0, wave * CB + c);
 #pragma unroll
         for (int u = 1; u < NW; ++u) t += sums(u, wave * CB + c);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[CB * i + c] = t[i];
-            if (p.bias) v[CB * i + c] += p.bias[min(n + CB * i + c, p.N - 1)];
-        }
+        for (int i = 0; i < 4; ++i) v[CB * i + c] = t[i] + bias[CB * i + c];
     }
     store_row<4 * CB>(static_cast<OutT*>(p.d) + (row0 + r) * p.N, n, p.N, v, p.accumulate);
 }
@@ -933,7 +948,7 @@ extern "C" int fp8_linear_backward(const void* dy, const void* x, int32_t in_dty
         return fail(GFG_EINVAL, "%s: dx and dw must be 8-byte aligned, dbias 4-byte", fn);
     hipStream_t s = static_cast<hipStream_t>(stream);
     if (M == 0) {                                  // the sums over no tokens
-        if (accumulate) return GFG_OK;
+        if (accumulate || (!dw && !dbias)) return GFG_OK;
         if (dw && dw_dtype == GFG_OUT_F32) zero(static_cast<float*>(dw), N * K, s);
         else if (dw) zero(static_cast<_Float16*>(dw), N * K, s);       // (bf16 and f16 zeros are the same bits)
         if (dbias) zero(dbias, N, s);

@@ -52,10 +52,10 @@ __device__ __forceinline__ void load_logits(float (&l)[NE], const L* row, int E,
     }
 }
 
-// Its softmax in `e` (zeros if every expert is masked) and logsumexp.
+// Its softmax in `e` (zeros if every expert is masked): e^(l - top) * inv; returns logsumexp.
 template <int NE>
-__device__ __forceinline__ float softmax_of(const float (&l)[NE], float (&e)[NE]) {
-    float top = l[0];
+__device__ __forceinline__ float softmax_of(const float (&l)[NE], float (&e)[NE], float& top, float& inv) {
+    top = l[0];
 #pragma unroll
     for (int j = 1; j < NE; ++j) top = fmaxf(top, l[j]);
     top = wave_reduce(top, [](float a, float b) { return fmaxf(a, b); });
@@ -67,7 +67,7 @@ __device__ __forceinline__ float softmax_of(const float (&l)[NE], float (&e)[NE]
         sum += e[j];
     }
     sum = wave_reduce(sum, add);
-    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+    inv = sum > 0.0f ? 1.0f / sum : 0.0f;
 #pragma unroll
     for (int j = 0; j < NE; ++j) e[j] *= inv;
     return sum > 0.0f ? top + __logf(sum) : 0.0f;
@@ -124,11 +124,11 @@ __global__ __launch_bounds__(256) void balance_sums_kernel(RouterArgs p) {
             const bool chosen = id >= 0 && id < p.E;
             if (!__any(chosen)) continue;
             if (chosen) atomicAdd(&count[id], 1);
-            float l[NE], e[NE];
+            float l[NE], e[NE], top, scale;
             load_logits(l, static_cast<const L*>(p.logits) + t * p.E, p.E, lane);
             if (p.score == GFG_SCORE_SOFTMAX || p.z != 0.0f) {
-                const float lse = softmax_of(l, e);
-                z += lse * lse;
+                const float lse = softmax_of(l, e, top, scale);
+                if (p.z != 0.0f) z += lse * lse;
             }
             if (p.score == GFG_SCORE_SIGMOID) {
                 float all = 0.0f, slope;
@@ -240,7 +240,7 @@ __global__ __launch_bounds__(256) void balance_finish_kernel(RouterArgs p) {
     if (threadIdx.x == 0) {
         if (blockIdx.x == 0) {
             p.factors[int64_t(s) * (p.E + 1) + p.E] = 2.0f * p.z * rs * rn;
-            part += p.z * rs * rn * zpart[0];
+            if (p.z != 0.0f) part += p.z * rs * rn * zpart[0];
         }
         const unsigned of = gridDim.x * gridDim.y, me = blockIdx.y * gridDim.x + blockIdx.x;
         __hip_atomic_store(&p.losses[me], part, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
@@ -279,9 +279,9 @@ __global__ __launch_bounds__(256) void router_backward_kernel(RouterBack p) {
         const int id = lane < p.k ? p.ids[t * p.k + lane] : -1;
         const bool chosen = id >= 0 && id < p.E;
         const L* const row = static_cast<const L*>(p.logits) + t * p.E;
-        float l[NE], e[NE], slope[NE], d[NE];
+        float l[NE], e[NE], slope[NE], d[NE], top, one;
         load_logits(l, row, p.E, lane);
-        const float lse = softmax_of(l, e);            // e: the softmax
+        const float lse = softmax_of(l, e, top, one);  // e: the softmax
 #pragma unroll
         for (int j = 0; j < NE; ++j) d[j] = 0.0f;
         const bool sigmoids = p.score == GFG_SCORE_SIGMOID;
@@ -305,7 +305,7 @@ __global__ __launch_bounds__(256) void router_backward_kernel(RouterBack p) {
             }
             if (in && __any(chosen)) {
                 const float* const f = p.factors + int64_t(s) * (p.E + 1);
-                const float up = *p.dloss, zf = f[p.E] * lse;
+                const float up = *p.dloss, zf = f[p.E] != 0.0f ? f[p.E] * lse : 0.0f;
                 float inv = 1.0f;
                 if (sigmoids) {
                     all = wave_reduce(all, add);
@@ -333,7 +333,7 @@ __global__ __launch_bounds__(256) void router_backward_kernel(RouterBack p) {
             if (sigmoids) {
                 sc = sigmoid(lc, &ds);
             } else {
-                sc = lc == -INFINITY ? 0.0f : lc == INFINITY ? 1.0f : __expf(lc - lse);
+                sc = lc == -INFINITY ? 0.0f : lc == top ? one : __expf(lc - top) * one;
             }
             if (p.renorm) {
                 const float total = wave_reduce(chosen ? sc : 0.0f, add);
@@ -471,8 +471,8 @@ extern "C" int moe_router_backward(const void* logits, int32_t in_dtype, const i
     const char* fn = "moe_router_backward";
     if (int rc = check_router(fn, in_dtype, T, E, k, S, score, seq_offsets)) return rc;
     if (!factors != !dloss) return fail(GFG_EINVAL, "%s: factors and dloss do not go together", fn);
-    if (!factors && !dweights) return fail(GFG_EINVAL, "%s: neither the loss's nor the weights' gradient is given", fn);
     if (T == 0) return GFG_OK;
+    if (!factors && !dweights) return fail(GFG_EINVAL, "%s: neither the loss's nor the weights' gradient is given", fn);
     if (!logits || !ids || !dlogits) return fail(GFG_EINVAL, "%s: null pointer argument", fn);
     const uintptr_t size = in_dtype == GFG_IN_F32 ? 4 : 2;
     if (misaligned(logits, size) || misaligned(dlogits, size) || misaligned(ids, 4) || misaligned(seq_offsets, 4) ||
