@@ -26,4 +26,9 @@ struct F8Params {
 };
 
 
+// The kernel on 256 x 256 tiles (gfg_fp8_dense256.hip): whether its 32-bit
+// offsets reach, and the launch.
+bool fp8_256_fits(const F8Params& p, int out_dtype);
+int launch_fp8_256(const F8Params& p, bool brow, int out_dtype, hipStream_t s);
+
 }  // namespace gfg

@@ -711,7 +711,15 @@ int launch_stream(F8Params p, int out_dtype, hipStream_t s) {
 // so an operand has to have that many rows: up to 16 rows of A go to RB = 1,
 // and the gradient of a weight has at least 16 of both.
 template <bool BROW>
-int launch_product(const F8Params& p, int out_dtype, hipStream_t s) {
+int launch_product(const char* fn, const F8Params& p, int out_dtype, hipStream_t s) {
+    int cus = 0;
+    if (int rc = device_cus(&cus)) return rc;
+    const int choice = tile_shape_choice();
+    const bool fits = fp8_256_fits(p, out_dtype);
+    if (choice == GFG_TILE_256x256 && !fits && p.rows >= 4 && p.N >= 4)
+        return fail(GFG_EUNSUPPORTED, "%s: the 256 x 256 tile's offsets do not reach over N=%d", fn, p.N);
+    if (fits && (choice == GFG_TILE_256x256 || (choice == GFG_TILE_AUTO && (p.rows + 127) / 128 * ((int64_t(p.N) + 127) / 128) > cus)))
+        return launch_fp8_256(p, BROW, out_dtype, s);
     if constexpr (!BROW)
         if (p.rows <= 16) return launch_stream<1, 2, 4, 4, false>(p, out_dtype, s);
     if (p.rows <= 32) return launch_stream<2, 2, 4, 2, BROW>(p, out_dtype, s);
@@ -894,7 +902,7 @@ extern "C" int fp8_gemm(const void* a, const uint8_t* a_scale, int64_t a_scale_l
     if (a_scale_ld < M) return fail(GFG_EINVAL, "%s: a_scale_ld=%lld is below M=%lld", fn, (long long)a_scale_ld, (long long)M);
     if (int rc = check_operands(fn, a, b, b_scale, bias, d)) return rc;
     if (!a_scale) return fail(GFG_EINVAL, "%s: null pointer argument", fn);
-    return launch_product<false>(product(a, a_scale, a_scale_ld, b, b_scale, 0, bias, d, M, N, K), out_dtype, static_cast<hipStream_t>(stream));
+    return launch_product<false>(fn, product(a, a_scale, a_scale_ld, b, b_scale, 0, bias, d, M, N, K), out_dtype, static_cast<hipStream_t>(stream));
 }
 
 extern "C" int64_t fp8_linear_workspace_bytes(int64_t M, int64_t K) {
@@ -917,7 +925,7 @@ extern "C" int fp8_linear(const void* x, int32_t in_dtype, const void* b, const 
     uint8_t *q = static_cast<uint8_t*>(workspace), *scale = q + M * K;
     const int64_t ld = up(M, 4);
     if (int rc = quantize_rows(x, in_dtype, q, scale, M, K, ld, s)) return rc;
-    return launch_product<false>(product(q, scale, ld, b, b_scale, 0, bias, d, M, N, K), out_dtype, s);
+    return launch_product<false>(fn, product(q, scale, ld, b, b_scale, 0, bias, d, M, N, K), out_dtype, s);
 }
 
 extern "C" int64_t fp8_linear_backward_workspace_bytes(int64_t M, int64_t N, int64_t K) {
@@ -975,9 +983,9 @@ extern "C" int fp8_linear_backward(const void* dy, const void* x, int32_t in_dty
         if (int rc = launched()) return rc;
     }
     if (dx)
-        if (int rc = launch_product<false>(product(ws + at.q, ws + at.qs, at.ldm, b_t, b_t_scale, 0, nullptr, dx, M, K, N), dx_dtype, s)) return rc;
+        if (int rc = launch_product<false>(fn, product(ws + at.q, ws + at.qs, at.ldm, b_t, b_t_scale, 0, nullptr, dx, M, K, N), dx_dtype, s)) return rc;
     if (!dw) return GFG_OK;
     F8Params p = product(ws + at.yt, ws + at.yts, at.ldn, ws + at.xt, ws + at.xts, at.ldk, nullptr, dw, N, K, at.Mp);
     p.accumulate = accumulate;
-    return launch_product<true>(p, dw_dtype, s);
+    return launch_product<true>(fn, p, dw_dtype, s);
 }

@@ -97,6 +97,42 @@ def test_product_of_whole_numbers_is_exact(M, N, K):
             assert bool((d[M] == 99.0).all())              # the row behind the last is left alone
 
 
+@pytest.mark.parametrize("M,N,K", [(5, 130, 272), (40, 96, 128), (300, 520, 400), (700, 1304, 528), (700, 1301, 272)])
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+def test_bias_in_every_tile(M, N, K, dt):
+    """Also over several tiles a workgroup (the bias of the next one is loaded while one is stored)."""
+    rng = np.random.default_rng(M + N)
+    a, b, bias = whole(rng, M, K), whole(rng, N, K), whole(rng, N) * 16
+    qa, sa = o.quantize_act_1x128(a)
+    qb, sb = o.quantize_weight_128x128(b[None])
+    ref = torch.from_numpy(a.astype(np.float64) @ b.astype(np.float64).T + bias).to(DT[dt])
+    for shape in (gfg.TILE_AUTO, gfg.TILE_128x256, gfg.TILE_256x256):
+        for limit in (0, 8):
+            gfg.set_tile_shape(shape)
+            gfg.set_grid_limit(limit)
+            d = torch.full((M + 1, N), 99.0, dtype=DT[dt], device="cuda")
+            gfg.fp8_gemm(dev(qa), dev(sa), dev(qb[0]), dev(sb[0]), d[:M], bias=dev(bias))
+            assert torch.equal(d[:M].cpu(), ref) and bool((d[M] == 99.0).all()), (shape, limit)
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("dwt", ["f32", "bf16"])
+def test_weight_gradient_over_several_tiles(accumulate, dwt):
+    if accumulate and dwt != "f32":
+        pytest.skip("refused")
+    rng = np.random.default_rng(8)
+    M, N, K = 260, 1040, 784
+    dy, x = whole(rng, M, N), whole(rng, M, K)
+    ref = torch.from_numpy(dy.T.astype(np.float64) @ x + (3.0 if accumulate else 0.0)).to(DT[dwt])
+    for shape in (gfg.TILE_AUTO, gfg.TILE_128x256, gfg.TILE_256x256):
+        for limit in (0, 8):
+            gfg.set_tile_shape(shape)
+            gfg.set_grid_limit(limit)
+            dw = torch.full((N, K), 3.0, dtype=DT[dwt], device="cuda")
+            gfg.fp8_linear_backward(dev(dy), dev(x), None, None, dw=dw, accumulate=accumulate)
+            assert torch.equal(dw.cpu(), ref), (shape, limit)
+
+
 def test_scales_differ_by_block():
     """A scale of its own for every row and block of A and every block of B, the whole range that sums can take."""
     rng = np.random.default_rng(9)
