@@ -24,63 +24,65 @@
 namespace gfg {
 namespace {
 
-constexpr int CH = 4;                          // chunks of 8 elements that a lane holds of a row
-constexpr int64_t kMaxH = 32768;               // 1024 lanes of them
-constexpr int64_t kMostGroups = 512;           // workgroups of the backward pass: rows of partial sums
+constexpr int64_t kMaxH = 32768;               // 1024 lanes of 4 chunks of 8 elements
+constexpr int64_t kMostGroups = 768;           // workgroups of the backward pass: rows of partial sums
 
 typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
 
-// Eight elements at any address of their type, the first n of them (zeros past those).
+// Eight neighbouring elements at any address of their type.
 template <typename T>
 struct Row8 {
     typedef T vec __attribute__((ext_vector_type(8), aligned(sizeof(T))));
-    T v[8];
-    __device__ __forceinline__ void load(const T* p, int n) {
-        if (n >= 8) {
-            const vec t = *reinterpret_cast<const vec*>(p);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = t[i];
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = i < n ? p[i] : T(0.0f);
-        }
-    }
-    __device__ __forceinline__ void zero() {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = T(0.0f);
-    }
+    vec v;
+    __device__ __forceinline__ void load(const T* p) { v = *reinterpret_cast<const vec*>(p); }
     __device__ __forceinline__ float at(int i) const { return float(v[i]); }
 };
+
+// A lane's chunk of a row: columns col .. col + 7, of which those from `skip` on
+// are its own.  Past the last whole chunk of the row a lane takes the row's last
+// eight columns, some of which (or all: skip 8) are another lane's, so every load
+// is one whole vector inside the row, by every lane: no branch stands between
+// the loads, and the waits for them stay exact.
+struct Chunk { int col, skip; };
+__device__ __forceinline__ Chunk chunk_of(int c, int H) {
+    const int col = min(8 * c, H - 8);
+    return Chunk{col, min(8 * c - col, 8)};
+}
+
+// Column i of a chunk where it is the lane's own, else 0.
+__device__ __forceinline__ float own(const Chunk& c, int i, float v) { return i >= c.skip ? v : 0.0f; }
+
 template <typename T>
-__device__ __forceinline__ void store8(T* p, int n, const float (&f)[8]) {
+__device__ __forceinline__ void store8(T* row, const Chunk& c, const float (&f)[8]) {
     typedef T vec __attribute__((ext_vector_type(8), aligned(sizeof(T))));
-    if (n >= 8) {
+    if (c.skip == 0) {
         vec t;
 #pragma unroll
         for (int i = 0; i < 8; ++i) t[i] = T(f[i]);
-        *reinterpret_cast<vec*>(p) = t;
+        *reinterpret_cast<vec*>(row + c.col) = t;
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (i < n) p[i] = T(f[i]);
+            if (i >= c.skip) row[c.col + i] = T(f[i]);
     }
 }
 
-// Sums of N values over the TPR threads that share a row; `turn` alternates
-// between two buffers, so one barrier is enough.
-template <int TPR, int N>
+// Sums of N values over the TPR threads that share a row, R rows a workgroup;
+// `turn` alternates between two buffers, so one barrier is enough.  Every thread
+// of the workgroup is here.
+template <int TPR, int R, int N>
 __device__ __forceinline__ void row_sums(float (&v)[N], GFG_LDS float* part, int& turn) {
 #pragma unroll
     for (int n = 0; n < N; ++n) v[n] = wave_reduce(v[n], [](float a, float b) { return a + b; });
     if constexpr (TPR > 64) {
         constexpr int W = TPR / 64;
-        GFG_LDS float* const p = part + turn * (N * W);
+        GFG_LDS float* const p = part + turn * (N * W * R) + (threadIdx.x / TPR) * (N * W);
         turn ^= 1;
         if ((threadIdx.x & 63) == 0) {
 #pragma unroll
-            for (int n = 0; n < N; ++n) p[n * W + (threadIdx.x >> 6)] = v[n];
+            for (int n = 0; n < N; ++n) p[n * W + (threadIdx.x % TPR >> 6)] = v[n];
         }
-        __syncthreads();
+        lds_barrier();
 #pragma unroll
         for (int n = 0; n < N; ++n) {
             float t = 0.0f;
@@ -104,8 +106,21 @@ struct NormArgs {
     int H;
 };
 
-template <int TPR> constexpr int kRows = TPR == 64 ? 4 : 1;       // rows a workgroup holds at a time
-template <int TPR> constexpr int kThreads = TPR == 64 ? 256 : TPR;
+// TPR lanes share a row, a workgroup holds 256 / TPR rows at a time, or one.
+template <int TPR> constexpr int kThreads = TPR < 256 ? 256 : TPR;
+template <int TPR> constexpr int kRows = kThreads<TPR> / TPR;
+
+// A row of `weights`, 1 where there are none, on a lane's own columns; 0 on the others.
+template <int CH>
+__device__ __forceinline__ void load_weights(float (&f)[CH][8], const float* weights, const Chunk (&c)[CH]) {
+#pragma unroll
+    for (int j = 0; j < CH; ++j) {
+        Row8<float> v;
+        if (weights) v.load(weights + c[j].col);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[j][i] = own(c[j], i, weights ? v.v[i] : 1.0f);
+    }
+}
 
 // The E8M0 byte of a block with largest magnitude bits `ab`, and 2^-t (0 for a
 // block that has none): t the smallest integer with 448 * 2^t >= max, at least -127.
@@ -127,76 +142,89 @@ __device__ __forceinline__ uint32_t block_scale(uint32_t ab, float* inv) {
     return uint32_t(t + 127);
 }
 
-template <typename Y, typename R, int TPR>
+// AHEAD: the next row is loaded while one is computed.
+template <typename Y, typename R, int TPR, int CH, bool AHEAD>
 __global__ __launch_bounds__(kThreads<TPR>) void residual_norm_kernel(NormArgs p) {
-    __shared__ float part_smem[TPR > 64 ? 2 * TPR / 64 : 1];
+    constexpr int ROWS = kRows<TPR>;
+    __shared__ float part_smem[2 * kThreads<TPR> / 64];
     GFG_LDS float* const part = (GFG_LDS float*)part_smem;
-    const int lane = threadIdx.x % TPR, chunks = (p.H + 7) / 8;
-    int turn = 0;
-    for (int64_t m = int64_t(blockIdx.x) * kRows<TPR> + threadIdx.x / TPR; m < p.M; m += int64_t(gridDim.x) * kRows<TPR>) {
-        Row8<Y> y[CH];
-        Row8<R> r[CH];
+    const int lane = threadIdx.x % TPR, in = threadIdx.x / TPR;
+    Chunk c[CH];
+#pragma unroll
+    for (int j = 0; j < CH; ++j) c[j] = chunk_of(lane + j * TPR, p.H);
+    const bool has_y = p.y != nullptr;
+    // without y its loads go to the residual's rows, which are at least as long, and are not used
+    const Y* const ys = static_cast<const Y*>(has_y ? p.y : p.residual);
+    const R* const rs = static_cast<const R*>(p.residual);
+    Row8<Y> y[CH], ny[CH];
+    Row8<R> r[CH], nr[CH];
+    auto load = [&](Row8<Y> (&a)[CH], Row8<R> (&b)[CH], int64_t m) {
+        m = m < p.M ? m : p.M - 1;
 #pragma unroll
         for (int j = 0; j < CH; ++j) {
-            const int c = lane + j * TPR, n = p.H - 8 * c;
-            y[j].zero();
-            r[j].zero();
-            if (c < chunks) {
-                if (p.y) y[j].load(static_cast<const Y*>(p.y) + m * p.H + 8 * c, n);
-                r[j].load(static_cast<const R*>(p.residual) + m * p.H + 8 * c, n);
-            }
+            a[j].load(ys + m * p.H + c[j].col);
+            b[j].load(rs + m * p.H + c[j].col);
         }
+    };
+    const int64_t step = int64_t(gridDim.x) * ROWS;
+    int64_t m = int64_t(blockIdx.x) * ROWS + in;
+    load(y, r, m);
+    float k[CH][8], w[CH][8];                  // post weight times a channel's gate; weight
+    load_weights(k, p.post, c);
+    if (p.gate_kind == GFG_GATE_CHANNEL) {
+        float g[CH][8];
+        load_weights(g, p.gate, c);
+#pragma unroll
+        for (int j = 0; j < CH; ++j)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) k[j][i] *= g[j][i];
+    }
+    load_weights(w, p.weight, c);
+    int turn = 0;
+    // (every thread takes part in the sums of its workgroup's rows, also past the last row)
+    for (int64_t base = int64_t(blockIdx.x) * ROWS; base < p.M; base += step, m += step) {
+        if constexpr (AHEAD) load(ny, nr, m + step);
+        const bool valid = m < p.M;
         float ry = 1.0f;
-        if (p.post && p.y) {
+        if (p.post && has_y) {
             float s[1] = {0.0f};
 #pragma unroll
             for (int j = 0; j < CH; ++j)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) s[0] += y[j].at(i) * y[j].at(i);
-            row_sums<TPR>(s, part, turn);
+                for (int i = 0; i < 8; ++i) {
+                    const float v = own(c[j], i, y[j].at(i));
+                    s[0] += v * v;
+                }
+            row_sums<TPR, ROWS>(s, part, turn);
             ry = rsqrtf(s[0] / float(p.H) + p.eps);
         }
-        const float token_gate = p.gate_kind == GFG_GATE_TOKEN ? p.gate[m] : 1.0f;
+        const float scale = ry * (p.gate_kind == GFG_GATE_TOKEN ? p.gate[valid ? m : p.M - 1] : 1.0f);
         float o[CH][8], s[1] = {0.0f};
 #pragma unroll
         for (int j = 0; j < CH; ++j) {
-            const int c = lane + j * TPR, n = p.H - 8 * c;
-            Row8<float> wp, g;
-            wp.zero();
-            g.zero();
-            if (c < chunks) {
-                if (p.post) wp.load(p.post + 8 * c, n);
-                if (p.gate_kind == GFG_GATE_CHANNEL) g.load(p.gate + 8 * c, n);
-            }
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                float u = y[j].at(i);
-                if (p.post) u = u * ry * wp.v[i];
-                u *= p.gate_kind == GFG_GATE_CHANNEL ? g.v[i] : token_gate;
-                o[j][i] = p.alpha * r[j].at(i) + u;
-                s[0] += o[j][i] * o[j][i];
+                o[j][i] = p.alpha * r[j].at(i) + (has_y ? y[j].at(i) * scale * k[j][i] : 0.0f);
+                const float v = own(c[j], i, o[j][i]);
+                s[0] += v * v;
             }
-            if (c < chunks && p.out) store8(static_cast<R*>(p.out) + m * p.H + 8 * c, n, o[j]);
+            if (p.out && valid) store8(static_cast<R*>(p.out) + m * p.H, c[j], o[j]);
         }
-        float ro = 1.0f;
         if (p.weight) {
-            row_sums<TPR>(s, part, turn);
-            ro = rsqrtf(s[0] / float(p.H) + p.eps);
+            row_sums<TPR, ROWS>(s, part, turn);
+            const float ro = rsqrtf(s[0] / float(p.H) + p.eps);
 #pragma unroll
             for (int j = 0; j < CH; ++j) {
-                const int c = lane + j * TPR, n = p.H - 8 * c;
-                Row8<float> w;
-                w.zero();
-                if (c < chunks) w.load(p.weight + 8 * c, n);
                 float z[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) z[i] = o[j][i] * ro * w.v[i];
-                if (p.normed && c < chunks) store8(static_cast<Y*>(p.normed) + m * p.H + 8 * c, n, z);
+                for (int i = 0; i < 8; ++i) z[i] = o[j][i] * ro * w[j][i];
+                if (p.normed && valid) store8(static_cast<Y*>(p.normed) + m * p.H, c[j], z);
                 if (p.q) {
-                    // 16 neighbouring lanes hold a block of 128 channels
+                    // 16 neighbouring lanes hold a block of 128 channels (z is 0 outside a lane's own)
                     uint32_t ab = 0;
 #pragma unroll
                     for (int i = 0; i < 8; ++i) ab = max(ab, __float_as_uint(z[i]) & 0x7FFFFFFFu);
+                    if (c[j].skip) ab = 0;                 // (0 times an infinity is NaN)
                     ab = max(ab, uint32_t(dpp<0x128>(int(ab))));
                     ab = max(ab, uint32_t(dpp<0x124>(int(ab))));
                     ab = max(ab, uint32_t(dpp<0x122>(int(ab))));
@@ -211,16 +239,23 @@ __global__ __launch_bounds__(kThreads<TPR>) void residual_norm_kernel(NormArgs p
                             code[h] = uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(z[4 * h + 2] * inv, z[4 * h + 3] * inv, lo, true));
                         }
                     }
-                    if (c < chunks) {
-                        *reinterpret_cast<u32x2*>(p.q + m * p.H + 8 * c) = code;
-                        if ((c & 15) == 0) p.scale[(c >> 4) * p.scale_ld + m] = uint8_t(byte);
+                    if (valid && !c[j].skip) {
+                        *reinterpret_cast<u32x2*>(p.q + m * p.H + c[j].col) = code;
+                        if ((c[j].col & 127) == 0) p.scale[(c[j].col >> 7) * p.scale_ld + m] = uint8_t(byte);
                     }
                 }
             }
+            if (p.stats && valid && lane == 0) p.stats[p.M + m] = ro;
         }
-        if (p.stats && lane == 0) {
-            p.stats[m] = ry;
-            if (p.weight) p.stats[p.M + m] = ro;
+        if (p.stats && valid && lane == 0) p.stats[m] = ry;
+        if constexpr (AHEAD) {
+#pragma unroll
+            for (int j = 0; j < CH; ++j) {
+                y[j] = ny[j];
+                r[j] = nr[j];
+            }
+        } else {
+            load(y, r, m + step);
         }
     }
 }
@@ -237,124 +272,128 @@ struct BackArgs {
     int H;
 };
 
-template <typename Y, typename R, int TPR>
+template <typename Y, typename R, int TPR, int CH, bool AHEAD>
 __global__ __launch_bounds__(kThreads<TPR>) void residual_norm_backward_kernel(BackArgs p) {
-    __shared__ float part_smem[TPR > 64 ? 6 * TPR / 64 : 1];
-    __shared__ float join_smem[TPR == 64 ? 2 * 64 * CH * 8 : 1];
+    constexpr int ROWS = kRows<TPR>;
+    __shared__ float part_smem[6 * kThreads<TPR> / 64];
+    __shared__ float join_smem[ROWS > 1 ? 2 * CH * 8 * TPR : 1];
     GFG_LDS float* const part = (GFG_LDS float*)part_smem;
-    const int lane = threadIdx.x % TPR, chunks = (p.H + 7) / 8;
-    const bool norm = p.dnormed && p.weight, post = p.post && p.y;
-    int turn = 0;
-    float sw[CH][8] = {}, sp[CH][8] = {};
-    for (int64_t m = int64_t(blockIdx.x) * kRows<TPR> + threadIdx.x / TPR; m < p.M; m += int64_t(gridDim.x) * kRows<TPR>) {
+    const int lane = threadIdx.x % TPR, in = threadIdx.x / TPR;
+    Chunk c[CH];
+#pragma unroll
+    for (int j = 0; j < CH; ++j) c[j] = chunk_of(lane + j * TPR, p.H);
+    const bool norm = p.dnormed && p.weight, post = p.post && p.y, has_y = p.y != nullptr, has_dout = p.dout != nullptr;
+    // what is not there is read from a tensor that is, of at least its length, and not used
+    const R* const louts = static_cast<const R*>(has_dout ? p.dout : p.out);
+    const R* const outs = static_cast<const R*>(norm ? p.out : louts);
+    const Y* const dzs = static_cast<const Y*>(norm ? p.dnormed : has_y ? p.y : static_cast<const void*>(louts));
+    const Y* const ys = static_cast<const Y*>(has_y ? p.y : static_cast<const void*>(dzs));
+    struct Rows {
         Row8<R> dout[CH], out[CH];
         Row8<Y> dz[CH], y[CH];
+    } a, b;
+    auto load = [&](Rows& v, int64_t m) {
+        m = m < p.M ? m : p.M - 1;
 #pragma unroll
         for (int j = 0; j < CH; ++j) {
-            const int c = lane + j * TPR, n = p.H - 8 * c;
-            dout[j].zero();
-            out[j].zero();
-            dz[j].zero();
-            y[j].zero();
-            if (c < chunks) {
-                const int64_t at = m * p.H + 8 * c;
-                if (p.dout) dout[j].load(static_cast<const R*>(p.dout) + at, n);
-                if (norm) {
-                    out[j].load(static_cast<const R*>(p.out) + at, n);
-                    dz[j].load(static_cast<const Y*>(p.dnormed) + at, n);
-                }
-                if (p.y) y[j].load(static_cast<const Y*>(p.y) + at, n);
-            }
+            const int64_t at = m * p.H + c[j].col;
+            v.out[j].load(outs + at);
+            v.dz[j].load(dzs + at);
+            v.dout[j].load(louts + at);
+            v.y[j].load(ys + at);
         }
-        const float ry = post ? p.stats[m] : 1.0f, ro = norm ? p.stats[p.M + m] : 0.0f;
-        const float token_gate = p.gate_kind == GFG_GATE_TOKEN ? p.gate[m] : 1.0f;
-        // A = sum h zh, B = sum wp g yh (dout + ro h), C = sum wp g yh zh (a token's g left out)
+    };
+    const int64_t step = int64_t(gridDim.x) * ROWS;
+    int64_t m = int64_t(blockIdx.x) * ROWS + in;
+    load(a, m);
+    float k[CH][8], w[CH][8];                  // post weight times a channel's gate; weight
+    load_weights(k, post ? p.post : nullptr, c);
+    if (p.gate_kind == GFG_GATE_CHANNEL) {
+        float g[CH][8];
+        load_weights(g, p.gate, c);
+#pragma unroll
+        for (int j = 0; j < CH; ++j)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) k[j][i] *= g[j][i];
+    }
+    load_weights(w, norm ? p.weight : nullptr, c);
+    float sw[CH][8] = {}, sp[CH][8] = {};
+    int turn = 0;
+    // (every thread takes part in the sums of its workgroup's rows, also past the last row)
+    for (int64_t base = int64_t(blockIdx.x) * ROWS; base < p.M; base += step, m += step) {
+        if constexpr (AHEAD) load(b, m + step);
+        const bool valid = m < p.M;
+        const int64_t at = valid ? m : p.M - 1;
+        const float ry = post ? p.stats[at] : 1.0f, ro = norm ? p.stats[p.M + at] : 0.0f;
+        const float token_gate = p.gate_kind == GFG_GATE_TOKEN ? p.gate[at] : 1.0f;
+        auto zh = [&](int j, int i) { return norm ? a.out[j].at(i) * ro : 0.0f; };
+        auto yh = [&](int j, int i) { return has_y ? a.y[j].at(i) * ry : 0.0f; };
+        auto h = [&](int j, int i) { return norm ? a.dz[j].at(i) * w[j][i] : 0.0f; };
+        auto dout = [&](int j, int i) { return has_dout ? a.dout[j].at(i) : 0.0f; };
+        // A = sum h zh, B = sum k yh (dout + ro h), C = sum k yh zh (w and k are 0 outside a lane's own)
         float s[3] = {0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int j = 0; j < CH; ++j) {
-            const int c = lane + j * TPR, n = p.H - 8 * c;
-            Row8<float> w, wp, g;
-            w.zero();
-            wp.zero();
-            g.zero();
-            if (c < chunks) {
-                if (norm) w.load(p.weight + 8 * c, n);
-                if (post) wp.load(p.post + 8 * c, n);
-                if (p.gate_kind == GFG_GATE_CHANNEL) g.load(p.gate + 8 * c, n);
-            }
+        for (int j = 0; j < CH; ++j)
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float h = dz[j].at(i) * w.v[i], zh = out[j].at(i) * ro;
-                float v = y[j].at(i) * ry;
-                if (post) v *= wp.v[i];
-                if (p.gate_kind == GFG_GATE_CHANNEL) v *= g.v[i];
-                s[0] += h * zh;
-                s[1] += v * (dout[j].at(i) + ro * h);
-                s[2] += v * zh;
+                const float v = yh(j, i) * k[j][i], z = zh(j, i), t = h(j, i);
+                s[0] += t * z;
+                s[1] += v * (dout(j, i) + ro * t);
+                s[2] += v * z;
             }
-        }
-        row_sums<TPR>(s, part, turn);
+        row_sums<TPR, ROWS>(s, part, turn);
         const float mean_h = s[0] / float(p.H);
-        const float row = s[1] - ro * mean_h * s[2];          // sum wp g yh G
-        if (p.gate_kind == GFG_GATE_TOKEN && p.dgate && lane == 0) p.dgate[m] = row;
+        const float row = s[1] - ro * mean_h * s[2];          // sum k yh G
         const float mean_y = token_gate * row / float(p.H);
+        if (valid) {
+            if (p.gate_kind == GFG_GATE_TOKEN && p.dgate && lane == 0) p.dgate[m] = row;
 #pragma unroll
-        for (int j = 0; j < CH; ++j) {
-            const int c = lane + j * TPR, n = p.H - 8 * c;
-            if (c >= chunks) continue;
-            Row8<float> w, wp, g;
-            w.zero();
-            wp.zero();
-            g.zero();
-            if (norm) w.load(p.weight + 8 * c, n);
-            if (post) wp.load(p.post + 8 * c, n);
-            if (p.gate_kind == GFG_GATE_CHANNEL) g.load(p.gate + 8 * c, n);
-            float dr[8], dy[8];
+            for (int j = 0; j < CH; ++j) {
+                float dr[8], dy[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float zh = out[j].at(i) * ro, yh = y[j].at(i) * ry;
-                const float G = dout[j].at(i) + ro * (dz[j].at(i) * w.v[i] - zh * mean_h);
-                const float du = (p.gate_kind == GFG_GATE_CHANNEL ? g.v[i] : token_gate) * G;
-                dr[i] = p.alpha * G;
-                dy[i] = post ? ry * (wp.v[i] * du - yh * mean_y) : du;
-                sw[j][i] += dz[j].at(i) * zh;
-                sp[j][i] += token_gate * G * yh;
+                for (int i = 0; i < 8; ++i) {
+                    const float z = zh(j, i), yv = yh(j, i);
+                    const float G = dout(j, i) + ro * (h(j, i) - z * mean_h);
+                    const float gG = token_gate * G;
+                    dr[i] = p.alpha * G;
+                    dy[i] = post ? ry * (k[j][i] * gG - yv * mean_y) : k[j][i] * gG;
+                    sw[j][i] += (norm ? a.dz[j].at(i) : 0.0f) * z;
+                    sp[j][i] += gG * yv;
+                }
+                if (p.dresidual) store8(static_cast<R*>(p.dresidual) + m * p.H, c[j], dr);
+                if (p.dy) store8(static_cast<Y*>(p.dy) + m * p.H, c[j], dy);
             }
-            if (p.dresidual) store8(static_cast<R*>(p.dresidual) + m * p.H + 8 * c, n, dr);
-            if (p.dy) store8(static_cast<Y*>(p.dy) + m * p.H + 8 * c, n, dy);
         }
+        if constexpr (AHEAD) a = b;
+        else load(a, m + step);
     }
     if (!p.sums) return;
-    float* const o = p.sums + int64_t(blockIdx.x) * 2 * p.H;
-    if constexpr (TPR == 64) {                 // the four rows' waves, in order
-        GFG_LDS float* const sum = (GFG_LDS float*)join_smem;      // [2][CH * 8][64]
-        const int wave = threadIdx.x >> 6;
-        for (int w = 0; w < 4; ++w) {
-            if (wave == w) {
+    if constexpr (ROWS > 1) {                  // the rows' lanes, in order
+        GFG_LDS float* const sum = (GFG_LDS float*)join_smem;      // [2][CH * 8][TPR]
+        for (int n = 0; n < ROWS; ++n) {
+            if (in == n) {
 #pragma unroll
                 for (int j = 0; j < CH; ++j)
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        GFG_LDS float* const at = sum + (j * 8 + i) * 64 + lane;
-                        if (w > 0) {
+                        GFG_LDS float* const at = sum + (j * 8 + i) * TPR + lane;
+                        if (n > 0) {
                             sw[j][i] += at[0];
-                            sp[j][i] += at[64 * CH * 8];
+                            sp[j][i] += at[TPR * CH * 8];
                         }
                         at[0] = sw[j][i];
-                        at[64 * CH * 8] = sp[j][i];
+                        at[TPR * CH * 8] = sp[j][i];
                     }
             }
-            __syncthreads();
+            lds_barrier();
         }
-        if (wave != 3) return;
+        if (in != ROWS - 1) return;
     }
+    float* const o = p.sums + int64_t(blockIdx.x) * 2 * p.H;
 #pragma unroll
     for (int j = 0; j < CH; ++j) {
-        const int c = lane + j * TPR, n = p.H - 8 * c;
-        if (c < chunks) {
-            store8(o + 8 * c, n, sw[j]);
-            store8(o + p.H + 8 * c, n, sp[j]);
-        }
+        store8(o, c[j], sw[j]);
+        store8(o + p.H, c[j], sp[j]);
     }
 }
 
@@ -389,14 +428,16 @@ __global__ __launch_bounds__(256) void norm_sums_kernel(const float* __restrict_
     if (gate_kind == GFG_GATE_CHANNEL) put(dgate, P > 0 && post ? post[c] * b : b);
 }
 
-// Lanes a row: enough for its chunks, CH each.
+// Lanes a row, and chunks that a lane holds.
+template <int T, int C> struct Width { static constexpr int TPR = T, CH = C; };
 template <typename F>
 void by_width(int64_t H, F f) {
-    if (H <= 64 * 8 * CH) f(std::integral_constant<int, 64>{});
-    else if (H <= 128 * 8 * CH) f(std::integral_constant<int, 128>{});
-    else if (H <= 256 * 8 * CH) f(std::integral_constant<int, 256>{});
-    else if (H <= 512 * 8 * CH) f(std::integral_constant<int, 512>{});
-    else f(std::integral_constant<int, 1024>{});
+    if (H <= 1024) f(Width<64, 2>{});
+    else if (H <= 2048) f(Width<128, 2>{});
+    else if (H <= 4096) f(Width<256, 2>{});
+    else if (H <= 8192) f(Width<512, 2>{});
+    else if (H <= 16384) f(Width<1024, 2>{});
+    else f(Width<1024, 4>{});
 }
 template <typename F>
 void by_type(int32_t dtype, int32_t residual_dtype, F f) {
@@ -407,9 +448,12 @@ void by_type(int32_t dtype, int32_t residual_dtype, F f) {
     else f(_Float16{}, float{});
 }
 
-int64_t groups(int64_t M, int64_t H) {
-    const int64_t rows = H <= 64 * 8 * CH ? 4 : 1, n = (M + rows - 1) / rows;
-    return n < kMostGroups ? n : kMostGroups;
+// Workgroups of a pass over M rows, at most `most`.
+int64_t groups(int64_t M, int64_t H, int64_t most) {
+    int64_t rows = 1;
+    by_width(H, [&](auto w) { rows = kRows<decltype(w)::TPR>; });
+    const int64_t n = (M + rows - 1) / rows;
+    return n < most ? n : most;
 }
 
 int launched() {
@@ -426,7 +470,7 @@ int check_norm(const char* fn, int64_t M, int64_t H, int32_t dtype, int32_t resi
     if (gate_kind != GFG_GATE_NONE && gate_kind != GFG_GATE_CHANNEL && gate_kind != GFG_GATE_TOKEN)
         return fail(GFG_EINVAL, "%s: gate_kind %d is not a GFG_GATE_* value", fn, gate_kind);
     if (M < 0 || H <= 0) return fail(GFG_EINVAL, "%s: bad sizes M=%lld H=%lld", fn, (long long)M, (long long)H);
-    if (H > kMaxH) return fail(GFG_EUNSUPPORTED, "%s: H=%lld above %lld", fn, (long long)H, (long long)kMaxH);
+    if (H < 8 || H > kMaxH) return fail(GFG_EUNSUPPORTED, "%s: H=%lld outside [8, %lld]", fn, (long long)H, (long long)kMaxH);
     if (M >= int64_t(1) << 31) return fail(GFG_EUNSUPPORTED, "%s: M=%lld is 2^31 or more", fn, (long long)M);
     if (M > 0 && (gate_kind != GFG_GATE_NONE) != (gate != nullptr))
         return fail(GFG_EINVAL, "%s: gate and gate_kind do not go together", fn);
@@ -444,12 +488,11 @@ int forward(const char* fn, NormArgs a, int32_t dtype, int32_t residual_dtype, v
         misaligned(a.out, size_of(residual_dtype)) || misaligned(a.q, 8) || misaligned(a.weight, 4) || misaligned(a.post, 4) ||
         misaligned(a.gate, 4) || misaligned(a.stats, 4))
         return fail(GFG_EINVAL, "%s: a pointer is not aligned to its elements (q: 8 bytes)", fn);
-    by_width(a.H, [&](auto lanes) {
-        constexpr int TPR = decltype(lanes)::value;
-        const int64_t wgs = (a.M + kRows<TPR> - 1) / kRows<TPR>, most = int64_t(1) << 21;
-        const dim3 grid(unsigned(wgs < most ? wgs : most)), block(kThreads<TPR>);
+    by_width(a.H, [&](auto width) {
+        constexpr int TPR = decltype(width)::TPR, CH = decltype(width)::CH;
+        const dim3 grid(unsigned(groups(a.M, a.H, 4096 * 64 / kThreads<TPR>))), block(kThreads<TPR>);
         by_type(dtype, residual_dtype, [&](auto y, auto r) {
-            hipLaunchKernelGGL((residual_norm_kernel<decltype(y), decltype(r), TPR>), grid, block, 0, static_cast<hipStream_t>(stream), a);
+            hipLaunchKernelGGL((residual_norm_kernel<decltype(y), decltype(r), TPR, CH, (CH == 2)>), grid, block, 0, static_cast<hipStream_t>(stream), a);
         });
     });
     return launched();
@@ -488,7 +531,7 @@ extern "C" int residual_norm_fp8(const void* y, const void* residual, const floa
 }
 
 extern "C" int64_t residual_norm_backward_workspace_bytes(int64_t M, int64_t H) {
-    return M > 0 && H > 0 ? groups(M, H) * 2 * H * 4 : 0;
+    return M > 0 && H > 0 ? groups(M, H, kMostGroups) * 2 * H * 4 : 0;
 }
 
 extern "C" int residual_norm_backward(const void* dout, const void* dnormed, const void* out, const void* y, const float* stats,
@@ -524,14 +567,15 @@ extern "C" int residual_norm_backward(const void* dout, const void* dnormed, con
                         (long long)residual_norm_backward_workspace_bytes(M, H));
     }
     hipStream_t s = static_cast<hipStream_t>(stream);
-    const int64_t P = M > 0 ? groups(M, H) : 0;
+    const int64_t P = M > 0 ? groups(M, H, kMostGroups) : 0;
     if (M > 0) {
         const BackArgs a{dout, dnormed, out, y, stats, weight, post_weight, gate, gate_kind, alpha, dresidual, dy, dgate,
                          sums ? static_cast<float*>(workspace) : nullptr, M, int(H)};
-        by_width(H, [&](auto lanes) {
-            constexpr int TPR = decltype(lanes)::value;
+        by_width(H, [&](auto width) {
+            constexpr int TPR = decltype(width)::TPR, CH = decltype(width)::CH;
             by_type(dtype, residual_dtype, [&](auto yt, auto rt) {
-                hipLaunchKernelGGL((residual_norm_backward_kernel<decltype(yt), decltype(rt), TPR>), dim3(unsigned(P)), dim3(kThreads<TPR>), 0, s, a);
+                hipLaunchKernelGGL((residual_norm_backward_kernel<decltype(yt), decltype(rt), TPR, CH, (TPR < 1024)>), dim3(unsigned(P)),
+                                   dim3(kThreads<TPR>), 0, s, a);
             });
         });
         if (int rc = launched()) return rc;

@@ -540,7 +540,7 @@ GFG_API int fp8_quantize_weight_device(const void* w, int32_t in_dtype, int32_t 
  * fp32's range); every output is rounded once.  Two calls give the same bytes.
  * Rows need no alignment beyond that of their elements.
  *
- * Sizes: M >= 0 (0 is a no-op but for the sums) and below 2^31, H in [1, 32768]
+ * Sizes: M >= 0 (0 is a no-op but for the sums) and below 2^31, H in [8, 32768]
  * (else GFG_EUNSUPPORTED).
  */
 enum gfg_gate { GFG_GATE_NONE = 0, GFG_GATE_CHANNEL = 1, GFG_GATE_TOKEN = 2 };

@@ -20,7 +20,7 @@ HALF = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11, torch.float32: 2.0
 F32 = 2.0 ** -16
 LEAST = {torch.float16: 2.0 ** -25}
 TYPES = [("bf16", "bf16"), ("bf16", "f32"), ("f16", "f16"), ("f16", "f32"), ("f32", "f32")]
-SIZES = [(1, 1), (1, 7168), (3, 8), (5, 33), (333, 2049), (17, 2048), (9, 4096), (4, 4104), (2, 8191), (3, 16384), (2, 32768), (1030, 64), (600, 300)]
+SIZES = [(1, 9), (1, 7168), (3, 8), (5, 33), (4, 15), (7, 1023), (8, 1025), (333, 2049), (17, 2048), (9, 4096), (4, 4104), (2, 8191), (3, 16384), (2, 32768), (1030, 64), (600, 300)]
 
 
 def dev(x, dtype=torch.float32):

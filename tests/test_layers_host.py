@@ -88,7 +88,7 @@ def test_weight_quantizer_refuses(change, code):
 NORM = dict(y=P, r=P, w=P, post=P, gate=P, kind=1, alpha=1.0, eps=1e-6, out=P, z=P, stats=P, M=3, H=32, dt=1, rdt=1, q=P, s=P, ld=3)
 NORM_BAD = [
     (dict(dt=3), EINVAL), (dict(dt=1, rdt=2), EINVAL), (dict(dt=0, rdt=1), EINVAL), (dict(kind=3), EINVAL), (dict(kind=0), EINVAL),
-    (dict(gate=None), EINVAL), (dict(M=-1), EINVAL), (dict(H=0), EINVAL), (dict(H=32784), EUNSUPPORTED), (dict(M=1 << 31), EUNSUPPORTED),
+    (dict(gate=None), EINVAL), (dict(M=-1), EINVAL), (dict(H=0), EINVAL), (dict(H=32784), EUNSUPPORTED), (dict(H=7), EUNSUPPORTED), (dict(M=1 << 31), EUNSUPPORTED),
     (dict(r=None), EINVAL), (dict(eps=-1.0), EINVAL), (dict(eps=float("nan")), EINVAL), (dict(y=P + 1), EINVAL), (dict(r=P + 1), EINVAL),
     (dict(out=P + 1), EINVAL), (dict(rdt=0, r=P + 2), EINVAL), (dict(w=P + 2), EINVAL), (dict(post=P + 2), EINVAL), (dict(gate=P + 1), EINVAL),
     (dict(stats=P + 2), EINVAL), (dict(w=None), EINVAL),
