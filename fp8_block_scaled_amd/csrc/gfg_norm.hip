@@ -25,7 +25,6 @@ namespace gfg {
 namespace {
 
 constexpr int64_t kMaxH = 32768;               // 1024 lanes of 4 chunks of 8 elements
-constexpr int64_t kMostGroups = 768;           // workgroups of the backward pass: rows of partial sums
 
 typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
 
@@ -397,35 +396,32 @@ __global__ __launch_bounds__(kThreads<TPR>) void residual_norm_backward_kernel(B
     }
 }
 
-// The sums over the workgroups' rows, in a fixed order: 16 lanes a channel.
-__global__ __launch_bounds__(256) void norm_sums_kernel(const float* __restrict__ sums, int64_t P, int H, const float* post,
-                                                        const float* gate, int gate_kind, float* dweight, float* dpost,
-                                                        float* dgate, int accumulate) {
-    __shared__ float part[2][16][17];
-    const int l = threadIdx.x & 15, g = threadIdx.x >> 4, c = int(blockIdx.x) * 16 + l;
-    float a = 0.0f, b = 0.0f;
+// The sums over the workgroups' rows, in a fixed order: 32 channels a workgroup,
+// 32 lanes each; blockIdx.y 0: dweight, 1: S, for the other two.
+__global__ __launch_bounds__(1024) void norm_sums_kernel(const float* __restrict__ sums, int P, int H, const float* post,
+                                                         const float* gate, int gate_kind, float* dweight, float* dpost,
+                                                         float* dgate, int accumulate) {
+    __shared__ float part[32][33];
+    const int l = threadIdx.x & 31, g = threadIdx.x >> 5, c = int(blockIdx.x) * 32 + l;
+    float t = 0.0f;
     if (c < H)
-        for (int64_t r = g; r < P; r += 16) {
-            a += sums[r * 2 * H + c];
-            b += sums[r * 2 * H + H + c];
-        }
-    part[0][g][l] = a;
-    part[1][g][l] = b;
+        for (int r = g; r < P; r += 32) t += sums[(int64_t(r) * 2 + blockIdx.y) * H + c];
+    part[g][l] = t;
     __syncthreads();
     if (g || c >= H) return;
-    a = b = 0.0f;
+    t = 0.0f;
 #pragma unroll
-    for (int w = 0; w < 16; ++w) {
-        a += part[0][w][l];
-        b += part[1][w][l];
-    }
+    for (int w = 0; w < 32; ++w) t += part[w][l];
     auto put = [&](float* p, float v) {
         if (p) p[c] = accumulate ? p[c] + v : v;
     };
-    put(dweight, a);
+    if (blockIdx.y == 0) {
+        put(dweight, t);
+        return;
+    }
     // (without rows the factors are not read)
-    put(dpost, P > 0 && gate_kind == GFG_GATE_CHANNEL ? gate[c] * b : b);
-    if (gate_kind == GFG_GATE_CHANNEL) put(dgate, P > 0 && post ? post[c] * b : b);
+    put(dpost, P > 0 && gate_kind == GFG_GATE_CHANNEL ? gate[c] * t : t);
+    if (gate_kind == GFG_GATE_CHANNEL) put(dgate, P > 0 && post ? post[c] * t : t);
 }
 
 // Lanes a row, and chunks that a lane holds.
@@ -448,10 +444,15 @@ void by_type(int32_t dtype, int32_t residual_dtype, F f) {
     else f(_Float16{}, float{});
 }
 
-// Workgroups of a pass over M rows, at most `most`.
-int64_t groups(int64_t M, int64_t H, int64_t most) {
-    int64_t rows = 1;
-    by_width(H, [&](auto w) { rows = kRows<decltype(w)::TPR>; });
+// Workgroups of a pass over M rows: at most `waves` waves in all, as many as the
+// registers leave room for on 256 CUs, each of which then walks rows.
+constexpr int64_t kForwardWaves = 4096, kBackwardWaves = 2048;
+int64_t groups(int64_t M, int64_t H, int64_t waves) {
+    int64_t rows = 1, most = 1;
+    by_width(H, [&](auto w) {
+        rows = kRows<decltype(w)::TPR>;
+        most = waves * 64 / kThreads<decltype(w)::TPR>;
+    });
     const int64_t n = (M + rows - 1) / rows;
     return n < most ? n : most;
 }
@@ -490,7 +491,7 @@ int forward(const char* fn, NormArgs a, int32_t dtype, int32_t residual_dtype, v
         return fail(GFG_EINVAL, "%s: a pointer is not aligned to its elements (q: 8 bytes)", fn);
     by_width(a.H, [&](auto width) {
         constexpr int TPR = decltype(width)::TPR, CH = decltype(width)::CH;
-        const dim3 grid(unsigned(groups(a.M, a.H, 4096 * 64 / kThreads<TPR>))), block(kThreads<TPR>);
+        const dim3 grid(unsigned(groups(a.M, a.H, kForwardWaves))), block(kThreads<TPR>);
         by_type(dtype, residual_dtype, [&](auto y, auto r) {
             hipLaunchKernelGGL((residual_norm_kernel<decltype(y), decltype(r), TPR, CH, (CH == 2)>), grid, block, 0, static_cast<hipStream_t>(stream), a);
         });
@@ -531,7 +532,7 @@ extern "C" int residual_norm_fp8(const void* y, const void* residual, const floa
 }
 
 extern "C" int64_t residual_norm_backward_workspace_bytes(int64_t M, int64_t H) {
-    return M > 0 && H > 0 ? groups(M, H, kMostGroups) * 2 * H * 4 : 0;
+    return M > 0 && H > 0 ? groups(M, H, kBackwardWaves) * 2 * H * 4 : 0;
 }
 
 extern "C" int residual_norm_backward(const void* dout, const void* dnormed, const void* out, const void* y, const float* stats,
@@ -567,7 +568,7 @@ extern "C" int residual_norm_backward(const void* dout, const void* dnormed, con
                         (long long)residual_norm_backward_workspace_bytes(M, H));
     }
     hipStream_t s = static_cast<hipStream_t>(stream);
-    const int64_t P = M > 0 ? groups(M, H, kMostGroups) : 0;
+    const int64_t P = M > 0 ? groups(M, H, kBackwardWaves) : 0;
     if (M > 0) {
         const BackArgs a{dout, dnormed, out, y, stats, weight, post_weight, gate, gate_kind, alpha, dresidual, dy, dgate,
                          sums ? static_cast<float*>(workspace) : nullptr, M, int(H)};
@@ -581,7 +582,7 @@ extern "C" int residual_norm_backward(const void* dout, const void* dnormed, con
         if (int rc = launched()) return rc;
     }
     if (!sums || (M == 0 && accumulate)) return GFG_OK;
-    hipLaunchKernelGGL(norm_sums_kernel, dim3(unsigned((H + 15) / 16)), dim3(256), 0, s, static_cast<const float*>(workspace), P, int(H),
+    hipLaunchKernelGGL(norm_sums_kernel, dim3(unsigned((H + 31) / 32), 2), dim3(1024), 0, s, static_cast<const float*>(workspace), int(P), int(H),
                        post_weight, gate, gate_kind, dweight, dpost_weight, dgate, accumulate);
     return launched();
 }

@@ -10,8 +10,9 @@
 //   weights w_j = scale v_j (/ sum v), v the softmax or the sigmoid of the chosen:
 //   dL/dv_j = scale dw_j, or scale (dw_j - sum dw v / sum v) / sum v
 //
-// A wave has a token, its lanes the experts lane, lane + 64, ...; a row of logits
-// is read once by each of the two passes.
+// LPT lanes share a token, NE neighbouring experts each (LPT also reaches k, so a
+// lane has at most one of the token's choices), and a wave has 64 / LPT tokens;
+// a row of logits is read once by each of the two passes.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -23,7 +24,7 @@
 namespace gfg {
 namespace {
 
-constexpr int64_t kMostChunks = 1024;          // token ranges of the loss, a workgroup each
+constexpr int64_t kMostChunks = 512;          // token ranges of the loss, a workgroup each
 
 struct RouterArgs {
     const void* logits;
@@ -39,26 +40,88 @@ struct RouterArgs {
     float alpha, z;
 };
 
-__device__ __forceinline__ float add(float a, float b) { return a + b; }
+// A lane's NE experts: those from `col` on, of which the ones from `skip` on are
+// its own.  Past the last whole NE of E a lane takes the row's last ones, some of
+// which (or all) are another lane's, so every load is one whole vector inside the
+// row, by every lane, and no branch stands between the loads.  TINY: fewer than
+// NE experts, loaded one by one, the last of them in place of those past it.
+template <typename T, int NE>
+struct Vec { typedef T type __attribute__((ext_vector_type(NE), aligned(sizeof(T)))); };
 
-// A token's logits, NaN as -infinity.
-template <typename L, int NE>
-__device__ __forceinline__ void load_logits(float (&l)[NE], const L* row, int E, int lane) {
-#pragma unroll
-    for (int j = 0; j < NE; ++j) {
-        const int e = lane + 64 * j;
-        const float v = e < E ? float(row[e]) : -INFINITY;
-        l[j] = v != v ? -INFINITY : v;
+template <int NE, bool TINY>
+struct Lane {
+    int col, skip, E;
+    __device__ __forceinline__ Lane(int l, int E) : E(E) {
+        col = TINY ? NE * l : min(NE * l, E - NE);
+        skip = min(NE * l - col, NE);
     }
+    __device__ __forceinline__ bool own(int j) const { return TINY ? col + j < E : j >= skip; }
+    template <typename T>
+    __device__ __forceinline__ typename Vec<T, NE>::type load(const T* row) const {
+        if constexpr (!TINY) return *reinterpret_cast<const typename Vec<T, NE>::type*>(row + col);
+        typename Vec<T, NE>::type v;
+#pragma unroll
+        for (int j = 0; j < NE; ++j) v[j] = row[min(col + j, E - 1)];
+        return v;
+    }
+    template <typename T>
+    __device__ __forceinline__ void store(T* row, const float (&v)[NE]) const {
+        if (!TINY && skip == 0) {
+            typename Vec<T, NE>::type w;
+#pragma unroll
+            for (int j = 0; j < NE; ++j) w[j] = T(v[j]);
+            *reinterpret_cast<typename Vec<T, NE>::type*>(row + col) = w;
+        } else if (skip < NE) {
+#pragma unroll
+            for (int j = 0; j < NE; ++j)
+                if (own(j)) row[col + j] = T(v[j]);
+        }
+    }
+    // where expert `id` lies in an array of the lanes' NE elements each
+    __device__ __forceinline__ int place(int id) const {
+        const int tail = TINY ? 0 : E & (NE - 1);
+        return tail && id >= E - tail ? id + NE - tail : id;
+    }
+    // a token's logits: NaN (the larger of a NaN and a number is the number) and another lane's as -infinity
+    template <typename T>
+    __device__ __forceinline__ void get(float (&f)[NE], T v) const {
+#pragma unroll
+        for (int j = 0; j < NE; ++j) f[j] = own(j) ? fmaxf(float(v[j]), -INFINITY) : -INFINITY;
+    }
+};
+
+// Reductions over the LPT lanes of a token: exchanges inside quads, between the
+// quads of 8 lanes and the halves of 16 (DPP), then between rows of 16.
+template <int LPT, typename Op>
+__device__ __forceinline__ float group_reduce(float v, Op op) {
+    auto with = [&](auto ctrl) { return __int_as_float(dpp<decltype(ctrl)::value>(__float_as_int(v))); };
+    if constexpr (LPT == 64) return wave_reduce(v, op);
+    if constexpr (LPT >= 2) v = op(v, with(std::integral_constant<int, 0xB1>{}));       // quad_perm 1,0,3,2
+    if constexpr (LPT >= 4) v = op(v, with(std::integral_constant<int, 0x4E>{}));       // quad_perm 2,3,0,1
+    if constexpr (LPT >= 8) v = op(v, with(std::integral_constant<int, 0x141>{}));      // row_half_mirror
+    if constexpr (LPT >= 16) v = op(v, with(std::integral_constant<int, 0x140>{}));     // row_mirror
+    if constexpr (LPT >= 32) v = op(v, __int_as_float(__builtin_amdgcn_ds_swizzle(__float_as_int(v), 0x401F)));   // lane ^ 16
+    return v;
+}
+template <int LPT>
+__device__ __forceinline__ float group_sum(float v) { return group_reduce<LPT>(v, [](float a, float b) { return a + b; }); }
+template <int LPT>
+__device__ __forceinline__ bool group_any(bool b, int lane) {
+    const uint64_t all = __ballot(b);
+    if constexpr (LPT == 64) return all != 0;
+    else return ((all >> (lane & ~(LPT - 1))) & ((uint64_t(1) << LPT) - 1)) != 0;
 }
 
-// Its softmax in `e` (zeros if every expert is masked): e^(l - top) * inv; returns logsumexp.
-template <int NE>
+// 1 / v to one unit of the last place; 0 for 0.
+__device__ __forceinline__ float reciprocal(float v) { return v > 0.0f ? __builtin_amdgcn_rcpf(v) : 0.0f; }
+
+// A token's softmax in `e` (zeros if every expert is masked): e^(l - top) * inv; returns logsumexp.
+template <int LPT, int NE>
 __device__ __forceinline__ float softmax_of(const float (&l)[NE], float (&e)[NE], float& top, float& inv) {
     top = l[0];
 #pragma unroll
     for (int j = 1; j < NE; ++j) top = fmaxf(top, l[j]);
-    top = wave_reduce(top, [](float a, float b) { return fmaxf(a, b); });
+    top = group_reduce<LPT>(top, [](float a, float b) { return fmaxf(a, b); });
     float sum = 0.0f;
 #pragma unroll
     for (int j = 0; j < NE; ++j) {
@@ -66,44 +129,62 @@ __device__ __forceinline__ float softmax_of(const float (&l)[NE], float (&e)[NE]
         if (l[j] == -INFINITY) e[j] = 0.0f;
         sum += e[j];
     }
-    sum = wave_reduce(sum, add);
-    inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+    sum = group_sum<LPT>(sum);
+    inv = reciprocal(sum);
 #pragma unroll
     for (int j = 0; j < NE; ++j) e[j] *= inv;
     return sum > 0.0f ? top + __logf(sum) : 0.0f;
 }
 
-// Sigmoid and its derivative s (1 - s), without cancellation.
+// Sigmoid s, and its derivative s (1 - s) = (e^-l s) s without cancellation; both
+// 0 for a masked expert.  (The hardware reciprocal is within one unit of the last
+// place, and 0 for infinity.)
 __device__ __forceinline__ float sigmoid(float l, float* slope) {
-    const float e = __expf(-fabsf(l)), r = 1.0f / (1.0f + e);
-    *slope = e * r * r;
-    return l >= 0.0f ? r : e * r;
+    const float e = __expf(-l), s = __builtin_amdgcn_rcpf(1.0f + e);
+    *slope = fminf(e, 0x1p126f) * s * s;
+    return s;
+}
+
+// p[i] of data that the kernel does not write; UNIFORM: i is the same for a wave,
+// and the load goes through the scalar cache.
+template <bool UNIFORM, typename T>
+__device__ __forceinline__ T read(const T* p, int i) {
+    if constexpr (UNIFORM) return ((const __attribute__((address_space(4))) T*)p)[__builtin_amdgcn_readfirstlane(i)];
+    else return p[i];
 }
 
 // The last sequence s with offsets[s] <= t (0 where there is none).
-__device__ __forceinline__ int sequence_of(const int32_t* offsets, int S, int64_t t) {
+template <bool UNIFORM>
+__device__ __forceinline__ int sequence_of(const int32_t* offsets, int S, int t) {
+    if constexpr (UNIFORM) t = __builtin_amdgcn_readfirstlane(t);
     int lo = 0, hi = S;
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (offsets[mid] <= t) lo = mid;
+        if (read<UNIFORM>(offsets, mid) <= t) lo = mid;
         else hi = mid;
     }
+    if constexpr (UNIFORM) return __builtin_amdgcn_readfirstlane(lo);
     return lo;
 }
 
 // A workgroup's range of tokens, piece by piece of the sequences in it.  Piece
 // (range r, sequence s) is number r + s: both only rise from one piece to the
 // next, so no two share one.
-template <typename L, int NE>
-__global__ __launch_bounds__(256) void balance_sums_kernel(RouterArgs p) {
-    __shared__ int count[64 * NE];
-    __shared__ float total[64 * NE];
-    __shared__ float zsum[4];
-    __shared__ int tokens[4];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+constexpr int SUMS_THREADS = 512;
+
+template <typename L, int LPT, int NE, bool TINY, int SCORE>
+__global__ __launch_bounds__(SUMS_THREADS) void balance_sums_kernel(RouterArgs p) {
+    constexpr int WAVES = SUMS_THREADS / 64, TPW = 64 / LPT;       // tokens a wave has at a time
+    __shared__ int count[LPT * NE];
+    __shared__ float total[WAVES][LPT * NE];
+    __shared__ float zsum[WAVES];
+    __shared__ int tokens[WAVES];
+    const int lane = threadIdx.x & 63, l = lane & (LPT - 1), slot = lane / LPT;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const Lane<NE, TINY> my(l, p.E);
     const int64_t begin = int64_t(blockIdx.x) * p.per, end = begin + p.per < p.T ? begin + p.per : p.T;
     if (blockIdx.x == 0 && threadIdx.x == 0) *p.arrived = 0u;
-    int s = p.offsets ? sequence_of(p.offsets, p.S, begin) : 0;
+    int s = p.offsets ? sequence_of<true>(p.offsets, p.S, int(begin)) : 0;
     for (int64_t at = begin; at < end;) {
         // the sequence's tokens in the range; those before the first one's start or
         // past the last one's end are in none
@@ -114,58 +195,81 @@ __global__ __launch_bounds__(256) void balance_sums_kernel(RouterArgs p) {
             last = p.offsets[s + 1];
             if (s + 1 < p.S && last > at && last < end) stop = last;
         }
-        for (int e = threadIdx.x; e < 64 * NE; e += 256) count[e] = 0;
+        for (int e = threadIdx.x; e < LPT * NE; e += SUMS_THREADS) count[e] = 0;
         __syncthreads();
         float sum[NE] = {}, z = 0.0f;
         int n = 0;
-        for (int64_t t = at + wave; t < stop; t += 4) {
-            if (t < first || t >= last) continue;
-            const int id = lane < p.k ? p.ids[t * p.k + lane] : -1;
-            const bool chosen = id >= 0 && id < p.E;
-            if (!__any(chosen)) continue;
+        typename Vec<L, NE>::type now, next;
+        int id, next_id;
+        // (a token past the piece is read as its last one, and does not count)
+        auto load = [&](typename Vec<L, NE>::type& v, int& i, int64_t t) {
+            t = t < stop ? t : stop - 1;
+            v = my.load(static_cast<const L*>(p.logits) + t * p.E);
+            i = p.ids[t * p.k + min(l, p.k - 1)];
+        };
+        load(now, id, at + wave * TPW + slot);
+        for (int64_t t0 = at + wave * TPW; t0 < stop; t0 += WAVES * TPW) {
+            const int64_t t = t0 + slot;
+            load(next, next_id, t + WAVES * TPW);
+            const bool chosen = l < p.k && id >= 0 && id < p.E && t >= first && t < last && t < stop;
+            const bool counts = group_any<LPT>(chosen, lane);
             if (chosen) atomicAdd(&count[id], 1);
-            float l[NE], e[NE], top, scale;
-            load_logits(l, static_cast<const L*>(p.logits) + t * p.E, p.E, lane);
-            if (p.score == GFG_SCORE_SOFTMAX || p.z != 0.0f) {
-                const float lse = softmax_of(l, e, top, scale);
-                if (p.z != 0.0f) z += lse * lse;
+            float lg[NE], e[NE], top, inv = 1.0f;
+            my.get(lg, now);
+            if (SCORE == GFG_SCORE_SOFTMAX || p.z != 0.0f) {
+                const float lse = softmax_of<LPT>(lg, e, top, inv);
+                if (p.z != 0.0f && counts && l == 0) z += lse * lse;
+                inv = 1.0f;
             }
-            if (p.score == GFG_SCORE_SIGMOID) {
+            if constexpr (SCORE == GFG_SCORE_SIGMOID) {
                 float all = 0.0f, slope;
 #pragma unroll
                 for (int j = 0; j < NE; ++j) {
-                    e[j] = sigmoid(l[j], &slope);
+                    e[j] = sigmoid(lg[j], &slope);
                     all += e[j];
                 }
-                all = wave_reduce(all, add);
-                const float inv = all > 0.0f ? 1.0f / all : 0.0f;
-#pragma unroll
-                for (int j = 0; j < NE; ++j) e[j] *= inv;
+                all = group_sum<LPT>(all);
+                inv = reciprocal(all);
             }
+            if (counts) {
 #pragma unroll
-            for (int j = 0; j < NE; ++j) sum[j] += e[j];
-            ++n;
+                for (int j = 0; j < NE; ++j) sum[j] += e[j] * inv;
+                n += l == 0;
+            }
+            now = next;
+            id = next_id;
         }
-        // the waves' sums in order
+        // the lanes' sums of an expert in a fixed order: a wave's slots, then the waves
+        z = wave_reduce(z, [](float a, float b) { return a + b; });
+        n = wave_reduce(n, [](int a, int b) { return a + b; });
         if (lane == 0) {
             zsum[wave] = z;
             tokens[wave] = n;
         }
-        for (int w = 0; w < 4; ++w) {
-            if (wave == w) {
 #pragma unroll
-                for (int j = 0; j < NE; ++j) total[lane + 64 * j] = w ? total[lane + 64 * j] + sum[j] : sum[j];
-            }
-            __syncthreads();
+        for (int j = 0; j < NE; ++j) {
+#pragma unroll
+            for (int x = LPT; x < 64; x <<= 1) sum[j] += __shfl_xor(sum[j], x, 64);
+            if (slot == 0) total[wave][NE * l + j] = sum[j];     // (another lane's are 0)
         }
+        __syncthreads();
         float* const out = p.sums + (int64_t(blockIdx.x) + s) * (2 * p.E + 2);
-        for (int e = threadIdx.x; e < p.E; e += 256) {
-            out[e] = total[e];
+        for (int e = threadIdx.x; e < p.E; e += SUMS_THREADS) {
+            float v = 0.0f;
+#pragma unroll
+            for (int w = 0; w < WAVES; ++w) v += total[w][my.place(e)];
+            out[e] = v;
             out[p.E + e] = __int_as_float(count[e]);
         }
         if (threadIdx.x == 0) {
-            out[2 * p.E] = (zsum[0] + zsum[1]) + (zsum[2] + zsum[3]);
-            out[2 * p.E + 1] = __int_as_float(tokens[0] + tokens[1] + tokens[2] + tokens[3]);
+            float zz = 0.0f;
+            int nn = 0;
+            for (int w = 0; w < WAVES; ++w) {
+                zz += zsum[w];
+                nn += tokens[w];
+            }
+            out[2 * p.E] = zz;
+            out[2 * p.E + 1] = __int_as_float(nn);
         }
         __syncthreads();                       // count and total are reused
         at = stop;
@@ -173,16 +277,17 @@ __global__ __launch_bounds__(256) void balance_sums_kernel(RouterArgs p) {
     }
 }
 
-// Workgroup (eb, s): experts 16 eb .. +15 of sequence s over its pieces, 16 lanes
+// Workgroup (eb, s): experts 32 eb .. +31 of sequence s over its pieces, 32 lanes
 // an expert, in a fixed order; the last workgroup to finish adds the losses up,
 // in order.
-__global__ __launch_bounds__(256) void balance_finish_kernel(RouterArgs p) {
-    __shared__ float fpart[16][17];
-    __shared__ int ipart[16][17];
-    __shared__ float zpart[256];
-    __shared__ int npart[256];
+__global__ __launch_bounds__(1024) void balance_finish_kernel(RouterArgs p) {
+    __shared__ float fpart[32][33];
+    __shared__ int ipart[32][33];
+    __shared__ float zpart[16];
+    __shared__ int npart[16];
     __shared__ bool is_last;
-    const int l = threadIdx.x & 15, g = threadIdx.x >> 4, e = int(blockIdx.x) * 16 + l, s = int(blockIdx.y);
+    const int l = threadIdx.x & 31, g = threadIdx.x >> 5, e = int(blockIdx.x) * 32 + l, s = int(blockIdx.y);
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     int64_t from = 0, to = p.T;
     if (p.offsets) {
         from = p.offsets[s];
@@ -195,36 +300,39 @@ __global__ __launch_bounds__(256) void balance_finish_kernel(RouterArgs p) {
     float P = 0.0f, zs = 0.0f;
     int c = 0, n = 0;
     if (e < p.E)
-        for (int64_t r = r0 + g; r < r1; r += 16) {
+        for (int64_t r = r0 + g; r < r1; r += 32) {
             const float* const piece = p.sums + (r + s) * stride;
             P += piece[e];
             c += __float_as_int(piece[p.E + e]);
         }
-    for (int64_t r = r0 + threadIdx.x; r < r1; r += 256) {
+    for (int64_t r = r0 + threadIdx.x; r < r1; r += 1024) {
         const float* const piece = p.sums + (r + s) * stride;
         zs += piece[2 * p.E];
         n += __float_as_int(piece[2 * p.E + 1]);
     }
     fpart[g][l] = P;
     ipart[g][l] = c;
-    zpart[threadIdx.x] = zs;
-    npart[threadIdx.x] = n;
-    __syncthreads();
-    for (int w = 128; w >= 1; w >>= 1) {
-        if (int(threadIdx.x) < w) {
-            zpart[threadIdx.x] += zpart[threadIdx.x + w];
-            npart[threadIdx.x] += npart[threadIdx.x + w];
-        }
-        __syncthreads();
+    zs = wave_reduce(zs, [](float a, float b) { return a + b; });
+    n = wave_reduce(n, [](int a, int b) { return a + b; });
+    if (lane == 0) {
+        zpart[wave] = zs;
+        npart[wave] = n;
     }
-    n = npart[0];
+    __syncthreads();
+    n = 0;
+    zs = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 16; ++w) {
+        n += npart[w];
+        zs += zpart[w];
+    }
     const float rn = n > 0 ? 1.0f / float(n) : 0.0f, rs = 1.0f / float(p.S);
     float part = 0.0f;
     if (g == 0 && e < p.E) {
         P = 0.0f;
         c = 0;
 #pragma unroll
-        for (int w = 0; w < 16; ++w) {
+        for (int w = 0; w < 32; ++w) {
             P += fpart[w][l];
             c += ipart[w][l];
         }
@@ -233,33 +341,30 @@ __global__ __launch_bounds__(256) void balance_finish_kernel(RouterArgs p) {
         p.factors[int64_t(s) * (p.E + 1) + e] = factor;
         part = factor * P;
     }
-    if (g == 0) {
-#pragma unroll
-        for (int w = 8; w >= 1; w >>= 1) part += __shfl_xor(part, w, 16);
-    }
+    if (wave == 0) part = wave_reduce(part, [](float a, float b) { return a + b; });     // (0 in its upper half)
     if (threadIdx.x == 0) {
         if (blockIdx.x == 0) {
             p.factors[int64_t(s) * (p.E + 1) + p.E] = 2.0f * p.z * rs * rn;
-            if (p.z != 0.0f) part += p.z * rs * rn * zpart[0];
+            if (p.z != 0.0f) part += p.z * rs * rn * zs;
         }
         const unsigned of = gridDim.x * gridDim.y, me = blockIdx.y * gridDim.x + blockIdx.x;
-        __hip_atomic_store(&p.losses[me], part, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        __threadfence();
-        is_last = __hip_atomic_fetch_add(p.arrived, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == of - 1;
+        if (of == 1) {
+            *p.loss = part;
+        } else {
+            __hip_atomic_store(&p.losses[me], part, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            __threadfence();
+            is_last = __hip_atomic_fetch_add(p.arrived, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == of - 1;
+        }
     }
+    if (gridDim.x * gridDim.y == 1) return;
     __syncthreads();
-    if (!is_last) return;
+    if (!is_last || wave) return;
     __threadfence();
     const int of = int(gridDim.x * gridDim.y);
     float t = 0.0f;
-    for (int i = threadIdx.x; i < of; i += 256) t += __hip_atomic_load(&p.losses[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    zpart[threadIdx.x] = t;
-    __syncthreads();
-    for (int w = 128; w >= 1; w >>= 1) {
-        if (int(threadIdx.x) < w) zpart[threadIdx.x] += zpart[threadIdx.x + w];
-        __syncthreads();
-    }
-    if (threadIdx.x == 0) *p.loss = zpart[0];
+    for (int i = lane; i < of; i += 64) t += __hip_atomic_load(&p.losses[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    t = wave_reduce(t, [](float a, float b) { return a + b; });
+    if (lane == 0) *p.loss = t;
 }
 
 struct RouterBack {
@@ -272,104 +377,168 @@ struct RouterBack {
     float scale;
 };
 
-template <typename L, int NE>
+template <typename L, int LPT, int NE, bool TINY, int SCORE>
 __global__ __launch_bounds__(256) void router_backward_kernel(RouterBack p) {
-    const int lane = threadIdx.x & 63;
-    for (int64_t t = int64_t(blockIdx.x) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); t < p.T; t += int64_t(gridDim.x) * 4) {
-        const int id = lane < p.k ? p.ids[t * p.k + lane] : -1;
-        const bool chosen = id >= 0 && id < p.E;
-        const L* const row = static_cast<const L*>(p.logits) + t * p.E;
-        float l[NE], e[NE], slope[NE], d[NE], top, one;
-        load_logits(l, row, p.E, lane);
-        const float lse = softmax_of(l, e, top, one);  // e: the softmax
-#pragma unroll
-        for (int j = 0; j < NE; ++j) d[j] = 0.0f;
-        const bool sigmoids = p.score == GFG_SCORE_SIGMOID;
-        float all = 0.0f;                              // of the sigmoids
-        float v[NE];                                   // the scores
-#pragma unroll
-        for (int j = 0; j < NE; ++j) {
-            v[j] = e[j];
-            if (sigmoids) {
-                v[j] = sigmoid(l[j], &slope[j]);
-                all += v[j];
-            }
-        }
-        // ---- the loss
+    constexpr int TPW = 64 / LPT;
+    constexpr bool SIGMOID = SCORE == GFG_SCORE_SIGMOID;
+    typedef float v4 __attribute__((ext_vector_type(4)));
+    __shared__ __attribute__((aligned(16))) float scatter_smem[4][TPW][LPT * NE];
+    const int lane = threadIdx.x & 63, l = lane & (LPT - 1), slot = lane / LPT;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    GFG_LDS float* const scatter = (GFG_LDS float*)scatter_smem + (wave * TPW + slot) * (LPT * NE);
+    auto lds_done = [] { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); };     // (a wave's own; LDS operations keep their order)
+    const Lane<NE, TINY> my(l, p.E);
+    typename Vec<L, NE>::type now, next;
+    int id, next_id;
+    float dw_in, next_dw;
+    // (a token past the last is read as the last, and not stored; without dweights
+    // the ids are read in their place, and not used)
+    const float* const dws = p.dweights ? p.dweights : reinterpret_cast<const float*>(p.ids);
+    auto load = [&](typename Vec<L, NE>::type& v, int& i, float& dw, int64_t t) {
+        t = t < p.T ? t : p.T - 1;
+        v = my.load(static_cast<const L*>(p.logits) + t * p.E);
+        const int64_t at = t * p.k + min(l, p.k - 1);
+        i = p.ids[at];
+        dw = dws[at];
+    };
+    const float up = p.dloss ? *p.dloss : 0.0f;
+    const int64_t step = int64_t(gridDim.x) * (4 * TPW);
+    int64_t mine = int64_t(blockIdx.x) * (4 * TPW) + wave * TPW + slot;
+    load(now, id, dw_in, mine);
+    for (int64_t first = int64_t(blockIdx.x) * (4 * TPW); first < p.T; first += step, mine += step) {
+        load(next, next_id, next_dw, mine + step);
+        const int64_t t = mine < p.T ? mine : p.T - 1;
+        const bool chosen = l < p.k && id >= 0 && id < p.E;
+        dw_in = chosen && p.dweights ? dw_in * p.scale : 0.0f;
+        const int place = chosen ? my.place(id) : 0;
+        // the loss's factors of the token's sequence
+        typename Vec<float, NE>::type c = {};
+        float zf = 0.0f;
+        bool counts = false;
         if (p.factors) {
             int s = 0;
-            bool in = true;
+            counts = group_any<LPT>(chosen, lane);
             if (p.offsets) {
-                s = sequence_of(p.offsets, p.S, t);
-                in = t >= p.offsets[s] && t < p.offsets[s + 1];
+                s = sequence_of<LPT == 64>(p.offsets, p.S, int(t));
+                counts = counts && t >= read<LPT == 64>(p.offsets, s) && t < read<LPT == 64>(p.offsets, s + 1);
             }
-            if (in && __any(chosen)) {
-                const float* const f = p.factors + int64_t(s) * (p.E + 1);
-                const float up = *p.dloss, zf = f[p.E] != 0.0f ? f[p.E] * lse : 0.0f;
-                float inv = 1.0f;
-                if (sigmoids) {
-                    all = wave_reduce(all, add);
-                    inv = all > 0.0f ? 1.0f / all : 0.0f;
-                }
-                float c[NE], dot = 0.0f;
-#pragma unroll
-                for (int j = 0; j < NE; ++j) {
-                    c[j] = lane + 64 * j < p.E ? f[lane + 64 * j] : 0.0f;
-                    dot += c[j] * v[j] * inv;
-                }
-                dot = wave_reduce(dot, add);
-#pragma unroll
-                for (int j = 0; j < NE; ++j)
-                    d[j] = up * ((sigmoids ? slope[j] * inv : e[j]) * (c[j] - dot) + (zf != 0.0f ? zf * e[j] : 0.0f));
-            }
+            const float* const f = p.factors + int64_t(s) * (p.E + 1);
+            c = my.load(f);
+            zf = read<LPT == 64>(f, p.E);
         }
-        // ---- the weights
+        float lg[NE], e[NE], v[NE], slope[NE], d[NE], top = 0.0f, one = 0.0f, lse = 0.0f;
+        my.get(lg, now);
+        float lc = -INFINITY;                                  // the logit of this lane's choice
         if (p.dweights) {
-            float dw = chosen ? p.dweights[t * p.k + lane] * p.scale : 0.0f;
-            // this lane's choice and its score
-            float lc = chosen ? float(row[id]) : -INFINITY;
-            if (lc != lc) lc = -INFINITY;
-            float ds, sc;
-            if (sigmoids) {
-                sc = sigmoid(lc, &ds);
-            } else {
-                sc = lc == -INFINITY ? 0.0f : lc == top ? one : __expf(lc - top) * one;
-            }
+#pragma unroll
+            for (int j = 0; j < NE; j += 4) *reinterpret_cast<GFG_LDS v4*>(scatter + NE * l + j) = v4{lg[j], lg[j + 1], lg[j + 2], lg[j + 3]};
+            lds_done();
+            if (chosen) lc = scatter[place];
+            lds_done();
+        }
+        if (!SIGMOID || zf != 0.0f) lse = softmax_of<LPT>(lg, e, top, one);        // e: the softmax
+        float sc, ds = 0.0f;                                   // the choice's score, and its slope
+        if constexpr (SIGMOID) sc = sigmoid(lc, &ds);
+        else sc = lc == -INFINITY ? 0.0f : lc == top ? one : __expf(lc - top) * one;
+        sc = chosen ? sc : 0.0f;
+        // all that is summed over the token's lanes
+        float all = 0.0f, dot = 0.0f;
+#pragma unroll
+        for (int j = 0; j < NE; ++j) {
+            v[j] = SIGMOID ? sigmoid(lg[j], &slope[j]) : e[j];
+            all += v[j];
+            dot += c[j] * v[j];
+        }
+        float g = dw_in, of_softmax = 0.0f;
+        if (p.dweights) {
+            float mean = group_sum<LPT>(dw_in * sc);
             if (p.renorm) {
-                const float total = wave_reduce(chosen ? sc : 0.0f, add);
-                const float inv = total > 0.0f ? 1.0f / total : 0.0f;
-                const float mean = wave_reduce(chosen ? dw * sc * inv : 0.0f, add);
-                dw = chosen ? (dw - mean) * inv : 0.0f;
+                const float inv = reciprocal(group_sum<LPT>(sc));
+                g = (dw_in - mean * inv) * inv;
+            } else {
+                of_softmax = SIGMOID ? 0.0f : mean;            // (renormalized, this sum is 0)
             }
-            // softmax: v (g - sum g v); sigmoid: g times its slope
-            const float dot = sigmoids ? 0.0f : wave_reduce(chosen ? dw * sc : 0.0f, add);
-            const float g = dw;
+            g = chosen ? g * (SIGMOID ? ds : sc) : 0.0f;
+        }
 #pragma unroll
-            for (int j = 0; j < NE; ++j)
-                if (!sigmoids) d[j] -= e[j] * dot;
-            for (int q = 0; q < p.k; ++q) {
-                const int i = __builtin_amdgcn_readlane(id, q);
-                const float gq = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(g), q));
-                if (i < 0 || i >= p.E) continue;
+        for (int j = 0; j < NE; ++j) d[j] = SIGMOID ? 0.0f : -(e[j] * of_softmax);
+        if (p.factors) {
+            float inv = 1.0f;
+            dot = group_sum<LPT>(dot);
+            if constexpr (SIGMOID) {
+                all = group_sum<LPT>(all);
+                inv = reciprocal(all);
+                dot *= inv;
+            }
+            if (counts) {
+                const float scale = up * inv;
 #pragma unroll
-                for (int j = 0; j < NE; ++j)
-                    if (i == lane + 64 * j) d[j] += gq * (sigmoids ? slope[j] : e[j]);
+                for (int j = 0; j < NE; ++j) d[j] += scale * (SIGMOID ? slope[j] : e[j]) * (c[j] - dot);
+                if (zf != 0.0f) {
+                    const float zl = up * zf * lse;
+#pragma unroll
+                    for (int j = 0; j < NE; ++j) d[j] += zl * e[j];
+                }
             }
         }
-        L* const out = static_cast<L*>(p.dlogits) + t * p.E;
+        // ---- the weights' part goes to the lanes that have its experts, through LDS
+        if (p.dweights) {
+            // a choice that stands twice is found by its place in the list, and added up in the list's order
+            GFG_LDS int* const places = (GFG_LDS int*)scatter;
+            if (chosen) places[place] = l;
+            lds_done();
+            const bool twice = chosen && places[place] != l;
+            bool writes = chosen;
+            lds_done();
+            if (__any(twice)) {
+                float sum = 0.0f;
+                bool last = true;
+                for (int q = 0; q < p.k; ++q) {
+                    const int iq = __shfl(id, q, LPT);
+                    const float gq = __shfl(g, q, LPT);
+                    if (iq == id) {
+                        sum += gq;
+                        last = q <= l;
+                    }
+                }
+                g = sum;
+                writes = chosen && last;
+            }
 #pragma unroll
-        for (int j = 0; j < NE; ++j)
-            if (lane + 64 * j < p.E) out[lane + 64 * j] = L(d[j]);
+            for (int j = 0; j < NE; j += 4) *reinterpret_cast<GFG_LDS v4*>(scatter + NE * l + j) = v4{0.0f, 0.0f, 0.0f, 0.0f};
+            lds_done();
+            if (writes) scatter[place] = g;
+            lds_done();
+#pragma unroll
+            for (int j = 0; j < NE; j += 4) {
+                const v4 w = *reinterpret_cast<GFG_LDS v4*>(scatter + NE * l + j);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) d[j + i] += w[i];
+            }
+            lds_done();
+        }
+        now = next;
+        id = next_id;
+        dw_in = next_dw;
+        if (mine < p.T) my.store(static_cast<L*>(p.dlogits) + t * p.E, d);
     }
 }
 
+// Lanes a token and experts a lane.
+template <int T, int N, bool S> struct Split {
+    static constexpr int LPT = T, NE = N;
+    static constexpr bool TINY = S;
+};
 template <typename F>
-void by_experts(int64_t E, F f) {
-    if (E <= 64) f(std::integral_constant<int, 1>{});
-    else if (E <= 128) f(std::integral_constant<int, 2>{});
-    else if (E <= 256) f(std::integral_constant<int, 4>{});
-    else if (E <= 512) f(std::integral_constant<int, 8>{});
-    else f(std::integral_constant<int, 16>{});
+void by_split(int64_t E, int64_t k, F f) {
+    const int64_t lanes = (E + 7) / 8 > k ? (E + 7) / 8 : k;
+    if (E < 8 && lanes <= 8) f(Split<8, 8, true>{});
+    else if (E < 8) f(Split<64, 8, true>{});
+    else if (lanes <= 8) f(Split<8, 8, false>{});
+    else if (lanes <= 16) f(Split<16, 8, false>{});
+    else if (lanes <= 32) f(Split<32, 8, false>{});
+    else if (lanes <= 64) f(Split<64, 8, false>{});
+    else f(Split<64, 16, false>{});
 }
 template <typename F>
 void by_type(int32_t dtype, F f) {
@@ -378,13 +547,16 @@ void by_type(int32_t dtype, F f) {
     else f(_Float16{});
 }
 
-int64_t tokens_a_range(int64_t T) {
+// Tokens of a workgroup's range: at least as many as it has lanes for at a time.
+int64_t tokens_a_range(int64_t T, int64_t E) {
     const int64_t n = (T + kMostChunks - 1) / kMostChunks;
-    return n < 16 ? 16 : n;
+    int64_t lanes = 8;
+    while (lanes < 64 && lanes * 8 < E) lanes *= 2;
+    return n < SUMS_THREADS / lanes ? SUMS_THREADS / lanes : n;
 }
-int64_t ranges(int64_t T) { return T > 0 ? (T + tokens_a_range(T) - 1) / tokens_a_range(T) : 0; }
-int64_t piece_bytes(int64_t T, int64_t E, int64_t S) { return (ranges(T) + S) * (2 * E + 2) * 4; }
-int64_t finishers(int64_t E, int64_t S) { return (E + 15) / 16 * S; }
+int64_t ranges(int64_t T, int64_t E) { return T > 0 ? (T + tokens_a_range(T, E) - 1) / tokens_a_range(T, E) : 0; }
+int64_t piece_bytes(int64_t T, int64_t E, int64_t S) { return (ranges(T, E) + S) * (2 * E + 2) * 4; }
+int64_t finishers(int64_t E, int64_t S) { return (E + 31) / 32 * S; }
 
 int launched() {
     const hipError_t e = hipGetLastError();
@@ -442,7 +614,7 @@ extern "C" int moe_balance_loss(const void* logits, int32_t in_dtype, const int3
     a.k = int(k);
     a.S = int(S);
     a.score = score;
-    a.per = int(tokens_a_range(T));
+    a.per = int(tokens_a_range(T, E));
     a.arrived = reinterpret_cast<unsigned*>(ws);
     a.sums = reinterpret_cast<float*>(ws + 16);
     a.losses = reinterpret_cast<float*>(ws + 16 + piece_bytes(T, E, S));
@@ -452,15 +624,19 @@ extern "C" int moe_balance_loss(const void* logits, int32_t in_dtype, const int3
     a.alpha = alpha;
     a.z = z;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    // (a range more than there are: without tokens one workgroup still clears `arrived`)
-    const unsigned grid = unsigned(T > 0 ? ranges(T) : 1);
-    by_experts(E, [&](auto n) {
+    // (without tokens one workgroup still clears `arrived`)
+    const unsigned grid = unsigned(T > 0 ? ranges(T, E) : 1);
+    by_split(E, k, [&](auto n) {
+        constexpr int LPT = decltype(n)::LPT, NE = decltype(n)::NE;
+        constexpr bool TINY = decltype(n)::TINY;
         by_type(in_dtype, [&](auto l) {
-            hipLaunchKernelGGL((balance_sums_kernel<decltype(l), decltype(n)::value>), dim3(grid), dim3(256), 0, s, a);
+            auto* kernel = score == GFG_SCORE_SOFTMAX ? balance_sums_kernel<decltype(l), LPT, NE, TINY, GFG_SCORE_SOFTMAX>
+                                                      : balance_sums_kernel<decltype(l), LPT, NE, TINY, GFG_SCORE_SIGMOID>;
+            hipLaunchKernelGGL(kernel, dim3(grid), dim3(SUMS_THREADS), 0, s, a);
         });
     });
     if (int rc = launched()) return rc;
-    hipLaunchKernelGGL(balance_finish_kernel, dim3(unsigned((E + 15) / 16), unsigned(S)), dim3(256), 0, s, a);
+    hipLaunchKernelGGL(balance_finish_kernel, dim3(unsigned((E + 31) / 32), unsigned(S)), dim3(1024), 0, s, a);
     return launched();
 }
 
@@ -479,11 +655,14 @@ extern "C" int moe_router_backward(const void* logits, int32_t in_dtype, const i
         misaligned(dweights, 4) || misaligned(factors, 4) || misaligned(dloss, 4))
         return fail(GFG_EINVAL, "%s: a pointer is not aligned to its elements", fn);
     const RouterBack a{logits, ids, seq_offsets, dweights, factors, dloss, dlogits, T, int(E), int(k), int(S), score, renormalize, scale};
-    const int64_t wgs = (T + 3) / 4, most = int64_t(1) << 22;
-    by_experts(E, [&](auto n) {
+    by_split(E, k, [&](auto n) {
+        constexpr int LPT = decltype(n)::LPT, NE = decltype(n)::NE;
+        constexpr bool TINY = decltype(n)::TINY;
+        const int64_t wgs = (T + 4 * (64 / LPT) - 1) / (4 * (64 / LPT)), most = 2048;     // 8 a CU, each of which walks tokens
         by_type(in_dtype, [&](auto l) {
-            hipLaunchKernelGGL((router_backward_kernel<decltype(l), decltype(n)::value>), dim3(unsigned(wgs < most ? wgs : most)), dim3(256), 0,
-                               static_cast<hipStream_t>(stream), a);
+            auto* kernel = score == GFG_SCORE_SOFTMAX ? router_backward_kernel<decltype(l), LPT, NE, TINY, GFG_SCORE_SOFTMAX>
+                                                      : router_backward_kernel<decltype(l), LPT, NE, TINY, GFG_SCORE_SIGMOID>;
+            hipLaunchKernelGGL(kernel, dim3(unsigned(wgs < most ? wgs : most)), dim3(256), 0, static_cast<hipStream_t>(stream), a);
         });
     });
     return launched();
