@@ -22,76 +22,22 @@
 #include "gfg.h"
 #include "gfg_device.h"
 #include "gfg_fp8_linear.h"
+#include "gfg_fp8_quant.h"
 #include "gfg_internal.h"
 
 namespace gfg {
 namespace {
 
-typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
-
 constexpr int QB = 128;                        // elements of a scale block
 constexpr uint32_t kOutside = 0x80000000u;     // past every buffer window used here (all below 2^31 bytes)
 
-// ------------------------------------------------------------------ encoding a block
-// Eight elements of a row as they lie in memory.
-template <typename T> struct Eight;
-template <> struct Eight<__bf16> {
-    u32x4 w;
-    __device__ __forceinline__ float at(int i) const {
-        return __uint_as_float((i & 1) ? w[i >> 1] & 0xFFFF0000u : w[i >> 1] << 16);
-    }
-};
-template <> struct Eight<_Float16> {
-    u32x4 w;
-    __device__ __forceinline__ float at(int i) const {
-        return float(__builtin_bit_cast(_Float16, uint16_t(w[i >> 1] >> (16 * (i & 1)))));
-    }
-};
-template <> struct Eight<float> {
-    u32x4 w, w2;
-    __device__ __forceinline__ float at(int i) const { return __uint_as_float(i < 4 ? w[i & 3] : w2[i & 3]); }
-};
+// The largest of 16 neighbouring lanes' magnitudes.
 template <typename T>
-__device__ __forceinline__ Eight<T> load8(const T* p) {
-    Eight<T> e;
-    e.w = reinterpret_cast<const u32x4*>(p)[0];
-    if constexpr (sizeof(T) == 4) e.w2 = reinterpret_cast<const u32x4*>(p)[1];
-    return e;
-}
-
-// Magnitude bits: their integer order is that of the magnitudes, with
-// infinities and NaN above every finite value.
-__device__ __forceinline__ uint32_t mag(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
-
-// The E8M0 byte of a block with largest magnitude `ab`, and 2^-t in *inv.  With
-// 448 = 1.75 * 2^8 and max|v| = 1.f * 2^e, t is e - 8 where 1.f <= 1.75 and e - 7
-// otherwise, at least -127 (which still keeps |v / 2^t| <= 448).  A block with an
-// infinity or a NaN has byte 255 (NaN) and *inv 0.
-__device__ __forceinline__ uint32_t block_scale(uint32_t ab, float* inv) {
-    if (ab >= 0x7F800000u) {
-        *inv = 0.0f;
-        return 255u;
-    }
-    int e = int(ab >> 23) - 127;
-    uint32_t mant = ab & 0x7FFFFFu;
-    if (e == -127) {                           // subnormal or zero
-        const int lz = __builtin_clz(mant | 1u) - 8;
-        mant = (mant << lz) & 0x7FFFFFu;
-        e = -126 - lz;
-    }
-    int t = mant <= 0x600000u ? e - 8 : e - 7;
-    t = t < -127 ? -127 : t;
-    if (ab == 0) t = 0;
-    *inv = __builtin_ldexpf(1.0f, -t);
-    return uint32_t(t + 127);
-}
-
-// Four codes, rounded to nearest even by the packed conversion; |v * inv| <= 448.
-// A block without a scale gets the codes of NaN.
-__device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d, float inv) {
-    if (inv == 0.0f) return 0x7F7F7F7Fu;
-    uint32_t w = uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(a * inv, b * inv, 0, false));
-    return uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(c * inv, d * inv, int(w), true));
+__device__ __forceinline__ uint32_t row_largest(uint32_t m) {
+    m = larger<T>(m, uint32_t(dpp<0x128>(int(m))));        // rotations by 8, 4, 2, 1
+    m = larger<T>(m, uint32_t(dpp<0x124>(int(m))));
+    m = larger<T>(m, uint32_t(dpp<0x122>(int(m))));
+    return larger<T>(m, uint32_t(dpp<0x121>(int(m))));
 }
 
 // ------------------------------------------------------------------ token quantizer
@@ -114,18 +60,9 @@ __global__ __launch_bounds__(256) void quant_rows_kernel(const T* __restrict__ x
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const int64_t r = r0 + 16 * u;
-        uint32_t ab = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) ab = max(ab, mag(v[u].at(i)));
-#pragma unroll
-        for (int w = 8; w >= 1; w >>= 1) ab = max(ab, uint32_t(__shfl_xor(int(ab), w, 16)));
-        float inv;
-        const uint32_t byte = block_scale(ab, &inv);
+        const uint32_t byte = scale_byte_of(as_f32<T>(row_largest<T>(largest(v[u]))));
         if (r >= R) continue;
-        if (col < C)
-            *reinterpret_cast<u32x2*>(q + r * C + col) =
-                u32x2{encode4(v[u].at(0), v[u].at(1), v[u].at(2), v[u].at(3), inv),
-                      encode4(v[u].at(4), v[u].at(5), v[u].at(6), v[u].at(7), inv)};
+        if (col < C) *reinterpret_cast<u32x2*>(q + r * C + col) = encode(v[u], byte);
         if ((threadIdx.x & 15) == 0) scale[kb * ld + r] = uint8_t(byte);
     }
 }
@@ -139,27 +76,47 @@ __global__ __launch_bounds__(256) void quant_rows_kernel(const T* __restrict__ x
 // matrices one after the other.  Thread (g, l) holds rows 8 g .. +7 and columns
 // 8 l .. +7, so a column's eight codes are one 8-byte word of the transposed
 // tile in LDS, whose words are XOR-swizzled by the column's l.
+struct TileJob {
+    const void* x;
+    uint8_t *q, *scale;
+    int64_t ld;
+    uint8_t* qt;
+    int64_t ldt, store_t;    // row stride of qt, and how many of a row's bytes are written
+    uint8_t* scale_t;
+    int64_t ld_t;
+    float* sums;
+    int64_t R;
+    int C;
+    unsigned tiles;
+};
+
+// Two rows' values of column i in one word (of 16 bits each).
+template <typename T>
+__device__ __forceinline__ uint32_t pair_of(const Eight<T>& a, const Eight<T>& b, int i) {
+    return __builtin_amdgcn_perm(b.w[i >> 1], a.w[i >> 1], (i & 1) ? 0x07060302u : 0x05040100u);
+}
+
 template <typename T, bool BLOCK>
-__global__ __launch_bounds__(256) void quant_tile_kernel(const T* __restrict__ x, uint8_t* __restrict__ q,
-                                                         uint8_t* __restrict__ scale, int64_t ld, uint8_t* __restrict__ qt,
-                                                         int64_t ldt, int64_t store_t, uint8_t* __restrict__ scale_t,
-                                                         int64_t ld_t, float* __restrict__ sums, int64_t R, int C) {
+__device__ __forceinline__ void quant_tile(TileJob p, unsigned item0) {
+    constexpr int PER = sizeof(T) == 4 ? 8 : 4;            // words of eight magnitudes
     __shared__ __attribute__((aligned(16))) uint8_t tile[QB * QB];
-    __shared__ uint32_t top[16][QB];
+    __shared__ uint32_t top[16][16 * PER];
     __shared__ float part[16][QB];
+    __shared__ uint32_t bytes[QB];
     const int l = threadIdx.x & 15, g = threadIdx.x >> 4;
-    const int CB = (C + QB - 1) / QB;
-    const int64_t RB = (R + QB - 1) / QB;
-    int64_t item = blockIdx.x;
+    const T* x = static_cast<const T*>(p.x);
+    const int CB = (p.C + QB - 1) / QB;
+    const int64_t RB = (p.R + QB - 1) / QB;
+    int64_t item = item0;
     if (BLOCK) {
         const int64_t per = RB * CB, gi = item / per;
         item -= gi * per;
-        x += gi * R * C;
-        q += gi * R * C;
-        scale += gi * per;
-        if (qt) {
-            qt += gi * R * C;
-            scale_t += gi * per;
+        x += gi * p.R * p.C;
+        p.q += gi * p.R * p.C;
+        p.scale += gi * per;
+        if (p.qt) {
+            p.qt += gi * p.R * p.C;
+            p.scale_t += gi * per;
         }
     }
     const int cb = int(item % CB);
@@ -169,48 +126,38 @@ __global__ __launch_bounds__(256) void quant_tile_kernel(const T* __restrict__ x
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
         v[u] = Eight<T>{};
-        if (r0 + u < R && col < C) v[u] = load8(x + (r0 + u) * C + col);
+        if (r0 + u < p.R && col < p.C) v[u] = load8(x + (r0 + u) * p.C + col);
     }
-    uint32_t whole = 0;
-    float block_inv = 0.0f;
     uint32_t block_byte = 0;
     if (BLOCK) {
+        uint32_t m = 0;
 #pragma unroll
-        for (int u = 0; u < 8; ++u)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) whole = max(whole, mag(v[u].at(i)));
+        for (int u = 0; u < 8; ++u) m = larger<T>(m, largest(v[u]));
+        uint32_t whole = as_f32<T>(m);
         whole = wave_reduce(whole, [](uint32_t a, uint32_t b) { return max(a, b); });
         if ((threadIdx.x & 63) == 0) top[0][threadIdx.x >> 6] = whole;
-        __syncthreads();
-        whole = max(max(top[0][0], top[0][1]), max(top[0][2], top[0][3]));
-        block_byte = block_scale(whole, &block_inv);
+        lds_barrier();
+        block_byte = scale_byte_of(max(max(top[0][0], top[0][1]), max(top[0][2], top[0][3])));
         if (threadIdx.x == 0) {
-            scale[rb * CB + cb] = uint8_t(block_byte);
-            if (qt) scale_t[cb * RB + rb] = uint8_t(block_byte);
+            p.scale[rb * CB + cb] = uint8_t(block_byte);
+            if (p.qt) p.scale_t[cb * RB + rb] = uint8_t(block_byte);
         }
     }
-    // ---- along the rows
-    if (q) {
+    // ---- along the columns: magnitudes, and sums of eight rows a thread
+    if (!BLOCK && p.qt) {
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-            float inv = block_inv;
-            if (!BLOCK) {
-                uint32_t ab = 0;
+        for (int i = 0; i < PER; ++i) {
+            uint32_t m = 0;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) ab = max(ab, mag(v[u].at(i)));
-#pragma unroll
-                for (int w = 8; w >= 1; w >>= 1) ab = max(ab, uint32_t(__shfl_xor(int(ab), w, 16)));
-                const uint32_t byte = block_scale(ab, &inv);
-                if (l == 0 && r0 + u < R) scale[cb * ld + r0 + u] = uint8_t(byte);
+            for (int u = 0; u < 8; ++u) {
+                uint32_t w = v[u].w[i & 3];
+                if constexpr (sizeof(T) == 4) w = i < 4 ? v[u].w[i & 3] : v[u].w2[i & 3];
+                m = larger<T>(m, magnitudes<T>(w));
             }
-            if (r0 + u < R && col < C)
-                *reinterpret_cast<u32x2*>(q + (r0 + u) * C + col) =
-                    u32x2{encode4(v[u].at(0), v[u].at(1), v[u].at(2), v[u].at(3), inv),
-                          encode4(v[u].at(4), v[u].at(5), v[u].at(6), v[u].at(7), inv)};
+            top[g][PER * l + i] = m;
         }
     }
-    // ---- the columns' sums, eight rows a thread, then the sixteen parts in order
-    if (!BLOCK && sums) {
+    if (!BLOCK && p.sums) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             float t = 0.0f;
@@ -219,54 +166,79 @@ __global__ __launch_bounds__(256) void quant_tile_kernel(const T* __restrict__ x
             part[g][8 * l + i] = t;
         }
     }
-    if (!qt && !sums) return;
-    // ---- along the columns
-    if (!BLOCK && qt) {
+    // ---- along the rows
+    if (p.q) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            uint32_t ab = 0;
-#pragma unroll
-            for (int u = 0; u < 8; ++u) ab = max(ab, mag(v[u].at(i)));
-            top[g][8 * l + i] = ab;
+        for (int u = 0; u < 8; ++u) {
+            uint32_t byte = block_byte;
+            if (!BLOCK) {
+                byte = scale_byte_of(as_f32<T>(row_largest<T>(largest(v[u]))));
+                if (l == 0 && r0 + u < p.R) p.scale[cb * p.ld + r0 + u] = uint8_t(byte);
+            }
+            if (r0 + u < p.R && col < p.C) *reinterpret_cast<u32x2*>(p.q + (r0 + u) * p.C + col) = encode(v[u], byte);
         }
     }
-    if (!BLOCK) __syncthreads();
-    if (!BLOCK && threadIdx.x < QB) {
+    if (!p.qt && !p.sums) return;
+    if (!BLOCK) {
+        lds_barrier();
         const int c = threadIdx.x;
-        if (qt) {
-            uint32_t ab = 0;
+        if (c < QB) {
+            if (p.qt) {
+                const int word = sizeof(T) == 4 ? c : c >> 1;
+                uint32_t m = 0;
 #pragma unroll
-            for (int w = 0; w < 16; ++w) ab = max(ab, top[w][c]);
-            float inv;
-            const uint32_t byte = block_scale(ab, &inv);
-            top[0][c] = __float_as_uint(inv);          // (column c's maxima are read by this thread alone)
-            if (cb * QB + c < C) scale_t[rb * ld_t + cb * QB + c] = uint8_t(byte);
-        }
-        if (sums && cb * QB + c < C) {
-            float t = 0.0f;
+                for (int w = 0; w < 16; ++w) m = larger<T>(m, top[w][word]);
+                const uint32_t byte = scale_byte_of(as_f32<T>(m, c & 1));
+                bytes[c] = byte;
+                if (cb * QB + c < p.C) p.scale_t[rb * p.ld_t + cb * QB + c] = uint8_t(byte);
+            }
+            if (p.sums && cb * QB + c < p.C) {
+                float t = 0.0f;
 #pragma unroll
-            for (int w = 0; w < 16; ++w) t += part[w][c];
-            sums[rb * C + cb * QB + c] = t;
+                for (int w = 0; w < 16; ++w) t += part[w][c];
+                p.sums[rb * p.C + cb * QB + c] = t;
+            }
         }
+        if (!p.qt) return;
+        lds_barrier();
     }
-    if (!qt) return;
-    if (!BLOCK) __syncthreads();
+    if (!p.qt) return;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const float inv = BLOCK ? block_inv : __uint_as_float(top[0][8 * l + i]);
-        *reinterpret_cast<u32x2*>(tile + (8 * l + i) * QB + ((g ^ l) << 3)) =
-            u32x2{encode4(v[0].at(i), v[1].at(i), v[2].at(i), v[3].at(i), inv),
-                  encode4(v[4].at(i), v[5].at(i), v[6].at(i), v[7].at(i), inv)};
+        const uint32_t byte = BLOCK ? block_byte : bytes[8 * l + i], none = none_of(byte);
+        const float scale = scale_of(byte);
+        u32x2 o;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            if constexpr (sizeof(T) == 4)
+                o[h] = four(v[4 * h].at(i), v[4 * h + 1].at(i), v[4 * h + 2].at(i), v[4 * h + 3].at(i), scale);
+            else
+                o[h] = two<T, true>(two<T, false>(0u, pair_of(v[4 * h], v[4 * h + 1], i), scale), pair_of(v[4 * h + 2], v[4 * h + 3], i), scale);
+            o[h] = or_nan(o[h], none);
+        }
+        *reinterpret_cast<u32x2*>(tile + (8 * l + i) * QB + ((g ^ l) << 3)) = o;
     }
-    __syncthreads();
+    lds_barrier();
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const int c = 32 * j + int(threadIdx.x >> 3), ch = threadIdx.x & 7, key = c >> 3;
         const u32x4 w = *reinterpret_cast<const u32x4*>(tile + c * QB + ((ch ^ (key >> 1)) << 4));
         const u32x4 o = (key & 1) ? u32x4{w[2], w[3], w[0], w[1]} : w;
-        if (cb * QB + c < C && rb * QB + 16 * ch < store_t)
-            *reinterpret_cast<u32x4*>(qt + (cb * QB + c) * ldt + rb * QB + 16 * ch) = o;
+        if (cb * QB + c < p.C && rb * QB + 16 * ch < p.store_t)
+            *reinterpret_cast<u32x4*>(p.qt + (cb * QB + c) * p.ldt + rb * QB + 16 * ch) = o;
     }
+}
+
+template <typename T, bool BLOCK>
+__global__ __launch_bounds__(256) void quant_tile_kernel(TileJob p) {
+    quant_tile<T, BLOCK>(p, blockIdx.x);
+}
+
+// Two tensors in one launch (dy and x of a backward pass).
+template <typename T>
+__global__ __launch_bounds__(256) void quant_tiles_kernel(TileJob a, TileJob b) {
+    const bool second = blockIdx.x >= a.tiles;
+    quant_tile<T, false>(second ? b : a, second ? blockIdx.x - a.tiles : blockIdx.x);
 }
 
 // db[c] (+)= the sum over the row blocks of sums [RB][C], in a fixed order: 16
@@ -661,6 +633,124 @@ __global__ __launch_bounds__(NW * 64) void fp8_stream_kernel(F8Params p) {
     walk(p.tiles, [&](unsigned w) { stream_tile<RB, CB, NW, D, BROW, OutT>(p, w); });
 }
 
+// ------------------------------------------------------------------ a few tokens, quantized on the way
+//
+// Up to 16 rows of x in 32 or 16 bits, one launch: a block's scale needs its 128
+// channels alone, so a wave quantizes each unit of K that it takes itself, in
+// registers, where lane (l16, lq) loads what it needs of row l16 for the matrix
+// instruction (the 16-byte chunks lq and lq + 4 of the unit's codes); the block's
+// maximum crosses the four lanes of a row.  The weights come as in the streamed
+// product, 16 CB columns a workgroup.
+// Lanes l16, 16 + l16, 32 + l16, 48 + l16 all get the largest of their four values.
+template <typename T>
+__device__ __forceinline__ uint32_t largest_of_rows(uint32_t v) {
+    auto a = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    v = larger<T>(uint32_t(a[0]), uint32_t(a[1]));
+    auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    return larger<T>(uint32_t(b[0]), uint32_t(b[1]));
+}
+
+template <typename X, int CB, int NW, int D, typename OutT>
+__global__ __launch_bounds__(NW * 64) void fp8_few_kernel(const X* __restrict__ xs, F8Params p) {
+    constexpr int TN = 16 * CB, UNIT = TN * QB, PER = UNIT / 1024;
+    constexpr int XL = 4 * (sizeof(X) / 2), OPS = PER + XL;        // vector-memory operations of a stage
+    static_assert(D == 4 && OPS * (D - 1) < 63, "ring depth");
+    __shared__ __attribute__((aligned(1024))) uint8_t s0[NW * UNIT], s1[NW * UNIT], s2[NW * UNIT], s3[NW * UNIT];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int l16 = lane & 15, lq = lane >> 4;
+    GFG_LDS uint8_t* const ring[D] = {(GFG_LDS uint8_t*)s0 + wave * UNIT, (GFG_LDS uint8_t*)s1 + wave * UNIT,
+                                      (GFG_LDS uint8_t*)s2 + wave * UNIT, (GFG_LDS uint8_t*)s3 + wave * UNIT};
+    const int M = int(p.rows), n0 = int(blockIdx.x) * TN, ncols = min(TN, p.N - n0);
+    const auto rx = make_rsrc(xs, uint32_t(M) * uint32_t(p.K) * uint32_t(sizeof(X)));
+    const auto rb = make_rsrc(p.b + int64_t(n0) * p.K, uint32_t(ncols) * uint32_t(p.K));
+    // (rows past M repeat the last one and are not stored)
+    const uint32_t xrow = uint32_t(min(l16, M - 1)) * uint32_t(p.K);
+    const uint8_t* const sb_row = uniform_ptr(p.b_scale + int64_t(n0 / QB) * p.KB);
+    Eight<X> x[D][4];
+    uint32_t sb[D];
+    auto load = [&](int d, int kb) {
+        __builtin_amdgcn_sched_barrier(0);
+        sb[d] = uint32_t(load_scale_word(sb_row, min(kb, p.KB - 1)));
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int k = kb * QB + 64 * h + 16 * lq;
+            const uint32_t at = k < p.K ? (xrow + uint32_t(k)) * uint32_t(sizeof(X)) : kOutside;
+            x[d][2 * h] = load8<X>(rx, at);
+            x[d][2 * h + 1] = load8<X>(rx, at + 8 * sizeof(X));
+        }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int R = 8 * i + (lane >> 3);
+            const int k = kb * QB + ((lane & 7) ^ Rows<CB>::key(R)) * 16;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (GFG_LDS void*)(ring[d] + i * 1024), 16,
+                                                     k < p.K ? uint32_t(Rows<CB>::swap(R)) * uint32_t(p.K) + uint32_t(k) : kOutside, 0, 0, 0);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    v4f acc[CB] = {};
+    auto step = [&](int d, int kb, auto ops) {
+        __builtin_amdgcn_sched_barrier(0);
+        GFG_WAITCNT((D - 1) * decltype(ops)::value, 15);
+        __builtin_amdgcn_sched_barrier(0);
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) m = larger<X>(m, largest(x[d][i]));
+        const uint32_t a_byte = scale_byte_of(as_f32<X>(largest_of_rows<X>(m)));
+        v8i af;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const u32x2 w = encode(x[d][i], a_byte);
+            af[2 * i] = int(w[0]);
+            af[2 * i + 1] = int(w[1]);
+        }
+        const int b_byte = scale_byte(int(sb[d]), sb_row, kb);
+#pragma unroll
+        for (int c = 0; c < CB; ++c) {
+            const int row = Rows<CB>::swap(CB * l16 + c), key = Rows<CB>::key(row);
+            auto part = [&](int ch) { return *reinterpret_cast<GFG_LDS u32x4*>(ring[d] + row * QB + ((ch ^ key) << 4)); };
+            acc[c] = mfma_at<0, 0>(join(part(lq), part(lq + 4)), af, acc[c], b_byte, int(a_byte));
+        }
+        load(d, kb + D * NW);                      // past K: zeros
+    };
+    constexpr std::integral_constant<int, OPS> all{};
+    constexpr std::integral_constant<int, PER> least{};
+#pragma unroll
+    for (int d = 0; d < D; ++d) load(d, wave + d * NW);
+    int kb = wave;                                 // (rounds as above)
+    for (; kb + (D - 1) * NW < p.KB; kb += D * NW) {
+#pragma unroll
+        for (int d = 0; d < D; ++d) step(d, kb + d * NW, all);
+    }
+    if (kb < p.KB) {
+        step(0, kb, least);
+        if (kb + NW < p.KB) {
+            step(1, kb + NW, least);
+            if (kb + 2 * NW < p.KB) step(2, kb + 2 * NW, least);
+        }
+    }
+    GFG_WAITCNT(0, 15);                            // the last loads land before the workgroup ends
+    static_assert(CB * 1024 <= UNIT, "the sums fit a stage");
+    auto sums = [&](int v, int i) -> GFG_LDS v4f& { return reinterpret_cast<GFG_LDS v4f*>((GFG_LDS uint8_t*)s0 + v * UNIT)[i * 64 + lane]; };
+#pragma unroll
+    for (int c = 0; c < CB; ++c) sums(wave, c) = acc[c];
+    __syncthreads();
+    if (wave || l16 >= M) return;
+    const int n = n0 + 4 * CB * lq;
+    float v[4 * CB], bias[4 * CB];
+    load_bias(bias, p, n);
+#pragma unroll
+    for (int c = 0; c < CB; ++c) {
+        v4f t = sums(0, c);
+#pragma unroll
+        for (int u = 1; u < NW; ++u) t += sums(u, c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[CB * i + c] = t[i] + bias[CB * i + c];
+    }
+    store_row<4 * CB>(static_cast<OutT*>(p.d) + int64_t(l16) * p.N, n, p.N, v, 0);
+}
+
 // Workgroups of a launch over p.tiles tiles: one for each, or as many as the
 // grid limit allows, which is rounded up to whole slots on every XCD.
 unsigned workgroups(const F8Params& p) {
@@ -720,10 +810,13 @@ int launch_product(const char* fn, const F8Params& p, int out_dtype, hipStream_t
         return fail(GFG_EUNSUPPORTED, "%s: the 256 x 256 tile's offsets do not reach over N=%d", fn, p.N);
     if (fits && (choice == GFG_TILE_256x256 || (choice == GFG_TILE_AUTO && (p.rows + 127) / 128 * ((int64_t(p.N) + 127) / 128) > cus)))
         return launch_fp8_256(p, BROW, out_dtype, s);
-    if constexpr (!BROW)
-        if (p.rows <= 16) return launch_stream<1, 2, 4, 4, false>(p, out_dtype, s);
-    if (p.rows <= 32) return launch_stream<2, 2, 4, 2, BROW>(p, out_dtype, s);
     auto tiles = [&](int64_t tm, int64_t tn) { return (p.rows + tm - 1) / tm * ((p.N + tn - 1) / tn); };
+    if constexpr (!BROW)
+        if (p.rows <= 16) {
+            if (p.N <= 16 * cus) return launch_stream<1, 1, 8, 4, false>(p, out_dtype, s);
+            return launch_stream<1, 2, 4, 4, false>(p, out_dtype, s);
+        }
+    if (p.rows <= 32) return launch_stream<2, 2, 4, 2, BROW>(p, out_dtype, s);
     if (tiles(128, 128) >= 192) return launch_ring<128, 128, 2, 4, BROW>(p, out_dtype, s);
     if (tiles(32, 32) <= 512) return launch_stream<2, 2, 4, 2, BROW>(p, out_dtype, s);
     return launch_ring<64, 64, 2, 2, BROW>(p, out_dtype, s);
@@ -767,25 +860,48 @@ int quantize_rows(const void* x, int32_t in_dtype, uint8_t* q, uint8_t* scale, i
     return launch_quant_rows<_Float16>(x, q, scale, R, C, ld, s);
 }
 
-struct TileOut {
-    uint8_t *q, *scale;
-    int64_t ld;
-    uint8_t* qt;
-    int64_t ldt, store_t;
-    uint8_t* scale_t;
-    int64_t ld_t;
-    float* sums;
-};
+// What goes this way: up to 16 rows whose elements every workgroup can load again
+// for less than a launch (cold weights, us, one launch and two: 1 x 7168 x 2304
+// 6.5, 7.8; 16 x 7168 x 2304 7.2, 8.1; 16 x 2048 x 7168 11.1, 11.5; 4 x 2048 x 16384
+// 14.0, 16.2; but 16 x 2048 x 16384 20.3, 18.5; 16 x 300 x 16384 18.9, 12.8).  A
+// workgroup has one tile, so not under a grid limit.  Tiles of 16 columns on eight
+// waves where they do not outnumber the CUs, else 32 on four (16 and 32: 1 x 2048 x
+// 7168 8.0, 9.4; 1 x 4096 x 4096 7.0, 7.3; 1 x 7168 x 2304 7.1, 6.5; 1 x 28672 x 4096
+// 32.2, 27.7).
+constexpr int64_t kFewTokens = 16, kFewElements = 1 << 17;
 
-template <bool BLOCK>
-int quantize_tiles(const void* x, int32_t in_dtype, int64_t R, int64_t C, int64_t G, const TileOut& o, hipStream_t s) {
-    const dim3 grid(unsigned((R + QB - 1) / QB * ((C + QB - 1) / QB) * G));
-    auto go = [&](auto* kernel, auto* xs) {
-        hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, xs, o.q, o.scale, o.ld, o.qt, o.ldt, o.store_t, o.scale_t, o.ld_t, o.sums, R, int(C));
-    };
-    if (in_dtype == GFG_IN_F32) go(quant_tile_kernel<float, BLOCK>, static_cast<const float*>(x));
-    else if (in_dtype == GFG_IN_BF16) go(quant_tile_kernel<__bf16, BLOCK>, static_cast<const __bf16*>(x));
-    else go(quant_tile_kernel<_Float16, BLOCK>, static_cast<const _Float16*>(x));
+template <typename X, int CB, int NW>
+int launch_few_on(const void* x, const F8Params& p, int out_dtype, hipStream_t s) {
+    const dim3 grid(unsigned((p.N + 16 * CB - 1) / (16 * CB))), block(NW * 64);
+    if (out_dtype == GFG_OUT_BF16)
+        hipLaunchKernelGGL((fp8_few_kernel<X, CB, NW, 4, __bf16>), grid, block, 0, s, static_cast<const X*>(x), p);
+    else
+        hipLaunchKernelGGL((fp8_few_kernel<X, CB, NW, 4, _Float16>), grid, block, 0, s, static_cast<const X*>(x), p);
+    return launched();
+}
+
+template <typename X>
+int launch_few(const void* x, const F8Params& p, int out_dtype, hipStream_t s) {
+    int cus = 0;
+    if (int rc = device_cus(&cus)) return rc;
+    if (p.N <= 16 * cus) return launch_few_on<X, 1, 8>(x, p, out_dtype, s);
+    return launch_few_on<X, 2, 4>(x, p, out_dtype, s);
+}
+
+TileJob job(const void* x, int64_t R, int64_t C, int64_t G) {
+    TileJob p{};
+    p.x = x;
+    p.R = R;
+    p.C = int(C);
+    p.tiles = unsigned((R + QB - 1) / QB * ((C + QB - 1) / QB) * G);
+    return p;
+}
+
+template <typename F>
+int by_type(int32_t in_dtype, F f) {
+    if (in_dtype == GFG_IN_F32) f(float{});
+    else if (in_dtype == GFG_IN_BF16) f(__bf16{});
+    else f(_Float16{});
     return launched();
 }
 
@@ -889,7 +1005,15 @@ extern "C" int fp8_quantize_weight_device(const void* w, int32_t in_dtype, int32
     if (misaligned(w, 16) || misaligned(q, 16) || misaligned(q_t, 16))
         return fail(GFG_EINVAL, "%s: w, q and q_t must be 16-byte aligned", fn);
     if (q_t && N % 16) return fail(GFG_EUNSUPPORTED, "%s: N=%lld must be a multiple of 16 for the transposed codes", fn, (long long)N);
-    return quantize_tiles<true>(w, in_dtype, N, K, G, TileOut{q, scale, 0, q_t, N, N, scale_t, 0, nullptr}, static_cast<hipStream_t>(stream));
+    TileJob p = job(w, N, K, G);
+    p.q = q;
+    p.scale = scale;
+    p.qt = q_t;
+    p.ldt = p.store_t = N;
+    p.scale_t = scale_t;
+    return by_type(in_dtype, [&](auto t) {
+        hipLaunchKernelGGL((quant_tile_kernel<decltype(t), true>), dim3(p.tiles), dim3(256), 0, static_cast<hipStream_t>(stream), p);
+    });
 }
 
 extern "C" int fp8_gemm(const void* a, const uint8_t* a_scale, int64_t a_scale_ld, const void* b, const uint8_t* b_scale,
@@ -923,6 +1047,12 @@ extern "C" int fp8_linear(const void* x, int32_t in_dtype, const void* b, const 
     if (int rc = check_workspace(fn, workspace, workspace_bytes, fp8_linear_workspace_bytes(M, K))) return rc;
     hipStream_t s = static_cast<hipStream_t>(stream);
     uint8_t *q = static_cast<uint8_t*>(workspace), *scale = q + M * K;
+    if (M <= kFewTokens && M * K <= kFewElements && grid_limit() == 0) {
+        const F8Params p = product(nullptr, nullptr, 0, b, b_scale, 0, bias, d, M, N, K);
+        if (in_dtype == GFG_IN_F32) return launch_few<float>(x, p, out_dtype, s);
+        if (in_dtype == GFG_IN_BF16) return launch_few<__bf16>(x, p, out_dtype, s);
+        return launch_few<_Float16>(x, p, out_dtype, s);
+    }
     const int64_t ld = up(M, 4);
     if (int rc = quantize_rows(x, in_dtype, q, scale, M, K, ld, s)) return rc;
     return launch_product<false>(fn, product(q, scale, ld, b, b_scale, 0, bias, d, M, N, K), out_dtype, s);
@@ -949,8 +1079,8 @@ extern "C" int fp8_linear_backward(const void* dy, const void* x, int32_t in_dty
         return fail(GFG_EUNSUPPORTED, "%s: N=%lld must be a multiple of 16 and at most %lld", fn, (long long)N, (long long)kMaxK);
     if (M > kMaxK) return fail(GFG_EUNSUPPORTED, "%s: M=%lld above %lld", fn, (long long)M, (long long)kMaxK);
     const int64_t MB = (M + QB - 1) / QB;
-    if (MB * ((N > K ? N : K) + QB) >= int64_t(1) << 31)
-        return fail(GFG_EUNSUPPORTED, "%s: dy or x (M=%lld, N=%lld, K=%lld) has 2^38 elements or more", fn, (long long)M, (long long)N, (long long)K);
+    if (MB * ((N + K + 2 * QB) / QB) >= int64_t(1) << 24)
+        return fail(GFG_EUNSUPPORTED, "%s: dy and x (M=%lld, N=%lld, K=%lld) are 2^24 tiles of 128 x 128 or more", fn, (long long)M, (long long)N, (long long)K);
     if (!dx && !dw && !dbias) return fail(GFG_EINVAL, "%s: dx, dw and dbias are all null", fn);
     if (misaligned(dx, 8) || misaligned(dw, 8) || misaligned(dbias, 4))
         return fail(GFG_EINVAL, "%s: dx and dw must be 8-byte aligned, dbias 4-byte", fn);
@@ -969,15 +1099,28 @@ extern "C" int fp8_linear_backward(const void* dy, const void* x, int32_t in_dty
     if (int rc = check_workspace(fn, workspace, workspace_bytes, at.bytes)) return rc;
     uint8_t* const ws = static_cast<uint8_t*>(workspace);
     float* const sums = reinterpret_cast<float*>(ws + at.sums);
-    if (int rc = quantize_tiles<false>(dy, in_dtype, M, N, 1,
-                                       TileOut{dx ? ws + at.q : nullptr, ws + at.qs, at.ldm, dw ? ws + at.yt : nullptr, at.Mp, at.Mp,
-                                               ws + at.yts, at.ldn, dbias ? sums : nullptr}, s))
-        return rc;
-    if (dw) {
-        if (int rc = quantize_tiles<false>(x, in_dtype, M, K, 1,
-                                           TileOut{nullptr, nullptr, 0, ws + at.xt, at.Mp, at.Mp, ws + at.xts, at.ldk, nullptr}, s))
-            return rc;
+    TileJob a = job(dy, M, N, 1), b = job(x, M, K, 1);
+    if (dx) {
+        a.q = ws + at.q;
+        a.scale = ws + at.qs;
+        a.ld = at.ldm;
     }
+    if (dw) {
+        a.qt = ws + at.yt;
+        b.qt = ws + at.xt;
+        a.ldt = a.store_t = b.ldt = b.store_t = at.Mp;
+        a.scale_t = ws + at.yts;
+        b.scale_t = ws + at.xts;
+        a.ld_t = at.ldn;
+        b.ld_t = at.ldk;
+    } else {
+        b.tiles = 0;
+    }
+    a.sums = dbias ? sums : nullptr;
+    if (int rc = by_type(in_dtype, [&](auto t) {
+            hipLaunchKernelGGL((quant_tiles_kernel<decltype(t)>), dim3(a.tiles + b.tiles), dim3(256), 0, s, a, b);
+        }))
+        return rc;
     if (dbias) {
         hipLaunchKernelGGL(column_sums_kernel, dim3(unsigned((N + 15) / 16)), dim3(256), 0, s, sums, dbias, at.MB, int(N), accumulate);
         if (int rc = launched()) return rc;

@@ -19,14 +19,13 @@
 
 #include "gfg.h"
 #include "gfg_device.h"
+#include "gfg_fp8_quant.h"
 #include "gfg_internal.h"
 
 namespace gfg {
 namespace {
 
 constexpr int64_t kMaxH = 32768;               // 1024 lanes of 4 chunks of 8 elements
-
-typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
 
 // Eight neighbouring elements at any address of their type.
 template <typename T>
@@ -121,26 +120,6 @@ __device__ __forceinline__ void load_weights(float (&f)[CH][8], const float* wei
     }
 }
 
-// The E8M0 byte of a block with largest magnitude bits `ab`, and 2^-t (0 for a
-// block that has none): t the smallest integer with 448 * 2^t >= max, at least -127.
-__device__ __forceinline__ uint32_t block_scale(uint32_t ab, float* inv) {
-    if (ab >= 0x7F800000u) {
-        *inv = 0.0f;
-        return 255u;
-    }
-    int e = int(ab >> 23) - 127;
-    uint32_t mant = ab & 0x7FFFFFu;
-    if (e == -127) {
-        const int lz = __builtin_clz(mant | 1u) - 8;
-        mant = (mant << lz) & 0x7FFFFFu;
-        e = -126 - lz;
-    }
-    int t = mant <= 0x600000u ? e - 8 : e - 7;
-    t = ab == 0 ? 0 : t < -127 ? -127 : t;
-    *inv = __builtin_ldexpf(1.0f, -t);
-    return uint32_t(t + 127);
-}
-
 // AHEAD: the next row is loaded while one is computed.
 template <typename Y, typename R, int TPR, int CH, bool AHEAD>
 __global__ __launch_bounds__(kThreads<TPR>) void residual_norm_kernel(NormArgs p) {
@@ -228,16 +207,9 @@ __global__ __launch_bounds__(kThreads<TPR>) void residual_norm_kernel(NormArgs p
                     ab = max(ab, uint32_t(dpp<0x124>(int(ab))));
                     ab = max(ab, uint32_t(dpp<0x122>(int(ab))));
                     ab = max(ab, uint32_t(dpp<0x121>(int(ab))));
-                    float inv;
-                    const uint32_t byte = block_scale(ab, &inv);
-                    u32x2 code = {0x7F7F7F7Fu, 0x7F7F7F7Fu};
-                    if (inv != 0.0f) {
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(z[4 * h] * inv, z[4 * h + 1] * inv, 0, false);
-                            code[h] = uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(z[4 * h + 2] * inv, z[4 * h + 3] * inv, lo, true));
-                        }
-                    }
+                    const uint32_t byte = scale_byte_of(ab), none = none_of(byte);
+                    const float by = scale_of(byte);
+                    const u32x2 code = {or_nan(four(z[0], z[1], z[2], z[3], by), none), or_nan(four(z[4], z[5], z[6], z[7], by), none)};
                     if (valid && !c[j].skip) {
                         *reinterpret_cast<u32x2*>(p.q + m * p.H + c[j].col) = code;
                         if ((c[j].col & 127) == 0) p.scale[(c[j].col >> 7) * p.scale_ld + m] = uint8_t(byte);
