@@ -797,6 +797,21 @@ int launch_stream(F8Params p, int out_dtype, hipStream_t s) {
     return launched();
 }
 
+// The tile by how many of each size there are (M x N x K, us, the product alone,
+// cold weights, the chosen tile first):
+//  * more tiles of 128 x 128 than CUs: 256 x 256 (4096 x 4096 x 16384: 205-240, 128 x
+//    128 346-370; 4096 x 7168 x 2304: 70, 110; 7168 x 2304 x 4096 with a scale a row of
+//    both: 62, 97);
+//  * up to 16 rows: streamed, 16 x 16 on eight waves where those do not outnumber
+//    the CUs (1 x 2048 x 7168: 6.7, 16 x 32 8.0; 16 x 2048 x 16384: 12.5, 16.0; 1 x
+//    4096 x 4096: 6.0, 6.3), else 16 x 32 (1 x 7168 x 2304: 5.8);
+//  * up to 32 rows: 32 x 32, streamed (32 x 4096 x 4096: 8.0);
+//  * 192 tiles of 128 x 128 or more: those (512 x 7168 x 2304, 224 of them: 14.8);
+//  * up to 512 tiles of 32 x 32: those, streamed (128 x 2048 x 7168: 10.5; 300 x 528 x
+//    1040: 3.9);
+//  * else 64 x 64 (512 x 2048 x 7168: 18.3; 512 x 4096 x 4096: 18.9).
+// The last two lists' borders are the int8 products', whose tiles these are.  All
+// of them take in about 50 GB/s a CU, which bounds 64 x 64.
 // A tile's lane loads the scale bytes of its RB (CB) neighbouring rows at once,
 // so an operand has to have that many rows: up to 16 rows of A go to RB = 1,
 // and the gradient of a weight has at least 16 of both.
