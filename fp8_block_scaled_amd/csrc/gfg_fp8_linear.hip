@@ -242,22 +242,28 @@ __global__ __launch_bounds__(256) void quant_tiles_kernel(TileJob a, TileJob b) 
 }
 
 // db[c] (+)= the sum over the row blocks of sums [RB][C], in a fixed order: 16
-// lanes of partial sums a column, then those.
-__global__ __launch_bounds__(256) void column_sums_kernel(const float* __restrict__ sums, float* __restrict__ out, int64_t RB,
-                                                          int C, int accumulate) {
+// lanes of partial sums a column, then those; 16 columns a workgroup.
+struct SumJob {
+    const float* sums;
+    float* out;
+    int64_t RB;
+    int C, accumulate;
+};
+__device__ __forceinline__ void column_sums(const SumJob& p, int block) {
     __shared__ float part[16][17];
-    const int c = int(blockIdx.x) * 16 + int(threadIdx.x & 15), g = threadIdx.x >> 4;
+    const int c = block * 16 + int(threadIdx.x & 15), g = threadIdx.x >> 4;
     float t = 0.0f;
-    if (c < C)
-        for (int64_t r = g; r < RB; r += 16) t += sums[r * C + c];
+    if (c < p.C)
+        for (int64_t r = g; r < p.RB; r += 16) t += p.sums[r * p.C + c];
     part[g][threadIdx.x & 15] = t;
     __syncthreads();
-    if (g || c >= C) return;
+    if (g || c >= p.C) return;
     t = 0.0f;
 #pragma unroll
     for (int w = 0; w < 16; ++w) t += part[w][threadIdx.x];
-    out[c] = accumulate ? out[c] + t : t;
+    p.out[c] = p.accumulate ? p.out[c] + t : t;
 }
+__global__ __launch_bounds__(256) void column_sums_kernel(SumJob p) { column_sums(p, int(blockIdx.x)); }
 
 template <typename T>
 __global__ __launch_bounds__(256) void zero_kernel(T* __restrict__ p, int64_t n) {
@@ -506,17 +512,16 @@ __global__ __launch_bounds__(WM * WN * 64) void fp8_ring_kernel(F8Params p) {
 // filled by direct-to-LDS loads.  No barrier stands between a load and its
 // MFMAs, every byte of the tile's rows enters the CU once and leaves the LDS
 // once; the waves' sums meet in LDS at the end, in wave order.
+template <int RB, int CB> constexpr int kUnit = 16 * (RB + CB) * QB;     // bytes of a wave's stage: A's rows, then B's
+
+// s0 .. s3: a stage of every wave each (NW * kUnit bytes; the last two with D = 4).
 template <int RB, int CB, int NW, int D, bool BROW, typename OutT>
-__device__ __forceinline__ void stream_tile(const F8Params& p, unsigned w) {
+__device__ __forceinline__ void stream_tile(const F8Params& p, unsigned w, uint8_t* s0, uint8_t* s1, uint8_t* s2, uint8_t* s3) {
     constexpr int TM = 16 * RB, TN = 16 * CB;
-    constexpr int UNIT = (TM + TN) * QB;           // bytes of a stage: A's rows, then B's
+    constexpr int UNIT = kUnit<RB, CB>;
     constexpr int PER = UNIT / 1024;               // loads per stage
     constexpr int OPS = PER + 1 + (BROW ? 1 : 0);
     static_assert((D == 2 || D == 4) && OPS * D < 64, "ring depth");
-    // an array for each stage: the compiler then knows that reading one need
-    // not wait for the loads into another
-    __shared__ __attribute__((aligned(1024))) uint8_t s0[NW * UNIT], s1[NW * UNIT];
-    __shared__ __attribute__((aligned(1024))) uint8_t s2[D > 2 ? NW * UNIT : 1024], s3[D > 2 ? NW * UNIT : 1024];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int l16 = lane & 15, lq = lane >> 4;
@@ -630,17 +635,21 @@ __device__ __forceinline__ void stream_tile(const F8Params& p, unsigned w) {
 
 template <int RB, int CB, int NW, int D, bool BROW, typename OutT>
 __global__ __launch_bounds__(NW * 64) void fp8_stream_kernel(F8Params p) {
-    walk(p.tiles, [&](unsigned w) { stream_tile<RB, CB, NW, D, BROW, OutT>(p, w); });
+    // an array for each stage: the compiler then knows that reading one need
+    // not wait for the loads into another
+    constexpr int BYTES = NW * kUnit<RB, CB>;
+    __shared__ __attribute__((aligned(1024))) uint8_t s0[BYTES], s1[BYTES], s2[D > 2 ? BYTES : 1024], s3[D > 2 ? BYTES : 1024];
+    walk(p.tiles, [&](unsigned w) { stream_tile<RB, CB, NW, D, BROW, OutT>(p, w, s0, s1, s2, s3); });
 }
 
 // ------------------------------------------------------------------ a few tokens, quantized on the way
 //
-// Up to 16 rows of x in 32 or 16 bits, one launch: a block's scale needs its 128
-// channels alone, so a wave quantizes each unit of K that it takes itself, in
-// registers, where lane (l16, lq) loads what it needs of row l16 for the matrix
-// instruction (the 16-byte chunks lq and lq + 4 of the unit's codes); the block's
-// maximum crosses the four lanes of a row.  The weights come as in the streamed
-// product, 16 CB columns a workgroup.
+// Tiles of 16 RB rows of x in 32 or 16 bits, one launch: a block's scale needs its
+// 128 channels alone, so a wave quantizes each unit of K that it takes itself, in
+// registers, where lane (l16, lq) loads what it needs of its rows RB l16 .. for the
+// matrix instruction (the 16-byte chunks lq and lq + 4 of the unit's codes); the
+// block's maximum crosses the four lanes of a row.  The weights come as in the
+// streamed product, 16 CB columns a workgroup.
 // Lanes l16, 16 + l16, 32 + l16, 48 + l16 all get the largest of their four values.
 template <typename T>
 __device__ __forceinline__ uint32_t largest_of_rows(uint32_t v) {
@@ -650,35 +659,40 @@ __device__ __forceinline__ uint32_t largest_of_rows(uint32_t v) {
     return larger<T>(uint32_t(b[0]), uint32_t(b[1]));
 }
 
-template <typename X, int CB, int NW, int D, typename OutT>
+template <typename X, int RB, int CB, int NW, int D, typename OutT>
 __global__ __launch_bounds__(NW * 64) void fp8_few_kernel(const X* __restrict__ xs, F8Params p) {
-    constexpr int TN = 16 * CB, UNIT = TN * QB, PER = UNIT / 1024;
-    constexpr int XL = 4 * (sizeof(X) / 2), OPS = PER + XL;        // vector-memory operations of a stage
-    static_assert(D == 4 && OPS * (D - 1) < 63, "ring depth");
-    __shared__ __attribute__((aligned(1024))) uint8_t s0[NW * UNIT], s1[NW * UNIT], s2[NW * UNIT], s3[NW * UNIT];
+    constexpr int TM = 16 * RB, TN = 16 * CB, UNIT = TN * QB, PER = UNIT / 1024;
+    constexpr int XL = RB * 4 * (sizeof(X) / 2), OPS = PER + XL;   // vector-memory operations of a stage
+    static_assert((D == 2 || D == 4) && OPS * (D - 1) < 63, "ring depth");
+    constexpr int SUMS = RB * CB * 1024;                           // bytes of a wave's sums
+    constexpr int STAGE = UNIT > SUMS ? UNIT : SUMS;
+    __shared__ __attribute__((aligned(1024))) uint8_t s0[NW * STAGE], s1[NW * UNIT];
+    __shared__ __attribute__((aligned(1024))) uint8_t s2[D > 2 ? NW * UNIT : 1024], s3[D > 2 ? NW * UNIT : 1024];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int l16 = lane & 15, lq = lane >> 4;
-    GFG_LDS uint8_t* const ring[D] = {(GFG_LDS uint8_t*)s0 + wave * UNIT, (GFG_LDS uint8_t*)s1 + wave * UNIT,
-                                      (GFG_LDS uint8_t*)s2 + wave * UNIT, (GFG_LDS uint8_t*)s3 + wave * UNIT};
-    const int M = int(p.rows), n0 = int(blockIdx.x) * TN, ncols = min(TN, p.N - n0);
-    const auto rx = make_rsrc(xs, uint32_t(M) * uint32_t(p.K) * uint32_t(sizeof(X)));
+    GFG_LDS uint8_t* const ring[4] = {(GFG_LDS uint8_t*)s0 + wave * STAGE, (GFG_LDS uint8_t*)s1 + wave * UNIT,
+                                      (GFG_LDS uint8_t*)s2 + (D > 2 ? wave * UNIT : 0), (GFG_LDS uint8_t*)s3 + (D > 2 ? wave * UNIT : 0)};
+    const int mt = int(blockIdx.x % unsigned(p.m_tiles)), n0 = int(blockIdx.x / unsigned(p.m_tiles)) * TN, ncols = min(TN, p.N - n0);
+    const int M = int(p.rows), row0 = mt * TM, lim = min(TM, M - row0);
+    const auto rx = make_rsrc(xs + int64_t(row0) * p.K, uint32_t(lim) * uint32_t(p.K) * uint32_t(sizeof(X)));
     const auto rb = make_rsrc(p.b + int64_t(n0) * p.K, uint32_t(ncols) * uint32_t(p.K));
-    // (rows past M repeat the last one and are not stored)
-    const uint32_t xrow = uint32_t(min(l16, M - 1)) * uint32_t(p.K);
     const uint8_t* const sb_row = uniform_ptr(p.b_scale + int64_t(n0 / QB) * p.KB);
-    Eight<X> x[D][4];
+    Eight<X> x[D][RB][4];
     uint32_t sb[D];
     auto load = [&](int d, int kb) {
         __builtin_amdgcn_sched_barrier(0);
         sb[d] = uint32_t(load_scale_word(sb_row, min(kb, p.KB - 1)));
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int k = kb * QB + 64 * h + 16 * lq;
-            const uint32_t at = k < p.K ? (xrow + uint32_t(k)) * uint32_t(sizeof(X)) : kOutside;
-            x[d][2 * h] = load8<X>(rx, at);
-            x[d][2 * h + 1] = load8<X>(rx, at + 8 * sizeof(X));
-        }
+        for (int f = 0; f < RB; ++f)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                // (rows past M repeat the last one and are not stored)
+                const int k = kb * QB + 64 * h + 16 * lq;
+                const uint32_t at = k < p.K ? (uint32_t(min(RB * l16 + f, lim - 1)) * uint32_t(p.K) + uint32_t(k)) * uint32_t(sizeof(X)) : kOutside;
+                x[d][f][2 * h] = load8<X>(rx, at);
+                x[d][f][2 * h + 1] = load8<X>(rx, at + 8 * sizeof(X));
+            }
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
@@ -689,28 +703,34 @@ __global__ __launch_bounds__(NW * 64) void fp8_few_kernel(const X* __restrict__ 
         }
         __builtin_amdgcn_sched_barrier(0);
     };
-    v4f acc[CB] = {};
+    v4f acc[RB][CB] = {};
     auto step = [&](int d, int kb, auto ops) {
         __builtin_amdgcn_sched_barrier(0);
         GFG_WAITCNT((D - 1) * decltype(ops)::value, 15);
         __builtin_amdgcn_sched_barrier(0);
-        uint32_t m = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) m = larger<X>(m, largest(x[d][i]));
-        const uint32_t a_byte = scale_byte_of(as_f32<X>(largest_of_rows<X>(m)));
-        v8i af;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const u32x2 w = encode(x[d][i], a_byte);
-            af[2 * i] = int(w[0]);
-            af[2 * i + 1] = int(w[1]);
-        }
-        const int b_byte = scale_byte(int(sb[d]), sb_row, kb);
+        v8i bf[CB];
 #pragma unroll
         for (int c = 0; c < CB; ++c) {
             const int row = Rows<CB>::swap(CB * l16 + c), key = Rows<CB>::key(row);
             auto part = [&](int ch) { return *reinterpret_cast<GFG_LDS u32x4*>(ring[d] + row * QB + ((ch ^ key) << 4)); };
-            acc[c] = mfma_at<0, 0>(join(part(lq), part(lq + 4)), af, acc[c], b_byte, int(a_byte));
+            bf[c] = join(part(lq), part(lq + 4));
+        }
+        const int b_byte = scale_byte(int(sb[d]), sb_row, kb);
+#pragma unroll
+        for (int f = 0; f < RB; ++f) {
+            uint32_t m = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) m = larger<X>(m, largest(x[d][f][i]));
+            const uint32_t a_byte = scale_byte_of(as_f32<X>(largest_of_rows<X>(m)));
+            v8i af;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const u32x2 w = encode(x[d][f][i], a_byte);
+                af[2 * i] = int(w[0]);
+                af[2 * i + 1] = int(w[1]);
+            }
+#pragma unroll
+            for (int c = 0; c < CB; ++c) acc[f][c] = mfma_at<0, 0>(bf[c], af, acc[f][c], b_byte, int(a_byte));
         }
         load(d, kb + D * NW);                      // past K: zeros
     };
@@ -725,30 +745,53 @@ __global__ __launch_bounds__(NW * 64) void fp8_few_kernel(const X* __restrict__ 
     }
     if (kb < p.KB) {
         step(0, kb, least);
-        if (kb + NW < p.KB) {
-            step(1, kb + NW, least);
-            if (kb + 2 * NW < p.KB) step(2, kb + 2 * NW, least);
+        if constexpr (D > 2) {
+            if (kb + NW < p.KB) {
+                step(1, kb + NW, least);
+                if (kb + 2 * NW < p.KB) step(2, kb + 2 * NW, least);
+            }
         }
     }
     GFG_WAITCNT(0, 15);                            // the last loads land before the workgroup ends
-    static_assert(CB * 1024 <= UNIT, "the sums fit a stage");
-    auto sums = [&](int v, int i) -> GFG_LDS v4f& { return reinterpret_cast<GFG_LDS v4f*>((GFG_LDS uint8_t*)s0 + v * UNIT)[i * 64 + lane]; };
+    // a wave's sums go where its first stage was; wave f sums and stores the rows of fragment f
+    auto sums = [&](int v, int i) -> GFG_LDS v4f& { return reinterpret_cast<GFG_LDS v4f*>((GFG_LDS uint8_t*)s0 + v * STAGE)[i * 64 + lane]; };
 #pragma unroll
-    for (int c = 0; c < CB; ++c) sums(wave, c) = acc[c];
+    for (int f = 0; f < RB; ++f)
+#pragma unroll
+        for (int c = 0; c < CB; ++c) sums(wave, f * CB + c) = acc[f][c];
     __syncthreads();
-    if (wave || l16 >= M) return;
+    static_assert(RB <= NW, "a wave for each row fragment");
+    const int r = RB * l16 + wave;
+    if (wave >= RB || r >= lim) return;
     const int n = n0 + 4 * CB * lq;
     float v[4 * CB], bias[4 * CB];
     load_bias(bias, p, n);
 #pragma unroll
     for (int c = 0; c < CB; ++c) {
-        v4f t = sums(0, c);
+        v4f t = sums(0, wave * CB + c);
 #pragma unroll
-        for (int u = 1; u < NW; ++u) t += sums(u, c);
+        for (int u = 1; u < NW; ++u) t += sums(u, wave * CB + c);
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[CB * i + c] = t[i] + bias[CB * i + c];
     }
-    store_row<4 * CB>(static_cast<OutT*>(p.d) + int64_t(l16) * p.N, n, p.N, v, 0);
+    store_row<4 * CB>(static_cast<OutT*>(p.d) + int64_t(row0 + r) * p.N, n, p.N, v, 0);
+}
+
+// The products of a small backward pass and its bias gradient in one launch: the
+// tiles of dx, then those of dW, then the columns.  Up to four tiles a CU (the whole
+// pass with its quantizers, us, tokens x N x K, one launch and three: 16 x 512 x 512
+// 9.1, 12.9; 300 x 528 x 1040, 891 tiles, 12.8, 16.0; 1024 x 512 x 512, 768 tiles, 14.4,
+// 16.2; but 2048 x 256 x 512, 1152 tiles, 17.0, 16.0; 1024 x 1024 x 1024, 2048 tiles,
+// 23.5, 20.0).  A workgroup has one tile of its own shape, so not under a grid limit
+// or a set shape; the gradient of one token has too few rows for these tiles.
+template <typename OutX, typename OutW>
+__global__ __launch_bounds__(256) void fp8_backward_kernel(F8Params dx, F8Params dw, SumJob db) {
+    constexpr int BYTES = 4 * kUnit<2, 2>;
+    __shared__ __attribute__((aligned(1024))) uint8_t s0[BYTES], s1[BYTES], none[1024];
+    const unsigned w = blockIdx.x;
+    if (w < dx.tiles) stream_tile<2, 2, 4, 2, false, OutX>(dx, w, s0, s1, none, none);
+    else if (w < dx.tiles + dw.tiles) stream_tile<2, 2, 4, 2, true, OutW>(dw, w - dx.tiles, s0, s1, none, none);
+    else column_sums(db, int(w - dx.tiles - dw.tiles));
 }
 
 // Workgroups of a launch over p.tiles tiles: one for each, or as many as the
@@ -875,32 +918,63 @@ int quantize_rows(const void* x, int32_t in_dtype, uint8_t* q, uint8_t* scale, i
     return launch_quant_rows<_Float16>(x, q, scale, R, C, ld, s);
 }
 
-// What goes this way: up to 16 rows whose elements every workgroup can load again
-// for less than a launch (cold weights, us, one launch and two: 1 x 7168 x 2304
-// 6.5, 7.8; 16 x 7168 x 2304 7.2, 8.1; 16 x 2048 x 7168 11.1, 11.5; 4 x 2048 x 16384
-// 14.0, 16.2; but 16 x 2048 x 16384 20.3, 18.5; 16 x 300 x 16384 18.9, 12.8).  A
-// workgroup has one tile, so not under a grid limit.  Tiles of 16 columns on eight
-// waves where they do not outnumber the CUs, else 32 on four (16 and 32: 1 x 2048 x
-// 7168 8.0, 9.4; 1 x 4096 x 4096 7.0, 7.3; 1 x 7168 x 2304 7.1, 6.5; 1 x 28672 x 4096
-// 32.2, 27.7).
-constexpr int64_t kFewTokens = 16, kFewElements = 1 << 17;
+// What goes this way (cold weights, us in a graph, one launch and two): rows whose
+// elements every workgroup can load again for less than a launch.
+//  * up to 16 rows: 1 x 7168 x 2304 6.5, 7.8; 16 x 7168 x 2304 7.2, 8.1; 16 x 2048 x
+//    7168 11.1, 11.5; 4 x 2048 x 16384 14.0, 16.2; but 16 x 2048 x 16384 20.3, 18.5;
+//    16 x 300 x 16384 18.9, 12.8;
+//  * more rows, in tiles of 32 x 32, with up to three units a wave (a lane's loads
+//    are 16 bytes of a row each, which costs more than the launch soon): bf16 77 x
+//    1003 x 1072 6.1, 6.7; 300 x 528 x 1040 6.1, 6.9; 512 x 512 x 512 4.5, 6.1; but 32 x
+//    7168 x 2304 10.0, 8.8; f32 128 x 512 x 512 4.7, 5.8, but 77 x 1003 x 1072 8.3, 6.7;
+//    and up to two tiles a CU: 128 x 4096 x 512 6.4, 7.3, but 256 x 4096 x 512 10.6, 7.0.
+// A workgroup has one tile of its own shape, so not under a grid limit or a set shape.
+bool few(const F8Params& p, int size, int cus) {
+    if (grid_limit() != 0 || tile_shape_choice() != GFG_TILE_AUTO) return false;
+    if (p.rows <= 16) return p.rows * p.K <= 1 << 17;
+    return p.KB <= (size == 2 ? 10 : 5) && (p.rows + 31) / 32 * ((p.N + 31) / 32) <= 2 * cus;
+}
 
-template <typename X, int CB, int NW>
-int launch_few_on(const void* x, const F8Params& p, int out_dtype, hipStream_t s) {
-    const dim3 grid(unsigned((p.N + 16 * CB - 1) / (16 * CB))), block(NW * 64);
+template <typename X, int RB, int CB, int NW, int D>
+int launch_few_on(const void* x, F8Params p, int out_dtype, hipStream_t s) {
+    p.m_tiles = int((p.rows + 16 * RB - 1) / (16 * RB));
+    const dim3 grid(unsigned((p.N + 16 * CB - 1) / (16 * CB) * p.m_tiles)), block(NW * 64);
     if (out_dtype == GFG_OUT_BF16)
-        hipLaunchKernelGGL((fp8_few_kernel<X, CB, NW, 4, __bf16>), grid, block, 0, s, static_cast<const X*>(x), p);
+        hipLaunchKernelGGL((fp8_few_kernel<X, RB, CB, NW, D, __bf16>), grid, block, 0, s, static_cast<const X*>(x), p);
     else
-        hipLaunchKernelGGL((fp8_few_kernel<X, CB, NW, 4, _Float16>), grid, block, 0, s, static_cast<const X*>(x), p);
+        hipLaunchKernelGGL((fp8_few_kernel<X, RB, CB, NW, D, _Float16>), grid, block, 0, s, static_cast<const X*>(x), p);
     return launched();
 }
 
+// Up to 16 rows: 16 columns a workgroup on eight waves where those do not outnumber
+// the CUs, else 32 on four (16 and 32: 1 x 2048 x 7168 8.0, 9.4; 1 x 4096 x 4096 7.0,
+// 7.3; 1 x 7168 x 2304 7.1, 6.5; 1 x 28672 x 4096 32.2, 27.7).
 template <typename X>
-int launch_few(const void* x, const F8Params& p, int out_dtype, hipStream_t s) {
-    int cus = 0;
-    if (int rc = device_cus(&cus)) return rc;
-    if (p.N <= 16 * cus) return launch_few_on<X, 1, 8>(x, p, out_dtype, s);
-    return launch_few_on<X, 2, 4>(x, p, out_dtype, s);
+int launch_few(const void* x, const F8Params& p, int cus, int out_dtype, hipStream_t s) {
+    if (p.rows > 16) return launch_few_on<X, 2, 2, 4, sizeof(X) == 4 ? 2 : 4>(x, p, out_dtype, s);
+    if (p.N <= 16 * cus) return launch_few_on<X, 1, 1, 8, 4>(x, p, out_dtype, s);
+    return launch_few_on<X, 1, 2, 4, 4>(x, p, out_dtype, s);
+}
+
+// Tiles of 32 x 32 of a product, which are set in it.
+int64_t few_tiles(F8Params* p) {
+    p->m_tiles = int((p->rows + 31) / 32);
+    const int64_t tiles = int64_t(p->m_tiles) * ((p->N + 31) / 32);
+    p->tiles = unsigned(tiles < (1 << 30) ? tiles : 1 << 30);
+    return tiles;
+}
+
+int launch_pair(const F8Params& dx, const F8Params& dw, const SumJob& db, unsigned db_groups, int dx_dtype, int dw_dtype, hipStream_t s) {
+    auto go = [&](auto* kernel) { hipLaunchKernelGGL(kernel, dim3(dx.tiles + dw.tiles + db_groups), dim3(256), 0, s, dx, dw, db); };
+    auto with = [&](auto x) {
+        typedef decltype(x) X;
+        if (dw_dtype == GFG_OUT_BF16) go(fp8_backward_kernel<X, __bf16>);
+        else if (dw_dtype == GFG_OUT_F16) go(fp8_backward_kernel<X, _Float16>);
+        else go(fp8_backward_kernel<X, float>);
+    };
+    if (dx_dtype == GFG_OUT_BF16) with(__bf16{});
+    else with(_Float16{});
+    return launched();
 }
 
 TileJob job(const void* x, int64_t R, int64_t C, int64_t G) {
@@ -1062,11 +1136,13 @@ extern "C" int fp8_linear(const void* x, int32_t in_dtype, const void* b, const 
     if (int rc = check_workspace(fn, workspace, workspace_bytes, fp8_linear_workspace_bytes(M, K))) return rc;
     hipStream_t s = static_cast<hipStream_t>(stream);
     uint8_t *q = static_cast<uint8_t*>(workspace), *scale = q + M * K;
-    if (M <= kFewTokens && M * K <= kFewElements && grid_limit() == 0) {
-        const F8Params p = product(nullptr, nullptr, 0, b, b_scale, 0, bias, d, M, N, K);
-        if (in_dtype == GFG_IN_F32) return launch_few<float>(x, p, out_dtype, s);
-        if (in_dtype == GFG_IN_BF16) return launch_few<__bf16>(x, p, out_dtype, s);
-        return launch_few<_Float16>(x, p, out_dtype, s);
+    int cus = 0;
+    if (int rc = device_cus(&cus)) return rc;
+    if (const F8Params p = product(nullptr, nullptr, 0, b, b_scale, 0, bias, d, M, N, K);
+        few(p, in_dtype == GFG_IN_F32 ? 4 : 2, cus)) {
+        if (in_dtype == GFG_IN_F32) return launch_few<float>(x, p, cus, out_dtype, s);
+        if (in_dtype == GFG_IN_BF16) return launch_few<__bf16>(x, p, cus, out_dtype, s);
+        return launch_few<_Float16>(x, p, cus, out_dtype, s);
     }
     const int64_t ld = up(M, 4);
     if (int rc = quantize_rows(x, in_dtype, q, scale, M, K, ld, s)) return rc;
@@ -1136,14 +1212,20 @@ extern "C" int fp8_linear_backward(const void* dy, const void* x, int32_t in_dty
             hipLaunchKernelGGL((quant_tiles_kernel<decltype(t)>), dim3(a.tiles + b.tiles), dim3(256), 0, s, a, b);
         }))
         return rc;
+    const SumJob db{sums, dbias, at.MB, int(N), accumulate};
+    const unsigned db_groups = dbias ? unsigned((N + 15) / 16) : 0u;
+    F8Params px = product(ws + at.q, ws + at.qs, at.ldm, b_t, b_t_scale, 0, nullptr, dx, M, K, N);
+    F8Params pw = product(ws + at.yt, ws + at.yts, at.ldn, ws + at.xt, ws + at.xts, at.ldk, nullptr, dw, N, K, at.Mp);
+    pw.accumulate = accumulate;
+    int cus = 0;
+    if (int rc = device_cus(&cus)) return rc;
+    if (dx && dw && M >= 2 && grid_limit() == 0 && tile_shape_choice() == GFG_TILE_AUTO && few_tiles(&px) + few_tiles(&pw) <= 4 * cus)
+        return launch_pair(px, pw, db, db_groups, dx_dtype, dw_dtype, s);
     if (dbias) {
-        hipLaunchKernelGGL(column_sums_kernel, dim3(unsigned((N + 15) / 16)), dim3(256), 0, s, sums, dbias, at.MB, int(N), accumulate);
+        hipLaunchKernelGGL(column_sums_kernel, dim3(db_groups), dim3(256), 0, s, db);
         if (int rc = launched()) return rc;
     }
     if (dx)
-        if (int rc = launch_product<false>(fn, product(ws + at.q, ws + at.qs, at.ldm, b_t, b_t_scale, 0, nullptr, dx, M, K, N), dx_dtype, s)) return rc;
-    if (!dw) return GFG_OK;
-    F8Params p = product(ws + at.yt, ws + at.yts, at.ldn, ws + at.xt, ws + at.xts, at.ldk, nullptr, dw, N, K, at.Mp);
-    p.accumulate = accumulate;
-    return launch_product<true>(fn, p, dw_dtype, s);
+        if (int rc = launch_product<false>(fn, px, dx_dtype, s)) return rc;
+    return dw ? launch_product<true>(fn, pw, dw_dtype, s) : GFG_OK;
 }

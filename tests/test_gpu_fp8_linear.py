@@ -248,8 +248,9 @@ def test_backward_of_whole_numbers_is_exact(M, N, K, accumulate):
     rng = np.random.default_rng(M * 5 + N)
     dy, x, w = operands(rng, M, N, K, torch.bfloat16, lambda *shape: whole(rng, *shape))
     _, _, qt, st = gfg.fp8_quantize_weight_device(dev(w), transposed=True)
-    for shape in (gfg.TILE_AUTO, gfg.TILE_128x256, gfg.TILE_256x256):
+    for shape, limit in ((gfg.TILE_AUTO, 0), (gfg.TILE_AUTO, 1 << 20), (gfg.TILE_AUTO, 5), (gfg.TILE_128x256, 0), (gfg.TILE_256x256, 0)):
         gfg.set_tile_shape(shape)
+        gfg.set_grid_limit(limit)
         dx = torch.empty(M, K, dtype=torch.float16, device="cuda")
         dw, db = torch.full((N, K), 5.0, device="cuda"), torch.full((N,), -3.0, device="cuda")
         gfg.fp8_linear_backward(dev(dy, torch.bfloat16), dev(x, torch.bfloat16), qt, st, dx=dx, dw=dw, dbias=db, accumulate=accumulate)
