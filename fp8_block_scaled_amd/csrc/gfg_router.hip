@@ -112,6 +112,13 @@ __device__ __forceinline__ bool group_any(bool b, int lane) {
     if constexpr (LPT == 64) return all != 0;
     else return ((all >> (lane & ~(LPT - 1))) & ((uint64_t(1) << LPT) - 1)) != 0;
 }
+// The first of the token's lanes with b (where there is none, any).
+template <int LPT>
+__device__ __forceinline__ int first_of(bool b, int lane) {
+    const int base = lane & ~(LPT - 1);
+    const uint64_t mine = (__ballot(b) >> base) << base;
+    return mine ? int(__builtin_ctzll(mine)) : lane;
+}
 
 // 1 / v to one unit of the last place; 0 for 0.
 __device__ __forceinline__ float reciprocal(float v) { return v > 0.0f ? __builtin_amdgcn_rcpf(v) : 0.0f; }
@@ -479,12 +486,14 @@ __global__ __launch_bounds__(256) void router_backward_kernel(RouterBack p) {
         }
         float g = dw_in, of_softmax = 0.0f;
         if (p.dweights) {
-            float mean = group_sum<LPT>(dw_in * sc);
             if (p.renorm) {
-                const float inv = reciprocal(group_sum<LPT>(sc));
-                g = (dw_in - mean * inv) * inv;
-            } else {
-                of_softmax = SIGMOID ? 0.0f : mean;            // (renormalized, this sum is 0)
+                // dw less the first choice's, which changes nothing but that equal ones, a
+                // single one above all, give 0 and not the rest of two roundings
+                const int first_choice = first_of<LPT>(chosen, lane);
+                const float less = chosen ? dw_in - __shfl(dw_in, first_choice, 64) : 0.0f, inv = reciprocal(group_sum<LPT>(sc));
+                g = (less - group_sum<LPT>(less * sc) * inv) * inv;
+            } else if (!SIGMOID) {
+                of_softmax = group_sum<LPT>(dw_in * sc);       // (renormalized, this sum is 0)
             }
             g = chosen ? g * (SIGMOID ? ds : sc) : 0.0f;
         }

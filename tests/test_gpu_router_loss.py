@@ -134,6 +134,26 @@ def test_masked_logits(score):
         assert not bool(d[0].any()) and not bool(d[2].any()) and not bool(d[1, :11].any())
 
 
+@pytest.mark.parametrize("E,k", [(8, 1), (64, 4), (100, 9), (300, 3), (600, 40)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_equal_gradients_of_normalized_weights_give_zero(E, k, score):
+    """Normalized weights add up to one whatever the logits, so equal gradients of them (one choice above all) have no
+    gradient, exactly, and nothing of it is left beside a far smaller one of the loss."""
+    torch.manual_seed(E)
+    l = torch.randn(200, E, device="cuda") * 3
+    ids = torch.topk(l, k)[1].int()
+    ids[::3, 0] = -1                                       # padding before the choices that are there
+    dw = torch.randn(200, 1, device="cuda").expand(200, k).contiguous()
+    d = torch.full_like(l, 9.0)
+    gfg.moe_router_backward(l, ids, d, dweights=dw, score=score, renormalize=True)
+    assert not bool(d.any())
+    factors, e = torch.randn(1, E + 1, device="cuda") * 1e-9, torch.empty_like(l)
+    one = torch.ones((), device="cuda")
+    gfg.moe_router_backward(l, ids, d, dweights=dw, score=score, renormalize=True, factors=factors, dloss=one)
+    gfg.moe_router_backward(l, ids, e, score=score, factors=factors, dloss=one)
+    assert torch.equal(d, e) and bool(d.any())
+
+
 def test_gradient_against_differences():
     """Differences of the calls themselves: moe_topk's weights and the loss, along one direction, step 2^-7 (fp32 noise of
     2^-21 over the step for each of T k weights, and the change of the difference between two steps)."""
