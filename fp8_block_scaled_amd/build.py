@@ -1,19 +1,24 @@
-"""Build libgfg.so (HIP kernels for gfx950 + host quantizers) in-tree with hipcc.
+"""Build libgfg.so (HIP kernels for gfx950 + host quantizers) in-tree with hipcc, and,
+where torch is installed, _args.so (the torch-facing calls' argument checks).
 
-    python -m fp8_block_scaled_amd.build          # writes fp8_block_scaled_amd/libgfg.so
+    python -m fp8_block_scaled_amd.build          # writes fp8_block_scaled_amd/libgfg.so and _args.so
 """
 from __future__ import annotations
 
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libgfg.so")
+ARGS = os.path.join(PKG, "_args.so")
 ARCH = "gfx950"
 
 
@@ -35,6 +40,17 @@ HIP_SOURCES = ["gfg_gemm.hip", "gfg_gemm256.hip", "gfg_quant.hip", "gfg_int8.hip
                "gfg_fp8_dense256.hip", "gfg_norm.hip", "gfg_router.hip", "gfg_ceiling.hip"]
 
 
+def _args_step(out: str):
+    """The command that compiles gfg_args.cpp against the installed torch; None without one."""
+    if importlib.util.find_spec("torch") is None:
+        return None
+    import torch
+    base = os.path.join(os.path.dirname(torch.__file__), "")
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            "-isystem", base + "include", "-isystem", base + "include/torch/csrc/api/include", "-I", sysconfig.get_paths()["include"],
+            os.path.join(CSRC, "gfg_args.cpp"), "-o", out, "-L", base + "lib", "-ltorch_python", "-ltorch_cpu", "-lc10"]
+
+
 def build(verbose: bool = False) -> str:
     hipcc = _hipcc()
     out_dir = os.path.join(ROOT, "_build")
@@ -46,14 +62,23 @@ def build(verbose: bool = False) -> str:
                   "-c", os.path.join(CSRC, "gfg_host.cpp"), "-o", o("gfg_host.o")])
     objs = [o(src.replace(".hip", ".o")) for src in HIP_SOURCES] + [o("gfg_host.o")]
     tmp = LIB + ".tmp"
-    steps.append([hipcc, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-pthread", *objs, "-o", tmp])
-    for cmd in steps:
+    args = _args_step(ARGS + ".tmp")
+    if args:
+        steps.append(args)
+
+    def run(cmd):
         if verbose:
             print(" ".join(cmd), flush=True)
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"build step failed ({r.returncode}): {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+
+    with ThreadPoolExecutor(4) as pool:                    # (a compiler holds up to a few GiB)
+        list(pool.map(run, steps))
+    run([hipcc, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-pthread", *objs, "-o", tmp])
     os.replace(tmp, LIB)
+    if args:
+        os.replace(ARGS + ".tmp", ARGS)
     return LIB
 
 

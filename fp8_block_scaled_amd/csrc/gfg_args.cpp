@@ -1,0 +1,52 @@
+// Python module `_args`: the checks of a tensor argument and its address in one
+// native call, a fifth of the time that the same questions take one by one in
+// Python (0.08 and 0.4 us a tensor; a call of a layer has four to fourteen, and a
+// launch takes 2 us).  It answers only for tensors that pass; every other one is
+// looked at again in Python, which words the error.
+#include <Python.h>
+#include <torch/csrc/Dtype.h>
+#include <torch/csrc/DynamicTypes.h>
+#include <torch/csrc/autograd/python_variable.h>
+
+namespace {
+
+// address(tensor, dtypes, shape, device index): the address of a dense tensor on
+// that GPU, of that shape (a tuple) and one of the types; None for anything else.
+PyObject* address(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    if (n != 4) {
+        PyErr_SetString(PyExc_TypeError, "address(tensor, dtypes, shape, device index)");
+        return nullptr;
+    }
+    try {
+        PyObject* const shape = args[2];
+        if (!THPVariable_Check(args[0]) || !PyTuple_Check(shape) || !PyLong_Check(args[3])) Py_RETURN_NONE;
+        const at::Tensor& t = THPVariable_Unpack(args[0]);
+        if (!t.defined() || !t.is_cuda() || t.get_device() != PyLong_AsLongLong(args[3])) Py_RETURN_NONE;
+        const at::IntArrayRef sizes = t.sizes();
+        if (Py_ssize_t(sizes.size()) != PyTuple_GET_SIZE(shape)) Py_RETURN_NONE;
+        for (size_t i = 0; i < sizes.size(); ++i) {
+            PyObject* const s = PyTuple_GET_ITEM(shape, i);
+            if (!PyLong_Check(s) || PyLong_AsLongLong(s) != sizes[i]) {
+                PyErr_Clear();                             // (a number past 64 bits)
+                Py_RETURN_NONE;
+            }
+        }
+        const int known = PySequence_Contains(args[1], reinterpret_cast<PyObject*>(torch::getTHPDtype(t.scalar_type())));
+        if (known < 0) return nullptr;
+        if (!known || !t.is_contiguous()) Py_RETURN_NONE;
+        return PyLong_FromVoidPtr(t.data_ptr());
+    } catch (...) {                                        // (a tensor without storage, for one)
+        PyErr_Clear();
+        Py_RETURN_NONE;
+    }
+}
+
+PyMethodDef methods[] = {
+    {"address", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(address)), METH_FASTCALL,
+     "address(tensor, dtypes, shape, device index) -> int or None"},
+    {nullptr, nullptr, 0, nullptr}};
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_args", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit__args() { return PyModule_Create(&module); }

@@ -14,6 +14,12 @@ import torch
 
 from . import IN_BF16, IN_F16, IN_F32, OUT_BF16, OUT_F16, _check, _check_stream, _on, load_library
 
+try:
+    from ._args import address as _address
+except ImportError:                                        # built for another torch, or without one: Python answers
+    def _address(t, dtypes, shape, index):
+        return None
+
 _IN = {torch.float32: IN_F32, torch.bfloat16: IN_BF16, torch.float16: IN_F16}
 _OUT = {torch.bfloat16: OUT_BF16, torch.float16: OUT_F16}
 _SCORE = {"softmax": 0, "sigmoid": 1}
@@ -23,6 +29,9 @@ _F8 = (torch.float8_e4m3fn, torch.uint8)
 
 def _ptr(t, name, dtypes, shape, device):
     """The address of a dense GPU tensor of one of the types, of that shape."""
+    at = _address(t, dtypes, shape, device.index)
+    if at is not None:
+        return at
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype in dtypes and t.shape == shape and t.device == device and t.is_contiguous():
