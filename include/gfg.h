@@ -454,7 +454,8 @@ GFG_API int moe_int8_layer(const void* x, int32_t dtype, const int32_t* topk_ids
  * fp8_linear: the same from x [M][K] (GFG_IN_F32, _BF16 or _F16), which it
  *   quantizes in blocks of 1 x 128 into the workspace (at least
  *   fp8_linear_workspace_bytes(M, K) bytes of device memory, 16-byte aligned,
- *   uninitialized; a call leaves nothing in it for the next).
+ *   uninitialized; a call leaves nothing in it for the next).  Few or short rows
+ *   are quantized inside the product's launch, others in one before it.
  *
  * The sums are fp32 sums of the matrix instruction's products of 128 k, inside
  * which a product 2^14 times smaller than another of its group of 16 may be
@@ -569,7 +570,8 @@ GFG_API int residual_norm_backward(const void* dout, const void* dnormed, const 
  *   P_e = mean of p_e: the softmax of the logits, or the sigmoids over their sum
  *   loss = 1/S sum_s (alpha * sum_e f_e P_e + z * mean(logsumexp(logits)^2))
  *
- * Logits of -infinity or NaN are of masked experts (p = 0).  A sequence without
+ * Logits of -infinity or NaN are of masked experts (p = 0), and so, in effect, is a
+ * sigmoid below fp32's normal range (a logit below about -87).  A sequence without
  * such tokens adds 0.
  *
  *   logits [T][E] (GFG_IN_*) ; ids [T][k] int32 (moe_topk's) ; seq_offsets [S+1]
@@ -588,7 +590,8 @@ GFG_API int residual_norm_backward(const void* dout, const void* dnormed, const 
  * and S as above) and dloss [1] float, both or neither NULL.  Ids outside [0, E)
  * have no weight; an id that stands twice has both.  dlogits is 0 where p is.
  *
- * Counts are exact, the sums fp32 in a fixed order: two calls give the same bytes.
+ * Equal dweights of renormalized weights (a single one above all) have a gradient
+ * of exactly 0.  Counts are exact, the sums fp32 in a fixed order: two calls give the same bytes.
  * Sizes: T >= 0 (0: loss and counts are 0) and below 2^31, E in [1, 1024],
  * k in [1, 64], S in [1, 65535] (else GFG_EUNSUPPORTED).
  */
@@ -634,16 +637,22 @@ GFG_API int moe_router_backward(const void* logits, int32_t in_dtype, const int3
  * follow the setting too: GFG_TILE_AUTO takes their large tiles (256 or 192 rows
  * by 256 columns) where tiles of 128 x 128 would outnumber the CUs,
  * GFG_TILE_128x256 the smaller ones, GFG_TILE_256x256 the large ones (N at most
- * 2^22); their results do not depend on it.
+ * 2^22); their results do not depend on it.  The dense FP8 products follow it in
+ * the same way: large tiles (256 x 256, an operand of at least 4 rows) where tiles of
+ * 128 x 128 would outnumber the CUs; GFG_TILE_256x256 needs N at most 2^21 (2^20
+ * with 32-bit outputs), else GFG_EUNSUPPORTED; with a set shape fp8_linear and
+ * fp8_linear_backward launch their quantizers and products apart.
  *
  * grouped_fp8_set_grid_limit: at most max_workgroups workgroups per GEMM
  * launch.  0, the default, is no limit: one per CU, fewer when there are fewer
  * tiles (the int8 products' smaller tiles: one per tile).  The grid of a GEMM
  * launch is then rounded up to a multiple of num_xcd.  Each workgroup walks
  * more tiles; the results do not change.  The limit covers the FP8, MX and int8
- * products (int8_linear of a few tokens then takes two launches) and, not
+ * products (int8_linear and fp8_linear of a few tokens and a small
+ * fp8_linear_backward then take a launch for each product) and, not
  * rounded up, the expert layer's two products, whose fp32 sums it may reorder;
- * not the quantizers, the router and the layer's last sum over a token's pairs.
+ * not the quantizers, the router and its training, the norms and the layer's last
+ * sum over a token's pairs.
  * Negative: GFG_EINVAL.
  */
 enum gfg_tile_shape { GFG_TILE_AUTO = 0, GFG_TILE_128x256 = 1, GFG_TILE_256x256 = 2 };
