@@ -22,6 +22,12 @@
 // window, where the hardware returns zeros, and K is rounded up to an even
 // number of steps.  A lane's four scale bytes are one load at any address, which
 // starts lower for rows past the end and is shifted down.
+//
+// Measured: 4096 x 4096 x 16384 194-240 us by run (2290-2830 TFLOP/s), matrix pipes busy
+// 62% of the cycles at 2.18 GHz, waves waiting 18% of theirs, the rest the wave's own
+// LDS reads, loads and barriers; a step takes 1.5 us and more.  4096 x
+// 7168 x 2304 70 us (448 tiles, 1.75 rounds), its weight's gradient 64, its tokens'
+// 88 (144 tiles on 256 CUs).
 #include <hip/hip_runtime.h>
 
 #include <cstdint>

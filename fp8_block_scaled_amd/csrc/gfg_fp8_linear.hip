@@ -43,7 +43,8 @@ __device__ __forceinline__ uint32_t row_largest(uint32_t m) {
 // ------------------------------------------------------------------ token quantizer
 // x [R][C] -> q [R][C], scale [ceil(C/128)][ld]: 16 lanes share a block, a
 // workgroup takes 16 U rows of one column of blocks, so that its scale bytes
-// are neighbours.  C a multiple of 16.
+// are neighbours.  C a multiple of 16.  Bound by HBM: 4096 x 16384 bf16, 201 MB in 33
+// us, 6.1 TB/s; 4096 x 2304 7.4 us.
 template <typename T, int U>
 __global__ __launch_bounds__(256) void quant_rows_kernel(const T* __restrict__ x, uint8_t* __restrict__ q,
                                                          uint8_t* __restrict__ scale, int64_t R, int C, int64_t ld) {
@@ -75,7 +76,9 @@ __global__ __launch_bounds__(256) void quant_rows_kernel(const T* __restrict__ x
 // for the whole tile in place of both (scale [RB][CB], scale_t [CB][RB]), G
 // matrices one after the other.  Thread (g, l) holds rows 8 g .. +7 and columns
 // 8 l .. +7, so a column's eight codes are one 8-byte word of the transposed
-// tile in LDS, whose words are XOR-swizzled by the column's l.
+// tile in LDS, whose words are XOR-swizzled by the column's l.  Bound by HBM: a weight
+// of 7168 x 2304 f32 in both orientations, 99 MB in 19 us, 5.2 TB/s; dy (4096 x 7168, both
+// ways and sums) and x (4096 x 2304, transposed), bf16, 148 MB in 28 us, 5.3 TB/s.
 struct TileJob {
     const void* x;
     uint8_t *q, *scale;

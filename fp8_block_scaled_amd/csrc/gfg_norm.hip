@@ -13,6 +13,14 @@
 // sum wp g yh (dout + ro h) - ro mean(h zh) sum wp g yh zh, so one round of
 // reductions a row serves both means.  A channel's dwp and dg are one sum over
 // the rows, S = sum G yh (with a token's gate inside: sum g G yh), times g or wp.
+//
+// A row's lanes hold it in registers (two chunks of 8 elements a lane, four above
+// 16384) between the sums and the outputs, so it is read once: both passes are bound
+// by HBM, or by a launch and one row's chain of load, sum and store.
+//   forward, 4096 x 7168 bf16 with an f32 residual: 354 MB in 69 us, 5.1 TB/s (a large
+//   copy: 5.06); the FP8 rows of 512 x 7168 9 us; one row 4.2 us
+//   backward, 8192 x 4096 bf16: 421 MB in 79-82 us, 5.2 TB/s, and the column sums 7 us;
+//   333 x 2049 f16 9.3 and 4.3 us
 #include <hip/hip_runtime.h>
 
 #include <cstdint>

