@@ -20,7 +20,7 @@
 //   forward, 4096 x 7168 bf16 with an f32 residual: 354 MB in 69 us, 5.1 TB/s (a large
 //   copy: 5.06); the FP8 rows of 512 x 7168 9 us; one row 4.2 us
 //   backward, 8192 x 4096 bf16: 421 MB in 79-82 us, 5.2 TB/s, and the column sums 7 us;
-//   333 x 2049 f16 9.3 and 4.3 us
+//   333 x 2049 f16 9.8 and 3.0 us
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -427,14 +427,27 @@ void by_type(int32_t dtype, int32_t residual_dtype, F f) {
 // Workgroups of a pass over M rows: at most `waves` waves in all, as many as the
 // registers leave room for on 256 CUs, each of which then walks rows.
 constexpr int64_t kForwardWaves = 4096, kBackwardWaves = 2048;
-int64_t groups(int64_t M, int64_t H, int64_t waves) {
+struct Grid { int64_t turns, most; };          // times a workgroup's rows that there are, and workgroups
+Grid grid_of(int64_t M, int64_t H, int64_t waves) {
     int64_t rows = 1, most = 1;
     by_width(H, [&](auto w) {
         rows = kRows<decltype(w)::TPR>;
         most = waves * 64 / kThreads<decltype(w)::TPR>;
     });
-    const int64_t n = (M + rows - 1) / rows;
-    return n < most ? n : most;
+    return Grid{(M + rows - 1) / rows, most};
+}
+int64_t forward_groups(int64_t M, int64_t H) {
+    const Grid g = grid_of(M, H, kForwardWaves);
+    return g.turns < g.most ? g.turns : g.most;
+}
+// Backward, each workgroup also writes sums that are read again: up to five turns a
+// CU one workgroup a CU, and all of them as many turns (both launches, us, 512 and
+// 256 workgroups at most: 512 x 4096 20.4, 17.1; 478 x 3033 21.1, 16.9; 1264 x 3791
+// 26.1, 25.5; but 2048 x 4096, eight turns, 29.1, 31.6).
+int64_t backward_groups(int64_t M, int64_t H) {
+    const Grid g = grid_of(M, H, kBackwardWaves);
+    const int64_t most = g.turns <= 5 * 256 && g.most > 256 ? 256 : g.most, each = (g.turns + most - 1) / most;
+    return (g.turns + each - 1) / each;
 }
 
 int launched() {
@@ -471,7 +484,7 @@ int forward(const char* fn, NormArgs a, int32_t dtype, int32_t residual_dtype, v
         return fail(GFG_EINVAL, "%s: a pointer is not aligned to its elements (q: 8 bytes)", fn);
     by_width(a.H, [&](auto width) {
         constexpr int TPR = decltype(width)::TPR, CH = decltype(width)::CH;
-        const dim3 grid(unsigned(groups(a.M, a.H, kForwardWaves))), block(kThreads<TPR>);
+        const dim3 grid(unsigned(forward_groups(a.M, a.H))), block(kThreads<TPR>);
         by_type(dtype, residual_dtype, [&](auto y, auto r) {
             hipLaunchKernelGGL((residual_norm_kernel<decltype(y), decltype(r), TPR, CH, (CH == 2)>), grid, block, 0, static_cast<hipStream_t>(stream), a);
         });
@@ -512,7 +525,7 @@ extern "C" int residual_norm_fp8(const void* y, const void* residual, const floa
 }
 
 extern "C" int64_t residual_norm_backward_workspace_bytes(int64_t M, int64_t H) {
-    return M > 0 && H > 0 ? groups(M, H, kBackwardWaves) * 2 * H * 4 : 0;
+    return M > 0 && H > 0 ? backward_groups(M, H) * 2 * H * 4 : 0;
 }
 
 extern "C" int residual_norm_backward(const void* dout, const void* dnormed, const void* out, const void* y, const float* stats,
@@ -548,7 +561,7 @@ extern "C" int residual_norm_backward(const void* dout, const void* dnormed, con
                         (long long)residual_norm_backward_workspace_bytes(M, H));
     }
     hipStream_t s = static_cast<hipStream_t>(stream);
-    const int64_t P = M > 0 ? groups(M, H, kBackwardWaves) : 0;
+    const int64_t P = M > 0 ? backward_groups(M, H) : 0;
     if (M > 0) {
         const BackArgs a{dout, dnormed, out, y, stats, weight, post_weight, gate, gate_kind, alpha, dresidual, dy, dgate,
                          sums ? static_cast<float*>(workspace) : nullptr, M, int(H)};
