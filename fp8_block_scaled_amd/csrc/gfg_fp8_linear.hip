@@ -364,23 +364,23 @@ __device__ __forceinline__ void load_bias(float (&v)[CNT], const F8Params& p, in
 }
 
 // TM x TN output tiles, WM x WN waves, K in steps of 128 through four LDS
-// stages filled by direct-to-LDS loads: three are in flight while one is
-// consumed, and a step has one barrier (a wave that passes it has seen every
+// stages (three of 256 x 128) filled by direct-to-LDS loads: all but one are in
+// flight while that is consumed, and a step has one barrier (a wave that passes it has seen every
 // wave finish the previous step, whose buffer the new loads go to).  Rows past
 // an operand's end and chunks past K lie outside the buffer window, where the
 // hardware returns zeros; zeros add nothing whatever their scale (which is a
 // clamped one of the operand's own).
 template <int TM, int TN, int WM, int WN, bool BROW, typename OutT>
 __device__ __forceinline__ void ring_tile(const F8Params& p, unsigned w) {
-    constexpr int S = 4, WAVES = WM * WN, BYTES = (TM + TN) * QB;
+    constexpr int WAVES = WM * WN, BYTES = (TM + TN) * QB, S = 4 * BYTES <= 128 * 1024 ? 4 : 3;
     constexpr int PER = BYTES / 1024 / WAVES, A_LOADS = TM / 8 / WAVES;
     constexpr int RB = TM / WM / 16, CB = TN / WN / 16;
     constexpr int OPS = PER + 1 + (BROW ? 1 : 0);      // vector-memory operations of a wave and stage
     static_assert(BYTES % (1024 * WAVES) == 0 && TM % (8 * WAVES) == 0 && WAVES % 4 == 0 && TN <= QB, "stage shape");
     // an array for each stage: the compiler then knows that reading one need
     // not wait for the loads into another
-    __shared__ __attribute__((aligned(1024))) uint8_t s0[BYTES], s1[BYTES], s2[BYTES], s3[BYTES];
-    GFG_LDS uint8_t* const buf[S] = {(GFG_LDS uint8_t*)s0, (GFG_LDS uint8_t*)s1, (GFG_LDS uint8_t*)s2, (GFG_LDS uint8_t*)s3};
+    __shared__ __attribute__((aligned(1024))) uint8_t s0[BYTES], s1[BYTES], s2[BYTES], s3[S > 3 ? BYTES : 1024];
+    GFG_LDS uint8_t* const buf[4] = {(GFG_LDS uint8_t*)s0, (GFG_LDS uint8_t*)s1, (GFG_LDS uint8_t*)s2, (GFG_LDS uint8_t*)s3};
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int l16 = lane & 15, lq = lane >> 4;
@@ -469,7 +469,8 @@ __device__ __forceinline__ void ring_tile(const F8Params& p, unsigned w) {
         step(0, kb, least);
         if (kb + 1 < p.KB) {
             step(1, kb + 1, least);
-            if (kb + 2 < p.KB) step(2, kb + 2, least);
+            if constexpr (S > 3)
+                if (kb + 2 < p.KB) step(2, kb + 2, least);
         }
     }
     GFG_WAITCNT(0, 15);                            // the last loads land before the workgroup ends
@@ -845,7 +846,10 @@ int launch_stream(F8Params p, int out_dtype, hipStream_t s) {
 
 // The tile by how many of each size there are (M x N x K, us, the product alone,
 // cold weights, the chosen tile first):
-//  * more tiles of 128 x 128 than CUs: 256 x 256 (4096 x 4096 x 16384: 205-240, 128 x
+//  * more tiles of 128 x 128 than CUs, but not of 256 x 128: those (1783 x 3777 x 14672:
+//    141, 256 x 256 186; 2048 x 4096 x 7168: 55, 75; 2200 x 2048 x 4096: 30, 45; 4000 x
+//    2000 x 528: 12.2, 17.5);
+//  * more of both: 256 x 256 (4096 x 4096 x 16384: 205-240, 128 x
 //    128 346-370; 4096 x 7168 x 2304: 70, 110; 7168 x 2304 x 4096 with a scale a row of
 //    both: 62, 97);
 //  * up to 16 rows: streamed, 16 x 16 on eight waves where those do not outnumber
@@ -869,9 +873,10 @@ int launch_product(const char* fn, const F8Params& p, int out_dtype, hipStream_t
     const bool fits = fp8_256_fits(p, out_dtype);
     if (choice == GFG_TILE_256x256 && !fits && p.rows >= 4 && p.N >= 4)
         return fail(GFG_EUNSUPPORTED, "%s: the 256 x 256 tile's offsets do not reach over N=%d", fn, p.N);
-    if (fits && (choice == GFG_TILE_256x256 || (choice == GFG_TILE_AUTO && (p.rows + 127) / 128 * ((int64_t(p.N) + 127) / 128) > cus)))
-        return launch_fp8_256(p, BROW, out_dtype, s);
     auto tiles = [&](int64_t tm, int64_t tn) { return (p.rows + tm - 1) / tm * ((p.N + tn - 1) / tn); };
+    if (choice == GFG_TILE_AUTO && tiles(128, 128) > cus && tiles(256, 128) <= cus)
+        return launch_ring<256, 128, 4, 2, BROW>(p, out_dtype, s);
+    if (fits && (choice == GFG_TILE_256x256 || (choice == GFG_TILE_AUTO && tiles(128, 128) > cus))) return launch_fp8_256(p, BROW, out_dtype, s);
     if constexpr (!BROW)
         if (p.rows <= 16) {
             if (p.N <= 16 * cus) return launch_stream<1, 1, 8, 4, false>(p, out_dtype, s);

@@ -639,9 +639,10 @@ GFG_API int moe_router_backward(const void* logits, int32_t in_dtype, const int3
  * GFG_TILE_128x256 the smaller ones, GFG_TILE_256x256 the large ones (N at most
  * 2^22); their results do not depend on it.  The dense FP8 products follow it in
  * the same way: large tiles (256 x 256, an operand of at least 4 rows) where tiles of
- * 128 x 128 would outnumber the CUs; GFG_TILE_256x256 needs N at most 2^21 (2^20
- * with 32-bit outputs), else GFG_EUNSUPPORTED; with a set shape fp8_linear and
- * fp8_linear_backward launch their quantizers and products apart.
+ * 256 x 128 would outnumber the CUs, those where tiles of 128 x 128 would;
+ * GFG_TILE_256x256 needs N at most 2^21 (2^20 with 32-bit outputs), else
+ * GFG_EUNSUPPORTED; with a set shape fp8_linear and fp8_linear_backward launch
+ * their quantizers and products apart.
  *
  * grouped_fp8_set_grid_limit: at most max_workgroups workgroups per GEMM
  * launch.  0, the default, is no limit: one per CU, fewer when there are fewer

@@ -59,7 +59,7 @@ def whole(rng, *shape):
 
 # rows from one on, odd and ragged in every direction; each kernel's tile and its edges
 SHAPES = [(1, 1, 16), (1, 7168, 2304), (2, 33, 144), (3, 257, 1040), (5, 1003, 1072), (16, 130, 128), (17, 64, 272), (31, 500, 4096), (33, 129, 112),
-          (77, 1003, 1072), (128, 128, 128), (129, 300, 528), (300, 2049, 640), (520, 4100, 400), (1500, 1999, 272), (2500, 2600, 144)]
+          (77, 1003, 1072), (128, 128, 128), (129, 300, 528), (300, 2049, 640), (520, 4100, 400), (1500, 1999, 272), (2500, 2600, 144), (4200, 2200, 144)]
 
 
 @pytest.mark.parametrize("M,N,K", SHAPES)
@@ -215,7 +215,7 @@ def test_weight_quantizer_marks_blocks_without_a_scale():
 
 
 # ------------------------------------------------------------------ gradients
-BACK = [(1, 16, 16), (2, 144, 48), (100, 16, 272), (127, 272, 128), (128, 128, 128), (129, 528, 1040), (300, 528, 1040), (257, 2048, 2112), (1000, 128, 384)]
+BACK = [(1, 16, 16), (2, 144, 48), (100, 16, 272), (127, 272, 128), (128, 128, 128), (129, 528, 1040), (300, 528, 1040), (257, 2048, 2112), (1000, 128, 384), (16, 4208, 2208)]
 
 
 def operands(rng, M, N, K, dtype, values=None):
