@@ -856,12 +856,13 @@ int launch_stream(F8Params p, int out_dtype, hipStream_t s) {
 //    the CUs (1 x 2048 x 7168: 6.7, 16 x 32 8.0; 16 x 2048 x 16384: 12.5, 16.0; 1 x
 //    4096 x 4096: 6.0, 6.3), else 16 x 32 (1 x 7168 x 2304: 5.8);
 //  * up to 32 rows: 32 x 32, streamed (32 x 4096 x 4096: 8.0);
-//  * 192 tiles of 128 x 128 or more: those (512 x 7168 x 2304, 224 of them: 14.8);
-//  * up to 512 tiles of 32 x 32: those, streamed (128 x 2048 x 7168: 10.5; 300 x 528 x
-//    1040: 3.9);
+//  * more tiles of 64 x 64 than two a CU, which is what fits: 128 x 128 (1100 x 1900 x
+//    7168: 29, 64 x 64 37; 1664 x 1792 x 2304: 13.0, 15.8; but 1408 x 1408 x 7168, 484
+//    of them: 30, 26; 100 x 16000 x 4096: 20.1, 18.2);
+//  * up to two tiles of 32 x 32 a CU: those, streamed (300 x 1500 x 2304: 6.8, 64 x 64
+//    7.7; 128 x 2048 x 7168: 7.9, 16.6; but 400 x 1500 x 2304, 611 of them: 8.8, 7.7);
 //  * else 64 x 64 (512 x 2048 x 7168: 18.3; 512 x 4096 x 4096: 18.9).
-// The last two lists' borders are the int8 products', whose tiles these are.  All
-// of them take in about 50 GB/s a CU, which bounds 64 x 64.
+// All of them take in about 50 GB/s a CU, which bounds 64 x 64.
 // A tile's lane loads the scale bytes of its RB (CB) neighbouring rows at once,
 // so an operand has to have that many rows: up to 16 rows of A go to RB = 1,
 // and the gradient of a weight has at least 16 of both.
@@ -883,8 +884,8 @@ int launch_product(const char* fn, const F8Params& p, int out_dtype, hipStream_t
             return launch_stream<1, 2, 4, 4, false>(p, out_dtype, s);
         }
     if (p.rows <= 32) return launch_stream<2, 2, 4, 2, BROW>(p, out_dtype, s);
-    if (tiles(128, 128) >= 192) return launch_ring<128, 128, 2, 4, BROW>(p, out_dtype, s);
-    if (tiles(32, 32) <= 512) return launch_stream<2, 2, 4, 2, BROW>(p, out_dtype, s);
+    if (tiles(64, 64) > 2 * cus) return launch_ring<128, 128, 2, 4, BROW>(p, out_dtype, s);
+    if (tiles(32, 32) <= 2 * cus) return launch_stream<2, 2, 4, 2, BROW>(p, out_dtype, s);
     return launch_ring<64, 64, 2, 2, BROW>(p, out_dtype, s);
 }
 
