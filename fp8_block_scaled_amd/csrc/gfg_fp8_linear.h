@@ -6,6 +6,14 @@
 
 namespace gfg {
 
+// out[c] (+)= the sum over the row blocks of sums [RB][C].
+struct SumJob {
+    const float* sums;
+    float* out;
+    int64_t RB;
+    int C, accumulate;
+};
+
 // One product d[m, n] = sum_k a[m, k] b[n, k] (+ bias[n]), both operands E4M3
 // with K fastest, one E8M0 byte per row of `a` and 128 k, and either one per
 // 128 x 128 block of `b` or one per row of `b` and 128 k.
@@ -23,8 +31,9 @@ struct F8Params {
     int group_m, num_xcd;
     int m_tiles;             // tiles along M of the kernel's height
     unsigned tiles;
+    unsigned sum_groups;     // workgroups behind the tiles' that take `sums` (0: none)
+    SumJob sums;
 };
-
 
 // The kernel on 256 x 256 tiles (gfg_fp8_dense256.hip): whether its 32-bit
 // offsets reach, and the launch.

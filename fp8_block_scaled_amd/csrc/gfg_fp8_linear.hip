@@ -244,29 +244,26 @@ __global__ __launch_bounds__(256) void quant_tiles_kernel(TileJob a, TileJob b) 
     quant_tile<T, false>(second ? b : a, second ? blockIdx.x - a.tiles : blockIdx.x);
 }
 
-// db[c] (+)= the sum over the row blocks of sums [RB][C], in a fixed order: 16
-// lanes of partial sums a column, then those; 16 columns a workgroup.
-struct SumJob {
-    const float* sums;
-    float* out;
-    int64_t RB;
-    int C, accumulate;
-};
-__device__ __forceinline__ void column_sums(const SumJob& p, int block) {
-    __shared__ float part[16][17];
-    const int c = block * 16 + int(threadIdx.x & 15), g = threadIdx.x >> 4;
+// A job's columns 16 block .. +15, in a fixed order: THREADS / 16 lanes of partial
+// sums a column, then those.
+constexpr int kSumColumns = 16;
+template <int THREADS>
+__device__ __forceinline__ void column_sums(const SumJob& p, unsigned block) {
+    constexpr int LANES = THREADS / kSumColumns;
+    __shared__ float part[LANES][kSumColumns + 1];
+    const int l = threadIdx.x % kSumColumns, g = threadIdx.x / kSumColumns, c = int(block) * kSumColumns + l;
     float t = 0.0f;
     if (c < p.C)
-        for (int64_t r = g; r < p.RB; r += 16) t += p.sums[r * p.C + c];
-    part[g][threadIdx.x & 15] = t;
+        for (int64_t r = g; r < p.RB; r += LANES) t += p.sums[r * p.C + c];
+    part[g][l] = t;
     __syncthreads();
     if (g || c >= p.C) return;
     t = 0.0f;
 #pragma unroll
-    for (int w = 0; w < 16; ++w) t += part[w][threadIdx.x];
+    for (int w = 0; w < LANES; ++w) t += part[w][l];
     p.out[c] = p.accumulate ? p.out[c] + t : t;
 }
-__global__ __launch_bounds__(256) void column_sums_kernel(SumJob p) { column_sums(p, int(blockIdx.x)); }
+__global__ __launch_bounds__(256) void column_sums_kernel(SumJob p) { column_sums<256>(p, blockIdx.x); }
 
 template <typename T>
 __global__ __launch_bounds__(256) void zero_kernel(T* __restrict__ p, int64_t n) {
@@ -506,6 +503,7 @@ __device__ __forceinline__ void walk(unsigned tiles, Tile tile) {
 
 template <int TM, int TN, int WM, int WN, bool BROW, typename OutT>
 __global__ __launch_bounds__(WM * WN * 64) void fp8_ring_kernel(F8Params p) {
+    if (blockIdx.x >= p.tiles) return column_sums<WM * WN * 64>(p.sums, blockIdx.x - p.tiles);
     walk(p.tiles, [&](unsigned w) { ring_tile<TM, TN, WM, WN, BROW, OutT>(p, w); });
 }
 
@@ -643,6 +641,7 @@ __global__ __launch_bounds__(NW * 64) void fp8_stream_kernel(F8Params p) {
     // not wait for the loads into another
     constexpr int BYTES = NW * kUnit<RB, CB>;
     __shared__ __attribute__((aligned(1024))) uint8_t s0[BYTES], s1[BYTES], s2[D > 2 ? BYTES : 1024], s3[D > 2 ? BYTES : 1024];
+    if (blockIdx.x >= p.tiles) return column_sums<NW * 64>(p.sums, blockIdx.x - p.tiles);
     walk(p.tiles, [&](unsigned w) { stream_tile<RB, CB, NW, D, BROW, OutT>(p, w, s0, s1, s2, s3); });
 }
 
@@ -789,13 +788,13 @@ __global__ __launch_bounds__(NW * 64) void fp8_few_kernel(const X* __restrict__ 
 // 23.5, 20.0).  A workgroup has one tile of its own shape, so not under a grid limit
 // or a set shape; the gradient of one token has too few rows for these tiles.
 template <typename OutX, typename OutW>
-__global__ __launch_bounds__(256) void fp8_backward_kernel(F8Params dx, F8Params dw, SumJob db) {
+__global__ __launch_bounds__(256) void fp8_backward_kernel(F8Params dx, F8Params dw) {
     constexpr int BYTES = 4 * kUnit<2, 2>;
     __shared__ __attribute__((aligned(1024))) uint8_t s0[BYTES], s1[BYTES], none[1024];
     const unsigned w = blockIdx.x;
     if (w < dx.tiles) stream_tile<2, 2, 4, 2, false, OutX>(dx, w, s0, s1, none, none);
     else if (w < dx.tiles + dw.tiles) stream_tile<2, 2, 4, 2, true, OutW>(dw, w - dx.tiles, s0, s1, none, none);
-    else column_sums(db, int(w - dx.tiles - dw.tiles));
+    else column_sums<256>(dx.sums, w - dx.tiles - dw.tiles);
 }
 
 // Workgroups of a launch over p.tiles tiles: one for each, or as many as the
@@ -816,9 +815,9 @@ template <int TM, int TN, int WM, int WN, bool BROW>
 int launch_ring(F8Params p, int out_dtype, hipStream_t s) {
     p.m_tiles = int((p.rows + TM - 1) / TM);
     const int64_t tiles = int64_t(p.m_tiles) * ((p.N + TN - 1) / TN);
-    if (tiles * (WM * WN * 64) >= int64_t(1) << 32) return fail(GFG_EUNSUPPORTED, "the output has too many tiles for one launch");
+    if ((tiles + p.sum_groups) * (WM * WN * 64) >= int64_t(1) << 32) return fail(GFG_EUNSUPPORTED, "the output has too many tiles for one launch");
     p.tiles = unsigned(tiles);
-    const dim3 grid(workgroups(p)), block(WM * WN * 64);
+    const dim3 grid(workgroups(p) + p.sum_groups), block(WM * WN * 64);
     if (out_dtype == GFG_OUT_BF16)
         hipLaunchKernelGGL((fp8_ring_kernel<TM, TN, WM, WN, BROW, __bf16>), grid, block, 0, s, p);
     else if (out_dtype == GFG_OUT_F16)
@@ -832,9 +831,9 @@ template <int RB, int CB, int NW, int D, bool BROW>
 int launch_stream(F8Params p, int out_dtype, hipStream_t s) {
     p.m_tiles = int((p.rows + 16 * RB - 1) / (16 * RB));
     const int64_t tiles = int64_t(p.m_tiles) * ((p.N + 16 * CB - 1) / (16 * CB));
-    if (tiles * (NW * 64) >= int64_t(1) << 32) return fail(GFG_EUNSUPPORTED, "the output has too many tiles for one launch");
+    if ((tiles + p.sum_groups) * (NW * 64) >= int64_t(1) << 32) return fail(GFG_EUNSUPPORTED, "the output has too many tiles for one launch");
     p.tiles = unsigned(tiles);
-    const dim3 grid(workgroups(p)), block(NW * 64);
+    const dim3 grid(workgroups(p) + p.sum_groups), block(NW * 64);
     if (out_dtype == GFG_OUT_BF16)
         hipLaunchKernelGGL((fp8_stream_kernel<RB, CB, NW, D, BROW, __bf16>), grid, block, 0, s, p);
     else if (out_dtype == GFG_OUT_F16)
@@ -866,18 +865,25 @@ int launch_stream(F8Params p, int out_dtype, hipStream_t s) {
 // A tile's lane loads the scale bytes of its RB (CB) neighbouring rows at once,
 // so an operand has to have that many rows: up to 16 rows of A go to RB = 1,
 // and the gradient of a weight has at least 16 of both.
+int64_t tiles_of(const F8Params& p, int64_t tm, int64_t tn) { return (p.rows + tm - 1) / tm * ((p.N + tn - 1) / tn); }
+bool tall(const F8Params& p, int cus) {
+    return tile_shape_choice() == GFG_TILE_AUTO && tiles_of(p, 128, 128) > cus && tiles_of(p, 256, 128) <= cus;
+}
+// Whether the product runs on the 256 x 256 tiles, which its workgroups walk.
+bool walks(const F8Params& p, int out_dtype, int cus) {
+    const int choice = tile_shape_choice();
+    return fp8_256_fits(p, out_dtype) && (choice == GFG_TILE_256x256 || (choice == GFG_TILE_AUTO && tiles_of(p, 128, 128) > cus && !tall(p, cus)));
+}
+
 template <bool BROW>
 int launch_product(const char* fn, const F8Params& p, int out_dtype, hipStream_t s) {
     int cus = 0;
     if (int rc = device_cus(&cus)) return rc;
-    const int choice = tile_shape_choice();
-    const bool fits = fp8_256_fits(p, out_dtype);
-    if (choice == GFG_TILE_256x256 && !fits && p.rows >= 4 && p.N >= 4)
+    if (tile_shape_choice() == GFG_TILE_256x256 && !fp8_256_fits(p, out_dtype) && p.rows >= 4 && p.N >= 4)
         return fail(GFG_EUNSUPPORTED, "%s: the 256 x 256 tile's offsets do not reach over N=%d", fn, p.N);
-    auto tiles = [&](int64_t tm, int64_t tn) { return (p.rows + tm - 1) / tm * ((p.N + tn - 1) / tn); };
-    if (choice == GFG_TILE_AUTO && tiles(128, 128) > cus && tiles(256, 128) <= cus)
-        return launch_ring<256, 128, 4, 2, BROW>(p, out_dtype, s);
-    if (fits && (choice == GFG_TILE_256x256 || (choice == GFG_TILE_AUTO && tiles(128, 128) > cus))) return launch_fp8_256(p, BROW, out_dtype, s);
+    auto tiles = [&](int64_t tm, int64_t tn) { return tiles_of(p, tm, tn); };
+    if (tall(p, cus)) return launch_ring<256, 128, 4, 2, BROW>(p, out_dtype, s);
+    if (walks(p, out_dtype, cus)) return launch_fp8_256(p, BROW, out_dtype, s);
     if constexpr (!BROW)
         if (p.rows <= 16) {
             if (p.N <= 16 * cus) return launch_stream<1, 1, 8, 4, false>(p, out_dtype, s);
@@ -973,8 +979,8 @@ int64_t few_tiles(F8Params* p) {
     return tiles;
 }
 
-int launch_pair(const F8Params& dx, const F8Params& dw, const SumJob& db, unsigned db_groups, int dx_dtype, int dw_dtype, hipStream_t s) {
-    auto go = [&](auto* kernel) { hipLaunchKernelGGL(kernel, dim3(dx.tiles + dw.tiles + db_groups), dim3(256), 0, s, dx, dw, db); };
+int launch_pair(const F8Params& dx, const F8Params& dw, int dx_dtype, int dw_dtype, hipStream_t s) {
+    auto go = [&](auto* kernel) { hipLaunchKernelGGL(kernel, dim3(dx.tiles + dw.tiles + dx.sum_groups), dim3(256), 0, s, dx, dw); };
     auto with = [&](auto x) {
         typedef decltype(x) X;
         if (dw_dtype == GFG_OUT_BF16) go(fp8_backward_kernel<X, __bf16>);
@@ -1221,19 +1227,24 @@ extern "C" int fp8_linear_backward(const void* dy, const void* x, int32_t in_dty
             hipLaunchKernelGGL((quant_tiles_kernel<decltype(t)>), dim3(a.tiles + b.tiles), dim3(256), 0, s, a, b);
         }))
         return rc;
-    const SumJob db{sums, dbias, at.MB, int(N), accumulate};
-    const unsigned db_groups = dbias ? unsigned((N + 15) / 16) : 0u;
     F8Params px = product(ws + at.q, ws + at.qs, at.ldm, b_t, b_t_scale, 0, nullptr, dx, M, K, N);
     F8Params pw = product(ws + at.yt, ws + at.yts, at.ldn, ws + at.xt, ws + at.xts, at.ldk, nullptr, dw, N, K, at.Mp);
     pw.accumulate = accumulate;
     int cus = 0;
     if (int rc = device_cus(&cus)) return rc;
-    if (dx && dw && M >= 2 && grid_limit() == 0 && tile_shape_choice() == GFG_TILE_AUTO && few_tiles(&px) + few_tiles(&pw) <= 4 * cus)
-        return launch_pair(px, pw, db, db_groups, dx_dtype, dw_dtype, s);
-    if (dbias) {
+    // the bias gradient: workgroups behind the first product's, or a launch of its own
+    // where that walks its tiles (all on 256 x 256 tiles, or under a grid limit)
+    const SumJob db{sums, dbias, at.MB, int(N), accumulate};
+    const unsigned db_groups = dbias ? unsigned((N + kSumColumns - 1) / kSumColumns) : 0u;
+    if (F8Params& first = dx ? px : pw; dbias && (dx || dw) && grid_limit() == 0 && !walks(first, dx ? dx_dtype : dw_dtype, cus)) {
+        first.sums = db;
+        first.sum_groups = db_groups;
+    } else if (dbias) {
         hipLaunchKernelGGL(column_sums_kernel, dim3(db_groups), dim3(256), 0, s, db);
         if (int rc = launched()) return rc;
     }
+    if (dx && dw && M >= 2 && grid_limit() == 0 && tile_shape_choice() == GFG_TILE_AUTO && few_tiles(&px) + few_tiles(&pw) <= 4 * cus)
+        return launch_pair(px, pw, dx_dtype, dw_dtype, s);
     if (dx)
         if (int rc = launch_product<false>(fn, px, dx_dtype, s)) return rc;
     return dw ? launch_product<true>(fn, pw, dw_dtype, s) : GFG_OK;

@@ -215,7 +215,7 @@ def test_weight_quantizer_marks_blocks_without_a_scale():
 
 
 # ------------------------------------------------------------------ gradients
-BACK = [(1, 16, 16), (2, 144, 48), (100, 16, 272), (127, 272, 128), (128, 128, 128), (129, 528, 1040), (300, 528, 1040), (257, 2048, 2112), (1000, 128, 384), (16, 4208, 2208)]
+BACK = [(1, 16, 16), (2, 144, 48), (100, 16, 272), (127, 272, 128), (128, 128, 128), (129, 528, 1040), (300, 528, 1040), (257, 2048, 2112), (1000, 128, 384), (16, 4208, 2208), (2100, 48, 2112)]
 
 
 def operands(rng, M, N, K, dtype, values=None):
