@@ -23,6 +23,7 @@
 //   333 x 2049 f16 9.8 and 3.0 us
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 
 #include "gfg.h"
@@ -53,6 +54,14 @@ struct Chunk { int col, skip; };
 __device__ __forceinline__ Chunk chunk_of(int c, int H) {
     const int col = min(8 * c, H - 8);
     return Chunk{col, min(8 * c - col, 8)};
+}
+
+// The chunk, of which the compiler knows no load before this one: what it held
+// instead would be spilled.
+__device__ __forceinline__ Chunk again(Chunk c) {
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("" : "+v"(c.col));
+    return c;
 }
 
 // Column i of a chunk where it is the lane's own, else 0.
@@ -128,8 +137,53 @@ __device__ __forceinline__ void load_weights(float (&f)[CH][8], const float* wei
     }
 }
 
-// AHEAD: the next row is loaded while one is computed.
-template <typename Y, typename R, int TPR, int CH, bool AHEAD>
+// The weights of a lane's columns, post weight times a channel's gate and weight, from
+// the registers that hold them for all rows, or from memory once more.
+template <int CH, bool HELD>
+struct Weights {
+    const float *post, *gate, *weight;
+    float k[HELD ? CH : 1][8], w[HELD ? CH : 1][8];
+    __device__ __forceinline__ Weights(const float* post, const float* gate, const float* weight, const Chunk (&c)[CH])
+        : post(post), gate(gate), weight(weight) {
+        if constexpr (HELD) {
+            load_weights(k, post, c);
+            if (gate) {
+                float g[CH][8];
+                load_weights(g, gate, c);
+#pragma unroll
+                for (int j = 0; j < CH; ++j)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) k[j][i] *= g[j][i];
+            }
+            load_weights(w, weight, c);
+        }
+    }
+    __device__ __forceinline__ void get_k(float (&f)[8], int j, const Chunk& c) const {
+        if constexpr (HELD) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] = k[j][i];
+        } else {
+            float g[1][8], h[1][8];
+            load_weights(h, post, {c});
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] = h[0][i];
+            if (!gate) return;
+            load_weights(g, gate, {c});
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] *= g[0][i];
+        }
+    }
+    __device__ __forceinline__ void get_w(float (&f)[8], int j, const Chunk& c) const {
+        float h[1][8];
+        if constexpr (!HELD) load_weights(h, weight, {c});
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = HELD ? w[HELD ? j : 0][i] : h[0][i];
+    }
+};
+
+// AHEAD: the next row is loaded while one is computed.  HELD: the weights stay in
+// registers (not with four chunks a lane: 1024 x 32768 bf16 56 us, HELD 102).
+template <typename Y, typename R, int TPR, int CH, bool AHEAD, bool HELD>
 __global__ __launch_bounds__(kThreads<TPR>) void residual_norm_kernel(NormArgs p) {
     constexpr int ROWS = kRows<TPR>;
     __shared__ float part_smem[2 * kThreads<TPR> / 64];
@@ -155,17 +209,7 @@ __global__ __launch_bounds__(kThreads<TPR>) void residual_norm_kernel(NormArgs p
     const int64_t step = int64_t(gridDim.x) * ROWS;
     int64_t m = int64_t(blockIdx.x) * ROWS + in;
     load(y, r, m);
-    float k[CH][8], w[CH][8];                  // post weight times a channel's gate; weight
-    load_weights(k, p.post, c);
-    if (p.gate_kind == GFG_GATE_CHANNEL) {
-        float g[CH][8];
-        load_weights(g, p.gate, c);
-#pragma unroll
-        for (int j = 0; j < CH; ++j)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) k[j][i] *= g[j][i];
-    }
-    load_weights(w, p.weight, c);
+    const Weights<CH, HELD> weights(p.post, p.gate_kind == GFG_GATE_CHANNEL ? p.gate : nullptr, p.weight, c);
     int turn = 0;
     // (every thread takes part in the sums of its workgroup's rows, also past the last row)
     for (int64_t base = int64_t(blockIdx.x) * ROWS; base < p.M; base += step, m += step) {
@@ -188,9 +232,11 @@ __global__ __launch_bounds__(kThreads<TPR>) void residual_norm_kernel(NormArgs p
         float o[CH][8], s[1] = {0.0f};
 #pragma unroll
         for (int j = 0; j < CH; ++j) {
+            float k[8];
+            weights.get_k(k, j, HELD ? c[j] : again(c[j]));
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                o[j][i] = p.alpha * r[j].at(i) + (has_y ? y[j].at(i) * scale * k[j][i] : 0.0f);
+                o[j][i] = p.alpha * r[j].at(i) + (has_y ? y[j].at(i) * scale * k[i] : 0.0f);
                 const float v = own(c[j], i, o[j][i]);
                 s[0] += v * v;
             }
@@ -201,9 +247,10 @@ __global__ __launch_bounds__(kThreads<TPR>) void residual_norm_kernel(NormArgs p
             const float ro = rsqrtf(s[0] / float(p.H) + p.eps);
 #pragma unroll
             for (int j = 0; j < CH; ++j) {
-                float z[8];
+                float z[8], w[8];
+                weights.get_w(w, j, HELD ? c[j] : again(c[j]));
 #pragma unroll
-                for (int i = 0; i < 8; ++i) z[i] = o[j][i] * ro * w[j][i];
+                for (int i = 0; i < 8; ++i) z[i] = o[j][i] * ro * w[i];
                 if (p.normed && valid) store8(static_cast<Y*>(p.normed) + m * p.H, c[j], z);
                 if (p.q) {
                     // 16 neighbouring lanes hold a block of 128 channels (z is 0 outside a lane's own)
@@ -251,7 +298,11 @@ struct BackArgs {
     int H;
 };
 
-template <typename Y, typename R, int TPR, int CH, bool AHEAD>
+// HELD: a row and the weights stay in registers, and the next row is loaded while
+// one is computed; otherwise (rows above 8192, whose 1024 lanes have 128 registers each)
+// both passes read them, a chunk at a time (1024 rows bf16, us, otherwise and HELD: 12288
+// 62, 161; 16384 73, 171; 32768 412, 1077).
+template <typename Y, typename R, int TPR, int CH, bool HELD>
 __global__ __launch_bounds__(kThreads<TPR>) void residual_norm_backward_kernel(BackArgs p) {
     constexpr int ROWS = kRows<TPR>;
     __shared__ float part_smem[6 * kThreads<TPR> / 64];
@@ -267,59 +318,64 @@ __global__ __launch_bounds__(kThreads<TPR>) void residual_norm_backward_kernel(B
     const R* const outs = static_cast<const R*>(norm ? p.out : louts);
     const Y* const dzs = static_cast<const Y*>(norm ? p.dnormed : has_y ? p.y : static_cast<const void*>(louts));
     const Y* const ys = static_cast<const Y*>(has_y ? p.y : static_cast<const void*>(dzs));
-    struct Rows {
-        Row8<R> dout[CH], out[CH];
-        Row8<Y> dz[CH], y[CH];
-    } a, b;
-    auto load = [&](Rows& v, int64_t m) {
-        m = m < p.M ? m : p.M - 1;
+    struct Part {
+        Row8<R> dout, out;
+        Row8<Y> dz, y;
+    };
+    auto part_of = [&](int64_t m, const Chunk& c) {
+        const int64_t at = (m < p.M ? m : p.M - 1) * p.H + c.col;
+        Part v;
+        v.out.load(outs + at);
+        v.dz.load(dzs + at);
+        v.dout.load(louts + at);
+        v.y.load(ys + at);
+        return v;
+    };
+    Part a[HELD ? CH : 1], b[HELD ? CH : 1];
+    auto load = [&](Part (&v)[HELD ? CH : 1], int64_t m) {
+        if constexpr (HELD) {
 #pragma unroll
-        for (int j = 0; j < CH; ++j) {
-            const int64_t at = m * p.H + c[j].col;
-            v.out[j].load(outs + at);
-            v.dz[j].load(dzs + at);
-            v.dout[j].load(louts + at);
-            v.y[j].load(ys + at);
+            for (int j = 0; j < CH; ++j) v[j] = part_of(m, c[j]);
         }
     };
     const int64_t step = int64_t(gridDim.x) * ROWS;
     int64_t m = int64_t(blockIdx.x) * ROWS + in;
     load(a, m);
-    float k[CH][8], w[CH][8];                  // post weight times a channel's gate; weight
-    load_weights(k, post ? p.post : nullptr, c);
-    if (p.gate_kind == GFG_GATE_CHANNEL) {
-        float g[CH][8];
-        load_weights(g, p.gate, c);
-#pragma unroll
-        for (int j = 0; j < CH; ++j)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) k[j][i] *= g[j][i];
-    }
-    load_weights(w, norm ? p.weight : nullptr, c);
+    const Weights<CH, HELD> weights(post ? p.post : nullptr, p.gate_kind == GFG_GATE_CHANNEL ? p.gate : nullptr, norm ? p.weight : nullptr, c);
     float sw[CH][8] = {}, sp[CH][8] = {};
     int turn = 0;
     // (every thread takes part in the sums of its workgroup's rows, also past the last row)
     for (int64_t base = int64_t(blockIdx.x) * ROWS; base < p.M; base += step, m += step) {
-        if constexpr (AHEAD) load(b, m + step);
+        load(b, m + step);
         const bool valid = m < p.M;
         const int64_t at = valid ? m : p.M - 1;
         const float ry = post ? p.stats[at] : 1.0f, ro = norm ? p.stats[p.M + at] : 0.0f;
         const float token_gate = p.gate_kind == GFG_GATE_TOKEN ? p.gate[at] : 1.0f;
-        auto zh = [&](int j, int i) { return norm ? a.out[j].at(i) * ro : 0.0f; };
-        auto yh = [&](int j, int i) { return has_y ? a.y[j].at(i) * ry : 0.0f; };
-        auto h = [&](int j, int i) { return norm ? a.dz[j].at(i) * w[j][i] : 0.0f; };
-        auto dout = [&](int j, int i) { return has_dout ? a.dout[j].at(i) : 0.0f; };
+        auto zh = [&](const Part& v, int i) { return norm ? v.out.at(i) * ro : 0.0f; };
+        auto yh = [&](const Part& v, int i) { return has_y ? v.y.at(i) * ry : 0.0f; };
+        auto h = [&](const Part& v, int i, const float (&w)[8]) { return norm ? v.dz.at(i) * w[i] : 0.0f; };
+        auto dout = [&](const Part& v, int i) { return has_dout ? v.dout.at(i) : 0.0f; };
+        auto take = [&](int j, float (&k)[8], float (&w)[8]) {
+            const Chunk now = HELD ? c[j] : again(c[j]);
+            weights.get_k(k, j, now);
+            weights.get_w(w, j, now);
+            if constexpr (HELD) return a[j];
+            else return part_of(m, now);
+        };
         // A = sum h zh, B = sum k yh (dout + ro h), C = sum k yh zh (w and k are 0 outside a lane's own)
         float s[3] = {0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int j = 0; j < CH; ++j)
+        for (int j = 0; j < CH; ++j) {
+            float k[8], w[8];
+            const Part x = take(j, k, w);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float v = yh(j, i) * k[j][i], z = zh(j, i), t = h(j, i);
+                const float v = yh(x, i) * k[i], z = zh(x, i), t = h(x, i, w);
                 s[0] += t * z;
-                s[1] += v * (dout(j, i) + ro * t);
+                s[1] += v * (dout(x, i) + ro * t);
                 s[2] += v * z;
             }
+        }
         row_sums<TPR, ROWS>(s, part, turn);
         const float mean_h = s[0] / float(p.H);
         const float row = s[1] - ro * mean_h * s[2];          // sum k yh G
@@ -328,23 +384,26 @@ __global__ __launch_bounds__(kThreads<TPR>) void residual_norm_backward_kernel(B
             if (p.gate_kind == GFG_GATE_TOKEN && p.dgate && lane == 0) p.dgate[m] = row;
 #pragma unroll
             for (int j = 0; j < CH; ++j) {
-                float dr[8], dy[8];
+                float dr[8], dy[8], k[8], w[8];
+                const Part x = take(j, k, w);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const float z = zh(j, i), yv = yh(j, i);
-                    const float G = dout(j, i) + ro * (h(j, i) - z * mean_h);
+                    const float z = zh(x, i), yv = yh(x, i);
+                    const float G = dout(x, i) + ro * (h(x, i, w) - z * mean_h);
                     const float gG = token_gate * G;
                     dr[i] = p.alpha * G;
-                    dy[i] = post ? ry * (k[j][i] * gG - yv * mean_y) : k[j][i] * gG;
-                    sw[j][i] += (norm ? a.dz[j].at(i) : 0.0f) * z;
+                    dy[i] = post ? ry * (k[i] * gG - yv * mean_y) : k[i] * gG;
+                    sw[j][i] += (norm ? x.dz.at(i) : 0.0f) * z;
                     sp[j][i] += gG * yv;
                 }
                 if (p.dresidual) store8(static_cast<R*>(p.dresidual) + m * p.H, c[j], dr);
                 if (p.dy) store8(static_cast<Y*>(p.dy) + m * p.H, c[j], dy);
             }
         }
-        if constexpr (AHEAD) a = b;
-        else load(a, m + step);
+        if constexpr (HELD) {
+#pragma unroll
+            for (int j = 0; j < CH; ++j) a[j] = b[j];
+        }
     }
     if (!p.sums) return;
     if constexpr (ROWS > 1) {                  // the rows' lanes, in order
@@ -425,14 +484,15 @@ void by_type(int32_t dtype, int32_t residual_dtype, F f) {
 }
 
 // Workgroups of a pass over M rows: at most `waves` waves in all, as many as the
-// registers leave room for on 256 CUs, each of which then walks rows.
+// registers leave room for on 256 CUs, one a CU at least, each of which then walks
+// rows.
 constexpr int64_t kForwardWaves = 4096, kBackwardWaves = 2048;
 struct Grid { int64_t turns, most; };          // times a workgroup's rows that there are, and workgroups
 Grid grid_of(int64_t M, int64_t H, int64_t waves) {
     int64_t rows = 1, most = 1;
     by_width(H, [&](auto w) {
         rows = kRows<decltype(w)::TPR>;
-        most = waves * 64 / kThreads<decltype(w)::TPR>;
+        most = std::max<int64_t>(waves * 64 / kThreads<decltype(w)::TPR>, 256);
     });
     return Grid{(M + rows - 1) / rows, most};
 }
@@ -486,7 +546,7 @@ int forward(const char* fn, NormArgs a, int32_t dtype, int32_t residual_dtype, v
         constexpr int TPR = decltype(width)::TPR, CH = decltype(width)::CH;
         const dim3 grid(unsigned(forward_groups(a.M, a.H))), block(kThreads<TPR>);
         by_type(dtype, residual_dtype, [&](auto y, auto r) {
-            hipLaunchKernelGGL((residual_norm_kernel<decltype(y), decltype(r), TPR, CH, (CH == 2)>), grid, block, 0, static_cast<hipStream_t>(stream), a);
+            hipLaunchKernelGGL((residual_norm_kernel<decltype(y), decltype(r), TPR, CH, (CH == 2), (CH == 2)>), grid, block, 0, static_cast<hipStream_t>(stream), a);
         });
     });
     return launched();
