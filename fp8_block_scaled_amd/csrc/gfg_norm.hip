@@ -307,6 +307,12 @@ __global__ __launch_bounds__(kThreads<TPR>) void residual_norm_backward_kernel(B
     constexpr int ROWS = kRows<TPR>;
     __shared__ float part_smem[6 * kThreads<TPR> / 64];
     __shared__ float join_smem[ROWS > 1 ? 2 * CH * 8 * TPR : 1];
+    // four chunks a lane: the sums S lie in LDS, each lane's own (128 KB; 1024 x 32768
+    // bf16 240 us, in registers 412)
+    constexpr bool IN_LDS = CH == 4;
+    typedef float v4 __attribute__((ext_vector_type(4)));
+    __shared__ __attribute__((aligned(16))) v4 s_smem[IN_LDS ? 2 * CH * TPR : 1];
+    GFG_LDS v4* const s_lds = (GFG_LDS v4*)s_smem + threadIdx.x;
     GFG_LDS float* const part = (GFG_LDS float*)part_smem;
     const int lane = threadIdx.x % TPR, in = threadIdx.x / TPR;
     Chunk c[CH];
@@ -342,7 +348,11 @@ __global__ __launch_bounds__(kThreads<TPR>) void residual_norm_backward_kernel(B
     int64_t m = int64_t(blockIdx.x) * ROWS + in;
     load(a, m);
     const Weights<CH, HELD> weights(post ? p.post : nullptr, p.gate_kind == GFG_GATE_CHANNEL ? p.gate : nullptr, norm ? p.weight : nullptr, c);
-    float sw[CH][8] = {}, sp[CH][8] = {};
+    float sw[CH][8] = {}, sp[IN_LDS ? 1 : CH][8] = {};
+    if constexpr (IN_LDS) {
+#pragma unroll
+        for (int j = 0; j < 2 * CH; ++j) s_lds[j * TPR] = v4{0.0f, 0.0f, 0.0f, 0.0f};
+    }
     int turn = 0;
     // (every thread takes part in the sums of its workgroup's rows, also past the last row)
     for (int64_t base = int64_t(blockIdx.x) * ROWS; base < p.M; base += step, m += step) {
@@ -394,7 +404,12 @@ __global__ __launch_bounds__(kThreads<TPR>) void residual_norm_backward_kernel(B
                     dr[i] = p.alpha * G;
                     dy[i] = post ? ry * (k[i] * gG - yv * mean_y) : k[i] * gG;
                     sw[j][i] += (norm ? x.dz.at(i) : 0.0f) * z;
-                    sp[j][i] += gG * yv;
+                    if constexpr (IN_LDS) sp[0][i] = gG * yv;
+                    else sp[j][i] += gG * yv;
+                }
+                if constexpr (IN_LDS) {
+                    s_lds[2 * j * TPR] += v4{sp[0][0], sp[0][1], sp[0][2], sp[0][3]};
+                    s_lds[(2 * j + 1) * TPR] += v4{sp[0][4], sp[0][5], sp[0][6], sp[0][7]};
                 }
                 if (p.dresidual) store8(static_cast<R*>(p.dresidual) + m * p.H, c[j], dr);
                 if (p.dy) store8(static_cast<Y*>(p.dy) + m * p.H, c[j], dy);
@@ -431,7 +446,13 @@ __global__ __launch_bounds__(kThreads<TPR>) void residual_norm_backward_kernel(B
 #pragma unroll
     for (int j = 0; j < CH; ++j) {
         store8(o, c[j], sw[j]);
-        store8(o + p.H, c[j], sp[j]);
+        if constexpr (IN_LDS) {
+            const v4 a = s_lds[2 * j * TPR], b = s_lds[(2 * j + 1) * TPR];
+            const float f[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+            store8(o + p.H, c[j], f);
+        } else {
+            store8(o + p.H, c[j], sp[j]);
+        }
     }
 }
 
