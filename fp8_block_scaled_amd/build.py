@@ -41,13 +41,14 @@ HIP_SOURCES = ["gfg_gemm.hip", "gfg_gemm256.hip", "gfg_quant.hip", "gfg_int8.hip
 
 
 def _args_step(out: str):
-    """The command that compiles gfg_args.cpp against the installed torch; None without one."""
-    if importlib.util.find_spec("torch") is None:
+    """The command that compiles gfg_args.cpp against the installed torch; None without one or without Python's headers."""
+    headers = sysconfig.get_paths()["include"]
+    if importlib.util.find_spec("torch") is None or not os.path.exists(os.path.join(headers, "Python.h")):
         return None
     import torch
     base = os.path.join(os.path.dirname(torch.__file__), "")
     return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
-            "-isystem", base + "include", "-isystem", base + "include/torch/csrc/api/include", "-I", sysconfig.get_paths()["include"],
+            "-isystem", base + "include", "-isystem", base + "include/torch/csrc/api/include", "-I", headers,
             os.path.join(CSRC, "gfg_args.cpp"), "-o", out, "-L", base + "lib", "-ltorch_python", "-ltorch_cpu", "-lc10"]
 
 
