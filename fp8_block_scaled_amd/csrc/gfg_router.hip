@@ -8,7 +8,8 @@
 //   sigmoid: p = s / sum s,          dl = s (1 - s) / (sum s) (c - sum c p)
 //   and 2 z / (S n) lse e^l / sum e^l from the last term
 //   weights w_j = scale v_j (/ sum v), v the softmax or the sigmoid of the chosen:
-//   dL/dv_j = scale dw_j, or scale (dw_j - sum dw v / sum v) / sum v
+//   dL/dv_j = scale dw_j, or scale (dw_j - sum dw v / sum v) / sum v, which meets the
+//   slope of v_j, of its size, before anything is as large as 1 / sum v
 //
 // LPT lanes share a token, NE neighbouring experts each (LPT also reaches k, so a
 // lane has at most one of the token's choices), and a wave has 64 / LPT tokens;
@@ -491,15 +492,26 @@ __global__ __launch_bounds__(256) void router_backward_kernel(RouterBack p) {
         float g = dw_in, of_softmax = 0.0f;
         if (p.dweights) {
             if (p.renorm) {
+                // A choice's share sc / sum sc is an ordinary number however small the scores:
+                // they are taken relative to the largest choice's, softmaxes always and
+                // sigmoids below e^-60, where s = s (1 - s) = e^l to fp32's last place.  Those
+                // that moe_topk holds as zero, whose weights are zero, stay out.
+                const float most = group_reduce<LPT>(lc, [](float a, float b) { return fmaxf(a, b); });
+                const bool held = chosen && lc > -INFINITY && (SIGMOID ? lc > -88.7f : lc == top || lc - top > -103.0f);
+                if (!SIGMOID || most < -60.0f) sc = ds = lc == most ? 1.0f : __expf(lc - most);
+                sc = held ? sc : 0.0f;
+                const float inv = reciprocal(group_sum<LPT>(sc)), share = sc * inv;
                 // dw less the first choice's, which changes nothing but that equal ones, a
                 // single one above all, give 0 and not the rest of two roundings
-                const int first_choice = first_of<LPT>(chosen, lane);
-                const float less = chosen ? dw_in - __shfl(dw_in, first_choice, 64) : 0.0f, inv = reciprocal(group_sum<LPT>(sc));
-                g = (less - group_sum<LPT>(less * sc) * inv) * inv;
+                const float first_dw = __shfl(dw_in, first_of<LPT>(held, lane), 64), less = held ? dw_in - first_dw : 0.0f;
+                g = (less - group_sum<LPT>(less * share)) * (SIGMOID ? ds * inv : share);
+                g = held ? g : 0.0f;
             } else if (!SIGMOID) {
                 of_softmax = group_sum<LPT>(dw_in * sc);       // (renormalized, this sum is 0)
+                g = chosen ? g * sc : 0.0f;
+            } else {
+                g = chosen ? g * ds : 0.0f;
             }
-            g = chosen ? g * (SIGMOID ? ds : sc) : 0.0f;
         }
 #pragma unroll
         for (int j = 0; j < NE; ++j) d[j] = SIGMOID ? 0.0f : -(e[j] * of_softmax);

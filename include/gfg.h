@@ -588,7 +588,10 @@ GFG_API int residual_norm_backward(const void* dout, const void* dnormed, const 
  * with moe_topk's weights (same score, renormalize and scale; the choice and the
  * bias have no gradient).  dweights [T][k] float or NULL ; factors (with seq_offsets
  * and S as above) and dloss [1] float, both or neither NULL.  Ids outside [0, E)
- * have no weight; an id that stands twice has both.  dlogits is 0 where p is.
+ * have no weight; an id that stands twice has both.  dlogits is 0 where p is.  The
+ * gradient of renormalized weights holds for all scores that fp32 does (softmaxes down
+ * to e^-103 of the token's largest, sigmoids of logits down to -88.7); smaller ones
+ * have none.
  *
  * Equal dweights of renormalized weights (a single one above all) have a gradient
  * of exactly 0.  Counts are exact, the sums fp32 in a fixed order: two calls give the same bytes.
