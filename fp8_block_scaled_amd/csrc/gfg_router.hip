@@ -487,7 +487,7 @@ __global__ __launch_bounds__(256) void router_backward_kernel(RouterBack p) {
         for (int j = 0; j < NE; ++j) {
             v[j] = SIGMOID ? sigmoid(lg[j], &slope[j]) : e[j];
             all += v[j];
-            dot += c[j] * v[j];
+            dot += SIGMOID ? c[j] * 0x1p64f * v[j] : c[j] * v[j];     // (factors of 1e-6 and sigmoids of 1e-37 meet above fp32's lowest)
         }
         float g = dw_in, of_softmax = 0.0f;
         if (p.dweights) {
@@ -521,12 +521,12 @@ __global__ __launch_bounds__(256) void router_backward_kernel(RouterBack p) {
             if constexpr (SIGMOID) {
                 all = group_sum<LPT>(all);
                 inv = reciprocal(all);
-                dot *= inv;
+                dot = dot * inv * 0x1p-64f;
             }
             if (counts) {
-                const float scale = up * inv;
+                // (a slope meets 1 / sum first: the product is at most 1, and dloss times 1 / sum may be anything)
 #pragma unroll
-                for (int j = 0; j < NE; ++j) d[j] += scale * (SIGMOID ? slope[j] : e[j]) * (c[j] - dot);
+                for (int j = 0; j < NE; ++j) d[j] += (SIGMOID ? slope[j] * inv : e[j]) * (up * (c[j] - dot));
                 if (zf != 0.0f) {
                     const float zl = up * zf * lse;
 #pragma unroll

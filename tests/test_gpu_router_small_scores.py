@@ -90,3 +90,23 @@ def test_weights_of_zero_have_no_gradient():
         bias[[2, 5, 9]] = 10.0
         chosen, _ = gfg.moe_topk(dev(logits), torch.empty_like(i), w, score=score, bias=bias)
         assert sorted(chosen[0].tolist()) == [2, 5, 9] and not bool(w.any())
+
+
+@pytest.mark.parametrize("E,k", [(8, 2), (64, 6), (385, 9), (600, 40)])
+@pytest.mark.parametrize("dloss", [1.0, 2.0 ** 16])
+@pytest.mark.parametrize("alpha", [0.01, 1e-6])
+def test_loss_of_tokens_with_small_sigmoids_alone(E, k, alpha, dloss):
+    r, ids = drawn(50, E, k, E)
+    logits = r.uniform(-86, -78, (50, E)).astype(np.float32)
+    l, i = dev(logits), dev(ids)
+    loss, _, factors = gfg.moe_balance_loss(l, i, score="sigmoid", alpha=alpha)
+    want = lo.balance(logits, ids, "sigmoid", alpha)[0]
+    assert abs(float(loss) - want) <= REL * want
+    d = torch.full((50, E), 9.0, device="cuda")
+    gfg.moe_router_backward(l, i, d, score="sigmoid", factors=factors, dloss=torch.tensor(dloss, device="cuda"))
+    f = factors.double().cpu().numpy()
+    ref = lo.router_backward(logits, ids, None, "sigmoid", True, 1.0, f, dloss)
+    p = lo._scores(logits, "sigmoid")[1]
+    size = dloss * p * (f[0, :E] + (f[0, :E] * p).sum(1, keepdims=True))
+    got = d.double().cpu().numpy()
+    assert np.isfinite(got).all() and (np.abs(got - ref) <= REL * size).all()
