@@ -161,10 +161,12 @@ def _gate(gate, M, H, device, name="gate"):
     return _ptr(gate, name, _F32, (H,), device), _GATE_CHANNEL
 
 
-def _norm_inputs(y, residual, weight, post_weight, gate):
+def _norm_inputs(y, residual, weight, post_weight, gate, normed=None):
     dev = _device(residual, "residual")
     M, H = _dims(residual, "residual", 2)
     dtype = residual.dtype if y is None else getattr(y, "dtype", None)
+    if y is None and dtype == torch.float32 and getattr(normed, "dtype", None) in _IN:
+        dtype = normed.dtype                               # (without y the normed rows alone have this type)
     if dtype not in _IN:
         raise TypeError(f"y has dtype {dtype}, expected one of {tuple(_IN)}")
     if residual.dtype not in (dtype, torch.float32):
@@ -182,11 +184,12 @@ def residual_norm(y, residual, weight, post_weight=None, gate=None, alpha=1.0, e
 
     y [M, H] float32, bfloat16 or float16, or None (u = 0); residual [M, H] of y's type or float32; weight and
     post_weight [H] float32 (weight None: no normed rows); gate float32, [H] (one a channel) or [M, 1] (one a row);
-    out like residual (may be residual itself), normed like y; stats [2, M] float32, rstd(y) and rstd(out), for the
-    backward call.  Returns (out, normed, stats); out is allocated where it is not given and there is a y, normed where
-    it is not given and there is a weight, stats never.
+    out like residual (may be residual itself), normed like y (without y of residual's type, or of any of the three beside
+    a float32 residual); stats [2, M] float32, rstd(y) and rstd(out), for the backward call.  Returns (out, normed,
+    stats); out is allocated where it is not given and there is a y, normed where it is not given and there is a weight,
+    stats never.
     """
-    dev, M, H, dtype, inputs = _norm_inputs(y, residual, weight, post_weight, gate)
+    dev, M, H, dtype, inputs = _norm_inputs(y, residual, weight, post_weight, gate, normed)
     if out is None and (y is not None or weight is None):
         out = _empty((M, H), residual.dtype, dev, stream)
     if normed is None and weight is not None:
