@@ -11,6 +11,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -48,8 +49,32 @@ def _args_step(out: str):
     import torch
     base = os.path.join(os.path.dirname(torch.__file__), "")
     return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            f'-DGFG_TORCH_VERSION="{torch.__version__}"',
             "-isystem", base + "include", "-isystem", base + "include/torch/csrc/api/include", "-I", headers,
             os.path.join(CSRC, "gfg_args.cpp"), "-o", out, "-L", base + "lib", "-ltorch_python", "-ltorch_cpu", "-lc10"]
+
+
+def build_args(verbose: bool = False) -> bool:
+    """Build _args.so; whether it is there now.  The calls work without it, a little slower, so a step that fails is a
+    warning, and a module of an earlier build does not stay."""
+    tmp = ARGS + ".tmp"
+    cmd = _args_step(tmp)
+    if cmd:
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        try:
+            r = subprocess.run(cmd, capture_output=True, text=True)
+            failure = None if r.returncode == 0 else f"({r.returncode}): {r.stdout}{r.stderr}"
+        except OSError as e:
+            failure = str(e)
+        if failure is None:
+            os.replace(tmp, ARGS)
+            return True
+        warnings.warn(f"the native argument checks were not built, Python checks in their place: {failure}")
+    for left in (tmp, ARGS):
+        if os.path.exists(left):
+            os.remove(left)
+    return False
 
 
 def build(verbose: bool = False) -> str:
@@ -63,9 +88,6 @@ def build(verbose: bool = False) -> str:
                   "-c", os.path.join(CSRC, "gfg_host.cpp"), "-o", o("gfg_host.o")])
     objs = [o(src.replace(".hip", ".o")) for src in HIP_SOURCES] + [o("gfg_host.o")]
     tmp = LIB + ".tmp"
-    args = _args_step(ARGS + ".tmp")
-    if args:
-        steps.append(args)
 
     def run(cmd):
         if verbose:
@@ -75,11 +97,11 @@ def build(verbose: bool = False) -> str:
             raise RuntimeError(f"build step failed ({r.returncode}): {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
 
     with ThreadPoolExecutor(4) as pool:                    # (a compiler holds up to a few GiB)
+        args = pool.submit(build_args, verbose)
         list(pool.map(run, steps))
+        args.result()
     run([hipcc, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-pthread", *objs, "-o", tmp])
     os.replace(tmp, LIB)
-    if args:
-        os.replace(ARGS + ".tmp", ARGS)
     return LIB
 
 

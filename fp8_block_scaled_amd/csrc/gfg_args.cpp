@@ -2,13 +2,37 @@
 // native call, a fifth of the time that the same questions take one by one in
 // Python (0.08 and 0.4 us a tensor; a call of a layer has four to fourteen, and a
 // launch takes 2 us).  It answers only for tensors that pass; every other one is
-// looked at again in Python, which words the error.
+// looked at again in Python, which words the error.  It reads tensors by the layout
+// of the torch that it was compiled against (GFG_TORCH_VERSION), and does not load
+// beside another one, nor in another Python.
 #include <Python.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/DynamicTypes.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cstring>
+
 namespace {
+
+// Sets ImportError and returns false where torch or Python is not the one compiled against.
+bool same_versions() {
+    char python[32];
+    const int n = PyOS_snprintf(python, sizeof python, "%d.%d.", PY_MAJOR_VERSION, PY_MINOR_VERSION);
+    if (std::strncmp(Py_GetVersion(), python, size_t(n)) != 0) {
+        PyErr_Format(PyExc_ImportError, "_args was built for Python %d.%d", PY_MAJOR_VERSION, PY_MINOR_VERSION);
+        return false;
+    }
+    PyObject* const torch = PyImport_ImportModule("torch");
+    PyObject* const version = torch ? PyObject_GetAttrString(torch, "__version__") : nullptr;
+    const bool same = version && PyUnicode_Check(version) && PyUnicode_CompareWithASCIIString(version, GFG_TORCH_VERSION) == 0;
+    Py_XDECREF(version);
+    Py_XDECREF(torch);
+    if (!same) {
+        PyErr_Clear();
+        PyErr_SetString(PyExc_ImportError, "_args was built for torch " GFG_TORCH_VERSION);
+    }
+    return same;
+}
 
 // address(tensor, dtypes, shape, device index): the address of a dense tensor on
 // that GPU, of that shape (a tuple) and one of the types; None for anything else.
@@ -49,4 +73,4 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_args", nullptr, -1, methods, null
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__args() { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__args() { return same_versions() ? PyModule_Create(&module) : nullptr; }

@@ -16,7 +16,7 @@ from . import IN_BF16, IN_F16, IN_F32, OUT_BF16, OUT_F16, _check, _check_stream,
 
 try:
     from ._args import address as _address
-except ImportError:                                        # built for another torch, or without one: Python answers
+except ImportError:                                        # built for another torch or not at all: Python answers
     def _address(t, dtypes, shape, index):
         return None
 

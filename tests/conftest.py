@@ -7,6 +7,17 @@ ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 if ROOT not in sys.path:
     sys.path.insert(0, ROOT)
 
+try:
+    import torch  # noqa: F401
+    from fp8_block_scaled_amd import _args  # noqa: F401
+    CHECKS = "native"
+except ImportError:                                        # an extra that needs Python's headers: its own tests need it
+    CHECKS, collect_ignore = "Python", ["test_tensor_arguments.py"]
+
+
+def pytest_report_header(config):
+    return f"checks of tensor arguments: {CHECKS}"
+
 
 def pytest_configure(config):
     config.addinivalue_line("markers", "gpu: needs an MI355X (gfx950) GPU and the built HIP library")
