@@ -530,6 +530,11 @@ int64_t backward_groups(int64_t M, int64_t H) {
     const int64_t most = g.turns <= 5 * 256 && g.most > 256 ? 256 : g.most, each = (g.turns + most - 1) / most;
     return (g.turns + each - 1) / each;
 }
+// The workspace holds as many workgroups' sums as M rows or fewer ever take.
+int64_t backward_bytes(int64_t M, int64_t H) {
+    const Grid g = grid_of(M, H, kBackwardWaves);
+    return std::min(g.turns, g.most) * 2 * H * 4;
+}
 
 int launched() {
     const hipError_t e = hipGetLastError();
@@ -606,7 +611,7 @@ extern "C" int residual_norm_fp8(const void* y, const void* residual, const floa
 }
 
 extern "C" int64_t residual_norm_backward_workspace_bytes(int64_t M, int64_t H) {
-    return M > 0 && H > 0 ? backward_groups(M, H) * 2 * H * 4 : 0;
+    return M > 0 && H > 0 ? backward_bytes(M, H) : 0;
 }
 
 extern "C" int residual_norm_backward(const void* dout, const void* dnormed, const void* out, const void* y, const float* stats,

@@ -600,19 +600,27 @@ void by_type(int32_t dtype, F f) {
     else f(_Float16{});
 }
 
-// Tokens of a workgroup's range: at least as many as it has lanes for at a time,
+// Tokens that a workgroup of the loss has lanes for.
+int64_t tokens_at_a_time(int64_t E) {
+    int64_t lanes = 8;
+    while (lanes < 64 && lanes * 8 < E) lanes *= 2;
+    return SUMS_THREADS / lanes;
+}
+// Tokens of a workgroup's range: at least as many as it has lanes for,
 // and up to four times as many where one range then has them all, which saves the
 // second launch (E = 64: 64 tokens 4.2 us, 256 6.2, 257 in two launches 8.5).
 int64_t tokens_a_range(int64_t T, int64_t E) {
-    const int64_t n = (T + kMostChunks - 1) / kMostChunks;
-    int64_t lanes = 8;
-    while (lanes < 64 && lanes * 8 < E) lanes *= 2;
-    const int64_t least = SUMS_THREADS / lanes;
+    const int64_t n = (T + kMostChunks - 1) / kMostChunks, least = tokens_at_a_time(E);
     if (T > least && T <= 4 * least) return T;
     return n < least ? least : n;
 }
 int64_t ranges(int64_t T, int64_t E) { return T > 0 ? (T + tokens_a_range(T, E) - 1) / tokens_a_range(T, E) : 0; }
-int64_t piece_bytes(int64_t T, int64_t E, int64_t S) { return (ranges(T, E) + S) * (2 * E + 2) * 4; }
+// The workspace holds as many pieces as T tokens or fewer ever have.
+int64_t most_ranges(int64_t T, int64_t E) {
+    const int64_t n = (T + tokens_at_a_time(E) - 1) / tokens_at_a_time(E);
+    return n < kMostChunks ? n : kMostChunks;
+}
+int64_t piece_bytes(int64_t T, int64_t E, int64_t S) { return (most_ranges(T, E) + S) * (2 * E + 2) * 4; }
 int64_t finishers(int64_t E, int64_t S) { return (E + 31) / 32 * S; }
 
 int launched() {

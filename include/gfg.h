@@ -534,8 +534,8 @@ GFG_API int fp8_quantize_weight_device(const void* w, int32_t in_dtype, int32_t 
  *   Each output may be NULL.  accumulate: dweight, dpost_weight and a channel
  *   gate's dgate are added to.  M = 0 writes zeros to those (unless accumulated).
  *   workspace: residual_norm_backward_workspace_bytes(M, H) bytes of device memory,
- *   16-byte aligned, uninitialized; needed for dweight, dpost_weight and a channel
- *   gate's dgate.
+ *   16-byte aligned, uninitialized (what M rows need serves fewer too); needed for
+ *   dweight, dpost_weight and a channel gate's dgate.
  *
  * All sums and statistics are fp32 (so a row's squares have to sum up within
  * fp32's range); every output is rounded once.  Two calls give the same bytes.
@@ -579,7 +579,7 @@ GFG_API int residual_norm_backward(const void* dout, const void* dnormed, const 
  *   loss [1] float ; counts [S][E] int32
  *   factors [S][E+1] float: alpha f_e / (S n), then 2 z / (S n), for the gradient
  *   workspace: moe_balance_workspace_bytes(T, E, S) bytes of device memory, 16-byte
- *   aligned, uninitialized
+ *   aligned, uninitialized (what T tokens need serves fewer too)
  *
  * moe_router_backward: dlogits [T][E] (the logits' type) of
  *
