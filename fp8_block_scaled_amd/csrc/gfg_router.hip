@@ -8,8 +8,8 @@
 //   sigmoid: p = s / sum s,          dl = s (1 - s) / (sum s) (c - sum c p)
 //   and 2 z / (S n) lse e^l / sum e^l from the last term
 //   weights w_j = scale v_j (/ sum v), v the softmax or the sigmoid of the chosen:
-//   dL/dv_j = scale dw_j, or scale (dw_j - sum dw v / sum v) / sum v, which meets the
-//   slope of v_j, of its size, before anything is as large as 1 / sum v
+//   dL/dv_j = scale dw_j, or scale (dw_j - sum dw v / sum v) / sum v
+//   (sums of scores below 2^-30 go a way of their own, on which 1 / sum stays in range)
 //
 // LPT lanes share a token, NE neighbouring experts each (LPT also reaches k, so a
 // lane has at most one of the token's choices), and a wave has 64 / LPT tokens;
@@ -407,6 +407,8 @@ __global__ __launch_bounds__(1024) void balance_finish_kernel(RouterArgs p) {
     if (lane == 0) *p.loss = t;
 }
 
+constexpr float kSmall = 0x1p-30f;            // sums of scores below it
+
 struct RouterBack {
     const void* logits;
     const int32_t *ids, *offsets;
@@ -487,31 +489,32 @@ __global__ __launch_bounds__(256) void router_backward_kernel(RouterBack p) {
         for (int j = 0; j < NE; ++j) {
             v[j] = SIGMOID ? sigmoid(lg[j], &slope[j]) : e[j];
             all += v[j];
-            dot += SIGMOID ? c[j] * 0x1p64f * v[j] : c[j] * v[j];     // (factors of 1e-6 and sigmoids of 1e-37 meet above fp32's lowest)
+            dot += c[j] * v[j];
         }
         float g = dw_in, of_softmax = 0.0f;
         if (p.dweights) {
             if (p.renorm) {
-                // A choice's share sc / sum sc is an ordinary number however small the scores:
-                // they are taken relative to the largest choice's, softmaxes always and
-                // sigmoids below e^-60, where s = s (1 - s) = e^l to fp32's last place.  Those
-                // that moe_topk holds as zero, whose weights are zero, stay out.
-                const float most = group_reduce<LPT>(lc, [](float a, float b) { return fmaxf(a, b); });
-                const bool held = chosen && lc > -INFINITY && (SIGMOID ? lc > -88.7f : lc == top || lc - top > -103.0f);
-                if (!SIGMOID || most < -60.0f) sc = ds = lc == most ? 1.0f : __expf(lc - most);
-                sc = held ? sc : 0.0f;
-                const float inv = reciprocal(group_sum<LPT>(sc)), share = sc * inv;
+                float total = group_sum<LPT>(sc);
+                if (total < kSmall) {
+                    // shares of small scores are ordinary numbers: they come from scores relative to
+                    // the largest choice's (sigmoids this small are e^l to fp32's last place, and so
+                    // is their slope).  Scores that moe_topk holds as zero, whose weights are zero,
+                    // stay out.
+                    const float most = group_reduce<LPT>(lc, [](float a, float b) { return fmaxf(a, b); });
+                    const bool held = lc > (SIGMOID ? -88.7f : fmaxf(top - 103.0f, -INFINITY));
+                    sc = held ? __expf(lc - most) : 0.0f;
+                    ds = sc;
+                    total = group_sum<LPT>(sc);
+                }
                 // dw less the first choice's, which changes nothing but that equal ones, a
                 // single one above all, give 0 and not the rest of two roundings
-                const float first_dw = __shfl(dw_in, first_of<LPT>(held, lane), 64), less = held ? dw_in - first_dw : 0.0f;
-                g = (less - group_sum<LPT>(less * share)) * (SIGMOID ? ds * inv : share);
-                g = held ? g : 0.0f;
+                const int first_choice = first_of<LPT>(chosen, lane);
+                const float less = chosen ? dw_in - __shfl(dw_in, first_choice, 64) : 0.0f, inv = reciprocal(total);
+                g = (less - group_sum<LPT>(less * sc) * inv) * inv;
             } else if (!SIGMOID) {
                 of_softmax = group_sum<LPT>(dw_in * sc);       // (renormalized, this sum is 0)
-                g = chosen ? g * sc : 0.0f;
-            } else {
-                g = chosen ? g * ds : 0.0f;
             }
+            g = chosen ? g * (SIGMOID ? ds : sc) : 0.0f;
         }
 #pragma unroll
         for (int j = 0; j < NE; ++j) d[j] = SIGMOID ? 0.0f : -(e[j] * of_softmax);
@@ -521,12 +524,23 @@ __global__ __launch_bounds__(256) void router_backward_kernel(RouterBack p) {
             if constexpr (SIGMOID) {
                 all = group_sum<LPT>(all);
                 inv = reciprocal(all);
-                dot = dot * inv * 0x1p-64f;
+                dot *= inv;
+                if (all < kSmall) {
+                    // (factors times sigmoids may lie below fp32's range, and dloss / sum above it)
+                    dot = 0.0f;
+#pragma unroll
+                    for (int j = 0; j < NE; ++j) {
+                        dot += c[j] * (v[j] * inv);
+                        slope[j] *= inv;
+                    }
+                    dot = group_sum<LPT>(dot);
+                    inv = 1.0f;
+                }
             }
             if (counts) {
-                // (a slope meets 1 / sum first: the product is at most 1, and dloss times 1 / sum may be anything)
+                const float scale = up * inv;
 #pragma unroll
-                for (int j = 0; j < NE; ++j) d[j] += (SIGMOID ? slope[j] * inv : e[j]) * (up * (c[j] - dot));
+                for (int j = 0; j < NE; ++j) d[j] += scale * (SIGMOID ? slope[j] : e[j]) * (c[j] - dot);
                 if (zf != 0.0f) {
                     const float zl = up * zf * lse;
 #pragma unroll

@@ -110,3 +110,31 @@ def test_loss_of_tokens_with_small_sigmoids_alone(E, k, alpha, dloss):
     size = dloss * p * (f[0, :E] + (f[0, :E] * p).sum(1, keepdims=True))
     got = d.double().cpu().numpy()
     assert np.isfinite(got).all() and (np.abs(got - ref) <= REL * size).all()
+
+
+@pytest.mark.parametrize("E,k", [(7, 2), (40, 4), (100, 9), (200, 6), (385, 9), (600, 40)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_small_scores_beside_ordinary_ones(E, k, score):
+    """Tokens that share a wave with others of either kind get the gradients that they have alone."""
+    r, ids = drawn(96, E, k, E + 3)
+    logits = r.standard_normal((96, E)).astype(np.float32)
+    small = r.random(96) < 0.5
+    if score == "sigmoid":
+        logits[small] = r.uniform(-86, -78, (int(small.sum()), E))
+    else:
+        low = logits.copy()
+        np.put_along_axis(low, ids, -r.uniform(75, 100, ids.shape).astype(np.float32), 1)
+        logits[small] = low[small]
+    dw = r.standard_normal(ids.shape).astype(np.float32)
+    factors = torch.rand(1, E + 1, device="cuda") * 1e-5
+
+    def gradient(rows):
+        d = torch.full((len(rows), E), 9.0, device="cuda")
+        gfg.moe_router_backward(dev(logits[rows]), dev(ids[rows]), d, dweights=dev(dw[rows]), score=score, factors=factors,
+                                dloss=torch.tensor(2.0 ** 16, device="cuda"))
+        return d
+
+    every = gradient(np.arange(96))
+    assert bool(torch.isfinite(every).all()) and bool((every != 0).any(1).all())
+    for rows in (np.flatnonzero(small), np.flatnonzero(~small), np.arange(95, -1, -1)):
+        assert torch.equal(gradient(rows), every[torch.from_numpy(rows.copy()).cuda()])
