@@ -843,14 +843,16 @@ int launch_stream(F8Params p, int out_dtype, hipStream_t s) {
     return launched();
 }
 
-// The tile by how many of each size there are (M x N x K, us, the product alone,
-// cold weights, the chosen tile first):
+// The tile by how many of each size there are, asked in this order (M x N x K, us, the
+// product alone, cold weights, the chosen tile first):
 //  * more tiles of 128 x 128 than CUs, but not of 256 x 128: those (1783 x 3777 x 14672:
 //    141, 256 x 256 186; 2048 x 4096 x 7168: 55, 75; 2200 x 2048 x 4096: 30, 45; 4000 x
 //    2000 x 528: 12.2, 17.5);
 //  * more of both: 256 x 256 (4096 x 4096 x 16384: 205-240, 128 x
 //    128 346-370; 4096 x 7168 x 2304: 70, 110; 7168 x 2304 x 4096 with a scale a row of
-//    both: 62, 97);
+//    both: 62, 97); also for few rows of an output so wide, from 4 rows and 32769 columns
+//    on, where it is the slower one (16 x 33024 x 7168: 77, streamed 53; 32: 78, 55; 64:
+//    78, 70; 128: 78, 83; 16 x 129280 x 7168: 177, 174);
 //  * up to 16 rows: streamed, 16 x 16 on eight waves where those do not outnumber
 //    the CUs (1 x 2048 x 7168: 6.7, 16 x 32 8.0; 16 x 2048 x 16384: 12.5, 16.0; 1 x
 //    4096 x 4096: 6.0, 6.3), else 16 x 32 (1 x 7168 x 2304: 5.8);
@@ -861,7 +863,9 @@ int launch_stream(F8Params p, int out_dtype, hipStream_t s) {
 //  * up to two tiles of 32 x 32 a CU: those, streamed (300 x 1500 x 2304: 6.8, 64 x 64
 //    7.7; 128 x 2048 x 7168: 7.9, 16.6; but 400 x 1500 x 2304, 611 of them: 8.8, 7.7);
 //  * else 64 x 64 (512 x 2048 x 7168: 18.3; 512 x 4096 x 4096: 18.9).
-// All of them take in about 50 GB/s a CU, which bounds 64 x 64.
+// Where a CU has one tile, what it takes in sets the time: 64 x 64 of 512 x 2048 x 7168
+// 917 KB in 18.3 us, 50 GB/s with 48 KB in flight, 12% of the matrix pipes; 32 x 32 of
+// 128 x 2048 x 7168 459 KB in 7.9, 58.
 // A tile's lane loads the scale bytes of its RB (CB) neighbouring rows at once,
 // so an operand has to have that many rows: up to 16 rows of A go to RB = 1,
 // and the gradient of a weight has at least 16 of both.
@@ -938,10 +942,12 @@ int quantize_rows(const void* x, int32_t in_dtype, uint8_t* q, uint8_t* scale, i
 //  * up to 16 rows: 1 x 7168 x 2304 6.5, 7.8; 16 x 7168 x 2304 7.2, 8.1; 16 x 2048 x
 //    7168 11.1, 11.5; 4 x 2048 x 16384 14.0, 16.2; but 16 x 2048 x 16384 20.3, 18.5;
 //    16 x 300 x 16384 18.9, 12.8;
-//  * more rows, in tiles of 32 x 32, with up to three units a wave (a lane's loads
-//    are 16 bytes of a row each, which costs more than the launch soon): bf16 77 x
-//    1003 x 1072 6.1, 6.7; 300 x 528 x 1040 6.1, 6.9; 512 x 512 x 512 4.5, 6.1; but 32 x
-//    7168 x 2304 10.0, 8.8; f32 128 x 512 x 512 4.7, 5.8, but 77 x 1003 x 1072 8.3, 6.7;
+//  * more rows, in tiles of 32 x 32, with up to ten units of K in 16 bits and five in 32
+//    (a lane's loads are 16 bytes of a row each, which costs more than the launch soon):
+//    bf16 77 x 1003 x 1072 6.1, 6.7; 300 x 528 x 1040 6.1, 6.9; 512 x 512 x 512 4.5, 6.1;
+//    77 x 1003 of 8, 10, 11, 12 and 14 units 5.7, 6.3; 6.5, 6.8; 6.9, 6.9; 6.8, 6.9; 7.3,
+//    7.3; 300 x 528 of 10, 12 and 14 6.6, 6.9; 7.1, 7.2; 7.8, 7.7; 32 x 7168 x 2304 10.0,
+//    8.8; f32 128 x 512 of 4, 5 and 6 units 4.6, 5.6; 5.5, 5.9; 5.9, 5.9;
 //    and up to two tiles a CU: 128 x 4096 x 512 6.4, 7.3, but 256 x 4096 x 512 10.6, 7.0.
 // A workgroup has one tile of its own shape, so not under a grid limit or a set shape.
 bool few(const F8Params& p, int size, int cus) {

@@ -15,8 +15,9 @@
 // the rows, S = sum G yh (with a token's gate inside: sum g G yh), times g or wp.
 //
 // A row's lanes hold it in registers (two chunks of 8 elements a lane, four above
-// 16384) between the sums and the outputs, so it is read once: both passes are bound
-// by HBM, or by a launch and one row's chain of load, sum and store.
+// 16384) between the sums and the outputs, so it is read once (but by the backward pass
+// above 8192, which reads it again): both passes are bound by HBM, or by a launch and one
+// row's chain of load, sum and store.
 //   forward, 4096 x 7168 bf16 with an f32 residual: 354 MB in 69 us, 5.1 TB/s (a large
 //   copy: 5.06); the FP8 rows of 512 x 7168 9 us; one row 4.2 us
 //   backward, 8192 x 4096 bf16: 421 MB in 79-82 us, 5.2 TB/s, and the column sums 7 us;
@@ -506,7 +507,8 @@ void by_type(int32_t dtype, int32_t residual_dtype, F f) {
 
 // Workgroups of a pass over M rows: at most `waves` waves in all, as many as the
 // registers leave room for on 256 CUs, one a CU at least, each of which then walks
-// rows.
+// rows.  (The whole GPU's CUs and not those that there are: the size of a workspace is
+// asked for without one, and must not change.)
 constexpr int64_t kForwardWaves = 4096, kBackwardWaves = 2048;
 struct Grid { int64_t turns, most; };          // times a workgroup's rows that there are, and workgroups
 Grid grid_of(int64_t M, int64_t H, int64_t waves) {

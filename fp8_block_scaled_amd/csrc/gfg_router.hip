@@ -15,9 +15,11 @@
 // lane has at most one of the token's choices), and a wave has 64 / LPT tokens;
 // a row of logits is read once by each of the two passes.  32768 tokens of 385, nine
 // choices, sigmoid, bf16: the loss 11 us and 7.5 for the sum over its 519 pieces, the
-// gradient 25, 10 thousand vector instructions a SIMD (exp, reciprocals, reductions):
-// arithmetic bounds both, at 2.2 TB/s of memory traffic.  Few tokens take a launch each
-// (77 of 64: 4.2 and 3.2 us).
+// gradient 25, at 2.2 TB/s of memory traffic.  Vector instructions (exp, reciprocals,
+// reductions) fill two thirds of both: the gradient's 10 thousand a SIMD keep it busy
+// for 42 thousand of some 62 thousand cycles; LDS is active for 12 thousand a CU, of
+// which 5.5 are bank conflicts of the choices' array; the rest is waiting.  Few tokens
+// take a launch each (77 of 64: 4.2 and 3.2 us).
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
